@@ -23,7 +23,8 @@ OUT_STAMPS = PKG / "libkda_stamps.so"
 BUILD = PKG / "_build"
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["kda_api.cpp", "kda_decay.hip", "kda_chunk.hip", "kda_decode.hip", "kda_bwd.hip", "kda_noalloc.hip"]
+SOURCES = ["kda_api.cpp", "kda_mix_api.cpp", "kda_decay.hip", "kda_chunk.hip", "kda_decode.hip", "kda_bwd.hip", "kda_noalloc.hip",
+           "kda_conv.hip", "kda_qknorm.hip"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -6,29 +6,14 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kda_check.h"
 #include "kda_launch.h"
 
-namespace {
-
-constexpr int kChunk = 64;
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool supported_d(int d) { return d == 64 || d == 128; }
-bool valid_dtype(int dt) { return dt == KDA_F32 || dt == KDA_BF16; }
-
-// Largest element count of any [B, T, H, d] tensor accepted (64-bit offsets
-// are used throughout; this only rejects sizes whose byte count overflows).
-bool size_ok(long long a, long long b, long long c, long long d) {
-  const long long lim = (1LL << 62);
-  long long x = a;
-  for (long long y : {b, c, d}) {
-    if (y <= 0 || x > lim / y) return false;
-    x *= y;
-  }
-  return true;
-}
-
-}  // namespace
+using kda::aligned16;
+using kda::kChunk;
+using kda::size_ok;
+using kda::supported_d;
+using kda::valid_dtype;
 
 extern "C" {
 
@@ -41,12 +26,14 @@ const char* kda_status_str(int s) {
     case KDA_ERR_SHAPE: return "a size is non-positive or too large";
     case KDA_ERR_DTYPE: return "dtype is not KDA_F32 or KDA_BF16";
     case KDA_ERR_ALIGN: return "a tensor pointer is not 16-byte aligned";
-    case KDA_ERR_UNSUPPORTED: return "unsupported dk/dv/chunk (dk, dv in {64,128}; chunk 64)";
+    case KDA_ERR_UNSUPPORTED: return "unsupported dk/dv/chunk (dk, dv in {64,128}; chunk 64), convolution width (2..4), "
+                                     "head width or rotation (multiples of 8, heads to 512)";
     case KDA_ERR_WORKSPACE: return "workspace missing or smaller than kda_fwd_workspace_bytes";
     case KDA_ERR_RANGE: return "input value out of range (log-decay outside [gmin, 0], or gmin outside [-5, 0))";
     case KDA_ERR_HIP: return "HIP launch failed";
     case KDA_ERR_INCOMPLETE:
       return "the fused prefill gave up on a hand-off wait (GPU shared with other work?): outputs incomplete";
+    case KDA_ERR_OVERLAP: return "an output overlaps a tensor it must be apart from";
     default: return "unknown status";
   }
 }

@@ -106,4 +106,73 @@ hipError_t launch_bwd_chunks(int is_bf16, const void* q, const void* k, const vo
                              int dv, float* dq, float* dk_, float* dv_, float* dg, float* dbeta, float* dh0,
                              hipStream_t st);
 
+// The sequences of one launch of the token-walking operators (short
+// convolution, state space scan).  n = 0: sequences of T tokens each, packed
+// one behind the other, `parts` parts each.  n > 0: packed sequences n0 ..
+// n0+n-1 of the call (at most kMaxVarSeq a launch): sequence n0+i is rows
+// cu[i] .. cu[i+1]-1, its parts are items cc[i] .. cc[i+1]-1 of the launch.
+struct SeqTab {
+  int n, n0, T, parts, part, items;
+  int cu[kMaxVarSeq + 1];
+  int cc[kMaxVarSeq + 1];
+};
+// The table of sequences n0 .. of a call, cut into parts of `part` tokens:
+// B sequences of T (cu == nullptr, one launch), or N packed ones from n0 on
+// (as many as one launch carries).  Returns the first sequence not covered.
+// items < 0: more items than a launch can number.
+int make_seq_tab(SeqTab& s, const int* cu, int N, int n0, int B, int T, int part);
+
+// out0[c] (c < n0) and out1[c - n0]: column sums of part [nrows][n0 + n1], in a
+// fixed order (either output may be null).
+hipError_t launch_sum_rows(const float* part, unsigned nrows, unsigned n0, unsigned n1, float* out0, float* out1,
+                           hipStream_t stream);
+
+// Short causal convolution: see kda_conv.hip.  dtypes: 0 fp32, 1 bf16.
+struct ConvArgs {
+  const void* x;
+  long long ldx;       // elements between tokens of x
+  const float* w;      // [D][W]
+  const float* bias;   // [D] or null
+  const void* s0;      // [N][W-1][D] or null
+  void* st;            // [N][W-1][D] or null
+  void* y;             // [rows][D]
+  int silu, D, W;
+};
+hipError_t launch_conv_fwd(int is_bf16, const ConvArgs& a, const int* cu, int N, int B, int T, hipStream_t stream);
+hipError_t launch_conv_step(int is_bf16, const ConvArgs& a, int B, hipStream_t stream);
+struct ConvBwdArgs {
+  ConvArgs f;          // y unused
+  const void* dy;      // [rows][D]
+  int dy_bf16;
+  const void* dst;     // [N][W-1][D] or null
+  void* dx;            // [rows][D]
+  float* dw;           // [D][W]
+  float* dbias;        // [D] or null
+  void* ds0;           // [N][W-1][D] or null
+  float* part;         // workspace
+};
+size_t conv_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D, int W);
+hipError_t launch_conv_bwd(int is_bf16, const ConvBwdArgs& a, const int* cu, int N, int B, int T, hipStream_t stream);
+
+// Norms of query and key heads with the position rotation: see kda_qknorm.hip.
+struct QkArgs {
+  const void* x[2];      // q, k: [tokens][H][d] with token strides ld
+  long long ld[2];
+  const float* w[2];     // [d] or null
+  void* y[2];            // [tokens][H][d]: normed rows, or dq / dk (backward)
+  const void* dy[2];     // backward: [tokens][H][d]
+  int H[2];              // H[1] may be 0
+  const float *cos, *sin;   // [n_pos][rot / 2]
+  const int* pos;        // [tokens] or null: pos0 + t
+  int pos0, n_pos;
+  int rms, inter, d, rot;
+  float eps;
+  long long tokens;
+  int T;
+  float* part;           // backward workspace
+};
+hipError_t launch_qk_fwd(int is_bf16, const QkArgs& a, hipStream_t stream);
+size_t qk_bwd_workspace_bytes(long long tokens, int Hq, int Hk, int d);
+hipError_t launch_qk_bwd(int is_bf16, int dy_bf16, const QkArgs& a, float* dwq, float* dwk, hipStream_t stream);
+
 }  // namespace kda

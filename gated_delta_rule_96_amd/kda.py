@@ -22,9 +22,11 @@ STAMPS_LIB_PATH = PKG / "libkda_stamps.so"
 STAMP_WGS, STAMP_WAVES, STAMP_SLOTS, STAMP_ROLE, STAMP_COUNT = 256, 8, 32, 29, 30
 
 KDA_F32, KDA_BF16 = 0, 1
-KDA_ERR_UNSUPPORTED, KDA_ERR_RANGE, KDA_ERR_INCOMPLETE = 5, 7, 9
+KDA_ERR_UNSUPPORTED, KDA_ERR_RANGE, KDA_ERR_INCOMPLETE, KDA_ERR_OVERLAP = 5, 7, 9, 10
 KDA_STAGES_UNBOUNDED = 4
 KDA_LAYER_QK_L2NORM = 1
+KDA_CONV_SILU = 1
+KDA_QK_RMS, KDA_QK_INTERLEAVED = 1, 2
 CHUNK = 64
 GMIN = -5.0
 
@@ -82,6 +84,17 @@ def lib() -> ctypes.CDLL:
         L.kda_fwd_status.argtypes = [P, P]
         L.kda_fwd_status_word.restype = P
         L.kda_fwd_status_word.argtypes = [P]
+        LL = ctypes.c_longlong
+        for name, res, args in (
+                ("kda_conv_fwd", I, [P, LL, P, P, P, P, P, I, I, I, I, I, I, P, I, P]),
+                ("kda_conv_step", I, [P, LL, P, P, P, P, P, I, I, I, I, I, P]),
+                ("kda_conv_bwd_workspace_bytes", S, [I, I, I, I, I]),
+                ("kda_conv_bwd", I, [P, LL, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, I, P, I, P, S, P]),
+                ("kda_qk_norm_rope", I, [P, LL, P, LL, P, P, P, P, P, I, I, F, P, P] + [I] * 8 + [P]),
+                ("kda_qk_bwd_workspace_bytes", S, [I, I, I, I, I]),
+                ("kda_qk_norm_rope_bwd", I, [P, LL, P, LL, P, P, P, P, P, I, I, F, P, P, I, P, P, P, P] + [I] * 8 + [P, S, P])):
+            getattr(L, name).restype = res
+            getattr(L, name).argtypes = args
         if hasattr(L, "kda_stamps_read"):
             L.kda_stamps_read.restype = I
             L.kda_stamps_read.argtypes = [P, S]
@@ -399,6 +412,225 @@ def decode_step_layer(q, k, v, z, A, beta, state, *, og=None, qk_l2norm=False, s
                                        float(scale), _ptr(state), _ptr(o), flags, dt, B, H, dk, dv,
                                        _stream(q.device)), "kda_decode_step_layer")
     return o
+
+
+# ---------------------------------------------------------------- operators around the recurrence
+def _rows(t, name, lead, inner):
+    """Pointer and token stride of an input [*lead, *inner] that may be a slice
+    of a wider tensor: inner elements contiguous, all tokens one distance apart."""
+    if tuple(t.shape) != lead + inner:
+        raise ValueError(f"{name} must be {list(lead + inner)}, got {list(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must live on the GPU")
+    st, n = t.stride(), 1
+    for size, stride in zip(reversed(inner), reversed(st[len(lead):])):
+        if size != 1 and stride != n:
+            raise ValueError(f"{name}: the elements of a token must be contiguous")
+        n *= size
+    ld = n
+    if len(lead) == 1:
+        ld = st[0] if lead[0] > 1 else n
+    elif lead[1] > 1:
+        ld = st[1]
+        if lead[0] > 1 and st[0] != lead[1] * ld:
+            raise ValueError(f"{name}: tokens must be one distance apart across the batch")
+    elif lead[0] > 1:
+        ld = st[0]
+    if ld < n:
+        raise ValueError(f"{name}: tokens overlap (an expanded tensor?)")
+    return t.data_ptr(), ld
+
+
+def _dense(t, name, shape, dtype):
+    """Pointer of a contiguous tensor of this shape and type (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _ptr(t)
+
+
+def _same_device(dev, **tensors):
+    for n, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, not on {dev}")
+
+
+def _call(dev, name, *args):
+    """Calls entry point `name` on dev's current stream (with dev the current device)."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(getattr(lib(), name)(*args, _stream(dev)), name)
+    else:
+        with torch.cuda.device(dev):
+            _check(getattr(lib(), name)(*args, _stream(dev)), name)
+
+
+def _packed(cu_seqlens, B, T):
+    """(host array or None, sequences) of a call's cu_seqlens."""
+    if cu_seqlens is None:
+        return None, B
+    arr, n = _cu_array(cu_seqlens)
+    if B != 1:
+        raise ValueError("packed sequences need B = 1")
+    if n < 1 or arr[0] != 0 or arr[n] != T or any(arr[i + 1] < arr[i] for i in range(n)):
+        raise ValueError(f"cu_seqlens must rise from 0 to {T}")
+    return arr, n
+
+
+def _given(out, shape, dtype, dev, name):
+    """`out` checked, or a new tensor."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _dense(out, name, shape, dtype)
+    return out
+
+
+def _scratch(workspace, nbytes, dev, name):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.numel() < nbytes:
+        raise ValueError(f"workspace must be uint8 of at least {name} = {nbytes} bytes")
+    return workspace
+
+
+def conv_fwd(x, w, bias=None, s0=None, *, silu=True, cu_seqlens=None, final_state=True, st=None, out=None):
+    """y, st = conv_fwd(x, w, bias, s0): short causal depthwise convolution
+    (kda_conv_fwd).  x [B,T,D] (bf16 or fp32, may be a slice of a wider
+    tensor); w [D,W] and bias [D] fp32, W in 2..4; s0 / st [N,W-1,D] of x's
+    type, the tokens before / the last tokens of each of the N = B sequences,
+    or of those cu_seqlens (host ints) cuts the packed axis into; st may be s0
+    itself.  silu: y = z Sigmoid(z)."""
+    B, T, D = x.shape
+    W = w.shape[-1]
+    dt = _dtype_code(x)
+    px, ld = _rows(x, "x", (B, T), (D,))
+    arr, N = _packed(cu_seqlens, B, T)
+    _same_device(x.device, w=w, bias=bias, s0=s0, st=st, out=out)
+    y = _given(out, (B, T, D), x.dtype, x.device, "out")
+    if final_state and st is None:
+        st = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device)
+    _call(x.device, "kda_conv_fwd", px, ld, _dense(w, "w", (D, W), torch.float32), _dense(bias, "bias", (D,), torch.float32),
+          _dense(s0, "s0", (N, W - 1, D), x.dtype), _dense(st if final_state else None, "st", (N, W - 1, D), x.dtype),
+          y.data_ptr(), KDA_CONV_SILU if silu else 0, dt, B, T, D, W, arr, N)
+    return y, (st if final_state else None)
+
+
+def conv_step(x, w, bias, state, *, silu=True, state_out=None, out=None):
+    """y = conv_step(x, w, bias, state): one token x [B,D] per sequence
+    against its state [B,W-1,D], which moves on in place, or into state_out
+    (the old state is then kept)."""
+    B, D = x.shape
+    W = w.shape[-1]
+    px, ld = _rows(x, "x", (B,), (D,))
+    _same_device(x.device, w=w, bias=bias, state=state, state_out=state_out, out=out)
+    y = _given(out, (B, D), x.dtype, x.device, "out")
+    so = state if state_out is None else state_out
+    _call(x.device, "kda_conv_step", px, ld, _dense(w, "w", (D, W), torch.float32), _dense(bias, "bias", (D,), torch.float32),
+          _dense(state, "state", (B, W - 1, D), x.dtype), _dense(so, "state_out", (B, W - 1, D), x.dtype), y.data_ptr(),
+          KDA_CONV_SILU if silu else 0, _dtype_code(x), B, D, W)
+    return y
+
+
+def conv_bwd(x, w, bias, dy, s0=None, dst=None, *, silu=True, cu_seqlens=None, workspace=None, out=None):
+    """Gradients of conv_fwd (kda_conv_bwd) from dy [B,T,D] (x's type or fp32)
+    and dst [N,W-1,D] (gradient of st, or None): a dict of dx (x's type), dw
+    [D,W] and dbias [D] fp32 (None without a bias) and ds0 [N,W-1,D] (None
+    without s0).  `out` may supply that dict to be filled in place."""
+    B, T, D = x.shape
+    W = w.shape[-1]
+    dev = x.device
+    px, ld = _rows(x, "x", (B, T), (D,))
+    arr, N = _packed(cu_seqlens, B, T)
+    dt, gt = _dtype_code(x), _dtype_code(dy)
+    if out is None:
+        out = {"dx": torch.empty((B, T, D), dtype=x.dtype, device=dev), "dw": torch.empty((D, W), dtype=torch.float32, device=dev),
+               "dbias": torch.empty(D, dtype=torch.float32, device=dev) if bias is not None else None,
+               "ds0": torch.empty((N, W - 1, D), dtype=x.dtype, device=dev) if s0 is not None else None}
+    ws = _scratch(workspace, lib().kda_conv_bwd_workspace_bytes(B, T, D, W, N if arr is not None else 0), dev,
+                  "kda_conv_bwd_workspace_bytes")
+    _same_device(dev, w=w, bias=bias, s0=s0, dy=dy, dst=dst, workspace=ws, **out)
+    _call(dev, "kda_conv_bwd", px, ld, _dense(w, "w", (D, W), torch.float32), _dense(bias, "bias", (D,), torch.float32),
+          _dense(s0, "s0", (N, W - 1, D), x.dtype), _dense(dy, "dy", (B, T, D), dy.dtype), gt,
+          _dense(dst, "dst", (N, W - 1, D), x.dtype), _dense(out["dx"], "dx", (B, T, D), x.dtype),
+          _dense(out["dw"], "dw", (D, W), torch.float32), _dense(out.get("dbias"), "dbias", (D,), torch.float32),
+          _dense(out.get("ds0"), "ds0", (N, W - 1, D), x.dtype), KDA_CONV_SILU if silu else 0, dt, B, T, D, W, arr, N,
+          _ptr(ws), ws.numel())
+    return out
+
+
+def _qk_setup(q, k, cos, sin, pos, pos0, mode, interleaved):
+    """Checked common arguments of the head norms: pointers, sizes and flags."""
+    B, T, Hq, d = q.shape
+    Hk = 0 if k is None else k.shape[2]
+    if k is not None and k.dtype != q.dtype:
+        raise TypeError(f"k dtype {k.dtype} != q dtype {q.dtype}")
+    if mode not in ("l2", "rms"):
+        raise ValueError("mode must be 'l2' or 'rms'")
+    pq, ldq = _rows(q, "q", (B, T), (Hq, d))
+    pk, ldk = (None, 0) if k is None else _rows(k, "k", (B, T), (Hk, d))
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    rot, n_pos = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
+    _dense(cos, "cos", (n_pos, rot // 2), torch.float32)
+    _dense(sin, "sin", (n_pos, rot // 2), torch.float32)
+    if rot == 0:
+        pos = None
+    _dense(pos, "pos", (B, T), torch.int32)
+    flags = (KDA_QK_RMS if mode == "rms" else 0) | (KDA_QK_INTERLEAVED if interleaved else 0)
+    ptr = lambda t: None if t is None or rot == 0 else t.data_ptr()
+    return (pq, ldq, pk, ldk), (ptr(cos), ptr(sin), ptr(pos), int(pos0), n_pos), (flags, _dtype_code(q), B, T, Hq, Hk, d, rot)
+
+
+def qk_norm_rope(q, k, wq=None, wk=None, *, cos=None, sin=None, pos=None, pos0=0, mode="l2", interleaved=False, eps=1e-6,
+                 out=None):
+    """qo, ko = qk_norm_rope(q, k, wq, wk): norms of the query and key heads
+    with the position rotation (kda_qk_norm_rope).  q [B,T,Hq,d], k [B,T,Hk,d]
+    or None (bf16 or fp32, may be slices of wider tensors); wq, wk [d] fp32 or
+    None.  mode 'l2': rows divided by sqrt(sum x^2 + eps); 'rms': by
+    sqrt(mean x^2 + eps).  cos, sin [n_pos, rot/2] fp32 turn the first rot
+    channels (pairs (i, i+rot/2), or neighbours if interleaved) by the row
+    pos [B,T] int32 gives, or pos0 + t; None: no rotation.  out: (qo, ko)
+    to write to, which may be contiguous q and k themselves."""
+    rows, table, sizes = _qk_setup(q, k, cos, sin, pos, pos0, mode, interleaved)
+    _, _, B, T, Hq, Hk, d, _ = sizes
+    _same_device(q.device, k=k, wq=wq, wk=wk, cos=cos, sin=sin, pos=pos)
+    qo, ko = (None, None) if out is None else out
+    qo = _given(qo, (B, T, Hq, d), q.dtype, q.device, "out[0]")
+    ko = None if k is None else _given(ko, (B, T, Hk, d), q.dtype, q.device, "out[1]")
+    _same_device(q.device, qo=qo, ko=ko)
+    _call(q.device, "kda_qk_norm_rope", *rows, _dense(wq, "wq", (d,), torch.float32), _dense(wk, "wk", (d,), torch.float32), *table,
+          float(eps), qo.data_ptr(), None if ko is None else ko.data_ptr(), *sizes)
+    return qo, ko
+
+
+def qk_norm_rope_bwd(q, k, dqo, dko, wq=None, wk=None, *, cos=None, sin=None, pos=None, pos0=0, mode="l2", interleaved=False,
+                     eps=1e-6, workspace=None, out=None):
+    """Gradients of qk_norm_rope (kda_qk_norm_rope_bwd) from dqo [B,T,Hq,d] and
+    dko (q's type or fp32): a dict of dq, dk (q's type) and dwq, dwk [d] fp32
+    (None without that weight).  `out` may supply that dict."""
+    rows, table, sizes = _qk_setup(q, k, cos, sin, pos, pos0, mode, interleaved)
+    _, _, B, T, Hq, Hk, d, _ = sizes
+    dev = q.device
+    if k is not None and (dko is None or dko.dtype != dqo.dtype):
+        raise TypeError("dqo and dko must have one type")
+    if out is None:
+        out = {"dq": torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev),
+               "dk": torch.empty((B, T, Hk, d), dtype=q.dtype, device=dev) if k is not None else None,
+               "dwq": torch.empty(d, dtype=torch.float32, device=dev) if wq is not None else None,
+               "dwk": torch.empty(d, dtype=torch.float32, device=dev) if wk is not None and k is not None else None}
+    nbytes = lib().kda_qk_bwd_workspace_bytes(B, T, Hq, Hk, d)
+    wanted = out.get("dwq") is not None or out.get("dwk") is not None
+    ws = _scratch(workspace, nbytes, dev, "kda_qk_bwd_workspace_bytes") if wanted else None
+    _same_device(dev, k=k, wq=wq, wk=wk, cos=cos, sin=sin, pos=pos, dqo=dqo, dko=dko, workspace=ws, **out)
+    _call(dev, "kda_qk_norm_rope_bwd", *rows, _dense(wq, "wq", (d,), torch.float32), _dense(wk, "wk", (d,), torch.float32), *table,
+          float(eps), _dense(dqo, "dqo", (B, T, Hq, d), dqo.dtype), _dense(dko if k is not None else None, "dko", (B, T, Hk, d), dqo.dtype),
+          _dtype_code(dqo), _dense(out["dq"], "dq", (B, T, Hq, d), q.dtype),
+          _dense(out["dk"] if k is not None else None, "dk", (B, T, Hk, d), q.dtype),
+          _dense(out.get("dwq"), "dwq", (d,), torch.float32), _dense(out.get("dwk"), "dwk", (d,), torch.float32), *sizes,
+          _ptr(ws), 0 if ws is None else ws.numel())
+    return out
 
 
 def stamps_read():

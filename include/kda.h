@@ -86,8 +86,10 @@ typedef enum kda_status {
   KDA_ERR_RANGE = 7,       /* a value outside its documented range (KDA_VALIDATE=1 */
                            /* checks, and gmin of kda_prepare_decay)              */
   KDA_ERR_HIP = 8,         /* a HIP launch failed (hipGetLastError)               */
-  KDA_ERR_INCOMPLETE = 9   /* kda_fwd_status: a hand-off wait of the fused        */
+  KDA_ERR_INCOMPLETE = 9,  /* kda_fwd_status: a hand-off wait of the fused        */
                            /* prefill expired; the call's outputs are incomplete  */
+  KDA_ERR_OVERLAP = 10     /* an output overlaps a tensor it must be apart from   */
+                           /* (the token-mixing and scan calls below)             */
 } kda_status;
 
 typedef enum kda_dtype { KDA_F32 = 0, KDA_BF16 = 1 } kda_dtype;
@@ -363,6 +365,110 @@ int kda_bwd_chunked(const void* q, const void* k, const void* v, const void* g, 
                     float* dk_, float* dv_, float* dg, float* dbeta, float* dh0, int dtype, int B,
                     int T, int H, int dk, int dv, int chunk, void* workspace,
                     size_t workspace_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The operators around the recurrence: the short causal convolution its
+ * inputs pass through and the norms (with the position rotation) of its
+ * query and key heads, both with their gradients.
+ *
+ * Beyond the shared conventions above:
+ *   - An input called "rows" may be a slice of a wider tensor: [B, T, ...]
+ *     with its inner elements contiguous, `ld` elements between consecutive
+ *     tokens and B*T tokens at that one distance (batch b starts at token
+ *     b*T).  Outputs are contiguous.
+ *   - Parameters (weights, biases, tables) and their gradients are fp32.
+ *   - Outputs must be apart from every input and from each other unless a
+ *     call says otherwise (KDA_ERR_OVERLAP).
+ *   - Packed sequences: cu_seqlens is a HOST array of N+1 ints as for
+ *     kda_fwd_chunked_varlen (B = 1; empty sequences allowed); NULL: B
+ *     sequences of T tokens, N ignored.  States are then [B, ...] instead of
+ *     [N, ...].  Up to 128 sequences run in one launch, more in several.
+ *   - T at most 2^30.  No call allocates or synchronises; results do not
+ *     depend on how the work is split (no atomics).
+ */
+
+/*
+ * Short causal depthwise convolution, width W in 2..4:
+ *   z[t,c] = bias[c] + sum_j w[c,j] x[t-(W-1-j),c];  y = z, or z Sigmoid(z)
+ *   with flags & KDA_CONV_SILU.
+ * x: rows [B,T,D] of dtype (any D; element alignment suffices; 16-byte rows
+ * are faster); w [D,W] fp32; bias [D] fp32 or NULL; s0 [N,W-1,D] of dtype:
+ * the W-1 tokens before each sequence, oldest first (NULL: zeros); st
+ * [N,W-1,D] or NULL: receives the last W-1 tokens (older ones from s0); may
+ * be s0 itself (in-place carry).  y [B,T,D] of dtype.
+ * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, ldx < D, cu_seqlens, flags),
+ *         KDA_ERR_DTYPE, KDA_ERR_ALIGN, KDA_ERR_UNSUPPORTED (W),
+ *         KDA_ERR_OVERLAP, KDA_ERR_HIP.
+ */
+#define KDA_CONV_SILU 1
+int kda_conv_fwd(const void* x, long long ldx, const float* w, const float* bias, const void* s0, void* st, void* y,
+                 int flags, int dtype, int B, int T, int D, int W, const int* cu_seqlens, int N, void* stream);
+
+/* One token per sequence: x rows [B,D], state [B,W-1,D] read, state_out
+ * (which may be state itself) written with the state behind the token,
+ * y [B,D].  With another state_out the old state is kept (a drafted token
+ * can be taken back).  Errors as kda_conv_fwd. */
+int kda_conv_step(const void* x, long long ldx, const float* w, const float* bias, const void* state, void* state_out,
+                  void* y, int flags, int dtype, int B, int D, int W, void* stream);
+
+/*
+ * Gradients of kda_conv_fwd from dy [B,T,D] (dy_dtype: dtype, or KDA_F32 as
+ * kda_bwd_chunked gives them) and dst [N,W-1,D] of dtype (gradient of st;
+ * NULL: none): dx [B,T,D] and ds0 [N,W-1,D] (NULL: not wanted) of dtype,
+ * dw [D,W] and dbias [D] (NULL: not wanted) fp32, all overwritten.
+ * workspace: kda_conv_bwd_workspace_bytes (0 for invalid sizes; N = 0 for a
+ * batch), 256-byte aligned, contents ignored on entry; calls that share one
+ * must not overlap on the device.  Errors as kda_conv_fwd,
+ * KDA_ERR_WORKSPACE.
+ */
+size_t kda_conv_bwd_workspace_bytes(int B, int T, int D, int W, int N);
+int kda_conv_bwd(const void* x, long long ldx, const float* w, const float* bias, const void* s0, const void* dy,
+                 int dy_dtype, const void* dst, void* dx, float* dw, float* dbias, void* ds0, int flags, int dtype, int B,
+                 int T, int D, int W, const int* cu_seqlens, int N, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Norms of query and key heads with the position rotation in the same pass.
+ * For each head row x of d channels (a multiple of 8, 8..512):
+ *   n = w x r, r = 1/sqrt(sum x^2 + eps), or 1/sqrt(mean x^2 + eps) with
+ *   flags & KDA_QK_RMS (w [d] fp32 or NULL: ones);
+ *   the first rot channels (a multiple of 8, 0..d) turn pairwise by the
+ *   token's angles: (a,b) -> (a cos - b sin, b cos + a sin), pairs (i,
+ *   i+rot/2), or neighbours (2i,2i+1) with flags & KDA_QK_INTERLEAVED.
+ * q: rows [B,T,Hq,d], k: rows [B,T,Hk,d] (Hk = 0: no keys, k NULL), token
+ * strides of 16 bytes' multiples.  cos, sin [n_pos, rot/2] fp32 (ignored for
+ * rot = 0).  pos [B,T] int32 on the device, or NULL: token t of every
+ * sequence is at pos0 + t.  A position outside [0, n_pos) reads nothing and
+ * makes the rotated channels NaN.  q_out [B,T,Hq,d] and k_out of dtype may
+ * be q and k themselves where those are contiguous.
+ * With the sum norm, w NULL and rot 0 it is the row normalisation
+ * kda_fwd_chunked_layer fuses.
+ * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides, pos0 + T > n_pos
+ *         without pos, flags, eps < 0), KDA_ERR_DTYPE, KDA_ERR_ALIGN,
+ *         KDA_ERR_UNSUPPORTED (d, rot), KDA_ERR_OVERLAP, KDA_ERR_HIP.
+ */
+#define KDA_QK_RMS 1
+#define KDA_QK_INTERLEAVED 2
+int kda_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk, const float* wq, const float* wk,
+                     const float* cos, const float* sin, const int* pos, int pos0, int n_pos, float eps, void* q_out,
+                     void* k_out, int flags, int dtype, int B, int T, int Hq, int Hk, int d, int rot, void* stream);
+
+/*
+ * Gradients of kda_qk_norm_rope from dq_out [B,T,Hq,d] and dk_out (dy_dtype:
+ * dtype, or KDA_F32 as kda_bwd_chunked gives them): dq, dk (contiguous) of
+ * dtype; dwq, dwk [d] fp32 (NULL: not wanted; given also for a NULL weight,
+ * as the gradient of a weight of ones).  workspace:
+ * kda_qk_bwd_workspace_bytes, 256-byte aligned, as for kda_conv_bwd; not
+ * read when neither dwq nor dwk is wanted (may be NULL then).  dq_out and
+ * dk_out may not be overwritten in place.  Errors as kda_qk_norm_rope,
+ * KDA_ERR_WORKSPACE.
+ */
+size_t kda_qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d);
+int kda_qk_norm_rope_bwd(const void* q, long long ldq, const void* k, long long ldk, const float* wq, const float* wk,
+                         const float* cos, const float* sin, const int* pos, int pos0, int n_pos, float eps,
+                         const void* dq_out, const void* dk_out, int dy_dtype, void* dq, void* dk, float* dwq, float* dwk,
+                         int flags, int dtype, int B, int T, int Hq, int Hk, int d, int rot, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,117 @@
+"""Argument checks of the operators around the recurrence (short convolution,
+norms of query and key heads): every bad call is refused before anything is
+enqueued, so these run without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from gated_delta_rule_96_amd import kda
+
+# 16-byte aligned addresses far apart, never dereferenced: a check fails first
+A = [(i + 1) << 36 for i in range(12)]
+
+
+def call(name, order, base, **kw):
+    a = dict(base)
+    a.update(kw)
+    return getattr(kda.lib(), name)(*[a[n] for n in order])
+
+
+CONV = dict(x=A[0], ldx=64, w=A[1], bias=A[2], s0=A[3], st=A[4], y=A[5], flags=1, dtype=1, B=2, T=10, D=64, W=4, cu=None, N=0,
+            stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), 1), (dict(w=None), 1), (dict(y=None), 1),
+    (dict(B=0), 2), (dict(T=0), 2), (dict(T=(1 << 30) + 1), 2), (dict(D=0), 2), (dict(ldx=63), 2), (dict(flags=2), 2),
+    (dict(dtype=2), 3), (dict(x=A[0] + 1), 4), (dict(w=A[1] + 4), 4), (dict(st=A[4] + 2), 4), (dict(y=A[5] + 8), 4),
+    (dict(W=1), 5), (dict(W=5), 5),
+    (dict(y=A[0]), 10), (dict(y=A[0] + 64), 10), (dict(st=A[5]), 10), (dict(st=A[3] + 16), 10), (dict(y=A[3]), 10),
+])
+def test_conv_fwd_refuses(kw, code):
+    assert call("kda_conv_fwd", CONV, CONV, **kw) == code
+
+
+def test_conv_refuses_bad_sequences():
+    cu = lambda *v: (ctypes.c_int * len(v))(*v)
+    for c, n, b in ((cu(0, 6, 5), 2, 1), (cu(1, 10), 1, 1), (cu(0, 9), 1, 1), (cu(0, 10), 0, 1), (cu(0, 10), 1, 2)):
+        assert call("kda_conv_fwd", CONV, CONV, cu=c, N=n, B=b) == 2
+
+
+STEP = dict(x=A[0], ldx=64, w=A[1], bias=None, state=A[3], so=A[3], y=A[5], flags=0, dtype=0, B=2, D=64, W=3, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [(dict(state=None), 1), (dict(so=None), 1), (dict(B=0), 2), (dict(dtype=9), 3), (dict(so=A[3] + 4), 4),
+                                     (dict(W=9), 5), (dict(so=A[3] + 16), 10), (dict(y=A[0]), 10), (dict(so=A[0]), 10)])
+def test_conv_step_refuses(kw, code):
+    assert call("kda_conv_step", STEP, STEP, **kw) == code
+
+
+CBWD = dict(x=A[0], ldx=64, w=A[1], bias=None, s0=A[3], dy=A[4], gt=0, dst=A[5], dx=A[6], dw=A[7], db=A[8], ds0=A[9], flags=1, dtype=1,
+            B=2, T=10, D=64, W=4, cu=None, N=0, ws=A[10], wsb=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dy=None), 1), (dict(dx=None), 1), (dict(dw=None), 1), (dict(T=-1), 2), (dict(gt=3), 3), (dict(dtype=0, gt=1), 3),
+    (dict(dst=A[5] + 4), 4), (dict(ws=A[10] + 16), 4), (dict(W=6), 5), (dict(ws=None), 6), (dict(wsb=16), 6),
+    (dict(dx=A[4]), 10), (dict(ds0=A[5]), 10), (dict(dw=A[8]), 10), (dict(dx=A[10]), 10),
+])
+def test_conv_bwd_refuses(kw, code):
+    assert call("kda_conv_bwd", CBWD, CBWD, **kw) == code
+
+
+def test_conv_workspace_bytes():
+    f = kda.lib().kda_conv_bwd_workspace_bytes
+    assert f(1, 100, 64, 4, 0) > 0 and f(1, 100, 64, 4, 0) % 256 == 0
+    assert f(1, 100, 64, 4, 300) >= f(1, 100, 64, 4, 0)
+    for bad in ((0, 1, 1, 4, 0), (1, 0, 1, 4, 0), (1, 1, 0, 4, 0), (1, 1, 1, 5, 0), (2, 1, 1, 4, 3), (1, 1, 1, 4, -1)):
+        assert f(*bad) == 0
+
+
+QK = dict(q=A[0], ldq=512, k=A[1], ldk=256, wq=A[2], wk=A[3], cos=A[4], sin=A[5], pos=A[6], pos0=0, n_pos=100, eps=1e-6, qo=A[7], ko=A[8],
+          flags=0, dtype=1, B=2, T=10, Hq=4, Hk=2, d=128, rot=64, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=None), 1), (dict(k=None), 1), (dict(cos=None), 1), (dict(qo=None), 1), (dict(ko=None), 1),
+    (dict(B=0), 2), (dict(Hq=0), 2), (dict(ldq=504), 2), (dict(ldk=128), 2), (dict(flags=4), 2), (dict(eps=-1.0), 2),
+    (dict(eps=float("nan")), 2), (dict(n_pos=0), 2), (dict(pos=None, pos0=91), 2), (dict(pos=None, pos0=-1), 2), (dict(rot=-8), 2),
+    (dict(dtype=5), 3), (dict(q=A[0] + 8), 4), (dict(ldq=516), 4), (dict(sin=A[5] + 4), 4), (dict(pos=A[6] + 2), 4), (dict(ko=A[8] + 8), 4),
+    (dict(d=100, ldq=400, ldk=200), 5), (dict(d=520, ldq=2080, ldk=1040), 5), (dict(rot=60), 5), (dict(rot=136), 5),
+    (dict(qo=A[1]), 10), (dict(qo=A[0] + 1024), 10), (dict(ko=A[7]), 10), (dict(ldq=1024, qo=A[0]), 10), (dict(qo=A[4]), 10),
+])
+def test_qk_refuses(kw, code):
+    assert call("kda_qk_norm_rope", QK, QK, **kw) == code
+
+
+QBWD = dict(q=A[0], ldq=512, k=A[1], ldk=256, wq=A[2], wk=A[3], cos=A[4], sin=A[5], pos=A[6], pos0=0, n_pos=100, eps=1e-6, dqo=A[7], dko=A[8],
+            gt=0, dq=A[9], dk=A[10], dwq=A[11], dwk=A[11] + 4096, flags=0, dtype=1, B=2, T=10, Hq=4, Hk=2, d=128, rot=64, ws=A[11] + (1 << 30),
+            wsb=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dqo=None), 1), (dict(dk=None), 1), (dict(gt=2), 3), (dict(dtype=0, gt=1), 3), (dict(dwk=A[11] + 4), 4), (dict(d=12), 5),
+    (dict(ws=None), 6), (dict(wsb=100), 6), (dict(dq=A[7]), 10), (dict(dk=A[1]), 10), (dict(dwk=A[11]), 10),
+])
+def test_qk_bwd_refuses(kw, code):
+    assert call("kda_qk_norm_rope_bwd", QBWD, QBWD, **kw) == code
+
+
+def test_status_text():
+    assert "overlap" in kda.status_str(kda.KDA_ERR_OVERLAP)
+
+
+def test_binding_checks_before_the_library():
+    # CPU tensors and shapes that do not fit are refused by name
+    x, w = torch.zeros(1, 4, 8), torch.zeros(8, 4)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.conv_fwd(x, w)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.qk_norm_rope(torch.zeros(1, 2, 3, 64), None)
+    with pytest.raises(ValueError, match="mode"):
+        kda.qk_norm_rope(torch.zeros(1, 2, 3, 64), None, mode="max")
+    with pytest.raises(ValueError, match="rise"):
+        kda._packed([0, 3, 2, 4], 1, 4)
+    with pytest.raises(ValueError, match="B = 1"):
+        kda._packed([0, 4], 2, 4)

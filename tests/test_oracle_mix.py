@@ -1,0 +1,82 @@
+"""Pins of oracle/mix.py: token-by-token sums, carry across a cut, finite
+differences, complex products."""
+import numpy as np
+import pytest
+
+from oracle import mix
+
+
+def rnd(*s, seed=0):
+    return np.random.default_rng(seed).standard_normal(s)
+
+
+@pytest.mark.parametrize("W", [2, 3, 4])
+def test_conv_is_the_sum_over_taps(W):
+    x, w, b, s0 = rnd(7, 3), rnd(3, W, seed=1), rnd(3, seed=2), rnd(W - 1, 3, seed=3)
+    y, st, _, _ = mix.conv_fwd(x, w, b, s0, False)
+    row = lambda t: x[t] if t >= 0 else s0[W - 1 + t]
+    for t in range(7):
+        assert np.allclose(y[t], b + sum(w[:, j] * row(t - (W - 1 - j)) for j in range(W)))
+    assert np.array_equal(st, np.concatenate([s0, x])[-(W - 1):])
+
+
+def test_conv_carry_across_a_cut():
+    x, w, s0 = rnd(9, 4), rnd(4, 4, seed=1), rnd(3, 4, seed=2)
+    y, st, _, _ = mix.conv_fwd(x, w, None, s0, True)
+    for cut in (0, 1, 2, 5, 9):
+        y1, s1, _, _ = mix.conv_fwd(x[:cut], w, None, s0, True)
+        y2, s2, _, _ = mix.conv_fwd(x[cut:], w, None, s1, True)
+        assert np.allclose(np.concatenate([y1, y2]), y) and np.array_equal(s2, st)
+
+
+def _diff(f, v, i, h=1e-6):
+    a, b = v.copy(), v.copy()
+    a.flat[i] += h
+    b.flat[i] -= h
+    return (f(a) - f(b)) / (2 * h)
+
+
+@pytest.mark.parametrize("silu", [False, True])
+@pytest.mark.parametrize("T", [1, 2, 6])
+def test_conv_gradients_by_differences(silu, T):
+    x, w, b, s0, dy, dst = rnd(T, 2), rnd(2, 4, seed=1), rnd(2, seed=2), rnd(3, 2, seed=3), rnd(T, 2, seed=4), rnd(3, 2, seed=5)
+    dx, dw, db, ds0, _ = mix.conv_bwd(x, w, b, s0, dy, dst, silu)
+
+    def loss(x=x, w=w, b=b, s0=s0):
+        y, st, _, _ = mix.conv_fwd(x, w, b, s0, silu)
+        return (y * dy).sum() + (st * dst).sum()
+    for name, v, g in (("x", x, dx), ("w", w, dw), ("b", b, db), ("s0", s0, ds0)):
+        for i in range(v.size):
+            assert np.isclose(_diff(lambda u: loss(**{name: u}), v, i), g.flat[i], atol=1e-7), (name, i)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_turn_is_a_complex_product(inter):
+    x, ang = rnd(5, 3, 16), rnd(5, 4, seed=1)
+    y = mix.turn(x, np.cos(ang)[:, None], np.sin(ang)[:, None], inter)
+    a, b = mix._halves(x, 8, inter)
+    z = (a + 1j * b) * np.exp(1j * ang)[:, None]
+    ya, yb = mix._halves(y, 8, inter)
+    assert np.allclose(ya, z.real) and np.allclose(yb, z.imag) and np.array_equal(y[..., 8:], x[..., 8:])
+    assert np.allclose((y * y).sum(-1), (x * x).sum(-1))
+    assert np.allclose(mix.turn(y, np.cos(ang)[:, None], -np.sin(ang)[:, None], inter), x)
+
+
+@pytest.mark.parametrize("rms", [False, True])
+def test_norm_lengths(rms):
+    x = rnd(4, 2, 8)
+    n = mix.qk_fwd(x, None, None, None, rms, False, eps=0.0)
+    assert np.allclose((n * n).sum(-1), 8 if rms else 1) and np.allclose(mix.qk_fwd(3 * x, None, None, None, rms, False, eps=0.0), n)
+    assert not mix.qk_fwd(0 * x, None, None, None, rms, False).any()
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+def test_norm_gradients_by_differences(rms, inter):
+    x, w, ang, dy = rnd(2, 2, 8), rnd(8, seed=1), rnd(2, 2, seed=2), rnd(2, 2, 8, seed=3)
+    c, s = np.cos(ang), np.sin(ang)
+    dx, dw = mix.qk_bwd(x, w, c, s, dy, rms, inter)
+    for i in range(x.size):
+        assert np.isclose(_diff(lambda u: (mix.qk_fwd(u, w, c, s, rms, inter) * dy).sum(), x, i), dx.flat[i], atol=1e-6)
+    for i in range(w.size):
+        assert np.isclose(_diff(lambda u: (mix.qk_fwd(x, u, c, s, rms, inter) * dy).sum(), w, i), dw.flat[i], atol=1e-6)
