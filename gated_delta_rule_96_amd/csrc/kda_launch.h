@@ -175,4 +175,25 @@ hipError_t launch_qk_fwd(int is_bf16, const QkArgs& a, hipStream_t stream);
 size_t qk_bwd_workspace_bytes(long long tokens, int Hq, int Hk, int d);
 hipError_t launch_qk_bwd(int is_bf16, int dy_bf16, const QkArgs& a, float* dwq, float* dwk, hipStream_t stream);
 
+// State space scan with one decay per head: see kda_ssm.hip.
+struct SsmArgs {
+  const void *x, *dt, *B, *C;        // rows [tokens][H][dv], [H], [G][dk], [G][dk]
+  long long ldx, lddt, ldb, ldc;
+  const float *A, *D, *bias;         // [H]; D and bias may be null
+  const float* h0;                   // [N][H][dk][dv] or null
+  float* ht;                         // [N][H][dk][dv] or null
+  void* y;                           // [tokens][H][dv]
+  int softplus, H, G;
+  float* seg;                        // workspace: states between a sequence's parts
+  float* start;                      // copies of h0 where ht replaces it (or null)
+  double* sum;                       // workspace: their decay sums
+};
+// Tokens of a part for these sizes, and the bytes of seg, start and sum together.
+int ssm_part(long long tokens, int H);
+size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv);
+hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
+                          hipStream_t stream);
+// One token per sequence: state h0 -> ht (may be the same).
+hipError_t launch_ssm_step(int is_bf16, const SsmArgs& a, int dk, int dv, int B, hipStream_t stream);
+
 }  // namespace kda

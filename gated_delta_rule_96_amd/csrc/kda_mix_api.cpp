@@ -1,6 +1,6 @@
 // C ABI of the operators around the recurrence (declared in include/kda.h):
 // short causal convolution, norms of query and key heads with the position
-// rotation.  Synchronous argument checks, then the launches on the caller's
+// rotation, state space scan.  Synchronous argument checks, then the launches on the caller's
 // stream; nothing is allocated and no state is kept.
 #include <hip/hip_runtime.h>
 
@@ -227,6 +227,93 @@ int kda_qk_norm_rope_bwd(const void* q, long long ldq, const void* k, long long 
   a.dy[1] = dk_out;
   a.part = static_cast<float*>(workspace);
   return hip_status(kda::launch_qk_bwd(dtype == KDA_BF16, dy_dtype == KDA_BF16, a, dwq, dwk, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"
+
+namespace {
+
+// The scan's sizes, strides and inputs.
+int check_ssm(const kda::SsmArgs& a, int flags, int dtype, int B, int T, int dk, int dv) {
+  if (!valid_dtype(dtype)) return KDA_ERR_DTYPE;
+  if (B <= 0 || T <= 0 || T > kMaxT || a.H <= 0 || a.G <= 0 || dk <= 0 || dv <= 0 || a.H % a.G || (flags & ~KDA_SSM_SOFTPLUS) ||
+      !size_ok(B, T, a.H, 8LL * dv) || !size_ok(B, a.H, dk, 4LL * dv) || (long long)B * T > (1LL << 40) ||
+      (long long)B * a.H > 0x7fffffffLL)
+    return KDA_ERR_SHAPE;
+  if (!kda::supported_d(dk) || !kda::supported_d(dv)) return KDA_ERR_UNSUPPORTED;
+  if (a.ldx < (long long)a.H * dv || a.lddt < a.H || a.ldb < (long long)a.G * dk || a.ldc < (long long)a.G * dk) return KDA_ERR_SHAPE;
+  for (long long ld : {a.ldx, a.lddt, a.ldb, a.ldc})
+    if (!size_ok(B, T, ld, 8)) return KDA_ERR_SHAPE;
+  if (!a.x || !a.dt || !a.A || !a.B || !a.C) return KDA_ERR_NULL;
+  const size_t esz = elem_size(dtype);
+  for (const void* p : {a.x, a.B, a.C, (const void*)a.A, (const void*)a.D, (const void*)a.bias, (const void*)a.h0})
+    if (!aligned16(p)) return KDA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(a.dt) % esz || (a.ldx * esz) % 16 || (a.ldb * esz) % 16 || (a.ldc * esz) % 16) return KDA_ERR_ALIGN;
+  return KDA_OK;
+}
+// The memory the scan's inputs cover.
+struct SsmSpans {
+  Span s[8];
+};
+SsmSpans ssm_spans(const kda::SsmArgs& a, size_t rows, size_t ns, int dk, int dv, size_t esz) {
+  return SsmSpans{{{a.x, rows_bytes(rows, a.ldx, (size_t)a.H * dv, esz)}, {a.dt, rows_bytes(rows, a.lddt, a.H, esz)},
+                   {a.B, rows_bytes(rows, a.ldb, (size_t)a.G * dk, esz)}, {a.C, rows_bytes(rows, a.ldc, (size_t)a.G * dk, esz)},
+                   {a.A, (size_t)a.H * 4}, {a.D, (size_t)a.H * 4}, {a.bias, (size_t)a.H * 4}, {a.h0, ns}}};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_ssm_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype) {
+  if (!valid_dtype(dtype) || B <= 0 || T <= 0 || T > kMaxT || H <= 0 || !kda::supported_d(dk) || !kda::supported_d(dv) ||
+      !size_ok(B, T, H, 8LL * dv) || (long long)B * T > (1LL << 40))
+    return 0;
+  return kda::ssm_seg_bytes((long long)B * T, H, dk, dv);
+}
+
+int kda_ssm_fwd_chunked(const void* x, long long ldx, const void* dt, long long lddt, const float* A, const void* Bm, long long ldb,
+                        const void* Cm, long long ldc, const float* D, const float* dt_bias, const float* h0, float* ht, void* y,
+                        int flags, int dtype, int B, int T, int H, int G, int dk, int dv, const int* cu_seqlens, int N,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  kda::SsmArgs a{};
+  a.x = x, a.dt = dt, a.B = Bm, a.C = Cm;
+  a.ldx = ldx, a.lddt = lddt, a.ldb = ldb, a.ldc = ldc;
+  a.A = A, a.D = D, a.bias = dt_bias, a.h0 = h0, a.ht = ht, a.y = y;
+  a.softplus = flags & KDA_SSM_SOFTPLUS, a.H = H, a.G = G;
+  int e = check_ssm(a, flags, dtype, B, T, dk, dv);
+  if (e != KDA_OK) return e;
+  if (!y) return KDA_ERR_NULL;
+  if (!aligned16(ht) || !aligned16(y)) return KDA_ERR_ALIGN;
+  if ((e = check_cu(cu_seqlens, N, B, T)) != KDA_OK) return e;
+  if (cu_seqlens && (long long)N * H > 0x7fffffffLL) return KDA_ERR_SHAPE;
+  const size_t need = kda_ssm_workspace_bytes(B, T, H, dk, dv, dtype);
+  if (need && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  if (need && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return KDA_ERR_ALIGN;
+  const size_t esz = elem_size(dtype), rows = (size_t)B * T, ns = (size_t)(cu_seqlens ? N : B) * H * dk * dv * 4;
+  const SsmSpans in = ssm_spans(a, rows, ns, dk, dv, esz);
+  const Span out[] = {{y, rows * H * dv * esz}, {ht, ns}, {workspace, need}};
+  if (!spans_apart(in.s, out, {-1, 7, -1})) return KDA_ERR_OVERLAP;
+  return hip_status(kda::launch_ssm_fwd(dtype == KDA_BF16, a, dk, dv, cu_seqlens, N, B, T, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int kda_ssm_step(const void* x, long long ldx, const void* dt, long long lddt, const float* A, const void* Bm, long long ldb,
+                 const void* Cm, long long ldc, const float* D, const float* dt_bias, const float* state, float* state_out, void* y,
+                 int flags, int dtype, int B, int H, int G, int dk, int dv, void* stream) {
+  kda::SsmArgs a{};
+  a.x = x, a.dt = dt, a.B = Bm, a.C = Cm;
+  a.ldx = ldx, a.lddt = lddt, a.ldb = ldb, a.ldc = ldc;
+  a.A = A, a.D = D, a.bias = dt_bias, a.h0 = state, a.ht = state_out, a.y = y;
+  a.softplus = flags & KDA_SSM_SOFTPLUS, a.H = H, a.G = G;
+  const int e = check_ssm(a, flags, dtype, B, 1, dk, dv);
+  if (e != KDA_OK) return e;
+  if (!state || !state_out || !y) return KDA_ERR_NULL;
+  if (!aligned16(state_out) || !aligned16(y)) return KDA_ERR_ALIGN;
+  const size_t esz = elem_size(dtype), rows = (size_t)B, ns = rows * H * dk * dv * 4;
+  const SsmSpans in = ssm_spans(a, rows, ns, dk, dv, esz);
+  const Span out[] = {{y, rows * H * dv * esz}, {state_out, ns}};
+  if (!spans_apart(in.s, out, {-1, 7})) return KDA_ERR_OVERLAP;
+  return hip_status(kda::launch_ssm_step(dtype == KDA_BF16, a, dk, dv, B, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

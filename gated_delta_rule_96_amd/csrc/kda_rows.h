@@ -59,7 +59,7 @@ template <> struct Rows<float, 8> {
 // starts at row `start` and has `len` tokens; `first` / `last`: its first and
 // last part.
 struct SeqPart {
-  int n, t0, t1, len;
+  int n, li, t0, t1, len;   // li: n counted from the launch's first sequence
   size_t start;
   bool first, last;
 };
@@ -67,7 +67,7 @@ __device__ __forceinline__ SeqPart seq_part(const SeqTab& s, int item) {
   SeqPart p;
   int k;   // part within the sequence
   if (s.n == 0) {
-    p.n = item / s.parts;
+    p.n = p.li = item / s.parts;
     k = item - p.n * s.parts;
     p.start = (size_t)p.n * s.T;
     p.len = s.T;
@@ -79,6 +79,7 @@ __device__ __forceinline__ SeqPart seq_part(const SeqTab& s, int item) {
       else hi = mid;
     }
     p.n = s.n0 + lo;
+    p.li = lo;
     k = item - s.cc[lo];
     p.start = (size_t)s.cu[lo];
     p.len = s.cu[lo + 1] - s.cu[lo];

@@ -1,0 +1,453 @@
+// Selective state space scan with one decay per head (scalar A), its chunked
+// form for prompts and its single-token step.
+//
+// Per head h, with S in R^{dk x dv} (state channels as rows), B and C of the
+// head's group g = h / (H/G), dt = raw + bias or Softplus(raw + bias):
+//   S_t = exp(dt_t A) S_{t-1} + dt_t B_t x_t^T
+//   y_t = S_t^T C_t + D x_t
+//
+// Chunks of Q = 64 tokens, cum_i the sum of dt A inside the chunk up to i:
+//   y_i = exp(cum_i) S_0^T C_i + sum_{j<=i} M_ij x_j + D x_i,
+//         M_ij = (C_i . B_j) exp(cum_i - cum_j) dt_j
+//   S_Q = exp(cum_Q) S_0 + sum_j exp(cum_Q - cum_j) dt_j B_j x_j^T
+// Every factor is exp of a difference that is <= 0 for A <= 0: nothing is
+// rescaled, any decay is in range.  Later tokens never reach an earlier one's
+// y, also not as 0 x inf or 0 x NaN.
+//
+// A work-group (4 waves) walks the chunks of one part of one sequence for
+// one head with the whole state in registers: wave w owns dv/4 value columns
+// (as MFMA accumulators, so that two stacked tiles are directly the operand
+// of the next chunk's S^T C product).  All products are formed transposed
+// (value columns as rows of the output tile): a lane then holds neighbouring
+// value columns of one token and stores them together.  M goes through LDS
+// once (wave w forms rows 16w.. of it), x and B are read with transposed LDS
+// reads where the token is the reduction index.
+//
+// Parts: a sequence is cut so that about two work-groups per CU run; a first
+// pass sums each part's own states (no y), a small kernel chains them, the
+// second pass starts every part from its state.  That reads x and B twice; it
+// keeps the chain of dependent chunks short without waits between
+// work-groups.
+//
+// Rounding (bf16): C, B and x are exact operands; M and the state as the
+// operand of S^T C are rounded to bf16 (2^-8 of each product's terms, like
+// y's own rounding).  The state itself is fp32 and its update splits
+// dt x exp(...) into three bf16 parts (24 bits), so that it is an fp32 result:
+// two parts (16 bits) leave a relative error of 2.7e-6, far above fp32's.
+// fp32 inputs: fp32 MFMA throughout, nothing rounded.
+#include "kda_ssm_dev.h"
+
+namespace kda {
+
+namespace {
+
+template <typename T, int DK, int DV>
+struct SsmLds {
+  static constexpr int PK = RowTile<T, DK>::kPitch, PV = RowTile<T, DV>::kPitch;
+  T c[kQ * PK];
+  T b[kQ * PK];
+  T x[kQ * PV];
+  Slab<T> m[8 * 64];          // M rows of tile it, slab js, at (2 it + js) 64 + lane
+  double cum[kQ];
+  float cumf[kQ], ecum[kQ], wdt[kQ], dt[kQ];
+};
+
+// Loads (or zeroes) the wave's columns of a state.  Tile t of the wave's
+// columns: output row m of the tile is column wave CPW + 4 NT (m/4) + 4t + m%4.
+template <int DK, int DV>
+struct State {
+  static constexpr int CPW = DV / kSsmWaves, NT = CPW / 16, KT = DK / 16;
+  f32x4 s[KT][NT];
+  static __device__ __forceinline__ int col(int t) {
+    const int l16 = lane_id() & 15, wave = threadIdx.x >> 6;
+    return wave * CPW + 4 * NT * (l16 >> 2) + 4 * t + (l16 & 3);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[k][t] = zero4();
+  }
+  __device__ __forceinline__ void load(const float* p) {
+    const int g = lane_id() >> 4;
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[k][t][r] = p[(size_t)(16 * k + 4 * g + r) * DV + col(t)];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    const int g = lane_id() >> 4;
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[(size_t)(16 * k + 4 * g + r) * DV + col(t)] = s[k][t][r];
+  }
+};
+
+// kOut: the whole scan of a part (y, final states).  Otherwise the part's own
+// state sums and decay, for every part but a sequence's last.
+template <typename T, int DK, int DV, bool kOut>
+__global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk_kernel(const SsmArgs a, const SeqTab sq) {
+  typedef SsmLds<T, DK, DV> Lds;
+  typedef State<DK, DV> St;
+  constexpr int NT = St::NT, KT = St::KT, PK = Lds::PK, PV = Lds::PV;
+  __shared__ __align__(16) char smem[sizeof(Lds)];
+  Lds& sm = *reinterpret_cast<Lds*>(smem);
+  ItemHead w;
+  if (!item_head(sq.items, a.H, w)) return;
+  const SeqPart p = seq_part(sq, w.item);
+  if (!kOut && p.last) return;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int h = w.h, grp = h / (a.H / a.G);
+  const double a2 = (double)a.A[h] * 1.4426950408889634074;
+  const float bias = a.bias ? a.bias[h] : 0.f, dskip = a.D ? a.D[h] : 0.f;
+  const T* x = (const T*)a.x + p.start * (size_t)a.ldx + (size_t)h * DV;
+  const T* bm = (const T*)a.B + p.start * (size_t)a.ldb + (size_t)grp * DK;
+  const T* cm = (const T*)a.C + p.start * (size_t)a.ldc + (size_t)grp * DK;
+  const T* dt = (const T*)a.dt + p.start * (size_t)a.lddt + h;
+  T* y = (T*)a.y + (p.start * (size_t)a.H + h) * DV;
+  const size_t yld = (size_t)a.H * DV;
+
+  St S;
+  const size_t sd = (size_t)DK * DV;
+  const size_t slot = (size_t)(w.item - p.li) * a.H + h;   // of this part's own sum (kOut: of the next part's start)
+  if (!kOut) S.zero();
+  else if (!p.first) S.load(a.seg + (slot - a.H) * sd);
+  else if (a.start && !p.last) S.load(a.start + slot * sd);
+  else if (a.h0) S.load(a.h0 + ((size_t)p.n * a.H + h) * sd);
+  else S.zero();
+  double total = 0.0;
+
+  RowTile<T, DK> rc, rb;
+  RowTile<T, DV> rx;
+  float raw = 0.f;
+  auto fetch = [&](int t) {
+    const int n = p.t1 - t;
+    if (kOut) rc.load(cm + (size_t)t * (size_t)a.ldc, a.ldc, n);
+    rb.load(bm + (size_t)t * (size_t)a.ldb, a.ldb, n);
+    rx.load(x + (size_t)t * (size_t)a.ldx, a.ldx, n);
+    raw = lane < n ? to_f32(dt[(size_t)(t + lane) * (size_t)a.lddt]) : 0.f;
+  };
+  if (p.t0 < p.t1) fetch(p.t0);
+  for (int t = p.t0; t < p.t1; t += kQ) {
+    const int n = min(p.t1 - t, kQ);
+    // step sizes and decay sums: every wave forms them, one array each is kept
+    StepSize s = step_size(raw, bias, a.softplus, a2);
+    if (lane >= n) s = StepSize{0.f, 0.0};
+    const double cum = wave_scan(s.a), last = lane63(cum);
+    __syncthreads();   // the chunk before is done with LDS
+    if (kOut) rc.store(sm.c);
+    rb.store(sm.b);
+    rx.store(sm.x);
+    if (wave == 0) {
+      sm.cum[lane] = cum;
+      sm.cumf[lane] = (float)cum;
+    } else if (wave == 1) {
+      sm.ecum[lane] = exp2_of(cum);
+    } else if (wave == 2) {
+      sm.wdt[lane] = exp2_of(last - cum) * s.dt;
+    } else {
+      sm.dt[lane] = s.dt;
+    }
+    if (t + kQ < p.t1) fetch(t + kQ);
+    __syncthreads();
+
+    if constexpr (kOut) {
+      // rows 16 wave .. of M, transposed tiles (rows j, columns i)
+      const int it = wave, i = 16 * it + l16;
+      Slab<T> cs[DK / 32];
+#pragma unroll
+      for (int k = 0; k < DK / 32; ++k) cs[k] = load_slab(sm.c + i * PK + 32 * k);
+      const double ci = sm.cum[i];
+      const float cif = sm.cumf[i];
+#pragma unroll
+      for (int js = 0; js < 2; ++js) {
+        if (2 * js > it) continue;
+        f32x4 v[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int jt = 2 * js + q;
+          if (jt > it) continue;
+          f32x4 acc = zero4();
+#pragma unroll
+          for (int k = 0; k < DK / 32; ++k) acc = mma(load_slab(sm.b + (16 * jt + l16) * PK + 32 * k), cs[k], acc);
+          const int j = 16 * jt + 4 * g;
+          const f32x4 dj = load4(sm.dt + j);
+          f32x4 ex;
+          if constexpr (sizeof(T) == 2) {
+            const f32x4 cj = load4(sm.cumf + j);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ex[r] = exp2_fast(cif - cj[r]);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ex[r] = exp2_of(ci - sm.cum[j + r]);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[q][r] = j + r <= i ? acc[r] * ex[r] * dj[r] : 0.f;
+        }
+        sm.m[(2 * it + js) * 64 + lane] = make_slab<T>(v[0], v[1]);
+      }
+      __syncthreads();
+    }
+
+    Slab<T> xs[2][NT];
+#pragma unroll
+    for (int js = 0; js < 2; ++js)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) xs[js][q] = slab_tr<T>(sm.x + 32 * js * PV, PV, wave * St::CPW + 4 * q, 4 * NT);
+
+    if constexpr (kOut) {
+      // a product with zeros is NaN exactly where x is not finite: the masked
+      // entries of M would then spread later tokens' values to earlier ones
+      f32x4 probe = zero4();
+#pragma unroll
+      for (int js = 0; js < 2; ++js)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) probe = mma(Slab<T>{}, xs[js][q], probe);
+      const bool finite = !__any(probe[0] != probe[0]);
+      f32x4 acc[4][NT];
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[it][q] = zero4();
+#pragma unroll
+      for (int k = 0; k < DK / 32; ++k) {
+        Slab<T> ss[NT];
+#pragma unroll
+        for (int q = 0; q < NT; ++q) ss[q] = make_slab<T>(S.s[2 * k][q], S.s[2 * k + 1][q]);
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+          const Slab<T> cs = load_slab(sm.c + (16 * it + l16) * PK + 32 * k);
+#pragma unroll
+          for (int q = 0; q < NT; ++q) acc[it][q] = mma(ss[q], cs, acc[it][q]);
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const int i = 16 * it + l16, c = wave * St::CPW + 4 * NT * g;
+        const float e = sm.ecum[i];
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[it][q] *= e;
+        if (finite) {
+#pragma unroll
+          for (int js = 0; js <= it / 2; ++js) {
+            const Slab<T> m = sm.m[(2 * it + js) * 64 + lane];
+#pragma unroll
+            for (int q = 0; q < NT; ++q) acc[it][q] = mma(xs[js][q], m, acc[it][q]);
+          }
+        } else {   // token by token, later ones left out
+#pragma unroll 1
+          for (int j = 0; j <= i; ++j) {
+            const T* mp = reinterpret_cast<const T*>(sm.m + (2 * it + (j >> 5)) * 64 + ((j >> 2) & 3) * 16 + l16);
+            const float m = to_f32(mp[4 * ((j >> 4) & 1) + (j & 3)]);
+#pragma unroll
+            for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(sm.x + j * PV + c + 4 * q));
+          }
+        }
+        float o[4 * NT];
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          const f32x4 xi = widen4(load4(sm.x + i * PV + c + 4 * q));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) o[4 * q + r] = a.D ? fmaf(dskip, xi[r], acc[it][q][r]) : acc[it][q][r];
+        }
+        if (i < n) Rows<T, 4 * NT>::store(y + (size_t)(t + i) * yld + c, o);
+      }
+    }
+
+    // state update
+    const float el = exp2_of(last);
+    total += last;
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) S.s[k][q] *= el;
+#pragma unroll
+    for (int js = 0; js < 2; ++js) {
+      const f32x4 w0 = load4(sm.wdt + 32 * js + 4 * g), w1 = load4(sm.wdt + 32 * js + 16 + 4 * g);
+      Split<T> xw[NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) xw[q] = scaled<T>(xs[js][q], w0, w1);
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const Slab<T> bs = slab_tr<T>(sm.b + 32 * js * PK, PK, 16 * k, 4);
+#pragma unroll
+        for (int q = 0; q < NT; ++q) S.s[k][q] = mma_split(bs, xw[q], S.s[k][q]);
+      }
+    }
+  }
+  if (!kOut) {
+    S.store(a.seg + slot * sd);
+    if (tid == 0) a.sum[slot] = total;
+  } else if (p.last && a.ht) {
+    S.store(a.ht + ((size_t)p.n * a.H + h) * sd);
+  }
+}
+
+// Chains a sequence's parts: slot k (the state part k adds, from zero) becomes
+// the state part k+1 starts from.  One thread a four-column piece of one
+// (sequence, head).
+__global__ __launch_bounds__(256) void ssm_chain_kernel(const SsmArgs a, const SeqTab sq, int sd4) {
+  const unsigned per = (unsigned)(sd4 / 256);
+  const unsigned nh = blockIdx.x / per;
+  const int li = (int)(nh / (unsigned)a.H), h = (int)(nh - (unsigned)li * a.H);
+  const int e = (int)((blockIdx.x - nh * per) * 256 + threadIdx.x);
+  const int first = sq.n ? sq.cc[li] : li * sq.parts, parts = sq.n ? sq.cc[li + 1] - first : sq.parts;
+  if (parts < 2) return;
+  const size_t n = (size_t)(sq.n ? sq.n0 + li : li);
+  f32x4 s = a.h0 ? load4(a.h0 + ((n * a.H + h) * sd4 + e) * 4) : zero4();
+  f32x4* seg = reinterpret_cast<f32x4*>(a.seg);
+  // where ht replaces h0, the first part may start after the last one has
+  // written: it reads this copy
+  if (a.start) reinterpret_cast<f32x4*>(a.start)[((size_t)(first - li) * a.H + h) * sd4 + e] = s;
+  for (int k = 0; k + 1 < parts; ++k) {
+    const size_t slot = (size_t)(first - li + k) * a.H + h;
+    s = s * exp2_of(a.sum[slot]) + seg[slot * sd4 + e];
+    seg[slot * sd4 + e] = s;
+  }
+}
+
+template <typename T, int DK, int DV>
+hipError_t fwd_go(const SsmArgs& a, const SeqTab& s, int seqs, bool split, hipStream_t st) {
+  dim3 grid;
+  if (!item_head_grid(s.items, a.H, grid)) return hipErrorInvalidConfiguration;
+  if (split) {
+    constexpr int sd4 = DK * DV / 4;
+    const long long blocks = (long long)seqs * a.H * (sd4 / 256);
+    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((ssm_chunk_kernel<T, DK, DV, false>), grid, dim3(kSsmThreads), 0, st, a, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(ssm_chain_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, s, sd4);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((ssm_chunk_kernel<T, DK, DV, true>), grid, dim3(kSsmThreads), 0, st, a, s);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int ssm_part(long long tokens, int H) {
+  // about two work-groups per CU; a part is at least four chunks, so that the
+  // extra pass and the chaining stay small beside it
+  const long long want = (tokens * H + 511) / 512;
+  const long long part = (want + kQ - 1) / kQ * kQ;
+  return (int)(part < 256 ? 256 : part > (1 << 30) ? (1 << 30) : part);
+}
+
+// A sequence of n parts keeps n - 1 states; n - 1 <= its tokens / part.
+static size_t seg_slots(long long tokens, int H) { return (size_t)(tokens / ssm_part(tokens, H)) * H; }
+
+size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv) {
+  const size_t slots = seg_slots(tokens, H);
+  return ((slots * (2 * (size_t)dk * dv * sizeof(float) + sizeof(double))) + 255) & ~(size_t)255;
+}
+
+hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a0, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
+                          hipStream_t st) {
+  const long long tokens = (long long)B * T;
+  const int part = ssm_part(tokens, a0.H), end = cu ? N : B;
+  SsmArgs a = a0;
+  a.seg = static_cast<float*>(workspace);
+  const size_t states = seg_slots(tokens, a.H) * (size_t)dk * dv;
+  a.start = a.ht && a.ht == a.h0 ? a.seg + states : nullptr;
+  a.sum = reinterpret_cast<double*>(a.seg + 2 * states);
+  for (int n = 0; n < end;) {
+    SeqTab s;
+    const int n0 = n;
+    n = make_seq_tab(s, cu, N, n, B, T, part);
+    if (s.items < 0) return hipErrorInvalidConfiguration;
+    const bool split = s.items > n - n0;   // some sequence has more than one part
+    hipError_t e;
+#define KDA_SSM_GO(T_, K_, V_) e = fwd_go<T_, K_, V_>(a, s, n - n0, split, st)
+    if (is_bf16) {
+      if (dk == 128 && dv == 128) KDA_SSM_GO(bf16, 128, 128);
+      else if (dk == 128) KDA_SSM_GO(bf16, 128, 64);
+      else if (dv == 128) KDA_SSM_GO(bf16, 64, 128);
+      else KDA_SSM_GO(bf16, 64, 64);
+    } else {
+      if (dk == 128 && dv == 128) KDA_SSM_GO(float, 128, 128);
+      else if (dk == 128) KDA_SSM_GO(float, 128, 64);
+      else if (dv == 128) KDA_SSM_GO(float, 64, 128);
+      else KDA_SSM_GO(float, 64, 64);
+    }
+#undef KDA_SSM_GO
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+// ---------------------------------------------------------------------------
+// Single token.  Bound by the state, read once and written once: a thread
+// keeps four value columns of DK / RG rows in registers, all rows' loads
+// issued first; the sums over the state channels are joined through LDS.
+namespace {
+
+constexpr int kStepThreads = 512;
+
+template <typename T, int DK, int DV>
+__global__ __launch_bounds__(kStepThreads) void ssm_step_kernel(const SsmArgs a) {
+  constexpr int CG = DV / 4, RG = kStepThreads / CG, RPT = DK / RG;
+  static_assert(RPT >= 1 && DK % RG == 0, "shape");
+  __shared__ float sb[DK], sc[DK], sx[DV];
+  __shared__ f32x4 red[RG][CG];
+  const int tid = threadIdx.x, cg = tid % CG, rg = tid / CG;
+  const int b = blockIdx.x / a.H, h = blockIdx.x - b * a.H, grp = h / (a.H / a.G);
+  const size_t at = (size_t)blockIdx.x * (DK * DV);
+  const f32x4* src = reinterpret_cast<const f32x4*>(a.h0 + at) + cg;
+  f32x4* dst = reinterpret_cast<f32x4*>(a.ht + at) + cg;
+  f32x4 s[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) s[i] = __builtin_nontemporal_load(src + (size_t)(rg + RG * i) * CG);
+  const float bias = a.bias ? a.bias[h] : 0.f;
+  const StepSize st = step_size(to_f32(((const T*)a.dt)[(size_t)b * (size_t)a.lddt + h]), bias, a.softplus,
+                                (double)a.A[h] * 1.4426950408889634074);
+  const float dec = exp2_of(st.a);
+  if (tid < DK) {
+    sb[tid] = to_f32(((const T*)a.B)[(size_t)b * (size_t)a.ldb + (size_t)grp * DK + tid]) * st.dt;
+    sc[tid] = to_f32(((const T*)a.C)[(size_t)b * (size_t)a.ldc + (size_t)grp * DK + tid]);
+  }
+  if (tid < DV) sx[tid] = to_f32(((const T*)a.x)[(size_t)b * (size_t)a.ldx + (size_t)h * DV + tid]);
+  __syncthreads();
+  const f32x4 x4 = load4(sx + 4 * cg);
+  f32x4 y = zero4();
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    const int r = rg + RG * i;
+    s[i] = s[i] * dec + sb[r] * x4;
+    y += sc[r] * s[i];
+    __builtin_nontemporal_store(s[i], dst + (size_t)r * CG);
+  }
+  red[rg][cg] = y;
+  __syncthreads();
+  if (tid < DV) {
+    float v = 0.f;
+#pragma unroll
+    for (int r = 0; r < RG; ++r) v += red[r][tid >> 2][tid & 3];
+    if (a.D) v = fmaf(a.D[h], sx[tid], v);
+    ((T*)a.y)[(size_t)blockIdx.x * DV + tid] = from_f32<T>(v);
+  }
+}
+
+template <typename T>
+hipError_t step_go(const SsmArgs& a, int dk, int dv, int B, hipStream_t st) {
+  const dim3 grid((unsigned)B * (unsigned)a.H), th(kStepThreads);
+  if (dk == 128 && dv == 128) hipLaunchKernelGGL((ssm_step_kernel<T, 128, 128>), grid, th, 0, st, a);
+  else if (dk == 128) hipLaunchKernelGGL((ssm_step_kernel<T, 128, 64>), grid, th, 0, st, a);
+  else if (dv == 128) hipLaunchKernelGGL((ssm_step_kernel<T, 64, 128>), grid, th, 0, st, a);
+  else hipLaunchKernelGGL((ssm_step_kernel<T, 64, 64>), grid, th, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_ssm_step(int is_bf16, const SsmArgs& a, int dk, int dv, int B, hipStream_t st) {
+  return is_bf16 ? step_go<bf16>(a, dk, dv, B, st) : step_go<float>(a, dk, dv, B, st);
+}
+
+}  // namespace kda

@@ -27,6 +27,7 @@ KDA_STAGES_UNBOUNDED = 4
 KDA_LAYER_QK_L2NORM = 1
 KDA_CONV_SILU = 1
 KDA_QK_RMS, KDA_QK_INTERLEAVED = 1, 2
+KDA_SSM_SOFTPLUS = 1
 CHUNK = 64
 GMIN = -5.0
 
@@ -92,7 +93,10 @@ def lib() -> ctypes.CDLL:
                 ("kda_conv_bwd", I, [P, LL, P, P, P, P, I, P, P, P, P, P, I, I, I, I, I, I, P, I, P, S, P]),
                 ("kda_qk_norm_rope", I, [P, LL, P, LL, P, P, P, P, P, I, I, F, P, P] + [I] * 8 + [P]),
                 ("kda_qk_bwd_workspace_bytes", S, [I, I, I, I, I]),
-                ("kda_qk_norm_rope_bwd", I, [P, LL, P, LL, P, P, P, P, P, I, I, F, P, P, I, P, P, P, P] + [I] * 8 + [P, S, P])):
+                ("kda_qk_norm_rope_bwd", I, [P, LL, P, LL, P, P, P, P, P, I, I, F, P, P, I, P, P, P, P] + [I] * 8 + [P, S, P]),
+                ("kda_ssm_workspace_bytes", S, [I] * 6),
+                ("kda_ssm_fwd_chunked", I, [P, LL, P, LL, P, P, LL, P, LL, P, P, P, P, P] + [I] * 8 + [P, I, P, S, P]),
+                ("kda_ssm_step", I, [P, LL, P, LL, P, P, LL, P, LL, P, P, P, P, P] + [I] * 7 + [P])):
             getattr(L, name).restype = res
             getattr(L, name).argtypes = args
         if hasattr(L, "kda_stamps_read"):
@@ -631,6 +635,59 @@ def qk_norm_rope_bwd(q, k, dqo, dko, wq=None, wk=None, *, cos=None, sin=None, po
           _dense(out.get("dwq"), "dwq", (d,), torch.float32), _dense(out.get("dwk"), "dwk", (d,), torch.float32), *sizes,
           _ptr(ws), 0 if ws is None else ws.numel())
     return out
+
+
+def _ssm_setup(x, dt, A, Bm, Cm, D, dt_bias, lead):
+    """Checked inputs of the scan: (x .. dt_bias of the C call, G, dk)."""
+    H, dv = x.shape[-2:]
+    G, dk = Bm.shape[-2:]
+    for n, t in (("dt", dt), ("Bm", Bm), ("Cm", Cm)):
+        if t.dtype != x.dtype:
+            raise TypeError(f"{n} dtype {t.dtype} != x dtype {x.dtype}")
+    _same_device(x.device, dt=dt, A=A, Bm=Bm, Cm=Cm, D=D, dt_bias=dt_bias)
+    vec = lambda t, n: _dense(t, n, (H,), torch.float32)
+    return (*_rows(x, "x", lead, (H, dv)), *_rows(dt, "dt", lead, (H,)), vec(A, "A"), *_rows(Bm, "Bm", lead, (G, dk)),
+            *_rows(Cm, "Cm", lead, (G, dk)), vec(D, "D"), vec(dt_bias, "dt_bias")), G, dk
+
+
+def ssm_fwd_chunked(x, dt, A, Bm, Cm, h0=None, *, D=None, dt_bias=None, softplus=False, cu_seqlens=None, final_state=True, ht=None,
+                    workspace=None, out=None):
+    """y, ht = ssm_fwd_chunked(x, dt, A, Bm, Cm, h0): state space scan of
+    prompts (kda_ssm_fwd_chunked), S_t = exp(dt A) S_{t-1} + dt B x^T, y = S^T C
+    + D x.  x [B,T,H,dv], dt [B,T,H], Bm, Cm [B,T,G,dk] (bf16 or fp32, may be
+    slices of wider tensors; G divides H); A, D, dt_bias [H] fp32; h0 / ht
+    [N,H,dk,dv] fp32 of the N = B sequences, or of those cu_seqlens (host ints)
+    cuts the packed axis into; ht may be h0 itself.  softplus: dt =
+    Softplus(dt + dt_bias)."""
+    B, T, H, dv = x.shape
+    args, G, dk = _ssm_setup(x, dt, A, Bm, Cm, D, dt_bias, (B, T))
+    arr, N = _packed(cu_seqlens, B, T)
+    code, dev, st = _dtype_code(x), x.device, (N, H, dk, dv)
+    y = _given(out, (B, T, H, dv), x.dtype, dev, "out")
+    if final_state and ht is None:
+        ht = torch.empty(st, dtype=torch.float32, device=dev)
+    n = lib().kda_ssm_workspace_bytes(B, T, H, dk, dv, code)
+    ws = _scratch(workspace, n, dev, "kda_ssm_workspace_bytes") if n else None
+    _same_device(dev, h0=h0, ht=ht, out=y, workspace=ws)
+    _call(dev, "kda_ssm_fwd_chunked", *args, _dense(h0, "h0", st, torch.float32),
+          _dense(ht if final_state else None, "ht", st, torch.float32), y.data_ptr(), KDA_SSM_SOFTPLUS if softplus else 0, code, B, T,
+          H, G, dk, dv, arr, N, _ptr(ws), 0 if ws is None else ws.numel())
+    return y, (ht if final_state else None)
+
+
+def ssm_step(x, dt, A, Bm, Cm, state, *, D=None, dt_bias=None, softplus=False, state_out=None, out=None):
+    """y = ssm_step(x, dt, A, Bm, Cm, state): one token per sequence
+    (kda_ssm_step), x [B,H,dv], dt [B,H], Bm, Cm [B,G,dk]; state [B,H,dk,dv]
+    fp32 moves on in place, or into state_out (the old state is then kept)."""
+    B, H, dv = x.shape
+    args, G, dk = _ssm_setup(x, dt, A, Bm, Cm, D, dt_bias, (B,))
+    so = state if state_out is None else state_out
+    y = _given(out, (B, H, dv), x.dtype, x.device, "out")
+    _same_device(x.device, state=state, state_out=so, out=y)
+    _call(x.device, "kda_ssm_step", *args, _dense(state, "state", (B, H, dk, dv), torch.float32),
+          _dense(so, "state_out", (B, H, dk, dv), torch.float32), y.data_ptr(), KDA_SSM_SOFTPLUS if softplus else 0, _dtype_code(x), B,
+          H, G, dk, dv)
+    return y
 
 
 def stamps_read():

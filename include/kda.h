@@ -470,6 +470,47 @@ int kda_qk_norm_rope_bwd(const void* q, long long ldq, const void* k, long long 
                          int flags, int dtype, int B, int T, int Hq, int Hk, int d, int rot, void* workspace,
                          size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Selective state space scan with one decay per head: the gated linear
+ * recurrence without the delta correction, on the same fp32 states
+ * [N,H,dk,dv] (state channel = row).  Head h takes group h / (H/G)'s B and C:
+ *   dt_t = raw_t + dt_bias[h], or Softplus(raw_t + dt_bias[h]) with
+ *          flags & KDA_SSM_SOFTPLUS
+ *   S_t = exp(dt_t A[h]) S_{t-1} + dt_t B_t x_t^T
+ *   y_t = S_t^T C_t + D[h] x_t
+ * x: rows [B,T,H,dv]; dt (raw): rows [B,T,H] (element alignment suffices);
+ * Bm, Cm: rows [B,T,G,dk], G a divisor of H; token strides of x, Bm and Cm in
+ * multiples of 16 bytes; dk, dv in {64, 128}.  A, D, dt_bias [H] fp32 (D, dt_bias NULL:
+ * none).  y [B,T,H,dv] of dtype (a projection of the same type reads it;
+ * fp32 sums, one rounding).  Precondition: A finite; dt A <= 0 is the
+ * intended range, larger values are computed as they are and may overflow.
+ * Conventions and errors as for the operators above, KDA_ERR_SHAPE also for
+ * G not dividing H.
+ */
+#define KDA_SSM_SOFTPLUS 1
+
+/* Bytes of device workspace of kda_ssm_fwd_chunked (0: none needed, or
+ * invalid sizes; packed sequences: B = 1, T tokens together). */
+size_t kda_ssm_workspace_bytes(int B, int T, int H, int dk, int dv, int dtype);
+
+/*
+ * Prompts: h0 [N,H,dk,dv] (NULL: zero), ht (NULL: not wanted) the states
+ * behind the sequences, may be h0 itself.  workspace as for kda_conv_bwd
+ * (NULL where 0 bytes are needed).
+ */
+int kda_ssm_fwd_chunked(const void* x, long long ldx, const void* dt, long long lddt, const float* A, const void* Bm,
+                        long long ldb, const void* Cm, long long ldc, const float* D, const float* dt_bias, const float* h0,
+                        float* ht, void* y, int flags, int dtype, int B, int T, int H, int G, int dk, int dv,
+                        const int* cu_seqlens, int N, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per sequence: x rows [B,H,dv], dt rows [B,H], Bm, Cm rows
+ * [B,G,dk]; state [B,H,dk,dv] read, state_out (may be state) written,
+ * y [B,H,dv]. */
+int kda_ssm_step(const void* x, long long ldx, const void* dt, long long lddt, const float* A, const void* Bm, long long ldb,
+                 const void* Cm, long long ldc, const float* D, const float* dt_bias, const float* state, float* state_out,
+                 void* y, int flags, int dtype, int B, int H, int G, int dk, int dv, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -81,3 +81,31 @@ def qk_bwd(x, w, cos, sin, dy, rms, inter, eps=1e-6):
     g = dn * (1.0 if w is None else w)
     dot = (g * x).sum(-1, keepdims=True) / (x.shape[-1] if rms else 1)
     return g * r - x * dot * r ** 3, dw
+
+
+def softplus(x):
+    return np.logaddexp(x, 0.0)
+
+
+def ssm_seq(x, raw, A, Bm, Cm, h0=None, D=None, bias=None, soft=False):
+    """One sequence of the scan token by token: x [T,H,dv], raw [T,H], Bm, Cm
+    [T,G,dk], h0 [H,dk,dv] -> (y, ht, size) with size the same recurrence on
+    absolute values (what the outputs' roundings are relative to)."""
+    T, H, dv = x.shape
+    G, dk = Bm.shape[1:]
+    dt = raw + (0.0 if bias is None else bias)
+    dt = softplus(dt) if soft else dt
+    b, c = np.repeat(Bm, H // G, 1), np.repeat(Cm, H // G, 1)
+    S = np.zeros((H, dk, dv)) if h0 is None else np.array(h0, dtype=np.float64)
+    Z = np.abs(S)
+    y, size = np.zeros((T, H, dv)), np.zeros((T, H, dv))
+    for t in range(T):
+        e = np.exp(dt[t] * A)[:, None, None]
+        S = S * e + (dt[t][:, None] * b[t])[:, :, None] * x[t][:, None]
+        Z = Z * e + (np.abs(dt[t])[:, None] * np.abs(b[t]))[:, :, None] * np.abs(x[t])[:, None]
+        y[t] = (S * c[t][:, :, None]).sum(1)
+        size[t] = (Z * np.abs(c[t])[:, :, None]).sum(1)
+        if D is not None:
+            y[t] += D[:, None] * x[t]
+            size[t] += np.abs(D[:, None] * x[t])
+    return y, S, size, Z

@@ -115,3 +115,38 @@ def test_binding_checks_before_the_library():
         kda._packed([0, 3, 2, 4], 1, 4)
     with pytest.raises(ValueError, match="B = 1"):
         kda._packed([0, 4], 2, 4)
+
+
+SSM = dict(x=A[0], ldx=256, dt=A[1], lddt=4, A=A[2], B=A[3], ldb=256, C=A[4], ldc=256, D=A[5], bias=A[6], h0=A[7], ht=A[8], y=A[9], flags=1,
+           dtype=1, Bn=2, T=1000, H=4, G=2, dk=128, dv=64, cu=None, N=0, ws=A[10], wsb=1 << 34, stream=None)
+SSM_ORDER = list(SSM)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), 1), (dict(dt=None), 1), (dict(A=None), 1), (dict(B=None), 1), (dict(C=None), 1), (dict(y=None), 1),
+    (dict(Bn=0), 2), (dict(T=0), 2), (dict(H=0), 2), (dict(G=3), 2), (dict(G=0), 2), (dict(ldx=255), 2), (dict(lddt=3), 2), (dict(ldb=128), 2),
+    (dict(flags=2), 2), (dict(dtype=4), 3), (dict(x=A[0] + 8), 4), (dict(ldx=260), 4), (dict(dt=A[1] + 1), 4), (dict(h0=A[7] + 4), 4),
+    (dict(ht=A[8] + 8), 4), (dict(ws=A[10] + 128), 4), (dict(dk=96), 5), (dict(dv=32), 5), (dict(ws=None), 6), (dict(wsb=100), 6),
+    (dict(y=A[0]), 10), (dict(ht=A[7] + 16), 10), (dict(ht=A[9]), 10), (dict(y=A[10]), 10),
+])
+def test_ssm_fwd_refuses(kw, code):
+    assert call("kda_ssm_fwd_chunked", SSM_ORDER, SSM, **kw) == code
+
+
+def test_ssm_refuses_bad_sequences_and_sizes():
+    cu = lambda *v: (ctypes.c_int * len(v))(*v)
+    for c, n, b in ((cu(0, 600, 500), 2, 1), (cu(0, 999), 1, 1), (cu(0, 1000), 0, 1), (cu(0, 1000), 1, 2)):
+        assert call("kda_ssm_fwd_chunked", SSM_ORDER, SSM, cu=c, N=n, Bn=b) == 2
+    f = kda.lib().kda_ssm_workspace_bytes
+    assert f(1, 100, 4, 128, 128, 1) == 0                    # one part: no states between parts
+    assert f(1, 100000, 4, 128, 128, 1) % 256 == 0 and f(1, 100000, 4, 128, 128, 1) > 0
+    assert f(1, 100000, 4, 96, 128, 1) == 0 and f(0, 100000, 4, 128, 128, 1) == 0
+
+
+SSTEP = {k: v for k, v in SSM.items() if k not in ("T", "cu", "N", "ws", "wsb")}
+
+
+@pytest.mark.parametrize("kw,code", [(dict(h0=None), 1), (dict(ht=None), 1), (dict(Bn=-1), 2), (dict(G=3), 2), (dict(dtype=2), 3), (dict(ldc=260), 4),
+                                     (dict(dk=32), 5), (dict(ht=A[7] + 16), 10), (dict(y=A[8]), 10)])
+def test_ssm_step_refuses(kw, code):
+    assert call("kda_ssm_step", list(SSTEP), SSTEP, **kw) == code

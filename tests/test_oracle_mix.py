@@ -80,3 +80,32 @@ def test_norm_gradients_by_differences(rms, inter):
         assert np.isclose(_diff(lambda u: (mix.qk_fwd(u, w, c, s, rms, inter) * dy).sum(), x, i), dx.flat[i], atol=1e-6)
     for i in range(w.size):
         assert np.isclose(_diff(lambda u: (mix.qk_fwd(x, u, c, s, rms, inter) * dy).sum(), w, i), dw.flat[i], atol=1e-6)
+
+
+def _scan_case(T, H, G, dk, dv, seed=3):
+    r = np.random.default_rng(seed)
+    return dict(x=r.standard_normal((T, H, dv)), raw=r.standard_normal((T, H)), A=-r.uniform(0.5, 4, H), Bm=r.standard_normal((T, G, dk)),
+                Cm=r.standard_normal((T, G, dk)), h0=r.standard_normal((H, dk, dv)), D=r.standard_normal(H), bias=r.standard_normal(H))
+
+
+def test_scan_is_the_lower_triangular_product():
+    c = _scan_case(9, 4, 2, 3, 5)
+    y, ht, size, _ = mix.ssm_seq(**c, soft=True)
+    dt = np.log1p(np.exp(c["raw"] + c["bias"]))
+    for h in range(4):
+        cum = np.cumsum(dt[:, h] * c["A"][h])
+        M = np.tril((c["Cm"][:, h // 2] @ c["Bm"][:, h // 2].T) * np.exp(np.minimum(cum[:, None] - cum[None], 0))) * dt[:, h]
+        want = M @ c["x"][:, h] + np.exp(cum)[:, None] * (c["Cm"][:, h // 2] @ c["h0"][h]) + c["D"][h] * c["x"][:, h]
+        assert np.allclose(y[:, h], want)
+    assert (size >= np.abs(y) - 1e-12).all()
+
+
+def test_scan_carry_and_identity():
+    c = _scan_case(8, 2, 1, 4, 4)
+    y, ht, _, _ = mix.ssm_seq(**c)
+    cut = lambda lo, hi, h0: mix.ssm_seq(**{**c, "x": c["x"][lo:hi], "raw": c["raw"][lo:hi], "Bm": c["Bm"][lo:hi], "Cm": c["Cm"][lo:hi], "h0": h0})
+    y1, h1, _, _ = cut(0, 3, c["h0"])
+    y2, h2, _, _ = cut(3, 8, h1)
+    assert np.allclose(np.concatenate([y1, y2]), y) and np.allclose(h2, ht)
+    z = dict(c, raw=np.zeros((8, 2)), bias=None)
+    assert np.allclose(mix.ssm_seq(**z)[1], c["h0"])   # steps of size zero leave the state
