@@ -24,7 +24,7 @@ BUILD = PKG / "_build"
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["kda_api.cpp", "kda_mix_api.cpp", "kda_decay.hip", "kda_chunk.hip", "kda_decode.hip", "kda_bwd.hip", "kda_noalloc.hip",
-           "kda_conv.hip", "kda_qknorm.hip", "kda_ssm.hip"]
+           "kda_conv.hip", "kda_qknorm.hip", "kda_ssm.hip", "kda_ssm_bwd.hip"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
@@ -65,7 +65,7 @@ def build(verbose: bool = False) -> Path:
     BUILD.mkdir(exist_ok=True)
     objs = []
     stamped = BUILD / (Path(STAMPED).stem + "_stamps.o")
-    with cf.ThreadPoolExecutor(max_workers=min(6, len(SOURCES) + 1)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + 1)) as ex:
         futs = {ex.submit(_compile, CSRC / STAMPED, stamped, ("-DKDA_CYCLE_STAMPS",)): STAMPED + " (stamps)"}
         for s in SOURCES:
             src = CSRC / s

@@ -341,6 +341,7 @@ int make_seq_tab(SeqTab& s, const int* cu, int N, int n0, int B, int T, int part
   s.n0 = n0;
   s.T = T;
   s.part = part;
+  s.chunks = (T + kSeqChunk - 1) / kSeqChunk;
   if (!cu) {
     s.n = 0;
     s.parts = (T + part - 1) / part;
@@ -350,44 +351,45 @@ int make_seq_tab(SeqTab& s, const int* cu, int N, int n0, int B, int T, int part
   }
   s.n = N - n0 < kMaxVarSeq ? N - n0 : kMaxVarSeq;
   s.parts = 0;
-  long long items = 0;
+  long long items = 0, chunks = 0;
   for (int i = 0; i <= s.n; ++i) {
     s.cu[i] = cu[n0 + i];
     s.cc[i] = (int)items;
+    s.cb[i] = (int)chunks;
     if (i == s.n) break;
-    const int len = cu[n0 + i + 1] - cu[n0 + i];
-    items += len > 0 ? ((long long)len + part - 1) / part : 1;
+    const long long len = cu[n0 + i + 1] - cu[n0 + i];
+    items += len > 0 ? (len + part - 1) / part : 1;
+    chunks += len > 0 ? (len + kSeqChunk - 1) / kSeqChunk : 1;
   }
   s.items = items > 0x7fffffffLL ? -1 : (int)items;
   return n0 + s.n;
 }
 
-// out0[c] and out1[c - n0]: sums of column c of part [nrows][n0 + n1] over its
-// rows.  A work-group takes 64 columns; its 16 waves take every 16th row and
-// are joined through LDS, always in the same order.
-__global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict__ part, unsigned nrows, unsigned n0, unsigned n1,
-                                                        float* __restrict__ out0, float* __restrict__ out1) {
-  __shared__ float red[16][64];
-  const unsigned l = threadIdx.x & 63, q = threadIdx.x >> 6, col = blockIdx.x * 64 + l, cols = n0 + n1;
-  float v = 0.f;
+// out[c]: sum of column c of part [nrows][n0 + n1 + n2] over its rows, the
+// columns in three outputs.  A work-group takes 64 columns; its 16 waves take
+// every 16th row and are joined through LDS, always in the same order.
+__global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict__ part, size_t nrows, unsigned n0, unsigned n1,
+                                                        unsigned n2, float* __restrict__ out0, float* __restrict__ out1,
+                                                        float* __restrict__ out2) {
+  __shared__ double red[16][64];
+  const unsigned l = threadIdx.x & 63, q = threadIdx.x >> 6, col = blockIdx.x * 64 + l, cols = n0 + n1 + n2;
+  double v = 0.0;
   if (col < cols)
 #pragma unroll 8
-    for (unsigned r = q; r < nrows; r += 16) v += part[(size_t)r * cols + col];
+    for (size_t r = q; r < nrows; r += 16) v += (double)part[r * cols + col];
   red[q][l] = v;
   __syncthreads();
   if (q != 0 || col >= cols) return;
-  v = 0.f;
+  v = 0.0;
 #pragma unroll
   for (int k = 0; k < 16; ++k) v += red[k][l];
-  if (col < n0) {
-    if (out0) out0[col] = v;
-  } else if (out1) {
-    out1[col - n0] = v;
-  }
+  float* out = col < n0 ? out0 : col < n0 + n1 ? out1 : out2;
+  if (out) out[col - (col < n0 ? 0 : col < n0 + n1 ? n0 : n0 + n1)] = (float)v;
 }
 
-hipError_t launch_sum_rows(const float* part, unsigned nrows, unsigned n0, unsigned n1, float* out0, float* out1, hipStream_t st) {
-  hipLaunchKernelGGL(sum_rows_kernel, dim3((n0 + n1 + 63) / 64), dim3(1024), 0, st, part, nrows, n0, n1, out0, out1);
+hipError_t launch_sum_rows(const float* part, size_t nrows, unsigned n0, unsigned n1, unsigned n2, float* out0, float* out1,
+                           float* out2, hipStream_t st) {
+  hipLaunchKernelGGL(sum_rows_kernel, dim3((n0 + n1 + n2 + 63) / 64), dim3(1024), 0, st, part, nrows, n0, n1, n2, out0, out1, out2);
   return hipGetLastError();
 }
 
@@ -456,7 +458,7 @@ hipError_t launch_conv_bwd(int is_bf16, const ConvBwdArgs& a, const int* cu, int
     if (e != hipSuccess) return e;
     rows += r;
   }
-  return launch_sum_rows(a.part, (unsigned)rows, (unsigned)(a.f.W * a.f.D), (unsigned)a.f.D, a.dw, a.dbias, st);
+  return launch_sum_rows(a.part, rows, (unsigned)(a.f.W * a.f.D), (unsigned)a.f.D, 0, a.dw, a.dbias, nullptr, st);
 }
 
 }  // namespace kda

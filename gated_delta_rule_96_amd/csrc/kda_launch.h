@@ -111,10 +111,14 @@ hipError_t launch_bwd_chunks(int is_bf16, const void* q, const void* k, const vo
 // one behind the other, `parts` parts each.  n > 0: packed sequences n0 ..
 // n0+n-1 of the call (at most kMaxVarSeq a launch): sequence n0+i is rows
 // cu[i] .. cu[i+1]-1, its parts are items cc[i] .. cc[i+1]-1 of the launch.
+// Chunks of kSeqChunk tokens are numbered the same way (an empty sequence has
+// one): `chunks` each, or cb[i] .. of packed ones.
+constexpr int kSeqChunk = 64;
 struct SeqTab {
-  int n, n0, T, parts, part, items;
+  int n, n0, T, parts, part, items, chunks;
   int cu[kMaxVarSeq + 1];
   int cc[kMaxVarSeq + 1];
+  int cb[kMaxVarSeq + 1];
 };
 // The table of sequences n0 .. of a call, cut into parts of `part` tokens:
 // B sequences of T (cu == nullptr, one launch), or N packed ones from n0 on
@@ -122,10 +126,10 @@ struct SeqTab {
 // items < 0: more items than a launch can number.
 int make_seq_tab(SeqTab& s, const int* cu, int N, int n0, int B, int T, int part);
 
-// out0[c] (c < n0) and out1[c - n0]: column sums of part [nrows][n0 + n1], in a
-// fixed order (either output may be null).
-hipError_t launch_sum_rows(const float* part, unsigned nrows, unsigned n0, unsigned n1, float* out0, float* out1,
-                           hipStream_t stream);
+// out[0][c], then out[1], out[2]: column sums of part [nrows][n0 + n1 + n2], in
+// a fixed order (any output may be null).
+hipError_t launch_sum_rows(const float* part, size_t nrows, unsigned n0, unsigned n1, unsigned n2, float* out0, float* out1,
+                           float* out2, hipStream_t stream);
 
 // Short causal convolution: see kda_conv.hip.  dtypes: 0 fp32, 1 bf16.
 struct ConvArgs {
@@ -190,10 +194,24 @@ struct SsmArgs {
 };
 // Tokens of a part for these sizes, and the bytes of seg, start and sum together.
 int ssm_part(long long tokens, int H);
+size_t ssm_slots(long long tokens, int H);   // states between parts
 size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv);
 hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
                           hipStream_t stream);
 // One token per sequence: state h0 -> ht (may be the same).
 hipError_t launch_ssm_step(int is_bf16, const SsmArgs& a, int dk, int dv, int B, hipStream_t stream);
+
+// Gradients of the scan: see kda_ssm_bwd.hip.  f: the forward's inputs.
+struct SsmBwdArgs {
+  SsmArgs f;
+  const void* dy;              // [tokens][H][dv]
+  const float* dht;            // [N][H][dk][dv] or null
+  void *dx, *ddt, *dB, *dC;    // of the inputs' type, contiguous
+  float *dA, *dD, *dbias;      // [H]; dD and dbias may be null
+  float* dh0;                  // or null
+};
+size_t ssm_bwd_workspace_bytes(int is_packed, int N, int B, int T, int H, int G, int dk, int dv);
+hipError_t launch_ssm_bwd(int is_bf16, const SsmBwdArgs& a, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
+                          hipStream_t stream);
 
 }  // namespace kda

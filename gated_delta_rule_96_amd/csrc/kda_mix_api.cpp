@@ -316,4 +316,44 @@ int kda_ssm_step(const void* x, long long ldx, const void* dt, long long lddt, c
   return hip_status(kda::launch_ssm_step(dtype == KDA_BF16, a, dk, dv, B, static_cast<hipStream_t>(stream)));
 }
 
+size_t kda_ssm_bwd_workspace_bytes(int B, int T, int H, int G, int dk, int dv, int dtype, int N) {
+  if (!valid_dtype(dtype) || B <= 0 || T <= 0 || T > kMaxT || H <= 0 || G <= 0 || H % G || !kda::supported_d(dk) ||
+      !kda::supported_d(dv) || N < 0 || (N > 0 && B != 1) || !size_ok(B, T, H, 8LL * dk * dv) || (long long)B * T > (1LL << 40))
+    return 0;
+  return kda::ssm_bwd_workspace_bytes(N > 0, N, B, T, H, G, dk, dv);
+}
+
+int kda_ssm_bwd_chunked(const void* x, long long ldx, const void* dt, long long lddt, const float* A, const void* Bm, long long ldb,
+                        const void* Cm, long long ldc, const float* D, const float* dt_bias, const float* h0, const void* dy,
+                        const float* dht, void* dx, void* ddt, float* dA, void* dBm, void* dCm, float* dD, float* ddt_bias,
+                        float* dh0, int flags, int dtype, int B, int T, int H, int G, int dk, int dv, const int* cu_seqlens, int N,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  kda::SsmBwdArgs a{};
+  kda::SsmArgs& f = a.f;
+  f.x = x, f.dt = dt, f.B = Bm, f.C = Cm;
+  f.ldx = ldx, f.lddt = lddt, f.ldb = ldb, f.ldc = ldc;
+  f.A = A, f.D = D, f.bias = dt_bias, f.h0 = h0;
+  f.softplus = flags & KDA_SSM_SOFTPLUS, f.H = H, f.G = G;
+  a.dy = dy, a.dht = dht, a.dx = dx, a.ddt = ddt, a.dA = dA, a.dB = dBm, a.dC = dCm, a.dD = dD, a.dbias = ddt_bias, a.dh0 = dh0;
+  int e = check_ssm(f, flags, dtype, B, T, dk, dv);
+  if (e != KDA_OK) return e;
+  if (!dy || !dx || !ddt || !dA || !dBm || !dCm) return KDA_ERR_NULL;
+  for (const void* p : {dy, (const void*)dht, (const void*)dx, (const void*)ddt, (const void*)dA, (const void*)dBm, (const void*)dCm,
+                        (const void*)dD, (const void*)ddt_bias, (const void*)dh0})
+    if (!aligned16(p)) return KDA_ERR_ALIGN;
+  if ((e = check_cu(cu_seqlens, N, B, T)) != KDA_OK) return e;
+  if (cu_seqlens && (long long)N * H > 0x7fffffffLL) return KDA_ERR_SHAPE;
+  const size_t need = kda_ssm_bwd_workspace_bytes(B, T, H, G, dk, dv, dtype, cu_seqlens ? N : 0);
+  if (need == 0) return KDA_ERR_SHAPE;
+  if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return KDA_ERR_ALIGN;
+  const size_t esz = elem_size(dtype), rows = (size_t)B * T, ns = (size_t)(cu_seqlens ? N : B) * H * dk * dv * 4;
+  const size_t nv = rows * H * dv * esz, nk = rows * G * dk * esz, nh = (size_t)H * 4;
+  const SsmSpans fs = ssm_spans(f, rows, ns, dk, dv, esz);
+  const Span in[] = {fs.s[0], fs.s[1], fs.s[2], fs.s[3], fs.s[4], fs.s[5], fs.s[6], fs.s[7], {dy, nv}, {dht, ns}};
+  const Span out[] = {{dx, nv}, {ddt, rows * H * esz}, {dA, nh}, {dBm, nk}, {dCm, nk}, {dD, nh}, {ddt_bias, nh}, {dh0, ns}, {workspace, need}};
+  if (!spans_apart(in, out, {-1, -1, -1, -1, -1, -1, -1, -1, -1})) return KDA_ERR_OVERLAP;
+  return hip_status(kda::launch_ssm_bwd(dtype == KDA_BF16, a, dk, dv, cu_seqlens, N, B, T, workspace, static_cast<hipStream_t>(stream)));
+}
+
 }  // extern "C"

@@ -328,7 +328,7 @@ hipError_t launch_qk_bwd(int is_bf16, int dy_bf16, const QkArgs& a0, float* dwq,
   const unsigned groups = bwd_groups(qk_tasks(a.tokens, a.H[0], a.H[1], a.d).n);
   const hipError_t e = a.inter ? bwd_types<true>(is_bf16, dy_bf16, a, groups, st) : bwd_types<false>(is_bf16, dy_bf16, a, groups, st);
   if (e != hipSuccess || !a.part) return e;
-  return launch_sum_rows(a.part, groups, (unsigned)a.d, (unsigned)a.d, dwq, dwk, st);
+  return launch_sum_rows(a.part, groups, (unsigned)a.d, (unsigned)a.d, 0, dwq, dwk, nullptr, st);
 }
 
 }  // namespace kda

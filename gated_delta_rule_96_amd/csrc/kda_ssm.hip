@@ -35,7 +35,7 @@
 // dt x exp(...) into three bf16 parts (24 bits), so that it is an fp32 result:
 // two parts (16 bits) leave a relative error of 2.7e-6, far above fp32's.
 // fp32 inputs: fp32 MFMA throughout, nothing rounded.
-#include "kda_ssm_dev.h"
+#include "kda_ssm_sweep.h"
 
 namespace kda {
 
@@ -52,55 +52,17 @@ struct SsmLds {
   float cumf[kQ], ecum[kQ], wdt[kQ], dt[kQ];
 };
 
-// Loads (or zeroes) the wave's columns of a state.  Tile t of the wave's
-// columns: output row m of the tile is column wave CPW + 4 NT (m/4) + 4t + m%4.
-template <int DK, int DV>
-struct State {
-  static constexpr int CPW = DV / kSsmWaves, NT = CPW / 16, KT = DK / 16;
-  f32x4 s[KT][NT];
-  static __device__ __forceinline__ int col(int t) {
-    const int l16 = lane_id() & 15, wave = threadIdx.x >> 6;
-    return wave * CPW + 4 * NT * (l16 >> 2) + 4 * t + (l16 & 3);
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) s[k][t] = zero4();
-  }
-  __device__ __forceinline__ void load(const float* p) {
-    const int g = lane_id() >> 4;
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) s[k][t][r] = p[(size_t)(16 * k + 4 * g + r) * DV + col(t)];
-  }
-  __device__ __forceinline__ void store(float* p) const {
-    const int g = lane_id() >> 4;
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) p[(size_t)(16 * k + 4 * g + r) * DV + col(t)] = s[k][t][r];
-  }
-};
-
-// kOut: the whole scan of a part (y, final states).  Otherwise the part's own
-// state sums and decay, for every part but a sequence's last.
-template <typename T, int DK, int DV, bool kOut>
+// The scan of a part: y and, for a sequence's last part, its final state.
+template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk_kernel(const SsmArgs a, const SeqTab sq) {
   typedef SsmLds<T, DK, DV> Lds;
-  typedef State<DK, DV> St;
-  constexpr int NT = St::NT, KT = St::KT, PK = Lds::PK, PV = Lds::PV;
+  typedef State<DK, DV, true> St;
+  constexpr int NT = St::NT, PK = Lds::PK, PV = Lds::PV;
   __shared__ __align__(16) char smem[sizeof(Lds)];
   Lds& sm = *reinterpret_cast<Lds*>(smem);
   ItemHead w;
   if (!item_head(sq.items, a.H, w)) return;
   const SeqPart p = seq_part(sq, w.item);
-  if (!kOut && p.last) return;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int h = w.h, grp = h / (a.H / a.G);
   const double a2 = (double)a.A[h] * 1.4426950408889634074;
@@ -114,20 +76,17 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
 
   St S;
   const size_t sd = (size_t)DK * DV;
-  const size_t slot = (size_t)(w.item - p.li) * a.H + h;   // of this part's own sum (kOut: of the next part's start)
-  if (!kOut) S.zero();
-  else if (!p.first) S.load(a.seg + (slot - a.H) * sd);
+  const size_t slot = (size_t)(w.item - p.li) * a.H + h;   // of the next part's start
+  if (!p.first) S.load(a.seg + (slot - a.H) * sd);
   else if (a.start && !p.last) S.load(a.start + slot * sd);
   else if (a.h0) S.load(a.h0 + ((size_t)p.n * a.H + h) * sd);
   else S.zero();
-  double total = 0.0;
-
   RowTile<T, DK> rc, rb;
   RowTile<T, DV> rx;
   float raw = 0.f;
   auto fetch = [&](int t) {
     const int n = p.t1 - t;
-    if (kOut) rc.load(cm + (size_t)t * (size_t)a.ldc, a.ldc, n);
+    rc.load(cm + (size_t)t * (size_t)a.ldc, a.ldc, n);
     rb.load(bm + (size_t)t * (size_t)a.ldb, a.ldb, n);
     rx.load(x + (size_t)t * (size_t)a.ldx, a.ldx, n);
     raw = lane < n ? to_f32(dt[(size_t)(t + lane) * (size_t)a.lddt]) : 0.f;
@@ -140,7 +99,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
     if (lane >= n) s = StepSize{0.f, 0.0};
     const double cum = wave_scan(s.a), last = lane63(cum);
     __syncthreads();   // the chunk before is done with LDS
-    if (kOut) rc.store(sm.c);
+    rc.store(sm.c);
     rb.store(sm.b);
     rx.store(sm.x);
     if (wave == 0) {
@@ -156,159 +115,104 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
     if (t + kQ < p.t1) fetch(t + kQ);
     __syncthreads();
 
-    if constexpr (kOut) {
-      // rows 16 wave .. of M, transposed tiles (rows j, columns i)
-      const int it = wave, i = 16 * it + l16;
-      Slab<T> cs[DK / 32];
+    // rows 16 wave .. of M, transposed tiles (rows j, columns i)
+    const int it = wave, i = 16 * it + l16;
+    Slab<T> cs[DK / 32];
 #pragma unroll
-      for (int k = 0; k < DK / 32; ++k) cs[k] = load_slab(sm.c + i * PK + 32 * k);
-      const double ci = sm.cum[i];
-      const float cif = sm.cumf[i];
+    for (int k = 0; k < DK / 32; ++k) cs[k] = load_slab(sm.c + i * PK + 32 * k);
+    const double ci = sm.cum[i];
+    const float cif = sm.cumf[i];
 #pragma unroll
-      for (int js = 0; js < 2; ++js) {
-        if (2 * js > it) continue;
-        f32x4 v[2] = {zero4(), zero4()};
+    for (int js = 0; js < 2; ++js) {
+      if (2 * js > it) continue;
+      f32x4 v[2] = {zero4(), zero4()};
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int jt = 2 * js + q;
-          if (jt > it) continue;
-          f32x4 acc = zero4();
+      for (int q = 0; q < 2; ++q) {
+        const int jt = 2 * js + q;
+        if (jt > it) continue;
+        f32x4 acc = zero4();
 #pragma unroll
-          for (int k = 0; k < DK / 32; ++k) acc = mma(load_slab(sm.b + (16 * jt + l16) * PK + 32 * k), cs[k], acc);
-          const int j = 16 * jt + 4 * g;
-          const f32x4 dj = load4(sm.dt + j);
-          f32x4 ex;
-          if constexpr (sizeof(T) == 2) {
-            const f32x4 cj = load4(sm.cumf + j);
+        for (int k = 0; k < DK / 32; ++k) acc = mma(load_slab(sm.b + (16 * jt + l16) * PK + 32 * k), cs[k], acc);
+        const int j = 16 * jt + 4 * g;
+        const f32x4 dj = load4(sm.dt + j);
+        f32x4 ex;
+        if constexpr (sizeof(T) == 2) {
+          const f32x4 cj = load4(sm.cumf + j);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) ex[r] = exp2_fast(cif - cj[r]);
-          } else {
+          for (int r = 0; r < 4; ++r) ex[r] = exp2_fast(cif - cj[r]);
+        } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) ex[r] = exp2_of(ci - sm.cum[j + r]);
-          }
-#pragma unroll
-          for (int r = 0; r < 4; ++r) v[q][r] = j + r <= i ? acc[r] * ex[r] * dj[r] : 0.f;
+          for (int r = 0; r < 4; ++r) ex[r] = exp2_of(ci - sm.cum[j + r]);
         }
-        sm.m[(2 * it + js) * 64 + lane] = make_slab<T>(v[0], v[1]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[q][r] = j + r <= i ? acc[r] * ex[r] * dj[r] : 0.f;
       }
-      __syncthreads();
+      sm.m[(2 * it + js) * 64 + lane] = make_slab<T>(v[0], v[1]);
     }
+    __syncthreads();
 
     Slab<T> xs[2][NT];
+    St::slabs(sm.x, PV, xs);
+    // a product with zeros is NaN exactly where x is not finite: the masked
+    // entries of M would then spread later tokens' values to earlier ones
+    f32x4 probe = zero4();
 #pragma unroll
     for (int js = 0; js < 2; ++js)
 #pragma unroll
-      for (int q = 0; q < NT; ++q) xs[js][q] = slab_tr<T>(sm.x + 32 * js * PV, PV, wave * St::CPW + 4 * q, 4 * NT);
-
-    if constexpr (kOut) {
-      // a product with zeros is NaN exactly where x is not finite: the masked
-      // entries of M would then spread later tokens' values to earlier ones
-      f32x4 probe = zero4();
+      for (int q = 0; q < NT; ++q) probe = mma(Slab<T>{}, xs[js][q], probe);
+    const bool finite = !__any(probe[0] != probe[0]);
+    f32x4 acc[4][NT];
 #pragma unroll
-      for (int js = 0; js < 2; ++js)
+    for (int it = 0; it < 4; ++it)
 #pragma unroll
-        for (int q = 0; q < NT; ++q) probe = mma(Slab<T>{}, xs[js][q], probe);
-      const bool finite = !__any(probe[0] != probe[0]);
-      f32x4 acc[4][NT];
+      for (int q = 0; q < NT; ++q) acc[it][q] = zero4();
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
+    for (int k = 0; k < DK / 32; ++k) {
+      Slab<T> ss[NT];
 #pragma unroll
-        for (int q = 0; q < NT; ++q) acc[it][q] = zero4();
-#pragma unroll
-      for (int k = 0; k < DK / 32; ++k) {
-        Slab<T> ss[NT];
-#pragma unroll
-        for (int q = 0; q < NT; ++q) ss[q] = make_slab<T>(S.s[2 * k][q], S.s[2 * k + 1][q]);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const Slab<T> cs = load_slab(sm.c + (16 * it + l16) * PK + 32 * k);
-#pragma unroll
-          for (int q = 0; q < NT; ++q) acc[it][q] = mma(ss[q], cs, acc[it][q]);
-        }
-      }
+      for (int q = 0; q < NT; ++q) ss[q] = make_slab<T>(S.s[2 * k][q], S.s[2 * k + 1][q]);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const int i = 16 * it + l16, c = wave * St::CPW + 4 * NT * g;
-        const float e = sm.ecum[i];
+        const Slab<T> cs = load_slab(sm.c + (16 * it + l16) * PK + 32 * k);
 #pragma unroll
-        for (int q = 0; q < NT; ++q) acc[it][q] *= e;
-        if (finite) {
+        for (int q = 0; q < NT; ++q) acc[it][q] = mma(ss[q], cs, acc[it][q]);
+      }
+    }
 #pragma unroll
-          for (int js = 0; js <= it / 2; ++js) {
-            const Slab<T> m = sm.m[(2 * it + js) * 64 + lane];
+    for (int it = 0; it < 4; ++it) {
+      const int i = 16 * it + l16, c = wave * St::CPW + 4 * NT * g;
+      const float e = sm.ecum[i];
 #pragma unroll
-            for (int q = 0; q < NT; ++q) acc[it][q] = mma(xs[js][q], m, acc[it][q]);
-          }
-        } else {   // token by token, later ones left out
+      for (int q = 0; q < NT; ++q) acc[it][q] *= e;
+      if (finite) {
+#pragma unroll
+        for (int js = 0; js <= it / 2; ++js) {
+          const Slab<T> m = sm.m[(2 * it + js) * 64 + lane];
+#pragma unroll
+          for (int q = 0; q < NT; ++q) acc[it][q] = mma(xs[js][q], m, acc[it][q]);
+        }
+      } else {   // token by token, later ones left out
 #pragma unroll 1
-          for (int j = 0; j <= i; ++j) {
-            const T* mp = reinterpret_cast<const T*>(sm.m + (2 * it + (j >> 5)) * 64 + ((j >> 2) & 3) * 16 + l16);
-            const float m = to_f32(mp[4 * ((j >> 4) & 1) + (j & 3)]);
+        for (int j = 0; j <= i; ++j) {
+          const T* mp = reinterpret_cast<const T*>(sm.m + (2 * it + (j >> 5)) * 64 + ((j >> 2) & 3) * 16 + l16);
+          const float m = to_f32(mp[4 * ((j >> 4) & 1) + (j & 3)]);
 #pragma unroll
-            for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(sm.x + j * PV + c + 4 * q));
-          }
+          for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(sm.x + j * PV + c + 4 * q));
         }
-        float o[4 * NT];
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          const f32x4 xi = widen4(load4(sm.x + i * PV + c + 4 * q));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) o[4 * q + r] = a.D ? fmaf(dskip, xi[r], acc[it][q][r]) : acc[it][q][r];
-        }
-        if (i < n) Rows<T, 4 * NT>::store(y + (size_t)(t + i) * yld + c, o);
       }
+      float o[4 * NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const f32x4 xi = widen4(load4(sm.x + i * PV + c + 4 * q));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[4 * q + r] = a.D ? fmaf(dskip, xi[r], acc[it][q][r]) : acc[it][q][r];
+      }
+      if (i < n) Rows<T, 4 * NT>::store(y + (size_t)(t + i) * yld + c, o);
     }
 
-    // state update
-    const float el = exp2_of(last);
-    total += last;
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int q = 0; q < NT; ++q) S.s[k][q] *= el;
-#pragma unroll
-    for (int js = 0; js < 2; ++js) {
-      const f32x4 w0 = load4(sm.wdt + 32 * js + 4 * g), w1 = load4(sm.wdt + 32 * js + 16 + 4 * g);
-      Split<T> xw[NT];
-#pragma unroll
-      for (int q = 0; q < NT; ++q) xw[q] = scaled<T>(xs[js][q], w0, w1);
-#pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        const Slab<T> bs = slab_tr<T>(sm.b + 32 * js * PK, PK, 16 * k, 4);
-#pragma unroll
-        for (int q = 0; q < NT; ++q) S.s[k][q] = mma_split(bs, xw[q], S.s[k][q]);
-      }
-    }
+    S.update(exp2_of(last), sm.b, PK, xs, sm.wdt);
   }
-  if (!kOut) {
-    S.store(a.seg + slot * sd);
-    if (tid == 0) a.sum[slot] = total;
-  } else if (p.last && a.ht) {
-    S.store(a.ht + ((size_t)p.n * a.H + h) * sd);
-  }
-}
-
-// Chains a sequence's parts: slot k (the state part k adds, from zero) becomes
-// the state part k+1 starts from.  One thread a four-column piece of one
-// (sequence, head).
-__global__ __launch_bounds__(256) void ssm_chain_kernel(const SsmArgs a, const SeqTab sq, int sd4) {
-  const unsigned per = (unsigned)(sd4 / 256);
-  const unsigned nh = blockIdx.x / per;
-  const int li = (int)(nh / (unsigned)a.H), h = (int)(nh - (unsigned)li * a.H);
-  const int e = (int)((blockIdx.x - nh * per) * 256 + threadIdx.x);
-  const int first = sq.n ? sq.cc[li] : li * sq.parts, parts = sq.n ? sq.cc[li + 1] - first : sq.parts;
-  if (parts < 2) return;
-  const size_t n = (size_t)(sq.n ? sq.n0 + li : li);
-  f32x4 s = a.h0 ? load4(a.h0 + ((n * a.H + h) * sd4 + e) * 4) : zero4();
-  f32x4* seg = reinterpret_cast<f32x4*>(a.seg);
-  // where ht replaces h0, the first part may start after the last one has
-  // written: it reads this copy
-  if (a.start) reinterpret_cast<f32x4*>(a.start)[((size_t)(first - li) * a.H + h) * sd4 + e] = s;
-  for (int k = 0; k + 1 < parts; ++k) {
-    const size_t slot = (size_t)(first - li + k) * a.H + h;
-    s = s * exp2_of(a.sum[slot]) + seg[slot * sd4 + e];
-    seg[slot * sd4 + e] = s;
-  }
+  if (p.last && a.ht) S.store(a.ht + ((size_t)p.n * a.H + h) * sd);
 }
 
 template <typename T, int DK, int DV>
@@ -316,17 +220,18 @@ hipError_t fwd_go(const SsmArgs& a, const SeqTab& s, int seqs, bool split, hipSt
   dim3 grid;
   if (!item_head_grid(s.items, a.H, grid)) return hipErrorInvalidConfiguration;
   if (split) {
-    constexpr int sd4 = DK * DV / 4;
-    const long long blocks = (long long)seqs * a.H * (sd4 / 256);
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((ssm_chunk_kernel<T, DK, DV, false>), grid, dim3(kSsmThreads), 0, st, a, s);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(ssm_chain_kernel, dim3((unsigned)blocks), dim3(256), 0, st, a, s, sd4);
-    e = hipGetLastError();
+    SweepArgs w{};
+    w.f = a;
+    w.cols = a.x;
+    w.ldcols = a.ldx;
+    w.rows = a.B;
+    w.ldrows = a.ldb;
+    w.from = a.h0;
+    hipError_t e = launch_sweep<T, DK, DV, false, false>(w, s, st);
+    if (e == hipSuccess) e = launch_chain(w, s, seqs, DK * DV, false, st);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_chunk_kernel<T, DK, DV, true>), grid, dim3(kSsmThreads), 0, st, a, s);
+  hipLaunchKernelGGL((ssm_chunk_kernel<T, DK, DV>), grid, dim3(kSsmThreads), 0, st, a, s);
   return hipGetLastError();
 }
 
@@ -341,10 +246,10 @@ int ssm_part(long long tokens, int H) {
 }
 
 // A sequence of n parts keeps n - 1 states; n - 1 <= its tokens / part.
-static size_t seg_slots(long long tokens, int H) { return (size_t)(tokens / ssm_part(tokens, H)) * H; }
+size_t ssm_slots(long long tokens, int H) { return (size_t)(tokens / ssm_part(tokens, H)) * H; }
 
 size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv) {
-  const size_t slots = seg_slots(tokens, H);
+  const size_t slots = ssm_slots(tokens, H);
   return ((slots * (2 * (size_t)dk * dv * sizeof(float) + sizeof(double))) + 255) & ~(size_t)255;
 }
 
@@ -354,7 +259,7 @@ hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a0, int dk, int dv, const 
   const int part = ssm_part(tokens, a0.H), end = cu ? N : B;
   SsmArgs a = a0;
   a.seg = static_cast<float*>(workspace);
-  const size_t states = seg_slots(tokens, a.H) * (size_t)dk * dv;
+  const size_t states = ssm_slots(tokens, a.H) * (size_t)dk * dv;
   a.start = a.ht && a.ht == a.h0 ? a.seg + states : nullptr;
   a.sum = reinterpret_cast<double*>(a.seg + 2 * states);
   for (int n = 0; n < end;) {

@@ -8,7 +8,7 @@ namespace kda {
 
 constexpr int kSsmThreads = 256;
 constexpr int kSsmWaves = 4;
-constexpr int kQ = 64;   // tokens per chunk
+constexpr int kQ = kSeqChunk;   // tokens per chunk
 
 // log(1 + e^x) without overflow; log1p keeps its relative accuracy for very
 // negative x.
@@ -125,6 +125,86 @@ __device__ __forceinline__ f32x4 mma_split(const Slab<T>& a, const Split<T>& b, 
   }
   return acc;
 }
+
+template <typename T>
+__device__ __forceinline__ f32x4 mma_split(const Split<T>& a, const Slab<T>& b, f32x4 acc) {
+  acc = mma(a.h, b, acc);
+  if constexpr (sizeof(T) == 2) {
+    acc = mma(a.m, b, acc);
+    acc = mma(a.l, b, acc);
+  }
+  return acc;
+}
+
+// A state in the accumulator layout: the wave's dv/4 value columns as NT
+// tiles, KT tiles of state channels.  kPerm: output row m of tile t is column
+// wave CPW + 4 NT (m/4) + 4t + m%4 (a lane of a transposed product then holds
+// neighbouring columns); otherwise wave CPW + 16 t + m.
+template <int DK, int DV, bool kPerm>
+struct State {
+  static constexpr int CPW = DV / kSsmWaves, NT = CPW / 16, KT = DK / 16;
+  f32x4 s[KT][NT];
+  static __device__ __forceinline__ int col(int t) {
+    const int l16 = lane_id() & 15, wave = threadIdx.x >> 6;
+    return wave * CPW + (kPerm ? 4 * NT * (l16 >> 2) + 4 * t + (l16 & 3) : 16 * t + l16);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) s[k][t] = zero4();
+  }
+  __device__ __forceinline__ void load(const float* p) {
+    const int g = lane_id() >> 4;
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[k][t][r] = p[(size_t)(16 * k + 4 * g + r) * DV + col(t)];
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    const int g = lane_id() >> 4;
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) p[(size_t)(16 * k + 4 * g + r) * DV + col(t)] = s[k][t][r];
+  }
+  // s = s el + rows^T (cols w) over a chunk: rows [kQ][DK] and cols [kQ][DV] in
+  // LDS (xs: the wave's operand slabs of cols), one weight per token.
+  template <typename T>
+  __device__ __forceinline__ void update(float el, const T* rows, int pitch, const Slab<T> (&xs)[2][NT], const float* w) {
+    const int g = lane_id() >> 4;
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) s[k][q] *= el;
+#pragma unroll
+    for (int js = 0; js < 2; ++js) {
+      const f32x4 w0 = load4(w + 32 * js + 4 * g), w1 = load4(w + 32 * js + 16 + 4 * g);
+      Split<T> xw[NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) xw[q] = scaled<T>(xs[js][q], w0, w1);
+#pragma unroll
+      for (int k = 0; k < KT; ++k) {
+        const Slab<T> bs = slab_tr<T>(rows + 32 * js * pitch, pitch, 16 * k, 4);
+#pragma unroll
+        for (int q = 0; q < NT; ++q) s[k][q] = mma_split(bs, xw[q], s[k][q]);
+      }
+    }
+  }
+  template <typename T>
+  static __device__ __forceinline__ void slabs(const T* cols, int pitch, Slab<T> (&xs)[2][NT]) {
+    const int wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int js = 0; js < 2; ++js)
+#pragma unroll
+      for (int q = 0; q < NT; ++q)
+        xs[js][q] = slab_tr<T>(cols + 32 * js * pitch, pitch, wave * CPW + (kPerm ? 4 : 16) * q, kPerm ? 4 * NT : 4);
+  }
+};
 
 // kQ rows of D elements from global memory (row stride ld) to LDS (padded),
 // through registers: load() issues the loads of rows < n (rows behind are

@@ -96,7 +96,9 @@ def lib() -> ctypes.CDLL:
                 ("kda_qk_norm_rope_bwd", I, [P, LL, P, LL, P, P, P, P, P, I, I, F, P, P, I, P, P, P, P] + [I] * 8 + [P, S, P]),
                 ("kda_ssm_workspace_bytes", S, [I] * 6),
                 ("kda_ssm_fwd_chunked", I, [P, LL, P, LL, P, P, LL, P, LL, P, P, P, P, P] + [I] * 8 + [P, I, P, S, P]),
-                ("kda_ssm_step", I, [P, LL, P, LL, P, P, LL, P, LL, P, P, P, P, P] + [I] * 7 + [P])):
+                ("kda_ssm_step", I, [P, LL, P, LL, P, P, LL, P, LL, P, P, P, P, P] + [I] * 7 + [P]),
+                ("kda_ssm_bwd_workspace_bytes", S, [I] * 8),
+                ("kda_ssm_bwd_chunked", I, [P, LL, P, LL, P, P, LL, P, LL] + [P] * 13 + [I] * 8 + [P, I, P, S, P])):
             getattr(L, name).restype = res
             getattr(L, name).argtypes = args
         if hasattr(L, "kda_stamps_read"):
@@ -688,6 +690,32 @@ def ssm_step(x, dt, A, Bm, Cm, state, *, D=None, dt_bias=None, softplus=False, s
           _dense(so, "state_out", (B, H, dk, dv), torch.float32), y.data_ptr(), KDA_SSM_SOFTPLUS if softplus else 0, _dtype_code(x), B,
           H, G, dk, dv)
     return y
+
+
+def ssm_bwd_chunked(x, dt, A, Bm, Cm, dy, h0=None, dht=None, *, D=None, dt_bias=None, softplus=False, cu_seqlens=None, workspace=None,
+                    out=None):
+    """Gradients of ssm_fwd_chunked (kda_ssm_bwd_chunked) from dy [B,T,H,dv]
+    (x's type) and dht [N,H,dk,dv] fp32 (gradient of ht, or None): a dict of
+    dx, ddt, dB, dC (x's type) and dA, dD, ddt_bias [H], dh0 [N,H,dk,dv] fp32
+    (None for an input that was not given).  `out` may supply that dict."""
+    B, T, H, dv = x.shape
+    args, G, dk = _ssm_setup(x, dt, A, Bm, Cm, D, dt_bias, (B, T))
+    arr, N = _packed(cu_seqlens, B, T)
+    code, dev, st = _dtype_code(x), x.device, (N, H, dk, dv)
+    shapes = {"dx": (B, T, H, dv), "ddt": (B, T, H), "dB": (B, T, G, dk), "dC": (B, T, G, dk)}
+    small = {"dA": ((H,), A), "dD": ((H,), D), "ddt_bias": ((H,), dt_bias), "dh0": (st, h0)}
+    if out is None:
+        out = {n: torch.empty(s, dtype=x.dtype, device=dev) for n, s in shapes.items()}
+        out.update({n: torch.empty(s, dtype=torch.float32, device=dev) if t is not None else None for n, (s, t) in small.items()})
+    ws = _scratch(workspace, lib().kda_ssm_bwd_workspace_bytes(B, T, H, G, dk, dv, code, N if arr is not None else 0), dev,
+                  "kda_ssm_bwd_workspace_bytes")
+    _same_device(dev, dy=dy, h0=h0, dht=dht, workspace=ws, **out)
+    p = {n: _dense(out[n], n, s, x.dtype) for n, s in shapes.items()}
+    p.update({n: _dense(out.get(n), n, s, torch.float32) for n, (s, _) in small.items()})
+    _call(dev, "kda_ssm_bwd_chunked", *args, _dense(h0, "h0", st, torch.float32), _dense(dy, "dy", (B, T, H, dv), x.dtype),
+          _dense(dht, "dht", st, torch.float32), p["dx"], p["ddt"], p["dA"], p["dB"], p["dC"], p["dD"], p["ddt_bias"], p["dh0"],
+          KDA_SSM_SOFTPLUS if softplus else 0, code, B, T, H, G, dk, dv, arr, N, _ptr(ws), ws.numel())
+    return out
 
 
 def stamps_read():

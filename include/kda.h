@@ -511,6 +511,23 @@ int kda_ssm_step(const void* x, long long ldx, const void* dt, long long lddt, c
                  const void* Cm, long long ldc, const float* D, const float* dt_bias, const float* state, float* state_out,
                  void* y, int flags, int dtype, int B, int H, int G, int dk, int dv, void* stream);
 
+/*
+ * Gradients of kda_ssm_fwd_chunked from dy [B,T,H,dv] of dtype and dht
+ * [N,H,dk,dv] fp32 (NULL: none): dx [B,T,H,dv], ddt [B,T,H], dBm and dCm
+ * [B,T,G,dk] (sums over a group's heads) of dtype; dA, dD (NULL: not wanted),
+ * ddt_bias (NULL: not wanted) [H] and dh0 [N,H,dk,dv] (NULL: not wanted)
+ * fp32.  All contiguous and overwritten.  The states are recomputed inside
+ * `workspace` (kda_ssm_bwd_workspace_bytes, 0 for invalid sizes; N = 0 for a
+ * batch; two states per chunk of 64 tokens and head), 256-byte aligned.
+ * A value that is not finite may spread to the other tokens of its chunk.
+ */
+size_t kda_ssm_bwd_workspace_bytes(int B, int T, int H, int G, int dk, int dv, int dtype, int N);
+int kda_ssm_bwd_chunked(const void* x, long long ldx, const void* dt, long long lddt, const float* A, const void* Bm,
+                        long long ldb, const void* Cm, long long ldc, const float* D, const float* dt_bias, const float* h0,
+                        const void* dy, const float* dht, void* dx, void* ddt, float* dA, void* dBm, void* dCm, float* dD,
+                        float* ddt_bias, float* dh0, int flags, int dtype, int B, int T, int H, int G, int dk, int dv,
+                        const int* cu_seqlens, int N, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -109,3 +109,46 @@ def ssm_seq(x, raw, A, Bm, Cm, h0=None, D=None, bias=None, soft=False):
             y[t] += D[:, None] * x[t]
             size[t] += np.abs(D[:, None] * x[t])
     return y, S, size, Z
+
+
+def ssm_seq_bwd(x, raw, A, Bm, Cm, dy, h0=None, dht=None, D=None, bias=None, soft=False):
+    """Gradients of ssm_seq, token by token against the sequence: a dict of dx,
+    ddt, dA, dB, dC, dD, ddt_bias, dh0, and under the same names with a "|"
+    the same sums over absolute values (what roundings are relative to)."""
+    T, H, dv = x.shape
+    G, dk = Bm.shape[1:]
+    v = raw + (0.0 if bias is None else bias)
+    dt = softplus(v) if soft else v
+    sg = sigmoid(v) if soft else np.ones_like(v)
+    b, c = np.repeat(Bm, H // G, 1), np.repeat(Cm, H // G, 1)
+    S = np.zeros((T + 1, H, dk, dv))
+    Z = np.zeros_like(S)
+    if h0 is not None:
+        S[0], Z[0] = h0, np.abs(h0)
+    e = np.exp(dt * A)[..., None, None]
+    for t in range(T):
+        S[t + 1] = S[t] * e[t] + (dt[t][:, None] * b[t])[:, :, None] * x[t][:, None]
+        Z[t + 1] = Z[t] * e[t] + (np.abs(dt[t])[:, None] * np.abs(b[t]))[:, :, None] * np.abs(x[t])[:, None]
+    dS = np.zeros((H, dk, dv)) if dht is None else np.array(dht, dtype=np.float64)
+    dZ = np.abs(dS)
+    o = {n: np.zeros(s) for n, s in (("dx", x.shape), ("ddt", raw.shape), ("dA", (H,)), ("dB", b.shape), ("dC", c.shape), ("dD", (H,)),
+                                     ("ddt_bias", (H,)))}
+    o.update({n + "|": np.zeros_like(a) for n, a in list(o.items())})
+    for sgn, SS, dd, f in (("", S, dS, lambda a: a), ("|", Z, dZ, np.abs)):
+        for t in range(T - 1, -1, -1):
+            bb, cc, xx, yy, tt = f(b[t]), f(c[t]), f(x[t]), f(dy[t]), f(dt[t])
+            o["dC" + sgn][t] = (SS[t + 1] * yy[:, None]).sum(2)
+            dd = dd + cc[:, :, None] * yy[:, None]
+            o["dx" + sgn][t] = tt[:, None] * (dd * bb[:, :, None]).sum(1) + (0 if D is None else f(D)[:, None] * yy)
+            o["dB" + sgn][t] = tt[:, None] * (dd * xx[:, None]).sum(2)
+            da = (dd * SS[t] * e[t]).sum((1, 2))
+            d = f(A) * da + (dd * bb[:, :, None] * xx[:, None]).sum((1, 2))
+            o["dA" + sgn] += tt * da
+            o["ddt" + sgn][t] = d * sg[t]
+            o["ddt_bias" + sgn] += d * sg[t]
+            o["dD" + sgn] += (xx * yy).sum(1)
+            dd = dd * e[t]
+        o["dh0" + sgn] = dd
+    for n in ("dB", "dC", "dB|", "dC|"):
+        o[n] = o[n].reshape(T, G, H // G, dk).sum(2)
+    return o

@@ -150,3 +150,25 @@ SSTEP = {k: v for k, v in SSM.items() if k not in ("T", "cu", "N", "ws", "wsb")}
                                      (dict(dk=32), 5), (dict(ht=A[7] + 16), 10), (dict(y=A[8]), 10)])
 def test_ssm_step_refuses(kw, code):
     assert call("kda_ssm_step", list(SSTEP), SSTEP, **kw) == code
+
+
+SBWD = dict(x=A[0], ldx=256, dt=A[1], lddt=4, A=A[2], B=A[3], ldb=256, C=A[4], ldc=256, D=None, bias=None, h0=None, dy=A[5], dht=None, dx=A[6],
+            ddt=A[7], dA=A[8], dB=A[9], dC=A[10], dD=None, dbias=None, dh0=None, flags=1, dtype=1, Bn=2, T=1000, H=4, G=2, dk=128, dv=64, cu=None,
+            N=0, ws=A[11], wsb=1 << 40, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dy=None), 1), (dict(dx=None), 1), (dict(ddt=None), 1), (dict(dA=None), 1), (dict(dB=None), 1), (dict(dC=None), 1), (dict(G=3), 2),
+    (dict(dtype=3), 3), (dict(dht=A[0] + 4), 4), (dict(ws=A[11] + 16), 4), (dict(dv=48), 5), (dict(ws=None), 6), (dict(wsb=1000), 6),
+    (dict(dx=A[5]), 10), (dict(dB=A[10]), 10), (dict(dA=A[2]), 10), (dict(dx=A[11]), 10),
+])
+def test_ssm_bwd_refuses(kw, code):
+    assert call("kda_ssm_bwd_chunked", list(SBWD), SBWD, **kw) == code
+
+
+def test_ssm_bwd_workspace_bytes():
+    f = kda.lib().kda_ssm_bwd_workspace_bytes
+    assert f(1, 64, 2, 1, 64, 64, 1, 0) % 256 == 0 and f(1, 6400, 2, 1, 64, 64, 1, 0) >= 100 * 2 * 2 * 64 * 64 * 4
+    assert f(1, 640, 2, 1, 64, 64, 1, 50) >= f(1, 640, 2, 1, 64, 64, 1, 0)
+    for bad in ((0, 1, 2, 1, 64, 64, 1, 0), (1, 1, 2, 3, 64, 64, 1, 0), (1, 1, 2, 1, 32, 64, 1, 0), (1, 1, 2, 1, 64, 64, 2, 0), (2, 1, 2, 1, 64, 64, 1, 3)):
+        assert f(*bad) == 0

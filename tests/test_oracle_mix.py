@@ -109,3 +109,22 @@ def test_scan_carry_and_identity():
     assert np.allclose(np.concatenate([y1, y2]), y) and np.allclose(h2, ht)
     z = dict(c, raw=np.zeros((8, 2)), bias=None)
     assert np.allclose(mix.ssm_seq(**z)[1], c["h0"])   # steps of size zero leave the state
+
+
+@pytest.mark.parametrize("soft", [False, True])
+def test_scan_gradients_by_differences(soft):
+    c = _scan_case(5, 4, 2, 2, 3)
+    if not soft:
+        c["raw"], c["bias"] = np.abs(c["raw"]), None
+    dy, dht = rnd(5, 4, 3, seed=8), rnd(4, 2, 3, seed=9)
+    g = mix.ssm_seq_bwd(**{k: v for k, v in c.items()}, dy=dy, dht=dht, soft=soft)
+
+    def loss(**kw):
+        y, ht, _, _ = mix.ssm_seq(**{**c, **kw}, soft=soft)
+        return (y * dy).sum() + (ht * dht).sum()
+    for n, gn in (("x", "dx"), ("raw", "ddt"), ("A", "dA"), ("Bm", "dB"), ("Cm", "dC"), ("D", "dD"), ("bias", "ddt_bias"), ("h0", "dh0")):
+        if c[n] is None:
+            continue
+        for i in range(c[n].size):
+            assert np.isclose(_diff(lambda u: loss(**{n: u}), c[n], i), g[gn].flat[i], rtol=1e-5, atol=1e-6), (n, i)
+        assert (g[gn + "|"] >= np.abs(g[gn]) - 1e-9).all()
