@@ -192,9 +192,11 @@ struct SsmArgs {
   float* start;                      // copies of h0 where ht replaces it (or null)
   double* sum;                       // workspace: their decay sums
 };
-// Tokens of a part for these sizes, and the bytes of seg, start and sum together.
-int ssm_part(long long tokens, int H);
-size_t ssm_slots(long long tokens, int H);   // states between parts
+// Tokens of a part for about `wgs` (part, head) work-groups.  A sequence of n
+// parts keeps n - 1 states; n - 1 <= its tokens / part.
+int ssm_part(long long tokens, int H, int wgs);
+inline size_t ssm_slots(long long tokens, int H, int wgs) { return (size_t)(tokens / ssm_part(tokens, H, wgs)) * H; }
+// Workspace bytes of the forward.
 size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv);
 hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
                           hipStream_t stream);

@@ -242,8 +242,8 @@ int check_ssm(const kda::SsmArgs& a, int flags, int dtype, int B, int T, int dk,
     return KDA_ERR_SHAPE;
   if (!kda::supported_d(dk) || !kda::supported_d(dv)) return KDA_ERR_UNSUPPORTED;
   if (a.ldx < (long long)a.H * dv || a.lddt < a.H || a.ldb < (long long)a.G * dk || a.ldc < (long long)a.G * dk) return KDA_ERR_SHAPE;
-  for (long long ld : {a.ldx, a.lddt, a.ldb, a.ldc})
-    if (!size_ok(B, T, ld, 8)) return KDA_ERR_SHAPE;
+  for (long long ld : {a.ldx, a.lddt, a.ldb, a.ldc})   // 32-bit offsets within a few rows
+    if (ld > (1 << 24) || !size_ok(B, T, ld, 8)) return KDA_ERR_SHAPE;
   if (!a.x || !a.dt || !a.A || !a.B || !a.C) return KDA_ERR_NULL;
   const size_t esz = elem_size(dtype);
   for (const void* p : {a.x, a.B, a.C, (const void*)a.A, (const void*)a.D, (const void*)a.bias, (const void*)a.h0})

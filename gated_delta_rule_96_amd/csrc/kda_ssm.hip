@@ -41,6 +41,9 @@ namespace kda {
 
 namespace {
 
+constexpr int kScanWgs = 256;   // one scan work-group per CU
+constexpr int kSubs = 2;        // a part's own sum is formed in two shares (two sweep work-groups per CU)
+
 template <typename T, int DK, int DV>
 struct SsmLds {
   static constexpr int PK = RowTile<T, DK>::kPitch, PV = RowTile<T, DV>::kPitch;
@@ -76,8 +79,8 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
 
   St S;
   const size_t sd = (size_t)DK * DV;
-  const size_t slot = (size_t)(w.item - p.li) * a.H + h;   // of the next part's start
-  if (!p.first) S.load(a.seg + (slot - a.H) * sd);
+  const size_t slot = (size_t)(w.item - p.li) * kSubs * a.H + h;   // of the next part's start
+  if (!p.first) S.load(a.seg + (slot - (size_t)kSubs * a.H) * sd);
   else if (a.start && !p.last) S.load(a.start + slot * sd);
   else if (a.h0) S.load(a.h0 + ((size_t)p.n * a.H + h) * sd);
   else S.zero();
@@ -86,9 +89,9 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
   float raw = 0.f;
   auto fetch = [&](int t) {
     const int n = p.t1 - t;
-    rc.load(cm + (size_t)t * (size_t)a.ldc, a.ldc, n);
-    rb.load(bm + (size_t)t * (size_t)a.ldb, a.ldb, n);
-    rx.load(x + (size_t)t * (size_t)a.ldx, a.ldx, n);
+    rc.load(cm + (size_t)t * (size_t)a.ldc, a.ldc, n, tid);
+    rb.load(bm + (size_t)t * (size_t)a.ldb, a.ldb, n, tid);
+    rx.load(x + (size_t)t * (size_t)a.ldx, a.ldx, n, tid);
     raw = lane < n ? to_f32(dt[(size_t)(t + lane) * (size_t)a.lddt]) : 0.f;
   };
   if (p.t0 < p.t1) fetch(p.t0);
@@ -99,9 +102,9 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
     if (lane >= n) s = StepSize{0.f, 0.0};
     const double cum = wave_scan(s.a), last = lane63(cum);
     __syncthreads();   // the chunk before is done with LDS
-    rc.store(sm.c);
-    rb.store(sm.b);
-    rx.store(sm.x);
+    rc.store(sm.c, tid);
+    rb.store(sm.b, tid);
+    rx.store(sm.x, tid);
     if (wave == 0) {
       sm.cum[lane] = cum;
       sm.cumf[lane] = (float)cum;
@@ -119,7 +122,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
     const int it = wave, i = 16 * it + l16;
     Slab<T> cs[DK / 32];
 #pragma unroll
-    for (int k = 0; k < DK / 32; ++k) cs[k] = load_slab(sm.c + i * PK + 32 * k);
+    for (int k = 0; k < DK / 32; ++k) cs[k] = slab_any(sm.c, PK, 16 * it, 32 * k);
     const double ci = sm.cum[i];
     const float cif = sm.cumf[i];
 #pragma unroll
@@ -132,7 +135,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
         if (jt > it) continue;
         f32x4 acc = zero4();
 #pragma unroll
-        for (int k = 0; k < DK / 32; ++k) acc = mma(load_slab(sm.b + (16 * jt + l16) * PK + 32 * k), cs[k], acc);
+        for (int k = 0; k < DK / 32; ++k) acc = mma(slab_any(sm.b, PK, 16 * jt, 32 * k), cs[k], acc);
         const int j = 16 * jt + 4 * g;
         const f32x4 dj = load4(sm.dt + j);
         f32x4 ex;
@@ -152,7 +155,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
     __syncthreads();
 
     Slab<T> xs[2][NT];
-    St::slabs(sm.x, PV, xs);
+    St::template slabs<PadTile<T, DV>>(sm.x, xs);
     // a product with zeros is NaN exactly where x is not finite: the masked
     // entries of M would then spread later tokens' values to earlier ones
     f32x4 probe = zero4();
@@ -173,7 +176,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
       for (int q = 0; q < NT; ++q) ss[q] = make_slab<T>(S.s[2 * k][q], S.s[2 * k + 1][q]);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const Slab<T> cs = load_slab(sm.c + (16 * it + l16) * PK + 32 * k);
+        const Slab<T> cs = slab_row(sm.c, PK, 16 * it, 32 * k);
 #pragma unroll
         for (int q = 0; q < NT; ++q) acc[it][q] = mma(ss[q], cs, acc[it][q]);
       }
@@ -197,20 +200,235 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
           const T* mp = reinterpret_cast<const T*>(sm.m + (2 * it + (j >> 5)) * 64 + ((j >> 2) & 3) * 16 + l16);
           const float m = to_f32(mp[4 * ((j >> 4) & 1) + (j & 3)]);
 #pragma unroll
-          for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(sm.x + j * PV + c + 4 * q));
+          for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(lds_at(sm.x, PV, j, c + 4 * q)));
         }
       }
       float o[4 * NT];
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
-        const f32x4 xi = widen4(load4(sm.x + i * PV + c + 4 * q));
+        const f32x4 xi = four_of_row(sm.x, PV, 16 * it, c + 4 * q);
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[4 * q + r] = a.D ? fmaf(dskip, xi[r], acc[it][q][r]) : acc[it][q][r];
       }
       if (i < n) Rows<T, 4 * NT>::store(y + (size_t)(t + i) * yld + c, o);
     }
 
-    S.update(exp2_of(last), sm.b, PK, xs, sm.wdt);
+    S.template update<false, PadTile<T, DK>>(exp2_of(last), sm.b, xs, sm.wdt);
+  }
+  if (p.last && a.ht) S.store(a.ht + ((size_t)p.n * a.H + h) * sd);
+}
+
+// The same scan for bf16 with the work of a chunk split over two sets of four
+// waves that run one chunk apart: the front waves fetch chunk k + 2 straight
+// into LDS, form chunk k + 1's M and chunk k + 2's step sizes, while the back
+// waves take chunk k's products with S, its y and the state's update.  One
+// barrier a chunk; the matrix instructions of one set cover the loads and
+// exponents of the other.
+constexpr int kPipeThreads = 2 * kSsmThreads;
+
+template <int DK, int DV>
+struct PipeLds {
+  bf16 c[3][kQ * DK];
+  bf16 b[3][kQ * DK];
+  bf16 x[3][kQ * DV];
+  Slab<bf16> m[2][6 * 64];   // M rows of tile it, slab js, at (it + max(it - 2, 0) + js) 64 + lane
+  struct Sizes {
+    float cum[kQ], ecum[kQ], wdt[kQ], dt[kQ];
+  } z[3];
+  float el[4];               // exp(cum_Q) of chunk k at k % 3
+};
+__device__ __forceinline__ int m_slab(int it, int js) { return it + (it > 2 ? it - 2 : 0) + js; }
+
+template <int DK, int DV>
+__global__ __launch_bounds__(kPipeThreads, 2) void ssm_pipe_kernel(const SsmArgs a, const SeqTab sq) {
+  typedef bf16 T;
+  typedef PipeLds<DK, DV> Lds;
+  typedef State<DK, DV, true> St;
+  typedef SwzTile<DK> TK;
+  typedef SwzTile<DV> TV;
+  constexpr int NT = St::NT;
+  __shared__ __align__(16) char smem[sizeof(Lds)];
+  Lds& sm = *reinterpret_cast<Lds*>(smem);
+  ItemHead w;
+  if (!item_head(sq.items, a.H, w)) return;
+  const SeqPart p = seq_part(sq, w.item);
+  const bool front = threadIdx.x >= kSsmThreads;   // waves 4..7
+  const int tid = threadIdx.x & (kSsmThreads - 1), wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int h = w.h, grp = h / (a.H / a.G);
+  const int nch = (p.t1 - p.t0 + kQ - 1) / kQ;
+  constexpr size_t sd = (size_t)DK * DV;
+
+  if (front) {
+    const double a2 = (double)a.A[h] * 1.4426950408889634074;
+    const float bias = a.bias ? a.bias[h] : 0.f;
+    const size_t t00 = p.start + p.t0;
+    const T* x = (const T*)a.x + t00 * (size_t)a.ldx + (size_t)h * DV;
+    const T* bm = (const T*)a.B + t00 * (size_t)a.ldb + (size_t)grp * DK;
+    const T* cm = (const T*)a.C + t00 * (size_t)a.ldc + (size_t)grp * DK;
+    const T* dt = (const T*)a.dt + t00 * (size_t)a.lddt + h;
+    const int len = p.t1 - p.t0;
+    // step sizes are loaded one chunk further ahead than the rows
+    // (and kept as loaded: converting them would wait for them)
+    unsigned raw = 0;
+    auto fetch_dt = [&](int k) {
+      if (len > 0) raw = reinterpret_cast<const unsigned short*>(dt)[(size_t)min(kQ * k + lane, len - 1) * (size_t)a.lddt];
+    };
+    auto fetch = [&](int k) {
+      if (k >= nch) return;
+      const int t = kQ * k, n = len - t, q = k % 3;
+      TK::load(sm.c[q], cm + (size_t)t * (size_t)a.ldc, a.ldc, n, tid);
+      TK::load(sm.b[q], bm + (size_t)t * (size_t)a.ldb, a.ldb, n, tid);
+      TV::load(sm.x[q], x + (size_t)t * (size_t)a.ldx, a.ldx, n, tid);
+    };
+    // step sizes and decay sums: every wave forms them, one array each is kept
+    auto sizes = [&](int k) {
+      StepSize s = step_size(__uint_as_float(raw << 16), bias, a.softplus, a2);
+      if (lane >= len - kQ * k) s = StepSize{0.f, 0.0};
+      const double cum = wave_scan(s.a), last = lane63(cum);
+      typename Lds::Sizes& z = sm.z[k % 3];
+      if (wave == 0) {
+        z.cum[lane] = (float)cum;
+      } else if (wave == 1) {
+        z.ecum[lane] = exp2_of(cum);
+        if (lane == 0) sm.el[k % 3] = exp2_of(last);
+      } else if (wave == 2) {
+        z.wdt[lane] = exp2_of(last - cum) * s.dt;
+      } else {
+        z.dt[lane] = s.dt;
+      }
+    };
+    // rows 16 wave .. of M, transposed tiles (rows j, columns i)
+    auto scores = [&](int k) {
+      if (k >= nch) return;
+      const T *tc = sm.c[k % 3], *tb = sm.b[k % 3];
+      const typename Lds::Sizes& z = sm.z[k % 3];
+      const int it = wave, i = 16 * it + l16;
+      Slab<T> cs[DK / 32];
+#pragma unroll
+      for (int q = 0; q < DK / 32; ++q) cs[q] = TK::any(tc, 16 * it, q);
+      const float ci = z.cum[i];
+#pragma unroll
+      for (int js = 0; js < 2; ++js) {
+        if (2 * js > it) continue;
+        f32x4 v[2] = {zero4(), zero4()};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int jt = 2 * js + q;
+          if (jt > it) continue;
+          f32x4 acc = zero4();
+#pragma unroll
+          for (int y = 0; y < DK / 32; ++y) acc = mma(TK::any(tb, 16 * jt, y), cs[y], acc);
+          const int j = 16 * jt + 4 * g;
+          const f32x4 dj = load4(z.dt + j), cj = load4(z.cum + j);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) v[q][r] = j + r <= i ? acc[r] * exp2_fast(ci - cj[r]) * dj[r] : 0.f;
+        }
+        sm.m[k & 1][m_slab(it, js) * 64 + lane] = make_slab<T>(v[0], v[1]);
+      }
+    };
+    // all of the wave's loads (the compiler counts those straight into LDS and
+    // waits for the step sizes where they are used: here, once)
+    auto rows_there = [&] { asm volatile("s_waitcnt vmcnt(0)" : "+v"(raw) : : "memory"); };
+    fetch_dt(0);
+    fetch(0);
+    sizes(0);
+    fetch_dt(1);
+    fetch(1);
+    sizes(1);
+    fetch_dt(2);
+    rows_there();
+    __syncthreads();
+    scores(0);
+    __syncthreads();
+    for (int k = 0; k < nch; ++k) {
+      fetch(k + 2);
+      sizes(k + 2);
+      fetch_dt(k + 3);
+      scores(k + 1);
+      rows_there();
+      __syncthreads();
+    }
+    return;
+  }
+
+  St S;
+  const size_t slot = (size_t)(w.item - p.li) * kSubs * a.H + h;   // of the next part's start
+  if (!p.first) S.load(a.seg + (slot - (size_t)kSubs * a.H) * sd);
+  else if (a.start && !p.last) S.load(a.start + slot * sd);
+  else if (a.h0) S.load(a.h0 + ((size_t)p.n * a.H + h) * sd);
+  else S.zero();
+  const float dskip = a.D ? a.D[h] : 0.f;
+  const size_t yld = (size_t)a.H * DV;
+  T* y = (T*)a.y + ((p.start + p.t0) * (size_t)a.H + h) * DV;
+  __syncthreads();
+  __syncthreads();
+  for (int k = 0; k < nch; ++k) {
+    const int buf = k % 3;
+    const T *tc = sm.c[buf], *tb = sm.b[buf], *tx = sm.x[buf];
+    const typename Lds::Sizes& z = sm.z[buf];
+    const Slab<T>* tm = sm.m[k & 1];
+    const int n = min(p.t1 - p.t0 - kQ * k, kQ);
+    // S^T C
+    f32x4 acc[4][NT];
+#pragma unroll
+    for (int it = 0; it < 4; ++it)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) acc[it][q] = zero4();
+#pragma unroll
+    for (int y4 = 0; y4 < DK / 32; ++y4) {
+      Slab<T> ss[NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) ss[q] = make_slab<T>(S.s[2 * y4][q], S.s[2 * y4 + 1][q]);
+#pragma unroll
+      for (int it = 0; it < 4; ++it) {
+        const Slab<T> cs = TK::row(tc, 16 * it, y4);
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[it][q] = mma(ss[q], cs, acc[it][q]);
+      }
+    }
+    Slab<T> xs[2][NT];
+    St::template slabs<TV>(tx, xs);
+    // a product with zeros is NaN exactly where x is not finite: the masked
+    // entries of M would then spread later tokens' values to earlier ones
+    f32x4 probe = zero4();
+#pragma unroll
+    for (int js = 0; js < 2; ++js)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) probe = mma(Slab<T>{}, xs[js][q], probe);
+    const bool finite = !__any(probe[0] != probe[0]);
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int i = 16 * it + l16, col = wave * St::CPW + 4 * NT * g;
+      const float e = z.ecum[i];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) acc[it][q] *= e;
+      if (finite) {
+#pragma unroll
+        for (int js = 0; js <= it / 2; ++js) {
+          const Slab<T> m = tm[m_slab(it, js) * 64 + lane];
+#pragma unroll
+          for (int q = 0; q < NT; ++q) acc[it][q] = mma(xs[js][q], m, acc[it][q]);
+        }
+      } else {   // token by token, later ones left out
+#pragma unroll 1
+        for (int j = 0; j <= i; ++j) {
+          const T* mp = reinterpret_cast<const T*>(tm + m_slab(it, j >> 5) * 64 + ((j >> 2) & 3) * 16 + l16);
+          const float m = to_f32(mp[4 * ((j >> 4) & 1) + (j & 3)]);
+#pragma unroll
+          for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(tx + TV::at(j, col + 4 * q)));
+        }
+      }
+      float o[4 * NT];
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const f32x4 xi = TV::four(tx, 16 * it, col + 4 * q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[4 * q + r] = a.D ? fmaf(dskip, xi[r], acc[it][q][r]) : acc[it][q][r];
+      }
+      if (i < n) Rows<T, 4 * NT>::store(y + (size_t)(kQ * k + i) * yld + col, o);
+    }
+    S.template update<false, TK>(sm.el[buf], tb, xs, z.wdt);
+    __syncthreads();
   }
   if (p.last && a.ht) S.store(a.ht + ((size_t)p.n * a.H + h) * sd);
 }
@@ -227,39 +445,40 @@ hipError_t fwd_go(const SsmArgs& a, const SeqTab& s, int seqs, bool split, hipSt
     w.rows = a.B;
     w.ldrows = a.ldb;
     w.from = a.h0;
-    hipError_t e = launch_sweep<T, DK, DV, false, false>(w, s, st);
+    w.subs = kSubs;
+    hipError_t e = launch_sweep<T, DK, DV, false, false, false>(w, s, st);
     if (e == hipSuccess) e = launch_chain(w, s, seqs, DK * DV, false, st);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL((ssm_chunk_kernel<T, DK, DV>), grid, dim3(kSsmThreads), 0, st, a, s);
+  if constexpr (sizeof(T) == 2)
+    hipLaunchKernelGGL((ssm_pipe_kernel<DK, DV>), grid, dim3(kPipeThreads), 0, st, a, s);
+  else
+    hipLaunchKernelGGL((ssm_chunk_kernel<T, DK, DV>), grid, dim3(kSsmThreads), 0, st, a, s);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int ssm_part(long long tokens, int H) {
-  // about two work-groups per CU; a part is at least four chunks, so that the
-  // extra pass and the chaining stay small beside it
-  const long long want = (tokens * H + 511) / 512;
-  const long long part = (want + kQ - 1) / kQ * kQ;
+int ssm_part(long long tokens, int H, int wgs) {
+  // a part is at least four chunks, so that the extra pass and the chaining
+  // stay small beside it, and a whole number of chunks for each of its shares
+  const long long want = (tokens * H + wgs - 1) / wgs, unit = (long long)kQ * kSubs;
+  const long long part = (want + unit - 1) / unit * unit;
   return (int)(part < 256 ? 256 : part > (1 << 30) ? (1 << 30) : part);
 }
 
-// A sequence of n parts keeps n - 1 states; n - 1 <= its tokens / part.
-size_t ssm_slots(long long tokens, int H) { return (size_t)(tokens / ssm_part(tokens, H)) * H; }
-
 size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv) {
-  const size_t slots = ssm_slots(tokens, H);
+  const size_t slots = kSubs * ssm_slots(tokens, H, kScanWgs);
   return ((slots * (2 * (size_t)dk * dv * sizeof(float) + sizeof(double))) + 255) & ~(size_t)255;
 }
 
 hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a0, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
                           hipStream_t st) {
   const long long tokens = (long long)B * T;
-  const int part = ssm_part(tokens, a0.H), end = cu ? N : B;
+  const int part = ssm_part(tokens, a0.H, kScanWgs), end = cu ? N : B;
   SsmArgs a = a0;
   a.seg = static_cast<float*>(workspace);
-  const size_t states = ssm_slots(tokens, a.H) * (size_t)dk * dv;
+  const size_t states = kSubs * ssm_slots(tokens, a.H, kScanWgs) * (size_t)dk * dv;
   a.start = a.ht && a.ht == a.h0 ? a.seg + states : nullptr;
   a.sum = reinterpret_cast<double*>(a.seg + 2 * states);
   for (int n = 0; n < end;) {

@@ -36,6 +36,8 @@ namespace kda {
 
 namespace {
 
+constexpr int kSweepWgs = 512;   // two sweep work-groups per CU
+
 struct ChunkBwd {
   SsmBwdArgs b;
   const float *S, *dS;     // [chunks][H][dk][dv]
@@ -47,7 +49,7 @@ struct ChunkBwd {
 
 template <typename T, int DK, int DV>
 struct BwdLds {
-  static constexpr int PK = RowTile<T, DK>::kPitch, PV = RowTile<T, DV>::kPitch, PM = kQ + LdsPad<T>::v;
+  static constexpr int PK = RowTile<T, DK>::kPitch, PV = RowTile<T, DV>::kPitch, PM = kQ + LdsRow<T>::pad;
   T c[kQ * PK];
   T b[kQ * PK];
   union {
@@ -109,21 +111,22 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
   // transposed tile: rows m of tile t are base + 4 N (m/4) + 4t + m%4.
   const int k0 = wave * CPK, c0 = wave * CPV;
   const int i_own = 16 * wave + l16;   // column of the strip this wave forms
+  T* m_own = sm.m + i_own * PM + LdsRow<T>::shift(i_own);
 
   RowTile<T, DV> rx, ry;
   float raw = 0.f;
   auto fetch = [&](int h) {
-    rx.load(x + (size_t)h * DV, f.ldx, n);
-    ry.load(dyp + (size_t)h * DV, vld, n);
+    rx.load(x + (size_t)h * DV, f.ldx, n, tid);
+    ry.load(dyp + (size_t)h * DV, vld, n, tid);
     raw = lane < n ? to_f32(dt[(size_t)lane * (size_t)f.lddt + h]) : 0.f;
   };
   {
     RowTile<T, DK> rc, rb;
-    rc.load((const T*)f.C + tok * (size_t)f.ldc + (size_t)grp * DK, f.ldc, n);
-    rb.load((const T*)f.B + tok * (size_t)f.ldb + (size_t)grp * DK, f.ldb, n);
+    rc.load((const T*)f.C + tok * (size_t)f.ldc + (size_t)grp * DK, f.ldc, n, tid);
+    rb.load((const T*)f.B + tok * (size_t)f.ldb + (size_t)grp * DK, f.ldb, n, tid);
     if (h0 < h1) fetch(h0);
-    rc.store(sm.c);
-    rb.store(sm.b);
+    rc.store(sm.c, tid);
+    rb.store(sm.b, tid);
   }
   __syncthreads();
   // P of the wave's strip, transposed tiles (rows j, columns i), for all heads
@@ -134,7 +137,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     if (jt > wave) continue;
 #pragma unroll
     for (int k = 0; k < DK / 32; ++k)
-      pt[jt] = mma(load_slab(sm.b + (16 * jt + l16) * PK + 32 * k), load_slab(sm.c + i_own * PK + 32 * k), pt[jt]);
+      pt[jt] = mma(slab_any(sm.b, PK, 16 * jt, 32 * k), slab_any(sm.c, PK, 16 * wave, 32 * k), pt[jt]);
   }
   f32x4 dC[4][NK], dB[4][NK];   // transposed: rows state channels, columns tokens
 #pragma unroll
@@ -149,8 +152,8 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     if (lane >= n) s = StepSize{0.f, 0.0};
     const double cum = wave_scan(s.a), last = lane63(cum);
     __syncthreads();   // the head before is done with LDS
-    rx.store(sm.x);
-    ry.store(sm.dy);
+    rx.store(sm.x, tid);
+    ry.store(sm.dy, tid);
     if (wave == 0) sm.cum[lane] = cum;
     else if (wave == 1) sm.ecum[lane] = exp2_of(cum);
     else if (wave == 2) sm.w[lane] = exp2_of(last - cum);
@@ -165,7 +168,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     {
       Slab<T> ys[DV / 32];
 #pragma unroll
-      for (int k = 0; k < DV / 32; ++k) ys[k] = load_slab(sm.dy + i_own * PV + 32 * k);
+      for (int k = 0; k < DV / 32; ++k) ys[k] = slab_any(sm.dy, PV, 16 * wave, 32 * k);
       const double ci = sm.cum[i_own];
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
@@ -176,7 +179,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
         if (jt <= wave) {
           f32x4 acc = zero4();
 #pragma unroll
-          for (int k = 0; k < DV / 32; ++k) acc = mma(load_slab(sm.x + (16 * jt + l16) * PV + 32 * k), ys[k], acc);
+          for (int k = 0; k < DV / 32; ++k) acc = mma(slab_any(sm.x, PV, 16 * jt, 32 * k), ys[k], acc);
           const int j = 16 * jt + 4 * g;
           const f32x4 dj = load4(sm.dt + j);
 #pragma unroll
@@ -197,7 +200,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
           }
         }
         ep[jt] = narrow4<T>(mm);
-        store4(sm.m + i_own * PM + 16 * jt + 4 * g, narrow4<T>(nn));
+        store4(m_own + 16 * jt + 4 * g, narrow4<T>(nn));
       }
       row = sum_groups(row);
       diag = sum_groups(diag);   // one lane of a column holds it
@@ -210,9 +213,9 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
 
     // S dy and dS x (transposed: rows the wave's state channels)
     const size_t st = ((size_t)item * f.H + h) * (size_t)(DK * DV);
-    float su[4], sv[4], gs = 0.f;
+    float su[4], sv[4], gs;
     {
-      f32x4 U[4][NK], Z[4][NK];
+      f32x4 U[4][NK], Z[4][NK], g4 = zero4();
 #pragma unroll
       for (int it = 0; it < 4; ++it)
 #pragma unroll
@@ -225,13 +228,13 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
           const size_t at = st + (size_t)(k0 + 4 * NK * (l16 >> 2) + 4 * q + (l16 & 3)) * DV + 32 * k + 4 * g;
           const f32x4 s0 = load4(a.S + at), s1 = load4(a.S + at + 16), d0 = load4(a.dS + at), d1 = load4(a.dS + at + 16);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) gs = fmaf(s0[r], d0[r], fmaf(s1[r], d1[r], gs));
+          for (int r = 0; r < 4; ++r) g4[r] = fmaf(s0[r], d0[r], fmaf(s1[r], d1[r], g4[r]));
           split_of(s0, s1, ss[q]);
           split_of(d0, d1, ds[q]);
         }
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          const Slab<T> ys = load_slab(sm.dy + (16 * it + l16) * PV + 32 * k), xs = load_slab(sm.x + (16 * it + l16) * PV + 32 * k);
+          const Slab<T> ys = slab_row(sm.dy, PV, 16 * it, 32 * k), xs = slab_row(sm.x, PV, 16 * it, 32 * k);
 #pragma unroll
           for (int q = 0; q < NK; ++q) {
             U[it][q] = mma_split(ss[q], ys, U[it][q]);
@@ -239,6 +242,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
           }
         }
       }
+      gs = (g4[0] + g4[1]) + (g4[2] + g4[3]);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
         const int i = 16 * it + l16;
@@ -246,7 +250,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
         float uu = 0.f, vv = 0.f;
 #pragma unroll
         for (int q = 0; q < NK; ++q) {
-          const f32x4 c4 = widen4(load4(sm.c + i * PK + k0 + 4 * NK * g + 4 * q)), b4 = widen4(load4(sm.b + i * PK + k0 + 4 * NK * g + 4 * q));
+          const f32x4 c4 = four_of_row(sm.c, PK, 16 * it, k0 + 4 * NK * g + 4 * q), b4 = four_of_row(sm.b, PK, 16 * it, k0 + 4 * NK * g + 4 * q);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             uu = fmaf(c4[r], U[it][q][r], uu);
@@ -282,11 +286,11 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     for (int js = 0; js < 2; ++js) {
 #pragma unroll
       for (int q = 0; q < NK; ++q) {
-        const Slab<T> bs = slab_tr<T>(sm.b + 32 * js * PK, PK, k0 + 4 * q, 4 * NK), cs = slab_tr<T>(sm.c + 32 * js * PK, PK, k0 + 4 * q, 4 * NK);
+        const Slab<T> bs = slab_tr<T>(sm.b, PK, 32 * js, k0 + 4 * q, 4 * NK), cs = slab_tr<T>(sm.c, PK, 32 * js, k0 + 4 * q, 4 * NK);
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
-          if (js <= it / 2) dC[it][q] = mma(bs, load_slab(sm.m + (16 * it + l16) * PM + 32 * js), dC[it][q]);
-          if (js >= it / 2) dB[it][q] = mma(cs, slab_tr<T>(sm.m + 32 * js * PM, PM, 16 * it, 4), dB[it][q]);
+          if (js <= it / 2) dC[it][q] = mma(bs, slab_row(sm.m, PM, 16 * it, 32 * js), dC[it][q]);
+          if (js >= it / 2) dB[it][q] = mma(cs, slab_tr<T>(sm.m, PM, 32 * js, 16 * it, 4), dB[it][q]);
         }
       }
     }
@@ -312,7 +316,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
       }
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const Slab<T> bs = load_slab(sm.b + (16 * it + l16) * PK + 32 * k);
+        const Slab<T> bs = slab_row(sm.b, PK, 16 * it, 32 * k);
 #pragma unroll
         for (int q = 0; q < NV; ++q) dx[it][q] = mma(ds[q], bs, dx[it][q]);
       }
@@ -320,22 +324,22 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     __syncthreads();   // E dt Qm is used up; the sums are complete
 #pragma unroll
     for (int jt = 0; jt < 4; ++jt)
-      if (jt <= (wave | 1)) store4(sm.m + i_own * PM + 16 * jt + 4 * g, ep[jt]);
+      if (jt <= (wave | 1)) store4(m_own + 16 * jt + 4 * g, ep[jt]);
     if (wave == 0) {
       // the chunk's per-token sums: lane = token
-      const float u = (sm.s.u[0][lane] + sm.s.u[1][lane]) + (sm.s.u[2][lane] + sm.s.u[3][lane]);
-      const float v = (sm.s.v[0][lane] + sm.s.v[1][lane]) + (sm.s.v[2][lane] + sm.s.v[3][lane]);
-      float cs = 0.f;   // a strip before token j's tile has no entry of column j
+      const double u = ((double)sm.s.u[0][lane] + sm.s.u[1][lane]) + ((double)sm.s.u[2][lane] + sm.s.u[3][lane]);
+      const double v = ((double)sm.s.v[0][lane] + sm.s.v[1][lane]) + ((double)sm.s.v[2][lane] + sm.s.v[3][lane]);
+      double cs = 0.0;   // a strip before token j's tile has no entry of column j
 #pragma unroll
       for (int q = 0; q < kSsmWaves; ++q)
-        if (q >= lane >> 4) cs += sm.s.col[q][lane];
-      const double vd = (double)v * s.dt;
-      const double net = (double)sm.s.row[lane] + u - (double)cs * s.dt - vd;
+        if (q >= lane >> 4) cs += (double)sm.s.col[q][lane];
+      const double vd = v * s.dt;
+      const double net = (double)sm.s.row[lane] + u - cs * s.dt - vd;
       const double gsum = ((double)sm.s.g[0] + sm.s.g[1]) + ((double)sm.s.g[2] + sm.s.g[3]);
       const double incl = wave_scan(net);
       const double all = lane63(incl) + lane63(wave_scan(vd)) + (double)exp2_of(last) * gsum;
       const double da = all - (incl - net);
-      double d = (double)f.A[h] * da + (double)cs + sm.s.diag[lane] + v;
+      double d = (double)f.A[h] * da + cs + sm.s.diag[lane] + v;
       if (f.softplus) d *= (double)sigmoid_fast(rawv + bias);
       if (lane >= n) d = 0.0;
       if (lane < n) ((T*)b.ddt)[(tok + lane) * (size_t)f.H + h] = from_f32<T>((float)d);
@@ -354,7 +358,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
 #pragma unroll
     for (int js = 0; js < 2; ++js)
 #pragma unroll
-      for (int q = 0; q < NV; ++q) ysT[js][q] = slab_tr<T>(sm.dy + 32 * js * PV, PV, c0 + 4 * q, 4 * NV);
+      for (int q = 0; q < NV; ++q) ysT[js][q] = slab_tr<T>(sm.dy, PV, 32 * js, c0 + 4 * q, 4 * NV);
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int j = 16 * it + l16, c = c0 + 4 * NV * g;
@@ -363,14 +367,14 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
       for (int q = 0; q < NV; ++q) dx[it][q] *= w;
 #pragma unroll
       for (int js = it / 2; js < 2; ++js) {
-        const Slab<T> ms = slab_tr<T>(sm.m + 32 * js * PM, PM, 16 * it, 4);
+        const Slab<T> ms = slab_tr<T>(sm.m, PM, 32 * js, 16 * it, 4);
 #pragma unroll
         for (int q = 0; q < NV; ++q) dx[it][q] = mma(ysT[js][q], ms, dx[it][q]);
       }
       float o[4 * NV];
 #pragma unroll
       for (int q = 0; q < NV; ++q) {
-        const f32x4 yj = widen4(load4(sm.dy + j * PV + c + 4 * q));
+        const f32x4 yj = four_of_row(sm.dy, PV, 16 * it, c + 4 * q);
 #pragma unroll
         for (int r = 0; r < 4; ++r) o[4 * q + r] = f.D ? fmaf(dskip, yj[r], dj * dx[it][q][r]) : dj * dx[it][q][r];
       }
@@ -431,7 +435,7 @@ struct BwdLayout {
   int shares;
 };
 BwdLayout bwd_layout(int is_packed, int N, int B, int T, int H, int G, int dk, int dv) {
-  const size_t tokens = (size_t)B * T, sd = (size_t)dk * dv * sizeof(float), slots = ssm_slots((long long)tokens, H);
+  const size_t tokens = (size_t)B * T, sd = (size_t)dk * dv * sizeof(float), slots = ssm_slots((long long)tokens, H, kSweepWgs);
   BwdLayout L{};
   L.chunks = is_packed ? (size_t)T / kQ + N : (size_t)B * (((size_t)T + kQ - 1) / kQ);
   L.shares = head_shares((long long)L.chunks, H, G);
@@ -456,7 +460,7 @@ BwdLayout bwd_layout(int is_packed, int N, int B, int T, int H, int G, int dk, i
 template <typename T, int DK, int DV>
 hipError_t bwd_go(const SsmBwdArgs& b, const BwdLayout& L, const int* cu, int N, int B, int Tn, char* ws, hipStream_t st) {
   const long long tokens = (long long)B * Tn;
-  const int part = ssm_part(tokens, b.f.H), end = cu ? N : B;
+  const int part = ssm_part(tokens, b.f.H, kSweepWgs), end = cu ? N : B;
   ChunkBwd a{};
   a.b = b;
   a.b.f.seg = reinterpret_cast<float*>(ws + L.seg);
@@ -485,13 +489,14 @@ hipError_t bwd_go(const SsmBwdArgs& b, const BwdLayout& L, const int* cu, int N,
     w.ldcols = b.f.ldx;
     w.from = b.f.h0;
     w.at = S;
+    w.subs = 1;
     hipError_t e = hipSuccess;
     if (split) {
-      e = launch_sweep<T, DK, DV, false, false>(w, s, st);
+      e = launch_sweep<T, DK, DV, false, false, true>(w, s, st);
       if (e == hipSuccess) e = launch_chain(w, s, n - n0, DK * DV, false, st);
       if (e != hipSuccess) return e;
     }
-    if ((e = launch_sweep<T, DK, DV, false, true>(w, s, st)) != hipSuccess) return e;
+    if ((e = launch_sweep<T, DK, DV, false, true, true>(w, s, st)) != hipSuccess) return e;
     w.rows = b.f.C;
     w.ldrows = b.f.ldc;
     w.cols = b.dy;
@@ -500,11 +505,11 @@ hipError_t bwd_go(const SsmBwdArgs& b, const BwdLayout& L, const int* cu, int N,
     w.to = b.dh0;
     w.at = dS;
     if (split) {
-      e = launch_sweep<T, DK, DV, true, false>(w, s, st);
+      e = launch_sweep<T, DK, DV, true, false, true>(w, s, st);
       if (e == hipSuccess) e = launch_chain(w, s, n - n0, DK * DV, true, st);
       if (e != hipSuccess) return e;
     }
-    if ((e = launch_sweep<T, DK, DV, true, true>(w, s, st)) != hipSuccess) return e;
+    if ((e = launch_sweep<T, DK, DV, true, true, true>(w, s, st)) != hipSuccess) return e;
     a.S = S;
     a.dS = dS;
     a.part = reinterpret_cast<float*>(ws + L.part) + at * 3;

@@ -10,9 +10,28 @@ constexpr int kSsmThreads = 256;
 constexpr int kSsmWaves = 4;
 constexpr int kQ = kSeqChunk;   // tokens per chunk
 
-// log(1 + e^x) without overflow; log1p keeps its relative accuracy for very
-// negative x.
-__device__ __forceinline__ float softplus_f(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+// Softplus(x) = log(1 + e^x) = max(x, 0) + log1p(u), u = e^-|x| in (0, 1], with
+// log1p(u) = 2 artanh(z), z = u / (2 + u) <= 1/3, by its series (the first
+// term left out is below 2e-9 of the sum): relative accuracy also for very
+// negative x, where the result is e^x.  e^-|x| as 2^(n + r) with the rounding
+// r of the product by log2(e) put back, so that large |x| costs no accuracy.
+__device__ __forceinline__ float softplus_f(float x) {
+  const float m = -fabsf(x);
+  const float n = m * kLog2e;
+  const float r = fmaf(m, 1.925963033500e-8f, fmaf(m, kLog2e, -n));   // log2(e) - fl(log2(e))
+  const float e = exp2_fast(n);
+  const float u = fmaf(e, r * 0.69314718f, e);
+  const float z = u * __builtin_amdgcn_rcpf(2.0f + u), q = z * z;
+  float t = 1.f / 15.f;
+  t = fmaf(t, q, 1.f / 13.f);
+  t = fmaf(t, q, 1.f / 11.f);
+  t = fmaf(t, q, 1.f / 9.f);
+  t = fmaf(t, q, 1.f / 7.f);
+  t = fmaf(t, q, 1.f / 5.f);
+  t = fmaf(t, q, 1.f / 3.f);
+  const float l = 2.f * z;
+  return fmaxf(x, 0.f) + fmaf(l * q, t, l);
+}
 
 // x from the lane that DPP control `ctrl` selects, 0 where there is none.
 template <int ctrl, int row_mask = 0xf>
@@ -55,26 +74,38 @@ __device__ __forceinline__ StepSize step_size(float raw, float bias, int softplu
   return s;
 }
 
-// Rows of LDS tiles are padded so that 16 rows' equal columns fall on
-// different banks.
-template <typename T> struct LdsPad;
-template <> struct LdsPad<bf16> { static constexpr int v = 8; };
-template <> struct LdsPad<float> { static constexpr int v = 4; };
+// Rows of LDS tiles.  16-bit types: a row's start is 8 (row % 8) + 4 (row / 8
+// % 2) banks on (row pitch D + 16 elements, rows 8..15 of every 16 another 8
+// elements on), so that both the slab reads (16 rows, 16 bytes each from half
+// a wave) and the transposed ones (8 rows, 32 bytes each) touch every bank
+// once.  fp32: 4 banks a row.
+template <typename T> struct LdsRow;
+template <> struct LdsRow<bf16> {
+  static constexpr int pad = 16;
+  static __device__ __forceinline__ int shift(int row) { return row & 8; }
+};
+template <> struct LdsRow<float> {
+  static constexpr int pad = 4;
+  static __device__ __forceinline__ int shift(int) { return 0; }
+};
+template <typename T> __device__ __forceinline__ const T* lds_at(const T* p, int pitch, int row, int col) {
+  return p + row * pitch + LdsRow<T>::shift(row) + col;
+}
 
-// Slab whose reduction index is the LDS row: rows r0 + {4g.., 16+4g..} of one
-// column per lane (l16 = lane % 16).  The column of l16 is c0 + step (l16 / 4)
+// Slab whose reduction index is the LDS row: rows r0 + {4g.., 16+4g..} (r0 a
+// multiple of 32) of one column per lane (l16 = lane % 16).  The column of l16 is c0 + step (l16 / 4)
 // + l16 % 4.  16-bit types: the transposed LDS read, whose lane 4q + s of a
 // group of 16 points at row 4g + q, columns 4s..4s+3 and gets column 4q + s.
 template <typename T>
-__device__ __forceinline__ Slab<T> slab_tr(const T* p, int pitch, int c0, int step) {
+__device__ __forceinline__ Slab<T> slab_tr(const T* p, int pitch, int r0, int c0, int step) {
   const int l = lane_id(), g = l >> 4, l16 = l & 15;
   Slab<T> s;
   if constexpr (sizeof(T) == 2) {
     typedef __attribute__((address_space(3))) bf16x4* LdsP;
-    const T* a = p + (4 * g + (l16 >> 2)) * pitch + c0 + step * (l16 & 3);
+    const T* a = lds_at(p, pitch, 4 * g + (l16 >> 2), step * (l16 & 3)) + r0 * pitch + c0;
     s = slab_of<T>(__builtin_amdgcn_ds_read_tr16_b64_v4bf16((LdsP)(a)), __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LdsP)(a + 16 * pitch)));
   } else {
-    const T* a = p + (4 * g) * pitch + c0 + step * (l16 >> 2) + (l16 & 3);
+    const T* a = p + (r0 + 4 * g) * pitch + c0 + step * (l16 >> 2) + (l16 & 3);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       s.lo[i] = a[i * pitch];
@@ -83,19 +114,59 @@ __device__ __forceinline__ Slab<T> slab_tr(const T* p, int pitch, int c0, int st
   }
   return s;
 }
+// Slab along a row: columns c0 + {4g.., 16+4g..} of row r0 + l16 (r0 a multiple
+// of 16).  The second half's address is hidden from the compiler: joined into
+// one two-address read the halves meet in the same banks.
+template <typename T>
+__device__ __forceinline__ Slab<T> slab_row(const T* p, int pitch, int r0, int c0) {
+  const int g = lane_id() >> 4;
+  const int at = (int)(lds_at((const T*)nullptr, pitch, lane_id() & 15, 4 * g) - (const T*)nullptr);
+  int far = at + 16;
+  if constexpr (sizeof(T) == 2) asm("" : "+v"(far));
+  return slab_of<T>(load4(p + at + (r0 * pitch + c0)), load4(p + far + (r0 * pitch + c0)));
+}
+// Slab of a product of two rows: columns c0 + 8g .. 8g+7, one 16-byte read
+// (bf16); any order of the reduction index serves if both operands have it.
+template <typename T>
+__device__ __forceinline__ Slab<T> slab_any(const T* p, int pitch, int r0, int c0) {
+  const T* a = lds_at(p, pitch, lane_id() & 15, 8 * (lane_id() >> 4)) + r0 * pitch + c0;
+  Slab<T> s;
+  if constexpr (sizeof(T) == 2) s.v = *reinterpret_cast<const bf16x8*>(a);
+  else s = slab_of<T>(load4(a), load4(a + 4));
+  return s;
+}
+// Four columns from c0 of row r0 + l16.
+template <typename T>
+__device__ __forceinline__ f32x4 four_of_row(const T* p, int pitch, int r0, int c0) {
+  return widen4(load4(lds_at(p, pitch, lane_id() & 15, 0) + r0 * pitch + c0));
+}
 
 // fp32 values as an operand of products that stay fp32 results: one slab
-// (fp32), or three bf16 slabs, each the rounding of what the ones before left
-// (8 significant bits each: 24 together).
+// (fp32), or three bf16 slabs that together are the values exactly: the upper
+// eight of the 24 significant bits, the next eight, the rest (truncations).
 template <typename T> struct Split;
 template <> struct Split<float> { Slab<float> h; };
 template <> struct Split<bf16> { Slab<bf16> h, m, l; };
 __device__ __forceinline__ void split_of(f32x4 lo, f32x4 hi, Split<float>& s) { s.h = Slab<float>{lo, hi}; }
+__device__ __forceinline__ float upper16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+// The upper halves of a and b as two bf16.
+__device__ __forceinline__ unsigned pack_upper(float a, float b) {
+  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+}
 __device__ __forceinline__ void split_of(f32x4 lo, f32x4 hi, Split<bf16>& s) {
-  const V4<bf16> a = narrow4<bf16>(lo), b = narrow4<bf16>(hi);
-  const f32x4 ra = lo - widen4(a), rb = hi - widen4(b);
-  s.h = slab_of<bf16>(a, b);
-  make_slab_split<bf16>(ra, rb, s.m, s.l);
+  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 h, m, l;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = k < 2 ? lo[2 * k] : hi[2 * k - 4], b = k < 2 ? lo[2 * k + 1] : hi[2 * k - 3];
+    const float ra = a - upper16(a), rb = b - upper16(b);
+    h[k] = pack_upper(a, b);
+    m[k] = pack_upper(ra, rb);
+    l[k] = pack_upper(ra - upper16(ra), rb - upper16(rb));
+  }
+  s.h.v = __builtin_bit_cast(bf16x8, h);
+  s.m.v = __builtin_bit_cast(bf16x8, m);
+  s.l.v = __builtin_bit_cast(bf16x8, l);
 }
 // x w elementwise along the reduction index.
 template <typename T>
@@ -115,26 +186,89 @@ __device__ __forceinline__ Split<T> scaled(const Slab<T>& x, f32x4 w0, f32x4 w1)
   split_of(a, b, s);
   return s;
 }
-// acc += A B with one operand in parts
-template <typename T>
-__device__ __forceinline__ f32x4 mma_split(const Slab<T>& a, const Split<T>& b, f32x4 acc) {
-  acc = mma(a, b.h, acc);
-  if constexpr (sizeof(T) == 2) {
-    acc = mma(a, b.m, acc);
-    acc = mma(a, b.l, acc);
-  }
+// lo += A B's lower parts, and acc + A B with one operand in parts.  The lower
+// parts have a sum of their own: a product of much larger terms cuts a small
+// accumulator off below its own last place (downwards: measured mean error
+// 1.2e-8 of the result, which sums over many tokens show), a sum of terms of
+// its own size is rounded to nearest (mean error below 1e-9).
+template <typename T> __device__ __forceinline__ f32x4 mma_low(const Slab<T>& a, const Split<T>& b, f32x4 lo) {
+  if constexpr (sizeof(T) == 2) lo = mma(a, b.m, mma(a, b.l, lo));
+  return lo;
+}
+template <typename T> __device__ __forceinline__ f32x4 mma_low(const Split<T>& a, const Slab<T>& b, f32x4 lo) {
+  if constexpr (sizeof(T) == 2) lo = mma(a.m, b, mma(a.l, b, lo));
+  return lo;
+}
+template <typename T> __device__ __forceinline__ f32x4 mma_split(const Split<T>& a, const Slab<T>& b, f32x4 acc) {
+  acc = mma(a.h, b, acc);
+  if constexpr (sizeof(T) == 2) acc += mma_low(a, b, zero4());
   return acc;
 }
 
-template <typename T>
-__device__ __forceinline__ f32x4 mma_split(const Split<T>& a, const Slab<T>& b, f32x4 acc) {
-  acc = mma(a.h, b, acc);
-  if constexpr (sizeof(T) == 2) {
-    acc = mma(a.m, b, acc);
-    acc = mma(a.l, b, acc);
+// bf16 rows in LDS without padding, filled by direct global-to-LDS loads (16
+// bytes a lane to 64 consecutive places of 16 bytes): row r's 16-byte pieces
+// are stored at piece ^ swz(r).  swz is chosen so that the reads below touch
+// every bank once: slabs along rows (16 rows, one piece each), and transposed
+// slabs (8 rows, two neighbouring pieces each).
+template <int D>
+struct SwzTile {
+  static constexpr int kElems = kQ * D;
+  static __device__ __forceinline__ int swz(int r) {
+    return D == 128 ? ((r & 7) << 1) | ((r >> 3) & 1) : (((r >> 1) & 3) << 1) | ((r >> 3) & 1);
   }
-  return acc;
-}
+  static __device__ __forceinline__ int at(int row, int col) { return row * D + ((((col >> 3) ^ swz(row)) << 3) | (col & 7)); }
+  // Rows 0..63 of p (row stride ld) by the four waves of a set (tid 0..255);
+  // rows >= n repeat row n - 1.  Completes with the wave's vector loads.
+  static __device__ __forceinline__ void load(bf16* lds, const bf16* p, long long ld, int n, int tid) {
+    typedef __attribute__((address_space(3))) void* LdsP;
+    typedef const __attribute__((address_space(1))) void* GlbP;
+    constexpr int kPieces = D / 8, kRows = 64 / kPieces;   // pieces of a row, rows a wave's load fills
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int r = kRows * wave + lane / kPieces, c = ((lane % kPieces) ^ swz(r)) * 8;
+#pragma unroll
+    for (int i = 0; i < 16 / kRows; ++i) {
+      constexpr int kStep = 4 * kRows;   // rows between a wave's loads (a multiple of 16)
+      bf16* to = lds + (kStep * i + kRows * wave) * D;
+      const int row = n >= kQ ? kStep * i + r : min(kStep * i + r, n - 1);
+      const unsigned off = ((unsigned)row * (unsigned)ld + (unsigned)c) * 2u;
+      __builtin_amdgcn_global_load_lds((GlbP)(reinterpret_cast<const char*>(p) + off), (LdsP)to, 16, 0, 0);
+    }
+  }
+  // Columns 32 z + 8g .. +7 of row r0 + l16: any order of the reduction index.
+  static __device__ __forceinline__ Slab<bf16> any(const bf16* t, int r0, int z) {
+    const int l16 = lane_id() & 15, g = lane_id() >> 4;
+    Slab<bf16> s;
+    s.v = *reinterpret_cast<const bf16x8*>(t + r0 * D + ((l16 * D + ((g ^ swz(l16)) << 3)) ^ (32 * z)));
+    return s;
+  }
+  // Columns 32 z + {4g.., 16+4g..} of row r0 + l16.
+  static __device__ __forceinline__ Slab<bf16> row(const bf16* t, int r0, int z) {
+    const int l16 = lane_id() & 15, g = lane_id() >> 4;
+    const int a = (l16 * D + ((((g >> 1) ^ swz(l16)) << 3) | ((g & 1) << 2))) ^ (32 * z);
+    return slab_of<bf16>(load4(t + r0 * D + a), load4(t + r0 * D + (a ^ 16)));
+  }
+  // Rows r0 + {4g.., 16+4g..} of column c0 + step (l16 / 4) + l16 % 4 (r0 a
+  // multiple of 32, c0 of 16 for step 4, of 4 within 32 for step 8).
+  static __device__ __forceinline__ Slab<bf16> tr(const bf16* t, int r0, int c0, int step) {
+    typedef __attribute__((address_space(3))) bf16x4* LdsP;
+    const int l16 = lane_id() & 15, g = lane_id() >> 4, r = 4 * g + (l16 >> 2), q = l16 & 3;
+    const bf16* a;
+    if (step == 4) a = t + r0 * D + ((r * D + ((((q >> 1) ^ swz(r)) << 3) | ((q & 1) << 2))) ^ c0);
+    else a = t + r0 * D + ((r * D + ((q ^ swz(r)) << 3)) ^ (c0 & ~7)) + (c0 & 7);
+    return slab_of<bf16>(__builtin_amdgcn_ds_read_tr16_b64_v4bf16((LdsP)(a)), __builtin_amdgcn_ds_read_tr16_b64_v4bf16((LdsP)(a + 16 * D)));
+  }
+  // Four columns from c (a multiple of 4) of row r0 + l16.
+  static __device__ __forceinline__ f32x4 four(const bf16* t, int r0, int c) {
+    const int l16 = lane_id() & 15;
+    return widen4(load4(t + r0 * D + l16 * D + ((((c >> 3) ^ swz(l16)) << 3) | (c & 7))));
+  }
+};
+// The same reads of a padded tile.
+template <typename T, int D>
+struct PadTile {
+  static constexpr int kPitch = D + LdsRow<T>::pad;
+  static __device__ __forceinline__ Slab<T> tr(const T* t, int r0, int c0, int step) { return slab_tr<T>(t, kPitch, r0, c0, step); }
+};
 
 // A state in the accumulator layout: the wave's dv/4 value columns as NT
 // tiles, KT tiles of state channels.  kPerm: output row m of tile t is column
@@ -145,7 +279,7 @@ struct State {
   static constexpr int CPW = DV / kSsmWaves, NT = CPW / 16, KT = DK / 16;
   f32x4 s[KT][NT];
   static __device__ __forceinline__ int col(int t) {
-    const int l16 = lane_id() & 15, wave = threadIdx.x >> 6;
+    const int l16 = lane_id() & 15, wave = (threadIdx.x >> 6) & (kSsmWaves - 1);
     return wave * CPW + (kPerm ? 4 * NT * (l16 >> 2) + 4 * t + (l16 & 3) : 16 * t + l16);
   }
   __device__ __forceinline__ void zero() {
@@ -173,62 +307,82 @@ struct State {
         for (int r = 0; r < 4; ++r) p[(size_t)(16 * k + 4 * g + r) * DV + col(t)] = s[k][t][r];
   }
   // s = s el + rows^T (cols w) over a chunk: rows [kQ][DK] and cols [kQ][DV] in
-  // LDS (xs: the wave's operand slabs of cols), one weight per token.
-  template <typename T>
-  __device__ __forceinline__ void update(float el, const T* rows, int pitch, const Slab<T> (&xs)[2][NT], const float* w) {
+  // LDS (xs: the wave's operand slabs of cols), one weight per token.  The
+  // chunk's sum is formed apart from the state: small parts are not rounded
+  // to the state's last place one by one.  kLow: the lower parts' sum stays
+  // apart to the end (mma_low); otherwise it starts the sum, one addition less
+  // per element and a mean error of 1e-8.
+  // Tile: how rows are laid out.
+  template <bool kLow, typename Tile, typename T>
+  __device__ __forceinline__ void update(float el, const T* rows, const Slab<T> (&xs)[2][NT], const float* w) {
     const int g = lane_id() >> 4;
-#pragma unroll
-    for (int k = 0; k < KT; ++k)
-#pragma unroll
-      for (int q = 0; q < NT; ++q) s[k][q] *= el;
+    Split<T> xw[2][NT];
 #pragma unroll
     for (int js = 0; js < 2; ++js) {
       const f32x4 w0 = load4(w + 32 * js + 4 * g), w1 = load4(w + 32 * js + 16 + 4 * g);
-      Split<T> xw[NT];
 #pragma unroll
-      for (int q = 0; q < NT; ++q) xw[q] = scaled<T>(xs[js][q], w0, w1);
+      for (int q = 0; q < NT; ++q) xw[js][q] = scaled<T>(xs[js][q], w0, w1);
+    }
 #pragma unroll
-      for (int k = 0; k < KT; ++k) {
-        const Slab<T> bs = slab_tr<T>(rows + 32 * js * pitch, pitch, 16 * k, 4);
+    for (int k = 0; k < KT; ++k) {
+      const Slab<T> b0 = Tile::tr(rows, 0, 16 * k, 4), b1 = Tile::tr(rows, 32, 16 * k, 4);
 #pragma unroll
-        for (int q = 0; q < NT; ++q) s[k][q] = mma_split(bs, xw[q], s[k][q]);
+      for (int q = 0; q < NT; ++q) {
+        const f32x4 low = mma_low(b1, xw[1][q], mma_low(b0, xw[0][q], zero4()));
+        const f32x4 sum = mma(b1, xw[1][q].h, mma(b0, xw[0][q].h, kLow ? zero4() : low));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[k][q][r] = fmaf(s[k][q][r], el, sum[r]);
+        if constexpr (kLow && sizeof(T) == 2) s[k][q] += low;
       }
     }
   }
-  template <typename T>
-  static __device__ __forceinline__ void slabs(const T* cols, int pitch, Slab<T> (&xs)[2][NT]) {
-    const int wave = threadIdx.x >> 6;
+  template <typename Tile, typename T>
+  static __device__ __forceinline__ void slabs(const T* cols, Slab<T> (&xs)[2][NT]) {
+    const int wave = (threadIdx.x >> 6) & (kSsmWaves - 1);
 #pragma unroll
     for (int js = 0; js < 2; ++js)
 #pragma unroll
       for (int q = 0; q < NT; ++q)
-        xs[js][q] = slab_tr<T>(cols + 32 * js * pitch, pitch, wave * CPW + (kPerm ? 4 : 16) * q, kPerm ? 4 * NT : 4);
+        xs[js][q] = Tile::tr(cols, 32 * js, wave * CPW + (kPerm ? 4 : 16) * q, kPerm ? 4 * NT : 4);
   }
 };
 
 // kQ rows of D elements from global memory (row stride ld) to LDS (padded),
-// through registers: load() issues the loads of rows < n (rows behind are
-// zeros), store() writes them.
+// through the registers of the first kSsmThreads threads: load() issues the
+// loads of rows < n (rows behind are zeros), store() writes them.
 template <typename T, int D>
 struct RowTile {
   static constexpr int VE = 16 / sizeof(T);
   static constexpr int kPer = kQ * D / VE / kSsmThreads;
-  static constexpr int kPitch = D + LdsPad<T>::v;
+  static constexpr int kRows = kSsmThreads * VE / D;   // rows between a thread's pieces (a multiple of 8)
+  static constexpr int kPitch = D + LdsRow<T>::pad;
   typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
   u32x4 v[kPer];
-  __device__ __forceinline__ void load(const T* p, long long ld, int n) {
+  // p and ld are the same for all threads: a scalar base per piece, and one
+  // 32-bit offset per thread (ld is at most 2^24 elements)
+  __device__ __forceinline__ void load(const T* p, long long ld, int n, int tid) {
+    const int r = tid * VE / D, c = tid * VE % D;
+    const unsigned off = ((unsigned)r * (unsigned)ld + (unsigned)c) * (unsigned)sizeof(T);
+    const char* base = reinterpret_cast<const char*>(p);
+    const size_t step = (size_t)kRows * (size_t)ld * sizeof(T);
+    if (n >= kQ) {
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int e = (k * kSsmThreads + (int)threadIdx.x) * VE, r = e / D, c = e % D;
-      v[k] = u32x4{0, 0, 0, 0};
-      if (r < n) v[k] = *reinterpret_cast<const u32x4*>(p + (size_t)r * (size_t)ld + c);
+      for (int k = 0; k < kPer; ++k) v[k] = *reinterpret_cast<const u32x4*>(base + k * step + off);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        v[k] = u32x4{0, 0, 0, 0};
+        if (k * kRows + r < n) v[k] = *reinterpret_cast<const u32x4*>(base + k * step + off);
+      }
     }
   }
-  __device__ __forceinline__ void store(T* lds) const {
+  __device__ __forceinline__ void store(T* lds, int tid) const {
+    const int r = tid * VE / D, c = tid * VE % D;
+    T* q = lds + r * kPitch + LdsRow<T>::shift(r) + c;
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      const int e = (k * kSsmThreads + (int)threadIdx.x) * VE, r = e / D, c = e % D;
-      *reinterpret_cast<u32x4*>(lds + r * kPitch + c) = v[k];
+      static_assert(kRows % 16 == 0 || kRows == 8 || sizeof(T) != 2, "rows keep their shift");
+      *reinterpret_cast<u32x4*>(q + k * kRows * kPitch) = v[k];
     }
   }
 };

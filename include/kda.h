@@ -481,7 +481,8 @@ int kda_qk_norm_rope_bwd(const void* q, long long ldq, const void* k, long long 
  *   y_t = S_t^T C_t + D[h] x_t
  * x: rows [B,T,H,dv]; dt (raw): rows [B,T,H] (element alignment suffices);
  * Bm, Cm: rows [B,T,G,dk], G a divisor of H; token strides of x, Bm and Cm in
- * multiples of 16 bytes; dk, dv in {64, 128}.  A, D, dt_bias [H] fp32 (D, dt_bias NULL:
+ * multiples of 16 bytes, every token stride at most 2^24 elements; dk, dv in
+ * {64, 128}.  A, D, dt_bias [H] fp32 (D, dt_bias NULL:
  * none).  y [B,T,H,dv] of dtype (a projection of the same type reads it;
  * fp32 sums, one rounding).  Precondition: A finite; dt A <= 0 is the
  * intended range, larger values are computed as they are and may overflow.
