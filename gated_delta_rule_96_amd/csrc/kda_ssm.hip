@@ -213,7 +213,9 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
       if (i < n) Rows<T, 4 * NT>::store(y + (size_t)(t + i) * yld + c, o);
     }
 
-    S.template update<false, PadTile<T, DK>>(exp2_of(last), sm.b, xs, sm.wdt);
+    Split<T> xw[2][NT];
+    St::weigh(xs, sm.wdt, xw);
+    S.template update<false, PadTile<T, DK>>(exp2_of(last), sm.b, xw);
   }
   if (p.last && a.ht) S.store(a.ht + ((size_t)p.n * a.H + h) * sd);
 }
@@ -360,6 +362,7 @@ __global__ __launch_bounds__(kPipeThreads, 2) void ssm_pipe_kernel(const SsmArgs
   const float dskip = a.D ? a.D[h] : 0.f;
   const size_t yld = (size_t)a.H * DV;
   T* y = (T*)a.y + ((p.start + p.t0) * (size_t)a.H + h) * DV;
+  const typename TK::RowBase rowb = TK::row_base();
   __syncthreads();
   __syncthreads();
   for (int k = 0; k < nch; ++k) {
@@ -368,6 +371,10 @@ __global__ __launch_bounds__(kPipeThreads, 2) void ssm_pipe_kernel(const SsmArgs
     const typename Lds::Sizes& z = sm.z[buf];
     const Slab<T>* tm = sm.m[k & 1];
     const int n = min(p.t1 - p.t0 - kQ * k, kQ);
+    Slab<T> xs[2][NT];
+    St::template slabs<TV>(tx, xs);
+    Split<T> xw[2][NT];
+    St::weigh(xs, z.wdt, xw);
     // S^T C
     f32x4 acc[4][NT];
 #pragma unroll
@@ -381,13 +388,11 @@ __global__ __launch_bounds__(kPipeThreads, 2) void ssm_pipe_kernel(const SsmArgs
       for (int q = 0; q < NT; ++q) ss[q] = make_slab<T>(S.s[2 * y4][q], S.s[2 * y4 + 1][q]);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const Slab<T> cs = TK::row(tc, 16 * it, y4);
+        const Slab<T> cs = TK::row(tc, rowb, it, y4);
 #pragma unroll
         for (int q = 0; q < NT; ++q) acc[it][q] = mma(ss[q], cs, acc[it][q]);
       }
     }
-    Slab<T> xs[2][NT];
-    St::template slabs<TV>(tx, xs);
     // a product with zeros is NaN exactly where x is not finite: the masked
     // entries of M would then spread later tokens' values to earlier ones
     f32x4 probe = zero4();
@@ -398,36 +403,48 @@ __global__ __launch_bounds__(kPipeThreads, 2) void ssm_pipe_kernel(const SsmArgs
     const bool finite = !__any(probe[0] != probe[0]);
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-      const int i = 16 * it + l16, col = wave * St::CPW + 4 * NT * g;
-      const float e = z.ecum[i];
+      const float e = z.ecum[16 * it + l16];
 #pragma unroll
       for (int q = 0; q < NT; ++q) acc[it][q] *= e;
-      if (finite) {
+    }
+    const int col = wave * St::CPW + 4 * NT * g;
+    if (finite) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
 #pragma unroll
         for (int js = 0; js <= it / 2; ++js) {
           const Slab<T> m = tm[m_slab(it, js) * 64 + lane];
 #pragma unroll
           for (int q = 0; q < NT; ++q) acc[it][q] = mma(xs[js][q], m, acc[it][q]);
         }
-      } else {   // token by token, later ones left out
+    } else {   // token by token, later ones left out
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
 #pragma unroll 1
-        for (int j = 0; j <= i; ++j) {
+        for (int j = 0; j <= 16 * it + l16; ++j) {
           const T* mp = reinterpret_cast<const T*>(tm + m_slab(it, j >> 5) * 64 + ((j >> 2) & 3) * 16 + l16);
           const float m = to_f32(mp[4 * ((j >> 4) & 1) + (j & 3)]);
 #pragma unroll
           for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(tx + TV::at(j, col + 4 * q)));
         }
-      }
+    }
+    S.template update<false, TK>(sm.el[buf], tb, xw);
+    if (a.D) {
+#pragma unroll
+      for (int it = 0; it < 4; ++it)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) acc[it][q] += dskip * TV::four(tx, 16 * it, col + 4 * q);
+    }
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      const int i = 16 * it + l16;
       float o[4 * NT];
 #pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        const f32x4 xi = TV::four(tx, 16 * it, col + 4 * q);
+      for (int q = 0; q < NT; ++q)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) o[4 * q + r] = a.D ? fmaf(dskip, xi[r], acc[it][q][r]) : acc[it][q][r];
-      }
+        for (int r = 0; r < 4; ++r) o[4 * q + r] = acc[it][q][r];
       if (i < n) Rows<T, 4 * NT>::store(y + (size_t)(kQ * k + i) * yld + col, o);
     }
-    S.template update<false, TK>(sm.el[buf], tb, xs, z.wdt);
     __syncthreads();
   }
   if (p.last && a.ht) S.store(a.ht + ((size_t)p.n * a.H + h) * sd);

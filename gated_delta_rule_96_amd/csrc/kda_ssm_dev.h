@@ -154,6 +154,7 @@ __device__ __forceinline__ unsigned pack_upper(float a, float b) {
   return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
 }
 __device__ __forceinline__ void split_of(f32x4 lo, f32x4 hi, Split<bf16>& s) {
+#pragma clang fp contract(off)   // the parts of the rounded value: exact
   typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
   u32x4 h, m, l;
 #pragma unroll
@@ -171,6 +172,7 @@ __device__ __forceinline__ void split_of(f32x4 lo, f32x4 hi, Split<bf16>& s) {
 // x w elementwise along the reduction index.
 template <typename T>
 __device__ __forceinline__ Split<T> scaled(const Slab<T>& x, f32x4 w0, f32x4 w1) {
+#pragma clang fp contract(off)
   f32x4 a, b;
   if constexpr (sizeof(T) == 2) {
 #pragma unroll
@@ -241,11 +243,25 @@ struct SwzTile {
     s.v = *reinterpret_cast<const bf16x8*>(t + r0 * D + ((l16 * D + ((g ^ swz(l16)) << 3)) ^ (32 * z)));
     return s;
   }
-  // Columns 32 z + {4g.., 16+4g..} of row r0 + l16.
-  static __device__ __forceinline__ Slab<bf16> row(const bf16* t, int r0, int z) {
+  // Columns 32 z + {4g.., 16+4g..} of row 16 it + l16.  RowBase holds the
+  // lane's place in each row tile, hidden from the compiler once: two such
+  // 8-byte reads joined into one two-address read would meet in the same
+  // banks.
+  struct RowBase {
+    int at[4];
+  };
+  static __device__ __forceinline__ RowBase row_base() {
     const int l16 = lane_id() & 15, g = lane_id() >> 4;
-    const int a = (l16 * D + ((((g >> 1) ^ swz(l16)) << 3) | ((g & 1) << 2))) ^ (32 * z);
-    return slab_of<bf16>(load4(t + r0 * D + a), load4(t + r0 * D + (a ^ 16)));
+    RowBase b;
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+      b.at[it] = (16 * it + l16) * D + ((((g >> 1) ^ swz(l16)) << 3) | ((g & 1) << 2));
+      asm("" : "+v"(b.at[it]));
+    }
+    return b;
+  }
+  static __device__ __forceinline__ Slab<bf16> row(const bf16* t, const RowBase& b, int it, int z) {
+    return slab_of<bf16>(load4(t + (b.at[it] ^ (32 * z))), load4(t + (b.at[it] ^ (32 * z + 16))));
   }
   // Rows r0 + {4g.., 16+4g..} of column c0 + step (l16 / 4) + l16 % 4 (r0 a
   // multiple of 32, c0 of 16 for step 4, of 4 within 32 for step 8).
@@ -306,23 +322,25 @@ struct State {
 #pragma unroll
         for (int r = 0; r < 4; ++r) p[(size_t)(16 * k + 4 * g + r) * DV + col(t)] = s[k][t][r];
   }
-  // s = s el + rows^T (cols w) over a chunk: rows [kQ][DK] and cols [kQ][DV] in
-  // LDS (xs: the wave's operand slabs of cols), one weight per token.  The
+  // s = s el + rows^T (cols w) over a chunk, in two steps: the weighted operand
+  // xw from the wave's slabs of cols [kQ][DV] and one weight per token, and the
+  // products with rows [kQ][DK] in LDS (Tile: how those are laid out).  The
   // chunk's sum is formed apart from the state: small parts are not rounded
   // to the state's last place one by one.  kLow: the lower parts' sum stays
   // apart to the end (mma_low); otherwise it starts the sum, one addition less
   // per element and a mean error of 1e-8.
-  // Tile: how rows are laid out.
-  template <bool kLow, typename Tile, typename T>
-  __device__ __forceinline__ void update(float el, const T* rows, const Slab<T> (&xs)[2][NT], const float* w) {
+  template <typename T>
+  static __device__ __forceinline__ void weigh(const Slab<T> (&xs)[2][NT], const float* w, Split<T> (&xw)[2][NT]) {
     const int g = lane_id() >> 4;
-    Split<T> xw[2][NT];
 #pragma unroll
     for (int js = 0; js < 2; ++js) {
       const f32x4 w0 = load4(w + 32 * js + 4 * g), w1 = load4(w + 32 * js + 16 + 4 * g);
 #pragma unroll
       for (int q = 0; q < NT; ++q) xw[js][q] = scaled<T>(xs[js][q], w0, w1);
     }
+  }
+  template <bool kLow, typename Tile, typename T>
+  __device__ __forceinline__ void update(float el, const T* rows, const Split<T> (&xw)[2][NT]) {
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
       const Slab<T> b0 = Tile::tr(rows, 0, 16 * k, 4), b1 = Tile::tr(rows, 32, 16 * k, 4);

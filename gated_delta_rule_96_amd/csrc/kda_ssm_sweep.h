@@ -97,7 +97,9 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_sweep
     __syncthreads();
     Slab<T> xs[2][St::NT];
     St::template slabs<PadTile<T, DV>>(sm.x, xs);
-    S.template update<kLow, PadTile<T, DK>>(exp2_of(last), sm.b, xs, sm.w);
+    Split<T> xw[2][St::NT];
+    St::weigh(xs, sm.w, xw);
+    S.template update<kLow, PadTile<T, DK>>(exp2_of(last), sm.b, xw);
     total += last;
   }
   if (!kKeep) {
