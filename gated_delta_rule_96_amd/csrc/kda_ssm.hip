@@ -77,6 +77,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
   T* y = (T*)a.y + (p.start * (size_t)a.H + h) * DV;
   const size_t yld = (size_t)a.H * DV;
 
+  const RowLanes rk = row_lanes<T>(PK);
   St S;
   const size_t sd = (size_t)DK * DV;
   const size_t slot = (size_t)(w.item - p.li) * kSubs * a.H + h;   // of the next part's start
@@ -176,7 +177,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
       for (int q = 0; q < NT; ++q) ss[q] = make_slab<T>(S.s[2 * k][q], S.s[2 * k + 1][q]);
 #pragma unroll
       for (int it = 0; it < 4; ++it) {
-        const Slab<T> cs = slab_row(sm.c, PK, 16 * it, 32 * k);
+        const Slab<T> cs = slab_row(sm.c, rk, 16 * it * PK + 32 * k);
 #pragma unroll
         for (int q = 0; q < NT; ++q) acc[it][q] = mma(ss[q], cs, acc[it][q]);
       }

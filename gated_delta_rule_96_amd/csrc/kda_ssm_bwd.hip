@@ -37,6 +37,10 @@ namespace kda {
 namespace {
 
 constexpr int kSweepWgs = 512;   // two sweep work-groups per CU
+// Eight waves a chunk: with four, the sums over the heads and the products of
+// one head do not fit the registers (1101 against 1415 us for 32K tokens x 16
+// heads even at one work-group per CU instead of two).
+constexpr int kBwdWaves = 8, kBwdThreads = 64 * kBwdWaves;
 
 struct ChunkBwd {
   SsmBwdArgs b;
@@ -54,8 +58,8 @@ struct BwdLds {
   T b[kQ * PK];
   union {
     T x[kQ * PV];
-    struct {   // when x has been used up: sums of the four waves
-      float u[kSsmWaves][kQ], v[kSsmWaves][kQ], col[kSsmWaves][kQ], row[kQ], diag[kQ], qd[kQ], g[kSsmWaves];
+    struct {   // when x has been used up: sums of the waves
+      float u[DK / 16][kQ], v[DK / 16][kQ], col[4][kQ], row[2][kQ], diag[kQ], qd[kQ], g[kBwdWaves];
     } s;
   };
   T dy[kQ * PV];
@@ -80,15 +84,16 @@ __device__ __forceinline__ float sum_groups(float x) {
 }
 
 template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_kernel(const ChunkBwd a, const SeqTab sq) {
+__global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd a, const SeqTab sq) {
   typedef BwdLds<T, DK, DV> Lds;
   constexpr int PK = Lds::PK, PV = Lds::PV, PM = Lds::PM;
-  constexpr int CPK = DK / kSsmWaves, NK = CPK / 16, CPV = DV / kSsmWaves, NV = CPV / 16;
+  // A wave's part of an output [tokens x D]: 16 columns of NK / NV token tiles.
+  constexpr int KT = DK / 16, VT = DV / 16, NK = 4 * KT / kBwdWaves, NV = 4 * VT / kBwdWaves;
   __shared__ __align__(16) char smem[sizeof(Lds)];
   Lds& sm = *reinterpret_cast<Lds*>(smem);
   const SsmBwdArgs& b = a.b;
   const SsmArgs& f = b.f;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, g = lane >> 4, l16 = lane & 15;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, g = lane >> 4, l16 = lane & 15;
   const int HG = f.H / f.G;
   const int item = (int)(blockIdx.x / (unsigned)(f.G * a.shares)), rest = (int)(blockIdx.x - (unsigned)item * (unsigned)(f.G * a.shares));
   const int share = rest / f.G, grp = rest - share * f.G;
@@ -107,13 +112,14 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
   const T* dt = (const T*)f.dt + tok * (size_t)f.lddt;
   const long long vld = (long long)f.H * DV;
 
-  // The output rows (state channels, value columns) of this lane in a
-  // transposed tile: rows m of tile t are base + 4 N (m/4) + 4t + m%4.
-  const int k0 = wave * CPK, c0 = wave * CPV;
-  const int i_own = 16 * wave + l16;   // column of the strip this wave forms
+  const int k0 = 16 * (wave % KT), tk = KT == kBwdWaves ? 0 : NK * (wave / KT);   // first state channel and token tile
+  const int c0 = 16 * (wave % VT), tv = VT == kBwdWaves ? 0 : NV * (wave / VT);   // first value column and token tile
+  // Half strips of the token x token products: tiles (is, 2 jh) and (is, 2 jh + 1).
+  const int is = wave & 3, jh = wave >> 2, i_own = 16 * is + l16;
   T* m_own = sm.m + i_own * PM + LdsRow<T>::shift(i_own);
 
-  RowTile<T, DV> rx, ry;
+  const RowLanes rk = row_lanes<T>(PK), rv = row_lanes<T>(PV), rm = row_lanes<T>(PM);
+  RowTile<T, DV, kBwdThreads> rx, ry;
   float raw = 0.f;
   auto fetch = [&](int h) {
     rx.load(x + (size_t)h * DV, f.ldx, n, tid);
@@ -121,7 +127,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     raw = lane < n ? to_f32(dt[(size_t)lane * (size_t)f.lddt + h]) : 0.f;
   };
   {
-    RowTile<T, DK> rc, rb;
+    RowTile<T, DK, kBwdThreads> rc, rb;
     rc.load((const T*)f.C + tok * (size_t)f.ldc + (size_t)grp * DK, f.ldc, n, tid);
     rb.load((const T*)f.B + tok * (size_t)f.ldb + (size_t)grp * DK, f.ldb, n, tid);
     if (h0 < h1) fetch(h0);
@@ -129,21 +135,19 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     rb.store(sm.b, tid);
   }
   __syncthreads();
-  // P of the wave's strip, transposed tiles (rows j, columns i), for all heads
-  f32x4 pt[4];
+  // P of the wave's half strip, transposed tiles (rows j, columns i), for all heads
+  f32x4 pt[2];
 #pragma unroll
-  for (int jt = 0; jt < 4; ++jt) {
-    pt[jt] = zero4();
-    if (jt > wave) continue;
+  for (int q = 0; q < 2; ++q) {
+    pt[q] = zero4();
+    const int jt = 2 * jh + q;
+    if (jt > is) continue;
 #pragma unroll
-    for (int k = 0; k < DK / 32; ++k)
-      pt[jt] = mma(slab_any(sm.b, PK, 16 * jt, 32 * k), slab_any(sm.c, PK, 16 * wave, 32 * k), pt[jt]);
+    for (int k = 0; k < DK / 32; ++k) pt[q] = mma(slab_any(sm.b, PK, 16 * jt, 32 * k), slab_any(sm.c, PK, 16 * is, 32 * k), pt[q]);
   }
-  f32x4 dC[4][NK], dB[4][NK];   // transposed: rows state channels, columns tokens
+  f32x4 dC[NK], dB[NK];   // transposed: rows state channels, columns tokens
 #pragma unroll
-  for (int it = 0; it < 4; ++it)
-#pragma unroll
-    for (int q = 0; q < NK; ++q) dC[it][q] = dB[it][q] = zero4();
+  for (int t = 0; t < NK; ++t) dC[t] = dB[t] = zero4();
 
   for (int h = h0; h < h1; ++h) {
     const double a2 = (double)f.A[h] * 1.4426950408889634074;
@@ -157,26 +161,27 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
     if (wave == 0) sm.cum[lane] = cum;
     else if (wave == 1) sm.ecum[lane] = exp2_of(cum);
     else if (wave == 2) sm.w[lane] = exp2_of(last - cum);
-    else sm.dt[lane] = s.dt;
+    else if (wave == 3) sm.dt[lane] = s.dt;
     if (h + 1 < h1) fetch(h + 1);
     __syncthreads();
 
-    // strip of Qm, and from it R's sums, E dt Qm (to LDS) and E P (kept)
+    // half strip of Qm, and from it R's sums, E dt Qm (to LDS) and E P (kept)
     float row = 0.f, diag = 0.f, qd = 0.f;
-    f32x4 col[4];
-    V4<T> ep[4];
+    f32x4 col[2];
+    V4<T> ep[2];
     {
       Slab<T> ys[DV / 32];
 #pragma unroll
-      for (int k = 0; k < DV / 32; ++k) ys[k] = slab_any(sm.dy, PV, 16 * wave, 32 * k);
+      for (int k = 0; k < DV / 32; ++k) ys[k] = slab_any(sm.dy, PV, 16 * is, 32 * k);
       const double ci = sm.cum[i_own];
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) {
-        col[jt] = zero4();
-        ep[jt] = narrow4<T>(zero4());
-        if (jt > (wave | 1)) continue;   // tile wave + 1 of an even strip: zeros complete its slab
+      for (int q = 0; q < 2; ++q) {
+        const int jt = 2 * jh + q;
+        col[q] = zero4();
+        ep[q] = narrow4<T>(zero4());
+        if (jt > (is | 1)) continue;   // tile is + 1 of an even strip: zeros complete its slab
         f32x4 nn = zero4(), mm = zero4();
-        if (jt <= wave) {
+        if (jt <= is) {
           f32x4 acc = zero4();
 #pragma unroll
           for (int k = 0; k < DV / 32; ++k) acc = mma(slab_any(sm.x, PV, 16 * jt, 32 * k), ys[k], acc);
@@ -186,7 +191,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
           for (int r = 0; r < 4; ++r) {
             const bool in = j + r <= i_own, on = j + r == i_own;
             const float e = exp2_of(ci - sm.cum[j + r]);
-            const float m = in ? e * pt[jt][r] : 0.f;
+            const float m = in ? e * pt[q][r] : 0.f;
             const float rr = in ? m * acc[r] : 0.f;
             mm[r] = m;
             nn[r] = in ? e * dj[r] * acc[r] : 0.f;
@@ -195,147 +200,147 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
               qd = acc[r];
             } else {
               row = fmaf(rr, dj[r], row);
-              col[jt][r] = rr;
+              col[q][r] = rr;
             }
           }
         }
-        ep[jt] = narrow4<T>(mm);
+        ep[q] = narrow4<T>(mm);
         store4(m_own + 16 * jt + 4 * g, narrow4<T>(nn));
       }
       row = sum_groups(row);
       diag = sum_groups(diag);   // one lane of a column holds it
       qd = sum_groups(qd);
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt)
+      for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) col[jt][r] = sum16(col[jt][r]);
+        for (int r = 0; r < 4; ++r) col[q][r] = sum16(col[q][r]);
     }
 
     // S dy and dS x (transposed: rows the wave's state channels)
     const size_t st = ((size_t)item * f.H + h) * (size_t)(DK * DV);
-    float su[4], sv[4], gs;
+    float su[NK], sv[NK], gs;
     {
-      f32x4 U[4][NK], Z[4][NK], g4 = zero4();
+      f32x4 U[NK], Z[NK], g4 = zero4();
 #pragma unroll
-      for (int it = 0; it < 4; ++it)
-#pragma unroll
-        for (int q = 0; q < NK; ++q) U[it][q] = Z[it][q] = zero4();
+      for (int t = 0; t < NK; ++t) U[t] = Z[t] = zero4();
+      const float *Sp = a.S + st + (size_t)(k0 + l16) * DV + 4 * g, *dSp = a.dS + st + (size_t)(k0 + l16) * DV + 4 * g;
 #pragma unroll 1
       for (int k = 0; k < DV / 32; ++k) {
-        Split<T> ss[NK], ds[NK];
+        const f32x4 s0 = load4(Sp + 32 * k), s1 = load4(Sp + 32 * k + 16), d0 = load4(dSp + 32 * k), d1 = load4(dSp + 32 * k + 16);
 #pragma unroll
-        for (int q = 0; q < NK; ++q) {
-          const size_t at = st + (size_t)(k0 + 4 * NK * (l16 >> 2) + 4 * q + (l16 & 3)) * DV + 32 * k + 4 * g;
-          const f32x4 s0 = load4(a.S + at), s1 = load4(a.S + at + 16), d0 = load4(a.dS + at), d1 = load4(a.dS + at + 16);
+        for (int r = 0; r < 4; ++r) g4[r] = fmaf(s0[r], d0[r], fmaf(s1[r], d1[r], g4[r]));
+        Split<T> ss, ds;
+        split_of(s0, s1, ss);
+        split_of(d0, d1, ds);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) g4[r] = fmaf(s0[r], d0[r], fmaf(s1[r], d1[r], g4[r]));
-          split_of(s0, s1, ss[q]);
-          split_of(d0, d1, ds[q]);
-        }
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          const Slab<T> ys = slab_row(sm.dy, PV, 16 * it, 32 * k), xs = slab_row(sm.x, PV, 16 * it, 32 * k);
-#pragma unroll
-          for (int q = 0; q < NK; ++q) {
-            U[it][q] = mma_split(ss[q], ys, U[it][q]);
-            Z[it][q] = mma_split(ds[q], xs, Z[it][q]);
-          }
+        for (int t = 0; t < NK; ++t) {
+          U[t] = mma_split(ss, slab_row(sm.dy, rv, 16 * (tk + t) * PV + 32 * k), U[t]);
+          Z[t] = mma_split(ds, slab_row(sm.x, rv, 16 * (tk + t) * PV + 32 * k), Z[t]);
         }
       }
-      gs = (g4[0] + g4[1]) + (g4[2] + g4[3]);
+      // waves that share state channels (other tokens) hold the same sum
+      gs = tk == 0 ? (g4[0] + g4[1]) + (g4[2] + g4[3]) : 0.f;
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const int i = 16 * it + l16;
+      for (int t = 0; t < NK; ++t) {
+        const int it = tk + t, i = 16 * it + l16;
         const float e = sm.ecum[i], w = sm.w[i], wd = w * sm.dt[i];
+        const f32x4 c4 = four_of_row(sm.c, PK, 16 * it, k0 + 4 * g), b4 = four_of_row(sm.b, PK, 16 * it, k0 + 4 * g);
         float uu = 0.f, vv = 0.f;
 #pragma unroll
-        for (int q = 0; q < NK; ++q) {
-          const f32x4 c4 = four_of_row(sm.c, PK, 16 * it, k0 + 4 * NK * g + 4 * q), b4 = four_of_row(sm.b, PK, 16 * it, k0 + 4 * NK * g + 4 * q);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            uu = fmaf(c4[r], U[it][q][r], uu);
-            vv = fmaf(b4[r], Z[it][q][r], vv);
-          }
-          dC[it][q] += e * U[it][q];
-          dB[it][q] += wd * Z[it][q];
+        for (int r = 0; r < 4; ++r) {
+          uu = fmaf(c4[r], U[t][r], uu);
+          vv = fmaf(b4[r], Z[t][r], vv);
         }
-        su[it] = e * sum_groups(uu);
-        sv[it] = w * sum_groups(vv);
+        dC[t] += e * U[t];
+        dB[t] += wd * Z[t];
+        su[t] = e * sum_groups(uu);
+        sv[t] = w * sum_groups(vv);
       }
     }
+    for (int off = 32; off >= 1; off >>= 1) gs += __shfl_xor(gs, off);
     __syncthreads();   // x is used up; E dt Qm is complete
     if (g == 0) {
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        sm.s.u[wave][16 * it + l16] = su[it];
-        sm.s.v[wave][16 * it + l16] = sv[it];
+      for (int t = 0; t < NK; ++t) {
+        sm.s.u[wave % KT][16 * (tk + t) + l16] = su[t];
+        sm.s.v[wave % KT][16 * (tk + t) + l16] = sv[t];
       }
-      sm.s.row[i_own] = row;
-      sm.s.diag[i_own] = diag;
-      sm.s.qd[i_own] = qd;
+      sm.s.row[jh][i_own] = row;
+      if (jh == is / 2) {
+        sm.s.diag[i_own] = diag;
+        sm.s.qd[i_own] = qd;
+      }
     }
     if (l16 == 0) {
 #pragma unroll
-      for (int jt = 0; jt < 4; ++jt) store4(&sm.s.col[wave][16 * jt + 4 * g], col[jt]);
+      for (int q = 0; q < 2; ++q) store4(&sm.s.col[is][16 * (2 * jh + q) + 4 * g], col[q]);
     }
-    for (int off = 32; off >= 1; off >>= 1) gs += __shfl_xor(gs, off);
     if (lane == 0) sm.s.g[wave] = gs;
 
     // dC += (E dt Qm) B, dB += (E dt Qm)^T C
 #pragma unroll
     for (int js = 0; js < 2; ++js) {
+      const Slab<T> bs = slab_tr<T>(sm.b, PK, 32 * js, k0, 4), cs = slab_tr<T>(sm.c, PK, 32 * js, k0, 4);
 #pragma unroll
-      for (int q = 0; q < NK; ++q) {
-        const Slab<T> bs = slab_tr<T>(sm.b, PK, 32 * js, k0 + 4 * q, 4 * NK), cs = slab_tr<T>(sm.c, PK, 32 * js, k0 + 4 * q, 4 * NK);
-#pragma unroll
-        for (int it = 0; it < 4; ++it) {
-          if (js <= it / 2) dC[it][q] = mma(bs, slab_row(sm.m, PM, 16 * it, 32 * js), dC[it][q]);
-          if (js >= it / 2) dB[it][q] = mma(cs, slab_tr<T>(sm.m, PM, 32 * js, 16 * it, 4), dB[it][q]);
-        }
+      for (int t = 0; t < NK; ++t) {
+        const int it = tk + t;
+        if (js <= it / 2) dC[t] = mma(bs, slab_row(sm.m, rm, 16 * it * PM + 32 * js), dC[t]);
+        if (js >= it / 2) dB[t] = mma(cs, slab_tr<T>(sm.m, PM, 32 * js, 16 * it, 4), dB[t]);
       }
     }
     // dS^T B (transposed: rows the wave's value columns, columns tokens j)
-    f32x4 dx[4][NV];
+    f32x4 dx[NV];
 #pragma unroll
-    for (int it = 0; it < 4; ++it)
+    for (int t = 0; t < NV; ++t) dx[t] = zero4();
 #pragma unroll
-      for (int q = 0; q < NV; ++q) dx[it][q] = zero4();
-#pragma unroll 1
     for (int k = 0; k < DK / 32; ++k) {
-      Slab<T> ds[NV];
+      const float* dp = a.dS + st + (size_t)(32 * k + 4 * g) * DV + c0 + l16;
+      f32x4 lo, hi;
 #pragma unroll
-      for (int q = 0; q < NV; ++q) {
-        const float* dp = a.dS + st + (size_t)(32 * k + 4 * g) * DV + c0 + 4 * NV * (l16 >> 2) + 4 * q + (l16 & 3);
-        f32x4 lo, hi;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          lo[r] = dp[(size_t)r * DV];
-          hi[r] = dp[(size_t)(16 + r) * DV];
-        }
-        ds[q] = make_slab<T>(lo, hi);
+      for (int r = 0; r < 4; ++r) {
+        lo[r] = dp[r * DV];
+        hi[r] = dp[(16 + r) * DV];
       }
+      const Slab<T> ds = make_slab<T>(lo, hi);
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
-        const Slab<T> bs = slab_row(sm.b, PK, 16 * it, 32 * k);
-#pragma unroll
-        for (int q = 0; q < NV; ++q) dx[it][q] = mma(ds[q], bs, dx[it][q]);
-      }
+      for (int t = 0; t < NV; ++t) dx[t] = mma(ds, slab_row(sm.b, rk, 16 * (tv + t) * PK + 32 * k), dx[t]);
     }
     __syncthreads();   // E dt Qm is used up; the sums are complete
 #pragma unroll
-    for (int jt = 0; jt < 4; ++jt)
-      if (jt <= (wave | 1)) store4(m_own + 16 * jt + 4 * g, ep[jt]);
+    for (int q = 0; q < 2; ++q)
+      if (2 * jh + q <= (is | 1)) store4(m_own + 16 * (2 * jh + q) + 4 * g, ep[q]);
+    __syncthreads();
+    // dx
+    const float dskip = f.D ? f.D[h] : 0.f;
+    const Slab<T> y0 = slab_tr<T>(sm.dy, PV, 0, c0, 4), y1 = slab_tr<T>(sm.dy, PV, 32, c0, 4);
+#pragma unroll
+    for (int t = 0; t < NV; ++t) {
+      const int it = tv + t, j = 16 * it + l16, c = c0 + 4 * g;
+      const float dj = sm.dt[j];
+      dx[t] *= sm.w[j];
+      if (it < 2) dx[t] = mma(y0, slab_tr<T>(sm.m, PM, 0, 16 * it, 4), dx[t]);
+      dx[t] = mma(y1, slab_tr<T>(sm.m, PM, 32, 16 * it, 4), dx[t]);
+      f32x4 o = dj * dx[t];
+      if (f.D) o += dskip * four_of_row(sm.dy, PV, 16 * it, c);
+      const float ov[4] = {o[0], o[1], o[2], o[3]};
+      if (j < n) Rows<T, 4>::store((T*)b.dx + (tok + j) * (size_t)vld + (size_t)h * DV + c, ov);
+    }
     if (wave == 0) {
       // the chunk's per-token sums: lane = token
-      const double u = ((double)sm.s.u[0][lane] + sm.s.u[1][lane]) + ((double)sm.s.u[2][lane] + sm.s.u[3][lane]);
-      const double v = ((double)sm.s.v[0][lane] + sm.s.v[1][lane]) + ((double)sm.s.v[2][lane] + sm.s.v[3][lane]);
-      double cs = 0.0;   // a strip before token j's tile has no entry of column j
+      double u = 0.0, v = 0.0, cs = 0.0, gsum = 0.0;
 #pragma unroll
-      for (int q = 0; q < kSsmWaves; ++q)
+      for (int q = 0; q < KT; ++q) {
+        u += (double)sm.s.u[q][lane];
+        v += (double)sm.s.v[q][lane];
+      }
+      // a strip before token j's tile has no entry of column j
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
         if (q >= lane >> 4) cs += (double)sm.s.col[q][lane];
+#pragma unroll
+      for (int q = 0; q < kBwdWaves; ++q) gsum += (double)sm.s.g[q];
       const double vd = v * s.dt;
-      const double net = (double)sm.s.row[lane] + u - cs * s.dt - vd;
-      const double gsum = ((double)sm.s.g[0] + sm.s.g[1]) + ((double)sm.s.g[2] + sm.s.g[3]);
+      const double net = ((double)sm.s.row[0][lane] + sm.s.row[1][lane]) + u - cs * s.dt - vd;
       const double incl = wave_scan(net);
       const double all = lane63(incl) + lane63(wave_scan(vd)) + (double)exp2_of(last) * gsum;
       const double da = all - (incl - net);
@@ -351,57 +356,21 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_bwd_k
         o[2 * f.H] = (float)sb;
       }
     }
-    __syncthreads();
-    // dx
-    const float dskip = f.D ? f.D[h] : 0.f;
-    Slab<T> ysT[2][NV];
-#pragma unroll
-    for (int js = 0; js < 2; ++js)
-#pragma unroll
-      for (int q = 0; q < NV; ++q) ysT[js][q] = slab_tr<T>(sm.dy, PV, 32 * js, c0 + 4 * q, 4 * NV);
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      const int j = 16 * it + l16, c = c0 + 4 * NV * g;
-      const float w = sm.w[j], dj = sm.dt[j];
-#pragma unroll
-      for (int q = 0; q < NV; ++q) dx[it][q] *= w;
-#pragma unroll
-      for (int js = it / 2; js < 2; ++js) {
-        const Slab<T> ms = slab_tr<T>(sm.m, PM, 32 * js, 16 * it, 4);
-#pragma unroll
-        for (int q = 0; q < NV; ++q) dx[it][q] = mma(ysT[js][q], ms, dx[it][q]);
-      }
-      float o[4 * NV];
-#pragma unroll
-      for (int q = 0; q < NV; ++q) {
-        const f32x4 yj = four_of_row(sm.dy, PV, 16 * it, c + 4 * q);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[4 * q + r] = f.D ? fmaf(dskip, yj[r], dj * dx[it][q][r]) : dj * dx[it][q][r];
-      }
-      if (j < n) Rows<T, 4 * NV>::store((T*)b.dx + (tok + j) * (size_t)vld + (size_t)h * DV + c, o);
-    }
   }
   // sums over the heads
 #pragma unroll
-  for (int it = 0; it < 4; ++it) {
-    const int i = 16 * it + l16;
+  for (int t = 0; t < NK; ++t) {
+    const int i = 16 * (tk + t) + l16;
     if (i >= n) continue;
-    const size_t at = ((tok + i) * (size_t)f.G + grp) * DK + k0 + 4 * NK * g;
-    float oc[4 * NK], ob[4 * NK];
-#pragma unroll
-    for (int q = 0; q < NK; ++q)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        oc[4 * q + r] = dC[it][q][r];
-        ob[4 * q + r] = dB[it][q][r];
-      }
+    const size_t at = ((tok + i) * (size_t)f.G + grp) * DK + k0 + 4 * g;
+    const float oc[4] = {dC[t][0], dC[t][1], dC[t][2], dC[t][3]}, ob[4] = {dB[t][0], dB[t][1], dB[t][2], dB[t][3]};
     if (a.shares > 1) {
       const size_t sh = (size_t)share * a.tokens * f.G * DK;
-      Rows<float, 4 * NK>::store(a.dCp + sh + at, oc);
-      Rows<float, 4 * NK>::store(a.dBp + sh + at, ob);
+      Rows<float, 4>::store(a.dCp + sh + at, oc);
+      Rows<float, 4>::store(a.dBp + sh + at, ob);
     } else {
-      Rows<T, 4 * NK>::store((T*)b.dC + at, oc);
-      Rows<T, 4 * NK>::store((T*)b.dB + at, ob);
+      Rows<T, 4>::store((T*)b.dC + at, oc);
+      Rows<T, 4>::store((T*)b.dB + at, ob);
     }
   }
 }
@@ -515,7 +484,7 @@ hipError_t bwd_go(const SsmBwdArgs& b, const BwdLayout& L, const int* cu, int N,
     a.part = reinterpret_cast<float*>(ws + L.part) + at * 3;
     const long long blocks = (long long)sc.items * b.f.G * a.shares;
     if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((ssm_bwd_kernel<T, DK, DV>), dim3((unsigned)blocks), dim3(kSsmThreads), 0, st, a, sc);
+    hipLaunchKernelGGL((ssm_bwd_kernel<T, DK, DV>), dim3((unsigned)blocks), dim3(kBwdThreads), 0, st, a, sc);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     done += (size_t)sc.items;
   }

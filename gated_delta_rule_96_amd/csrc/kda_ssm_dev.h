@@ -115,15 +115,24 @@ __device__ __forceinline__ Slab<T> slab_tr(const T* p, int pitch, int r0, int c0
   return s;
 }
 // Slab along a row: columns c0 + {4g.., 16+4g..} of row r0 + l16 (r0 a multiple
-// of 16).  The second half's address is hidden from the compiler: joined into
-// one two-address read the halves meet in the same banks.
+// of 16).  RowLanes: where the lane's two halves are in a tile of this pitch;
+// the second is hidden from the compiler (once per kernel): joined into one
+// two-address read the halves would meet in the same banks.
+struct RowLanes {
+  int near, far;
+};
 template <typename T>
-__device__ __forceinline__ Slab<T> slab_row(const T* p, int pitch, int r0, int c0) {
-  const int g = lane_id() >> 4;
-  const int at = (int)(lds_at((const T*)nullptr, pitch, lane_id() & 15, 4 * g) - (const T*)nullptr);
-  int far = at + 16;
-  if constexpr (sizeof(T) == 2) asm("" : "+v"(far));
-  return slab_of<T>(load4(p + at + (r0 * pitch + c0)), load4(p + far + (r0 * pitch + c0)));
+__device__ __forceinline__ RowLanes row_lanes(int pitch) {
+  const int l16 = lane_id() & 15, g = lane_id() >> 4;
+  RowLanes r;
+  r.near = l16 * pitch + LdsRow<T>::shift(l16) + 4 * g;
+  r.far = r.near + 16;
+  asm("" : "+v"(r.far));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ Slab<T> slab_row(const T* p, const RowLanes& rl, int at) {   // at = r0 pitch + c0
+  return slab_of<T>(load4(p + at + rl.near), load4(p + at + rl.far));
 }
 // Slab of a product of two rows: columns c0 + 8g .. 8g+7, one 16-byte read
 // (bf16); any order of the reduction index serves if both operands have it.
@@ -366,13 +375,13 @@ struct State {
 };
 
 // kQ rows of D elements from global memory (row stride ld) to LDS (padded),
-// through the registers of the first kSsmThreads threads: load() issues the
-// loads of rows < n (rows behind are zeros), store() writes them.
-template <typename T, int D>
+// through the registers of kThreads threads: load() issues the loads of rows
+// < n (rows behind are zeros), store() writes them.
+template <typename T, int D, int kThreads = kSsmThreads>
 struct RowTile {
   static constexpr int VE = 16 / sizeof(T);
-  static constexpr int kPer = kQ * D / VE / kSsmThreads;
-  static constexpr int kRows = kSsmThreads * VE / D;   // rows between a thread's pieces (a multiple of 8)
+  static constexpr int kPer = kQ * D / VE / kThreads;
+  static constexpr int kRows = kThreads * VE / D;   // rows between a thread's pieces (a multiple of 8)
   static constexpr int kPitch = D + LdsRow<T>::pad;
   typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
   u32x4 v[kPer];
