@@ -64,8 +64,12 @@ struct BwdLds {
   };
   T dy[kQ * PV];
   T m[kQ * PM];              // E dt Qm, then E P: [i][j]
+  // dS rounded to T, [state channel][value column] (fp32: read from memory
+  // again, as there is no room)
+  static constexpr bool kKeepDS = sizeof(T) == 2;
+  T ds[kKeepDS ? DK * PV : 1];
   double cum[kQ];
-  float ecum[kQ], w[kQ], dt[kQ];
+  float ecum[kQ], w[kQ], dt[kQ], slope[kQ];   // slope: of the softplus (or 1)
 };
 
 // Sum over the 16 lanes of a row of lanes, by lane permutations.
@@ -115,10 +119,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
   const int k0 = 16 * (wave % KT), tk = KT == kBwdWaves ? 0 : NK * (wave / KT);   // first state channel and token tile
   const int c0 = 16 * (wave % VT), tv = VT == kBwdWaves ? 0 : NV * (wave / VT);   // first value column and token tile
   // Half strips of the token x token products: tiles (is, 2 jh) and (is, 2 jh + 1).
-  const int is = wave & 3, jh = wave >> 2, i_own = 16 * is + l16;
-  T* m_own = sm.m + i_own * PM + LdsRow<T>::shift(i_own);
+  const int is = wave & 3, jh = wave >> 2;
 
-  const RowLanes rk = row_lanes<T>(PK), rv = row_lanes<T>(PV), rm = row_lanes<T>(PM);
   RowTile<T, DV, kBwdThreads> rx, ry;
   float raw = 0.f;
   auto fetch = [&](int h) {
@@ -150,10 +152,34 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
   for (int t = 0; t < NK; ++t) dC[t] = dB[t] = zero4();
 
   for (int h = h0; h < h1; ++h) {
+    // the lane's places, formed anew for every head: kept over the loop they
+    // would take about a hundred registers and spill
+    int ln = lane;
+    asm volatile("" : "+v"(ln));
+    const int g = ln >> 4, l16 = ln & 15, i_own = 16 * is + l16;
+    T* m_own = sm.m + i_own * PM + LdsRow<T>::shift(i_own);
+    const RowLanes rk = row_lanes<T>(PK, ln), rv = row_lanes<T>(PV, ln), rm = row_lanes<T>(PM, ln);
+    // S and dS, 16 rows a wave, in slabs of 32 value columns loaded two ahead of
+    // their use (all of them at once, or a head ahead, spill, and a reload
+    // from scratch waits for every load before it)
+    const size_t st = ((size_t)item * f.H + h) * (size_t)(DK * DV);
+    f32x4 sS[DV / 32][2], sD[DV / 32][2];
+    auto fetch_states = [&](int k) {
+      const float *pS = a.S + st + (size_t)k0 * DV + 32 * k, *pD = a.dS + st + (size_t)k0 * DV + 32 * k;
+      const unsigned off = (unsigned)(l16 * DV + 4 * g);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        sS[k][q] = load4(pS + off + 16 * q);
+        sD[k][q] = load4(pD + off + 16 * q);
+      }
+    };
+    fetch_states(0);
+    fetch_states(1);
     const double a2 = (double)f.A[h] * 1.4426950408889634074;
-    const float bias = f.bias ? f.bias[h] : 0.f, rawv = raw;
+    const float bias = f.bias ? f.bias[h] : 0.f;
     StepSize s = step_size(raw, bias, f.softplus, a2);
     if (lane >= n) s = StepSize{0.f, 0.0};
+    const float slope = f.softplus ? sigmoid_fast(raw + bias) : 1.f;
     const double cum = wave_scan(s.a), last = lane63(cum);
     __syncthreads();   // the head before is done with LDS
     rx.store(sm.x, tid);
@@ -162,6 +188,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
     else if (wave == 1) sm.ecum[lane] = exp2_of(cum);
     else if (wave == 2) sm.w[lane] = exp2_of(last - cum);
     else if (wave == 3) sm.dt[lane] = s.dt;
+    else if (wave == 4) sm.slope[lane] = slope;
     if (h + 1 < h1) fetch(h + 1);
     __syncthreads();
 
@@ -172,7 +199,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
     {
       Slab<T> ys[DV / 32];
 #pragma unroll
-      for (int k = 0; k < DV / 32; ++k) ys[k] = slab_any(sm.dy, PV, 16 * is, 32 * k);
+      for (int k = 0; k < DV / 32; ++k) ys[k] = slab_any(sm.dy, PV, 16 * is, 32 * k, ln);
       const double ci = sm.cum[i_own];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -184,7 +211,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
         if (jt <= is) {
           f32x4 acc = zero4();
 #pragma unroll
-          for (int k = 0; k < DV / 32; ++k) acc = mma(slab_any(sm.x, PV, 16 * jt, 32 * k), ys[k], acc);
+          for (int k = 0; k < DV / 32; ++k) acc = mma(slab_any(sm.x, PV, 16 * jt, 32 * k, ln), ys[k], acc);
           const int j = 16 * jt + 4 * g;
           const f32x4 dj = load4(sm.dt + j);
 #pragma unroll
@@ -217,26 +244,32 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
     }
 
     // S dy and dS x (transposed: rows the wave's state channels)
-    const size_t st = ((size_t)item * f.H + h) * (size_t)(DK * DV);
     float su[NK], sv[NK], gs;
     {
       f32x4 U[NK], Z[NK], g4 = zero4();
 #pragma unroll
       for (int t = 0; t < NK; ++t) U[t] = Z[t] = zero4();
-      const float *Sp = a.S + st + (size_t)(k0 + l16) * DV + 4 * g, *dSp = a.dS + st + (size_t)(k0 + l16) * DV + 4 * g;
-#pragma unroll 1
+      T* dsp = sm.ds + (k0 + l16) * PV + LdsRow<T>::shift(l16) + 4 * g;
+#pragma unroll
       for (int k = 0; k < DV / 32; ++k) {
-        const f32x4 s0 = load4(Sp + 32 * k), s1 = load4(Sp + 32 * k + 16), d0 = load4(dSp + 32 * k), d1 = load4(dSp + 32 * k + 16);
+        if (k + 2 < DV / 32) fetch_states(k + 2);
+        const f32x4 s0 = sS[k][0], s1 = sS[k][1], d0 = sD[k][0], d1 = sD[k][1];
 #pragma unroll
         for (int r = 0; r < 4; ++r) g4[r] = fmaf(s0[r], d0[r], fmaf(s1[r], d1[r], g4[r]));
-        Split<T> ss, ds;
-        split_of(s0, s1, ss);
-        split_of(d0, d1, ds);
-#pragma unroll
-        for (int t = 0; t < NK; ++t) {
-          U[t] = mma_split(ss, slab_row(sm.dy, rv, 16 * (tk + t) * PV + 32 * k), U[t]);
-          Z[t] = mma_split(ds, slab_row(sm.x, rv, 16 * (tk + t) * PV + 32 * k), Z[t]);
+        if constexpr (Lds::kKeepDS) {   // (waves that share the rows write the same values)
+          store4(dsp + 32 * k, narrow4<T>(d0));
+          store4(dsp + 32 * k + 16, narrow4<T>(d1));
         }
+        // one operand's parts at a time: more do not fit the registers
+        Split<T> sp;
+        split_of(s0, s1, sp);
+#pragma unroll
+        for (int t = 0; t < NK; ++t) U[t] = mma_split(sp, slab_row(sm.dy, rv, 16 * (tk + t) * PV + 32 * k), U[t]);
+        __builtin_amdgcn_sched_barrier(0);
+        split_of(d0, d1, sp);
+#pragma unroll
+        for (int t = 0; t < NK; ++t) Z[t] = mma_split(sp, slab_row(sm.x, rv, 16 * (tk + t) * PV + 32 * k), Z[t]);
+        __builtin_amdgcn_sched_barrier(0);
       }
       // waves that share state channels (other tokens) hold the same sum
       gs = tk == 0 ? (g4[0] + g4[1]) + (g4[2] + g4[3]) : 0.f;
@@ -244,7 +277,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
       for (int t = 0; t < NK; ++t) {
         const int it = tk + t, i = 16 * it + l16;
         const float e = sm.ecum[i], w = sm.w[i], wd = w * sm.dt[i];
-        const f32x4 c4 = four_of_row(sm.c, PK, 16 * it, k0 + 4 * g), b4 = four_of_row(sm.b, PK, 16 * it, k0 + 4 * g);
+        const f32x4 c4 = four_of_row(sm.c, PK, 16 * it, k0 + 4 * g, ln), b4 = four_of_row(sm.b, PK, 16 * it, k0 + 4 * g, ln);
         float uu = 0.f, vv = 0.f;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -280,12 +313,12 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
     // dC += (E dt Qm) B, dB += (E dt Qm)^T C
 #pragma unroll
     for (int js = 0; js < 2; ++js) {
-      const Slab<T> bs = slab_tr<T>(sm.b, PK, 32 * js, k0, 4), cs = slab_tr<T>(sm.c, PK, 32 * js, k0, 4);
+      const Slab<T> bs = slab_tr<T>(sm.b, PK, 32 * js, k0, 4, ln), cs = slab_tr<T>(sm.c, PK, 32 * js, k0, 4, ln);
 #pragma unroll
       for (int t = 0; t < NK; ++t) {
         const int it = tk + t;
         if (js <= it / 2) dC[t] = mma(bs, slab_row(sm.m, rm, 16 * it * PM + 32 * js), dC[t]);
-        if (js >= it / 2) dB[t] = mma(cs, slab_tr<T>(sm.m, PM, 32 * js, 16 * it, 4), dB[t]);
+        if (js >= it / 2) dB[t] = mma(cs, slab_tr<T>(sm.m, PM, 32 * js, 16 * it, 4, ln), dB[t]);
       }
     }
     // dS^T B (transposed: rows the wave's value columns, columns tokens j)
@@ -294,14 +327,19 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
     for (int t = 0; t < NV; ++t) dx[t] = zero4();
 #pragma unroll
     for (int k = 0; k < DK / 32; ++k) {
-      const float* dp = a.dS + st + (size_t)(32 * k + 4 * g) * DV + c0 + l16;
-      f32x4 lo, hi;
+      Slab<T> ds;
+      if constexpr (Lds::kKeepDS) {
+        ds = slab_tr<T>(sm.ds, PV, 32 * k, c0, 4, ln);
+      } else {
+        const float* dp = a.dS + st + (size_t)(32 * k + 4 * g) * DV + c0 + l16;
+        f32x4 lo, hi;
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        lo[r] = dp[r * DV];
-        hi[r] = dp[(16 + r) * DV];
+        for (int r = 0; r < 4; ++r) {
+          lo[r] = dp[r * DV];
+          hi[r] = dp[(16 + r) * DV];
+        }
+        ds = make_slab<T>(lo, hi);
       }
-      const Slab<T> ds = make_slab<T>(lo, hi);
 #pragma unroll
       for (int t = 0; t < NV; ++t) dx[t] = mma(ds, slab_row(sm.b, rk, 16 * (tv + t) * PK + 32 * k), dx[t]);
     }
@@ -312,16 +350,16 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
     __syncthreads();
     // dx
     const float dskip = f.D ? f.D[h] : 0.f;
-    const Slab<T> y0 = slab_tr<T>(sm.dy, PV, 0, c0, 4), y1 = slab_tr<T>(sm.dy, PV, 32, c0, 4);
+    const Slab<T> y0 = slab_tr<T>(sm.dy, PV, 0, c0, 4, ln), y1 = slab_tr<T>(sm.dy, PV, 32, c0, 4, ln);
 #pragma unroll
     for (int t = 0; t < NV; ++t) {
       const int it = tv + t, j = 16 * it + l16, c = c0 + 4 * g;
       const float dj = sm.dt[j];
       dx[t] *= sm.w[j];
-      if (it < 2) dx[t] = mma(y0, slab_tr<T>(sm.m, PM, 0, 16 * it, 4), dx[t]);
-      dx[t] = mma(y1, slab_tr<T>(sm.m, PM, 32, 16 * it, 4), dx[t]);
+      if (it < 2) dx[t] = mma(y0, slab_tr<T>(sm.m, PM, 0, 16 * it, 4, ln), dx[t]);
+      dx[t] = mma(y1, slab_tr<T>(sm.m, PM, 32, 16 * it, 4, ln), dx[t]);
       f32x4 o = dj * dx[t];
-      if (f.D) o += dskip * four_of_row(sm.dy, PV, 16 * it, c);
+      if (f.D) o += dskip * four_of_row(sm.dy, PV, 16 * it, c, ln);
       const float ov[4] = {o[0], o[1], o[2], o[3]};
       if (j < n) Rows<T, 4>::store((T*)b.dx + (tok + j) * (size_t)vld + (size_t)h * DV + c, ov);
     }
@@ -339,16 +377,15 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
         if (q >= lane >> 4) cs += (double)sm.s.col[q][lane];
 #pragma unroll
       for (int q = 0; q < kBwdWaves; ++q) gsum += (double)sm.s.g[q];
-      const double vd = v * s.dt;
-      const double net = ((double)sm.s.row[0][lane] + sm.s.row[1][lane]) + u - cs * s.dt - vd;
+      const double dts = (double)sm.dt[lane], vd = v * dts;
+      const double net = ((double)sm.s.row[0][lane] + sm.s.row[1][lane]) + u - cs * dts - vd;
       const double incl = wave_scan(net);
-      const double all = lane63(incl) + lane63(wave_scan(vd)) + (double)exp2_of(last) * gsum;
+      const double all = lane63(incl) + lane63(wave_scan(vd)) + (double)exp2_of(sm.cum[kQ - 1]) * gsum;
       const double da = all - (incl - net);
-      double d = (double)f.A[h] * da + cs + sm.s.diag[lane] + v;
-      if (f.softplus) d *= (double)sigmoid_fast(rawv + bias);
+      double d = ((double)f.A[h] * da + cs + sm.s.diag[lane] + v) * (double)sm.slope[lane];
       if (lane >= n) d = 0.0;
       if (lane < n) ((T*)b.ddt)[(tok + lane) * (size_t)f.H + h] = from_f32<T>((float)d);
-      const double sA = lane63(wave_scan(da * s.dt)), sD = lane63(wave_scan((double)sm.s.qd[lane])), sb = lane63(wave_scan(d));
+      const double sA = lane63(wave_scan(da * dts)), sD = lane63(wave_scan((double)sm.s.qd[lane])), sb = lane63(wave_scan(d));
       if (lane == 0) {
         float* o = a.part + (size_t)item * 3 * f.H + h;
         o[0] = (float)sA;

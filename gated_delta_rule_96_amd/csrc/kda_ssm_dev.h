@@ -92,13 +92,15 @@ template <typename T> __device__ __forceinline__ const T* lds_at(const T* p, int
   return p + row * pitch + LdsRow<T>::shift(row) + col;
 }
 
+// The readers below take the lane (a kernel may hand it over hidden from the
+// compiler, so that a loop does not keep all their addresses in registers).
 // Slab whose reduction index is the LDS row: rows r0 + {4g.., 16+4g..} (r0 a
 // multiple of 32) of one column per lane (l16 = lane % 16).  The column of l16 is c0 + step (l16 / 4)
 // + l16 % 4.  16-bit types: the transposed LDS read, whose lane 4q + s of a
 // group of 16 points at row 4g + q, columns 4s..4s+3 and gets column 4q + s.
 template <typename T>
-__device__ __forceinline__ Slab<T> slab_tr(const T* p, int pitch, int r0, int c0, int step) {
-  const int l = lane_id(), g = l >> 4, l16 = l & 15;
+__device__ __forceinline__ Slab<T> slab_tr(const T* p, int pitch, int r0, int c0, int step, int l = lane_id()) {
+  const int g = l >> 4, l16 = l & 15;
   Slab<T> s;
   if constexpr (sizeof(T) == 2) {
     typedef __attribute__((address_space(3))) bf16x4* LdsP;
@@ -122,8 +124,8 @@ struct RowLanes {
   int near, far;
 };
 template <typename T>
-__device__ __forceinline__ RowLanes row_lanes(int pitch) {
-  const int l16 = lane_id() & 15, g = lane_id() >> 4;
+__device__ __forceinline__ RowLanes row_lanes(int pitch, int l = lane_id()) {
+  const int l16 = l & 15, g = l >> 4;
   RowLanes r;
   r.near = l16 * pitch + LdsRow<T>::shift(l16) + 4 * g;
   r.far = r.near + 16;
@@ -137,8 +139,8 @@ __device__ __forceinline__ Slab<T> slab_row(const T* p, const RowLanes& rl, int 
 // Slab of a product of two rows: columns c0 + 8g .. 8g+7, one 16-byte read
 // (bf16); any order of the reduction index serves if both operands have it.
 template <typename T>
-__device__ __forceinline__ Slab<T> slab_any(const T* p, int pitch, int r0, int c0) {
-  const T* a = lds_at(p, pitch, lane_id() & 15, 8 * (lane_id() >> 4)) + r0 * pitch + c0;
+__device__ __forceinline__ Slab<T> slab_any(const T* p, int pitch, int r0, int c0, int l = lane_id()) {
+  const T* a = lds_at(p, pitch, l & 15, 8 * (l >> 4)) + r0 * pitch + c0;
   Slab<T> s;
   if constexpr (sizeof(T) == 2) s.v = *reinterpret_cast<const bf16x8*>(a);
   else s = slab_of<T>(load4(a), load4(a + 4));
@@ -146,8 +148,8 @@ __device__ __forceinline__ Slab<T> slab_any(const T* p, int pitch, int r0, int c
 }
 // Four columns from c0 of row r0 + l16.
 template <typename T>
-__device__ __forceinline__ f32x4 four_of_row(const T* p, int pitch, int r0, int c0) {
-  return widen4(load4(lds_at(p, pitch, lane_id() & 15, 0) + r0 * pitch + c0));
+__device__ __forceinline__ f32x4 four_of_row(const T* p, int pitch, int r0, int c0, int l = lane_id()) {
+  return widen4(load4(lds_at(p, pitch, l & 15, 0) + r0 * pitch + c0));
 }
 
 // fp32 values as an operand of products that stay fp32 results: one slab
