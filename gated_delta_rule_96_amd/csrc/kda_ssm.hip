@@ -59,7 +59,7 @@ struct SsmLds {
 template <typename T, int DK, int DV>
 __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk_kernel(const SsmArgs a, const SeqTab sq) {
   typedef SsmLds<T, DK, DV> Lds;
-  typedef State<DK, DV, true> St;
+  typedef State<DK, DV> St;
   constexpr int NT = St::NT, PK = Lds::PK, PV = Lds::PV;
   __shared__ __align__(16) char smem[sizeof(Lds)];
   Lds& sm = *reinterpret_cast<Lds*>(smem);
@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
 
     Split<T> xw[2][NT];
     St::weigh(xs, sm.wdt, xw);
-    S.template update<false, PadTile<T, DK>>(exp2_of(last), sm.b, xw);
+    S.template update<PadTile<T, DK>>(exp2_of(last), sm.b, xw);
   }
   if (p.last && a.ht) S.store(a.ht + ((size_t)p.n * a.H + h) * sd);
 }
@@ -246,7 +246,7 @@ template <int DK, int DV>
 __global__ __launch_bounds__(kPipeThreads, 2) void ssm_pipe_kernel(const SsmArgs a, const SeqTab sq) {
   typedef bf16 T;
   typedef PipeLds<DK, DV> Lds;
-  typedef State<DK, DV, true> St;
+  typedef State<DK, DV> St;
   typedef SwzTile<DK> TK;
   typedef SwzTile<DV> TV;
   constexpr int NT = St::NT;
@@ -429,7 +429,7 @@ __global__ __launch_bounds__(kPipeThreads, 2) void ssm_pipe_kernel(const SsmArgs
           for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(tx + TV::at(j, col + 4 * q)));
         }
     }
-    S.template update<false, TK>(sm.el[buf], tb, xw);
+    S.template update<TK>(sm.el[buf], tb, xw);
     if (a.D) {
 #pragma unroll
       for (int it = 0; it < 4; ++it)

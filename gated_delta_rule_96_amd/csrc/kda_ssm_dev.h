@@ -298,16 +298,16 @@ struct PadTile {
 };
 
 // A state in the accumulator layout: the wave's dv/4 value columns as NT
-// tiles, KT tiles of state channels.  kPerm: output row m of tile t is column
-// wave CPW + 4 NT (m/4) + 4t + m%4 (a lane of a transposed product then holds
-// neighbouring columns); otherwise wave CPW + 16 t + m.
-template <int DK, int DV, bool kPerm>
+// tiles, KT tiles of state channels.  Output row m of tile t is column wave CPW
+// + 4 NT (m/4) + 4t + m%4: a lane of a transposed product then holds
+// neighbouring columns.
+template <int DK, int DV>
 struct State {
   static constexpr int CPW = DV / kSsmWaves, NT = CPW / 16, KT = DK / 16;
   f32x4 s[KT][NT];
   static __device__ __forceinline__ int col(int t) {
     const int l16 = lane_id() & 15, wave = (threadIdx.x >> 6) & (kSsmWaves - 1);
-    return wave * CPW + (kPerm ? 4 * NT * (l16 >> 2) + 4 * t + (l16 & 3) : 16 * t + l16);
+    return wave * CPW + 4 * NT * (l16 >> 2) + 4 * t + (l16 & 3);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -337,9 +337,9 @@ struct State {
   // xw from the wave's slabs of cols [kQ][DV] and one weight per token, and the
   // products with rows [kQ][DK] in LDS (Tile: how those are laid out).  The
   // chunk's sum is formed apart from the state: small parts are not rounded
-  // to the state's last place one by one.  kLow: the lower parts' sum stays
-  // apart to the end (mma_low); otherwise it starts the sum, one addition less
-  // per element and a mean error of 1e-8.
+  // to the state's last place one by one.  The lower parts start the sum (one
+  // addition less per element than a sum of their own, and a mean error of
+  // 1e-8, see mma_low).
   template <typename T>
   static __device__ __forceinline__ void weigh(const Slab<T> (&xs)[2][NT], const float* w, Split<T> (&xw)[2][NT]) {
     const int g = lane_id() >> 4;
@@ -350,7 +350,7 @@ struct State {
       for (int q = 0; q < NT; ++q) xw[js][q] = scaled<T>(xs[js][q], w0, w1);
     }
   }
-  template <bool kLow, typename Tile, typename T>
+  template <typename Tile, typename T>
   __device__ __forceinline__ void update(float el, const T* rows, const Split<T> (&xw)[2][NT]) {
 #pragma unroll
     for (int k = 0; k < KT; ++k) {
@@ -358,10 +358,9 @@ struct State {
 #pragma unroll
       for (int q = 0; q < NT; ++q) {
         const f32x4 low = mma_low(b1, xw[1][q], mma_low(b0, xw[0][q], zero4()));
-        const f32x4 sum = mma(b1, xw[1][q].h, mma(b0, xw[0][q].h, kLow ? zero4() : low));
+        const f32x4 sum = mma(b1, xw[1][q].h, mma(b0, xw[0][q].h, low));
 #pragma unroll
         for (int r = 0; r < 4; ++r) s[k][q][r] = fmaf(s[k][q][r], el, sum[r]);
-        if constexpr (kLow && sizeof(T) == 2) s[k][q] += low;
       }
     }
   }
@@ -372,7 +371,63 @@ struct State {
     for (int js = 0; js < 2; ++js)
 #pragma unroll
       for (int q = 0; q < NT; ++q)
-        xs[js][q] = Tile::tr(cols, 32 * js, wave * CPW + (kPerm ? 4 : 16) * q, kPerm ? 4 * NT : 4);
+        xs[js][q] = Tile::tr(cols, 32 * js, wave * CPW + 4 * q, 4 * NT);
+  }
+};
+
+// A state kept transposed (nothing multiplies it): tile (k, q) of the wave holds
+// value columns wave CPW + 16 q + 4g .. +3 of state channel 16 k + l16, so that
+// it is read and written 16 bytes a lane.
+template <int DK, int DV>
+struct SweepState {
+  static constexpr int CPW = DV / kSsmWaves, NT = CPW / 16, KT = DK / 16;
+  f32x4 s[KT][NT];
+  static __device__ __forceinline__ int at(int k, int q) {
+    const int l16 = lane_id() & 15, g = lane_id() >> 4, wave = (threadIdx.x >> 6) & (kSsmWaves - 1);
+    return (16 * k + l16) * DV + wave * CPW + 16 * q + 4 * g;
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) s[k][q] = zero4();
+  }
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) s[k][q] = load4(p + at(k, q));
+  }
+  __device__ __forceinline__ void store(float* p) const {
+#pragma unroll
+    for (int k = 0; k < KT; ++k)
+#pragma unroll
+      for (int q = 0; q < NT; ++q) *reinterpret_cast<f32x4*>(p + at(k, q)) = s[k][q];
+  }
+  // As State::weigh and update, with the products the other way round.  kLow:
+  // the lower parts' sum stays apart to the end.
+  template <bool kLow, typename TileK, typename TileV, typename T>
+  __device__ __forceinline__ void update(float el, const T* rows, const T* cols, const float* w) {
+    const int g = lane_id() >> 4, wave = (threadIdx.x >> 6) & (kSsmWaves - 1);
+    Split<T> xw[2][NT];
+#pragma unroll
+    for (int js = 0; js < 2; ++js) {
+      const f32x4 w0 = load4(w + 32 * js + 4 * g), w1 = load4(w + 32 * js + 16 + 4 * g);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) xw[js][q] = scaled<T>(TileV::tr(cols, 32 * js, wave * CPW + 16 * q, 4), w0, w1);
+    }
+#pragma unroll
+    for (int k = 0; k < KT; ++k) {
+      const Slab<T> b0 = TileK::tr(rows, 0, 16 * k, 4), b1 = TileK::tr(rows, 32, 16 * k, 4);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        const f32x4 low = mma_low(xw[1][q], b1, mma_low(xw[0][q], b0, zero4()));
+        const f32x4 sum = mma(xw[1][q].h, b1, mma(xw[0][q].h, b0, kLow ? zero4() : low));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[k][q][r] = fmaf(s[k][q][r], el, sum[r]);
+        if constexpr (kLow && sizeof(T) == 2) s[k][q] += low;
+      }
+    }
   }
 };
 
