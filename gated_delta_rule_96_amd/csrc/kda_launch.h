@@ -195,6 +195,9 @@ struct SsmArgs {
 // Tokens of a part for about `wgs` (part, head) work-groups.  A sequence of n
 // parts keeps n - 1 states; n - 1 <= its tokens / part.
 int ssm_part(long long tokens, int H, int wgs);
+// The same, but long enough for the longest sequence where that pays (in
+// kda_ssm.hip).
+int ssm_part_of(int H, int wgs, const int* cu, int N, int B, int T);
 inline size_t ssm_slots(long long tokens, int H, int wgs) { return (size_t)(tokens / ssm_part(tokens, H, wgs)) * H; }
 // Workspace bytes of the forward.
 size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv);

@@ -14,20 +14,29 @@
 // rescaled, any decay is in range.  Later tokens never reach an earlier one's
 // y, also not as 0 x inf or 0 x NaN.
 //
-// A work-group (4 waves) walks the chunks of one part of one sequence for
-// one head with the whole state in registers: wave w owns dv/4 value columns
+// A work-group walks the chunks of one part of one sequence for one head with
+// the whole state in registers: of four waves, wave w owns dv/4 value columns
 // (as MFMA accumulators, so that two stacked tiles are directly the operand
 // of the next chunk's S^T C product).  All products are formed transposed
 // (value columns as rows of the output tile): a lane then holds neighbouring
 // value columns of one token and stores them together.  M goes through LDS
 // once (wave w forms rows 16w.. of it), x and B are read with transposed LDS
-// reads where the token is the reduction index.
+// reads where the token is the reduction index.  bf16 has four waves more,
+// which load and form M one chunk ahead (ssm_pipe_kernel).
 //
-// Parts: a sequence is cut so that about two work-groups per CU run; a first
-// pass sums each part's own states (no y), a small kernel chains them, the
-// second pass starts every part from its state.  That reads x and B twice; it
-// keeps the chain of dependent chunks short without waits between
+// Parts: a sequence is cut so that one work-group per CU runs; a first pass
+// (kda_ssm_sweep.h) sums each part's own states (no y), a small kernel chains
+// them, the second pass starts every part from its state.  That reads x and B
+// twice; it keeps the chain of dependent chunks short without waits between
 // work-groups.
+//
+// Measured (65536 tokens, 32 heads of 128 x 128, bf16): 618 us, 1.8 TB/s of
+// the inputs and outputs and 220 TFLOP/s of the products (kernel by kernel, at
+// the lower clock of a traced run: first pass 244, chaining 12, scan 491).
+// Neither rate binds: a chunk's 144 matrix instructions per state wave are 147
+// us of the scan's time at 2 GHz; the rest are their LDS operands, the exact
+// splits, the state's scaling and y's stores of the same four waves, one
+// work-group per CU, whose tiles and state fill LDS and registers.
 //
 // Rounding (bf16): C, B and x are exact operands; M and the state as the
 // operand of S^T C are rounded to bf16 (2^-8 of each product's terms, like
@@ -41,24 +50,29 @@ namespace kda {
 
 namespace {
 
-constexpr int kScanWgs = 256;   // one scan work-group per CU
-constexpr int kSubs = 2;        // a part's own sum is formed in two shares (two sweep work-groups per CU)
+// One scan work-group per CU (64K tokens x 32 heads: 634 us; 128 in all 937,
+// 512 658).
+constexpr int kScanWgs = 256;
+// A part's own sum is formed in two shares: two sweep work-groups per CU (the
+// same tokens: 634 us; one share 664, four 643).
+constexpr int kSubs = 2;
 
-template <typename T, int DK, int DV>
-struct SsmLds {
-  static constexpr int PK = RowTile<T, DK>::kPitch, PV = RowTile<T, DV>::kPitch;
-  T c[kQ * PK];
-  T b[kQ * PK];
-  T x[kQ * PV];
-  Slab<T> m[8 * 64];          // M rows of tile it, slab js, at (2 it + js) 64 + lane
+template <int DK, int DV>
+struct ChunkLds {
+  static constexpr int PK = RowTile<float, DK>::kPitch, PV = RowTile<float, DV>::kPitch;
+  float c[kQ * PK];
+  float b[kQ * PK];
+  float x[kQ * PV];
+  Slab<float> m[8 * 64];      // M rows of tile it, slab js, at (2 it + js) 64 + lane
   double cum[kQ];
-  float cumf[kQ], ecum[kQ], wdt[kQ], dt[kQ];
+  float ecum[kQ], wdt[kQ], dt[kQ];
 };
 
-// The scan of a part: y and, for a sequence's last part, its final state.
-template <typename T, int DK, int DV>
-__global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk_kernel(const SsmArgs a, const SeqTab sq) {
-  typedef SsmLds<T, DK, DV> Lds;
+// The scan of a part, fp32: y and, for a sequence's last part, its final state.
+template <int DK, int DV>
+__global__ __launch_bounds__(kSsmThreads) void ssm_chunk_kernel(const SsmArgs a, const SeqTab sq) {
+  typedef float T;
+  typedef ChunkLds<DK, DV> Lds;
   typedef State<DK, DV> St;
   constexpr int NT = St::NT, PK = Lds::PK, PV = Lds::PV;
   __shared__ __align__(16) char smem[sizeof(Lds)];
@@ -93,7 +107,7 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
     rc.load(cm + (size_t)t * (size_t)a.ldc, a.ldc, n, tid);
     rb.load(bm + (size_t)t * (size_t)a.ldb, a.ldb, n, tid);
     rx.load(x + (size_t)t * (size_t)a.ldx, a.ldx, n, tid);
-    raw = lane < n ? to_f32(dt[(size_t)(t + lane) * (size_t)a.lddt]) : 0.f;
+    raw = lane < n ? dt[(size_t)(t + lane) * (size_t)a.lddt] : 0.f;
   };
   if (p.t0 < p.t1) fetch(p.t0);
   for (int t = p.t0; t < p.t1; t += kQ) {
@@ -108,7 +122,6 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
     rx.store(sm.x, tid);
     if (wave == 0) {
       sm.cum[lane] = cum;
-      sm.cumf[lane] = (float)cum;
     } else if (wave == 1) {
       sm.ecum[lane] = exp2_of(cum);
     } else if (wave == 2) {
@@ -125,7 +138,6 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
 #pragma unroll
     for (int k = 0; k < DK / 32; ++k) cs[k] = slab_any(sm.c, PK, 16 * it, 32 * k);
     const double ci = sm.cum[i];
-    const float cif = sm.cumf[i];
 #pragma unroll
     for (int js = 0; js < 2; ++js) {
       if (2 * js > it) continue;
@@ -139,17 +151,8 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
         for (int k = 0; k < DK / 32; ++k) acc = mma(slab_any(sm.b, PK, 16 * jt, 32 * k), cs[k], acc);
         const int j = 16 * jt + 4 * g;
         const f32x4 dj = load4(sm.dt + j);
-        f32x4 ex;
-        if constexpr (sizeof(T) == 2) {
-          const f32x4 cj = load4(sm.cumf + j);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) ex[r] = exp2_fast(cif - cj[r]);
-        } else {
-#pragma unroll
-          for (int r = 0; r < 4; ++r) ex[r] = exp2_of(ci - sm.cum[j + r]);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) v[q][r] = j + r <= i ? acc[r] * ex[r] * dj[r] : 0.f;
+        for (int r = 0; r < 4; ++r) v[q][r] = j + r <= i ? acc[r] * exp2_of(ci - sm.cum[j + r]) * dj[r] : 0.f;
       }
       sm.m[(2 * it + js) * 64 + lane] = make_slab<T>(v[0], v[1]);
     }
@@ -199,9 +202,9 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
 #pragma unroll 1
         for (int j = 0; j <= i; ++j) {
           const T* mp = reinterpret_cast<const T*>(sm.m + (2 * it + (j >> 5)) * 64 + ((j >> 2) & 3) * 16 + l16);
-          const float m = to_f32(mp[4 * ((j >> 4) & 1) + (j & 3)]);
+          const float m = mp[4 * ((j >> 4) & 1) + (j & 3)];
 #pragma unroll
-          for (int q = 0; q < NT; ++q) acc[it][q] += m * widen4(load4(lds_at(sm.x, PV, j, c + 4 * q)));
+          for (int q = 0; q < NT; ++q) acc[it][q] += m * load4(lds_at(sm.x, PV, j, c + 4 * q));
         }
       }
       float o[4 * NT];
@@ -226,7 +229,8 @@ __global__ __launch_bounds__(kSsmThreads, sizeof(T) == 2 ? 2 : 1) void ssm_chunk
 // into LDS, form chunk k + 1's M and chunk k + 2's step sizes, while the back
 // waves take chunk k's products with S, its y and the state's update.  One
 // barrier a chunk; the matrix instructions of one set cover the loads and
-// exponents of the other.
+// exponents of the other (64K tokens x 32 heads: this kernel 491 us; 628 with
+// four waves that do one thing after the other).
 constexpr int kPipeThreads = 2 * kSsmThreads;
 
 template <int DK, int DV>
@@ -471,7 +475,7 @@ hipError_t fwd_go(const SsmArgs& a, const SeqTab& s, int seqs, bool split, hipSt
   if constexpr (sizeof(T) == 2)
     hipLaunchKernelGGL((ssm_pipe_kernel<DK, DV>), grid, dim3(kPipeThreads), 0, st, a, s);
   else
-    hipLaunchKernelGGL((ssm_chunk_kernel<T, DK, DV>), grid, dim3(kSsmThreads), 0, st, a, s);
+    hipLaunchKernelGGL((ssm_chunk_kernel<DK, DV>), grid, dim3(kSsmThreads), 0, st, a, s);
   return hipGetLastError();
 }
 
@@ -479,10 +483,36 @@ hipError_t fwd_go(const SsmArgs& a, const SeqTab& s, int seqs, bool split, hipSt
 
 int ssm_part(long long tokens, int H, int wgs) {
   // a part is at least four chunks, so that the extra pass and the chaining
-  // stay small beside it, and a whole number of chunks for each of its shares
+  // stay small beside it (1000 tokens x 32 heads: 42 us; at least two 46, eight
+  // 48), and a whole number of chunks for each of its shares
   const long long want = (tokens * H + wgs - 1) / wgs, unit = (long long)kQ * kSubs;
   const long long part = (want + unit - 1) / unit * unit;
   return (int)(part < 256 ? 256 : part > (1 << 30) ? (1 << 30) : part);
+}
+
+// Cutting a sequence adds a pass that costs about half of the one it shortens,
+// and two launches: a longest sequence of up to 1.5 parts + 256 tokens stays
+// whole, and with it every other one; of up to 2 parts + 256 where the parts
+// would be more than the work-groups that run at once.  Whole against cut, us
+// (bf16, 32 heads, lengths behind the name of the work-groups' share of the
+// tokens): 256: 640 32 against 36, 1000 49 against 42; 1024: 1500 + 7 x 928 75
+// against 128, 2000 + 7 x 864 91 against 126; 2048: 3600 + 13 x 950 191
+// against 208.
+int ssm_part_of(int H, int wgs, const int* cu, int N, int B, int T) {
+  const int part = ssm_part((long long)B * T, H, wgs);
+  long long longest = T, parts = 0;
+  if (cu) {
+    longest = 0;
+    for (int n = 0; n < N; ++n) {
+      const long long len = cu[n + 1] - cu[n];
+      longest = longest > len ? longest : len;
+      parts += (len + part - 1) / part;
+    }
+  } else {
+    parts = (long long)B * ((T + part - 1) / part);
+  }
+  const long long whole = (long long)part + (parts * H > wgs ? part : part / 2) + 256, unit = (long long)kQ * kSubs;
+  return longest > part && longest <= whole ? (int)((longest + unit - 1) / unit * unit) : part;
 }
 
 size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv) {
@@ -493,7 +523,7 @@ size_t ssm_seg_bytes(long long tokens, int H, int dk, int dv) {
 hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a0, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
                           hipStream_t st) {
   const long long tokens = (long long)B * T;
-  const int part = ssm_part(tokens, a0.H, kScanWgs), end = cu ? N : B;
+  const int part = ssm_part_of(a0.H, kScanWgs, cu, N, B, T), end = cu ? N : B;
   SsmArgs a = a0;
   a.seg = static_cast<float*>(workspace);
   const size_t states = kSubs * ssm_slots(tokens, a.H, kScanWgs) * (size_t)dk * dv;

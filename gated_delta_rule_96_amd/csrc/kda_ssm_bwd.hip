@@ -23,8 +23,14 @@
 // d(dt_bias) over the chunks.  Everything is written once: no atomics, the
 // same result every time.
 //
-// Bound by HBM: a state and its gradient per chunk and head, written and read
-// (4 dk dv 4 bytes each way), are the bulk beside the inputs.
+// A state and its gradient per chunk and head, written and read once (2 dk dv 4
+// bytes each way), are the bulk of the traffic beside the inputs.
+// Measured (4 x 8192 tokens, 16 heads of 128 x 128, one group, bf16): 897 us:
+// this kernel 529, sweeps that keep states 137 + 136 (0.54 GB written each, 3.9
+// TB/s), own sums of the parts 67 + 65, chaining 24, last sums 5.  This kernel
+// reads 1.1 GB of states (2.1 TB/s); it is bound by waits: for the states,
+// which the registers only allow to be fetched two slabs of 32 columns ahead,
+// and at the four barriers of a head.
 //
 // Rounding (bf16): the elementwise weights of the products that end in dx, dB
 // and dC (bf16 outputs) are rounded to bf16 once, dS^T B's operand dS too; S
@@ -36,10 +42,12 @@ namespace kda {
 
 namespace {
 
-constexpr int kSweepWgs = 512;   // two sweep work-groups per CU
+// Two sweep work-groups per CU (32K tokens x 16 heads: 895 us in all; one 960,
+// four 935).
+constexpr int kSweepWgs = 512;
 // Eight waves a chunk: with four, the sums over the heads and the products of
-// one head do not fit the registers (1101 against 1415 us for 32K tokens x 16
-// heads even at one work-group per CU instead of two).
+// one head do not fit the registers (32K tokens x 16 heads: 1101 us in all,
+// with eight 1018).
 constexpr int kBwdWaves = 8, kBwdThreads = 64 * kBwdWaves;
 
 struct ChunkBwd {
@@ -429,10 +437,12 @@ __global__ __launch_bounds__(256) void ssm_shares_kernel(const float* __restrict
   Rows<T, 8>::store((id < n8 ? dB : dC) + at, s);
 }
 
-// Work-groups a group's heads are split over: enough for about two per CU.
+// Work-groups a group's heads are split over: enough for about one per CU (1000
+// tokens x 32 heads: 127 us; for two per CU, the sums over the shares make it
+// 139).
 int head_shares(long long chunks, int H, int G) {
   long long s = 1;
-  while (s < H / G && chunks * G * s < 512) s *= 2;
+  while (s < H / G && chunks * G * s < 256) s *= 2;
   return (int)(s < H / G ? s : H / G);
 }
 
@@ -466,7 +476,7 @@ BwdLayout bwd_layout(int is_packed, int N, int B, int T, int H, int G, int dk, i
 template <typename T, int DK, int DV>
 hipError_t bwd_go(const SsmBwdArgs& b, const BwdLayout& L, const int* cu, int N, int B, int Tn, char* ws, hipStream_t st) {
   const long long tokens = (long long)B * Tn;
-  const int part = ssm_part(tokens, b.f.H, kSweepWgs), end = cu ? N : B;
+  const int part = ssm_part_of(b.f.H, kSweepWgs, cu, N, B, Tn), end = cu ? N : B;
   ChunkBwd a{};
   a.b = b;
   a.b.f.seg = reinterpret_cast<float*>(ws + L.seg);
