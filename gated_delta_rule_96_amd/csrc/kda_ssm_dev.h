@@ -14,9 +14,10 @@ constexpr int kQ = kSeqChunk;   // tokens per chunk
 // log1p(u) = 2 artanh(z), z = u / (2 + u) <= 1/3, by its series (the first
 // term left out is below 2e-9 of the sum): relative accuracy also for very
 // negative x, where the result is e^x.  e^-|x| as 2^(n + r) with the rounding
-// r of the product by log2(e) put back, so that large |x| costs no accuracy.
+// r of the product by log2(e) put back, so that large |x| costs no accuracy;
+// e^-|x| is zero from |x| = 200 on (also for infinities; NaN stays NaN).
 __device__ __forceinline__ float softplus_f(float x) {
-  const float m = -fabsf(x);
+  const float ax = fabsf(x), m = ax > 200.f ? -200.f : -ax;
   const float n = m * kLog2e;
   const float r = fmaf(m, 1.925963033500e-8f, fmaf(m, kLog2e, -n));   // log2(e) - fl(log2(e))
   const float e = exp2_fast(n);

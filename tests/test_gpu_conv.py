@@ -1,9 +1,8 @@
 """GPU parity of the short causal convolution (kda_conv_fwd, kda_conv_step,
 kda_conv_bwd) against the fp64 oracle (oracle/mix.py) on the cast inputs.
 
-Tolerances, per element.  u = 2^-24, h = half a step of the output type (2^-9
-relative to the value for bf16's 8-bit significand is eps / 2 = 2^-8 / 2 ...
-taken as finfo.eps / 2).  The sum of W products and the bias is at most W + 1
+Tolerances, per element.  u = 2^-24, h = half a step of the output type,
+finfo.eps / 2 relative to the value.  The sum of W products and the bias is at most W + 1
 roundings of partial sums below M = |bias| + sum |w x|: |dz_err| <= (W+1) u M.
 Sigmoid through 2^(-z log2 e): relative error (|z| + 4) u.  |act'| <= 1.1,
 |act''| <= 0.5.  With the product z Sigmoid(z): |y_err| <= 1.1 (W+1) u M +

@@ -85,7 +85,7 @@ def call(c, lens=None, B=None, **kw):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("lens", [[1], [63], [64], [65], [5, 0, 1, 130, 64, 0], [300, 700], [0, 2], [2] * 131], ids=lambda l: f"{len(l)}x{sum(l)}")
+@pytest.mark.parametrize("lens", [[1], [63], [64], [65], [5, 0, 1, 130, 64, 0], [300, 700], [0, 2], [2] * 131, [3] * 130 + [800, 2]], ids=lambda l: f"{len(l)}x{sum(l)}")
 @pytest.mark.parametrize("H,G,dk,dv,skip,soft,state,rows", [(2, 1, 64, 64, True, True, True, False), (4, 2, 128, 128, False, False, True, False),
                                                             (3, 3, 128, 64, True, True, False, True), (2, 2, 64, 128, True, True, True, True)])
 def test_packed(dtype, lens, H, G, dk, dv, skip, soft, state, rows):
@@ -99,7 +99,7 @@ def test_packed(dtype, lens, H, G, dk, dv, skip, soft, state, rows):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("B,T,H,G,slow", [(1, 2500, 4, 1, False), (3, 600, 2, 2, True), (2, 257, 1, 1, True)])
+@pytest.mark.parametrize("B,T,H,G,slow", [(1, 2500, 4, 1, False), (3, 600, 2, 2, True), (2, 257, 1, 1, True), (2, 1100, 2, 2, True)])
 def test_parts_of_long_sequences_and_in_place_state(dtype, B, T, H, G, slow):
     # parts of 256 tokens: chained states, h0 replaced in place by ht
     say(f"ssm batch {dtype} B={B} T={T} H={H} G={G}")
@@ -162,6 +162,33 @@ def test_rows_behind_and_other_sequences_untouched():
     y, ht = call(c, lens, out=big[:, :160])
     assert torch.equal(y[0, :50], y0[0, :50]) and torch.equal(y[0, 130:], y0[0, 130:]) and torch.isnan(y[0, 51:130]).all()
     assert torch.equal(ht[0], h0[0]) and torch.equal(ht[2], h0[2]) and (big[0, 160:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", ["x", "B", "C", "dt"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf"), "lowest"])
+def test_a_bad_token_stays_out_of_the_tokens_before_it(dtype, name, bad):
+    # token 170 is in the middle of the second chunk of 64 of its sequence: the
+    # tokens before it and the other sequences do not see it
+    say(f"ssm bad token {dtype} {name} {bad}")
+    lens = [100, 600, 30]
+    c = make(lens, 2, 1, 64, 64, dtype, 38, rate=2.0)
+    y_ref, _, ty, _ = oracle(c, lens, dtype)
+    y0, h0 = call(c, lens)
+    c[name][170] = torch.finfo(dtype).min if bad == "lowest" else bad
+    y, ht = call(c, lens)
+    assert torch.equal(y[0, :164], y0[0, :164]) and torch.equal(y[0, 700:], y0[0, 700:])
+    check("y before", y[0, 164:170], y_ref[164:170], ty[164:170], dtype)   # (a chunk with a bad x sums in another order)
+    assert torch.equal(ht[0], h0[0]) and torch.equal(ht[2], h0[2])
+    if name == "dt" and bad in ("lowest", float("-inf")):   # Softplus of it is zero: the token leaves the state alone
+        assert torch.isfinite(y).all() and torch.isfinite(ht).all()
+        y_ref, h_ref, ty, th = oracle(dict(c, dt=c["dt"].clamp(min=-1e3)), lens, dtype)
+        check("y", y[0], y_ref, ty, dtype)
+        check("ht", ht, h_ref, th, torch.float32)
+    elif name == "C" and bad != "lowest":
+        assert not torch.isfinite(y[0, 170]).any() and torch.equal(y[0, 171:], y0[0, 171:]) and torch.equal(ht, h0)
+    elif bad != "lowest":
+        assert not torch.isfinite(y[0, 170]).all() and not torch.isfinite(ht[1]).all()
 
 
 def test_captured_and_replayed():

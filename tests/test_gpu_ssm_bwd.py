@@ -71,7 +71,7 @@ def compare(c, g, o, lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("lens", [[1], [63], [64], [65], [5, 0, 1, 130, 64, 0], [600], [0, 2], [2] * 131], ids=lambda l: f"{len(l)}x{sum(l)}")
+@pytest.mark.parametrize("lens", [[1], [63], [64], [65], [5, 0, 1, 130, 64, 0], [600], [0, 2], [2] * 131, [3] * 130 + [800, 2]], ids=lambda l: f"{len(l)}x{sum(l)}")
 @pytest.mark.parametrize("H,G,dk,dv,skip,soft,state,rows", [(2, 1, 64, 64, True, True, True, False), (4, 2, 128, 128, False, False, True, False),
                                                             (3, 3, 128, 64, True, True, False, True), (3, 1, 64, 128, True, True, True, True)])
 def test_packed(dtype, lens, H, G, dk, dv, skip, soft, state, rows):
@@ -87,7 +87,7 @@ def test_packed(dtype, lens, H, G, dk, dv, skip, soft, state, rows):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("B,T,H,G", [(2, 300, 8, 1), (1, 64, 12, 2), (9, 100, 2, 1)])
+@pytest.mark.parametrize("B,T,H,G", [(2, 300, 8, 1), (1, 64, 12, 2), (9, 100, 2, 1), (2, 1300, 2, 1)])
 def test_batch(dtype, B, T, H, G):
     say(f"ssm bwd batch {dtype} B={B} T={T} H={H} G={G}")
     lens = [T] * B
@@ -95,6 +95,40 @@ def test_batch(dtype, B, T, H, G):
     g = run(c, B=B)
     torch.cuda.synchronize()
     compare(c, g, oracle(c, lens), lens, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", ["x", "B", "C", "dt", "dy"])
+def test_a_nan_token_stays_in_its_sequence_and_before_or_behind_its_chunk(dtype, name):
+    # token 64 + 20 of the second sequence: x, B and dt reach later tokens, dy
+    # (and C beside it) earlier ones; a whole chunk of 64 may become NaN
+    say(f"ssm bwd bad token {dtype} {name}")
+    lens = [100, 300, 30]
+    c = grads(make(lens, 2, 1, 64, 64, dtype, 45, rate=2.0), lens, dht=False)
+    want = run(c, lens)
+    c[name][100 + 84] = float("nan")
+    got = run(c, lens)
+    for n in ("dx", "ddt", "dB", "dC"):
+        a, b = got[n][0], want[n][0]
+        assert torch.equal(a[:100], b[:100]) and torch.equal(a[400:], b[400:]), n
+        if name in ("x", "B"):
+            assert torch.equal(a[100:164], b[100:164]), n
+        if name in ("dy", "C"):
+            assert torch.equal(a[228:400], b[228:400]), n
+    assert torch.equal(got["dh0"][0], want["dh0"][0]) and torch.equal(got["dh0"][2], want["dh0"][2])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_masked_tokens(dtype):
+    # raw step sizes of -inf and of the type's lowest value: Softplus and its
+    # slope are zero there, the tokens leave the states alone
+    lens = [100, 90]
+    c = grads(make(lens, 2, 1, 64, 64, dtype, 46, rate=2.0), lens)
+    c["dt"][20:30] = float("-inf")
+    c["dt"][95:110] = torch.finfo(dtype).min
+    g = run(c, lens)
+    torch.cuda.synchronize()
+    compare(c, g, oracle(dict(c, dt=c["dt"].clamp(min=-1e3)), lens), lens, dtype)
 
 
 def test_captured_and_replayed():
