@@ -486,6 +486,8 @@ int kda_qk_norm_rope_bwd(const void* q, long long ldq, const void* k, long long 
  * none).  y [B,T,H,dv] of dtype (a projection of the same type reads it;
  * fp32 sums, one rounding).  Precondition: A finite; dt A <= 0 is the
  * intended range, larger values are computed as they are and may overflow.
+ * A raw step size of -inf under the Softplus is a step of zero: the token
+ * leaves the state alone.
  * Conventions and errors as for the operators above, KDA_ERR_SHAPE also for
  * G not dividing H.
  */
