@@ -430,6 +430,8 @@ def _rows(t, name, lead, inner):
         raise ValueError(f"{name} must be {list(lead + inner)}, got {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
+    if t.is_contiguous():
+        return t.data_ptr(), math.prod(inner)
     st, n = t.stride(), 1
     for size, stride in zip(reversed(inner), reversed(st[len(lead):])):
         if size != 1 and stride != n:
@@ -457,7 +459,9 @@ def _dense(t, name, shape, dtype):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return _ptr(t)
+    if not (t.is_cuda and t.is_contiguous()):
+        return _ptr(t)   # (says which)
+    return t.data_ptr()
 
 
 def _same_device(dev, **tensors):
@@ -581,14 +585,11 @@ def _qk_setup(q, k, cos, sin, pos, pos0, mode, interleaved):
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     rot, n_pos = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
-    _dense(cos, "cos", (n_pos, rot // 2), torch.float32)
-    _dense(sin, "sin", (n_pos, rot // 2), torch.float32)
-    if rot == 0:
-        pos = None
-    _dense(pos, "pos", (B, T), torch.int32)
+    cos = _dense(cos, "cos", (n_pos, rot // 2), torch.float32)
+    sin = _dense(sin, "sin", (n_pos, rot // 2), torch.float32)
+    pos = _dense(pos, "pos", (B, T), torch.int32) if rot else None
     flags = (KDA_QK_RMS if mode == "rms" else 0) | (KDA_QK_INTERLEAVED if interleaved else 0)
-    ptr = lambda t: None if t is None or rot == 0 else t.data_ptr()
-    return (pq, ldq, pk, ldk), (ptr(cos), ptr(sin), ptr(pos), int(pos0), n_pos), (flags, _dtype_code(q), B, T, Hq, Hk, d, rot)
+    return (pq, ldq, pk, ldk), (cos, sin, pos, int(pos0), n_pos), (flags, _dtype_code(q), B, T, Hq, Hk, d, rot)
 
 
 def qk_norm_rope(q, k, wq=None, wk=None, *, cos=None, sin=None, pos=None, pos0=0, mode="l2", interleaved=False, eps=1e-6,
