@@ -584,6 +584,8 @@ def _qk_setup(q, k, cos, sin, pos, pos0, mode, interleaved):
     pk, ldk = (None, 0) if k is None else _rows(k, "k", (B, T), (Hk, d))
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
+    if cos is not None and cos.dim() != 2:
+        raise ValueError(f"cos must be [n_pos, rot/2], got {list(cos.shape)}")
     rot, n_pos = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
     cos = _dense(cos, "cos", (n_pos, rot // 2), torch.float32)
     sin = _dense(sin, "sin", (n_pos, rot // 2), torch.float32)
