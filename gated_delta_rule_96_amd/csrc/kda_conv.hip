@@ -9,14 +9,16 @@
 // token t reads rows t .. t+W-1, and the final state is rows len .. len+W-2.
 //
 // Bound by HBM: every input once, every output once, 2W operations each.
-// One thread owns VE neighbouring channels (one 16-byte access in bf16) of a
-// strip of tokens and walks it with the last W-1 rows in registers, eight
+// One thread owns VE = 4 neighbouring channels (their weights are 16 bytes a
+// channel: with eight channels a thread a wave's weights lie in twice as many
+// cache lines per load) of a strip of tokens and walks it with the last W-1 rows in registers, eight
 // rows' loads in flight; only the W-1 rows before a strip are read twice
 // (from the caches).  All sums in fp32, one rounding to the output type.
-// Measured (bf16): 65536 tokens x 4096 channels 208 us (5.2 TB/s); 8191 packed
-// tokens x 4352 channels 40 us (3.6 TB/s, rows of a wider tensor); gradients of
-// 32768 tokens x 2048 channels from fp32 dy 122 us (4.4 TB/s); a token for 256
-// sequences x 4352 channels 10 us, which is the call's time on the host.
+// Measured (bf16): 65536 tokens x 4096 channels 196 us (5.5 TB/s; with eight
+// channels a thread 207); 8191 packed tokens x 4352 channels 30 us (4.7 TB/s,
+// rows of a wider tensor; 34); gradients of 32768 tokens x 2048 channels from
+// fp32 dy 111 us (4.8 TB/s; 123); a token for 256 sequences x 4352 channels 4.4
+// us (4.0 TB/s), twice that through the Python binding.
 #include "kda_rows.h"
 
 namespace kda {
@@ -24,9 +26,9 @@ namespace kda {
 namespace {
 
 constexpr int kConvThreads = 256;
-// Rows loaded together: forward (64K tokens x 4096 channels: 215 us, four
-// 222), and x and dy rows of the backward (32K x 2048: 125 us; four 127, eight
-// 195).
+// Rows loaded together: forward (64K tokens x 4096 channels: 203 us; four 217,
+// sixteen 220), and x and dy rows of the backward (32K x 2048: 111 us; four 151;
+// one as good, but 98 against 80 for fp32 inputs).
 constexpr int kFwdRows = 8;
 constexpr int kBwdRows = 2;
 
@@ -117,29 +119,38 @@ __global__ __launch_bounds__(kConvThreads) void conv_state_kernel(const ConvArgs
 }
 
 // One token per sequence: y from the state's rows and x, and the state moved
-// on by one row (st may be s0: a thread reads all its rows first).
-template <typename T, int W, int VE>
-__global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs a, unsigned B, unsigned CG) {
+// on by one row (st may be s0: a thread reads all its rows first).  A thread
+// takes one channel, so that a wave's weights are one contiguous piece, of S
+// sequences, whose weights it loads once.
+template <typename T, int W, int S>
+__global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs a, unsigned B) {
   const unsigned id = blockIdx.x * kConvThreads + threadIdx.x;
-  const unsigned n = id / CG;
-  if (n >= B) return;
-  const int c = (int)(id - n * CG) * VE;
-  float r[W][VE], w[W][VE], b[VE], o[VE];
-  const size_t base = (size_t)n * (W - 1) * a.D + c;
+  const unsigned D = (unsigned)a.D, n0 = id / D * S;
+  if (n0 >= B) return;
+  const int c = (int)(id % D);
+  float r[S][W], w[W][1], b[1];
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) Rows<T, VE>::load((const T*)a.s0 + base + (size_t)k * a.D, r[k]);
-  Rows<T, VE>::load((const T*)a.x + (size_t)n * (size_t)a.ldx + c, r[W - 1]);
-  load_taps<W, VE>(a, c, w, b);
+  for (int q = 0; q < S; ++q) {
+    // a sequence past the last re-reads that one and is not stored
+    const size_t n = min(n0 + q, B - 1);
+    const T* s0 = (const T*)a.s0 + n * (W - 1) * D + c;
 #pragma unroll
-  for (int i = 0; i < VE; ++i) {
-    float z = b[i];
-#pragma unroll
-    for (int j = 0; j < W; ++j) z = fmaf(w[j][i], r[j][i], z);
-    o[i] = act_of(z, a.silu);
+    for (int k = 0; k < W - 1; ++k) r[q][k] = to_f32(s0[(size_t)k * D]);
+    r[q][W - 1] = to_f32(((const T*)a.x)[n * (size_t)a.ldx + c]);
   }
-  Rows<T, VE>::store((T*)a.y + (size_t)n * a.D + c, o);
+  load_taps<W, 1>(a, c, w, b);
 #pragma unroll
-  for (int k = 0; k < W - 1; ++k) Rows<T, VE>::store((T*)a.st + base + (size_t)k * a.D, r[k + 1]);
+  for (int q = 0; q < S; ++q) {
+    const size_t n = n0 + q;
+    if (n >= B) return;
+    float z = b[0];
+#pragma unroll
+    for (int j = 0; j < W; ++j) z = fmaf(w[j][0], r[q][j], z);
+    ((T*)a.y)[n * D + c] = from_f32<T>(act_of(z, a.silu));
+    T* st = (T*)a.st + n * (W - 1) * D + c;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) st[(size_t)k * D] = from_f32<T>(r[q][k + 1]);
+  }
 }
 
 // Gradients.  With dz = dy act'(z) (z recomputed from x), row e of [state,
@@ -269,21 +280,20 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
   }
 }
 
-// Eight channels a thread where every row starts on 16 bytes (channels and
-// the token stride a multiple of 8, x aligned); one channel otherwise (16384
-// tokens x 4096 channels of a tensor 8 wider: 52 us; 13 wider: 65).
-int vec_of(const ConvArgs& a) {
-  return a.D % 8 == 0 && a.ldx % 8 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 ? 8 : 1;
+// Four channels a thread where every row starts on the size of four elements
+// (channels and the token stride a multiple of 4, x aligned); one channel
+// otherwise (16384 tokens x 4096 channels: 45 us; of rows 13 elements wider: 63).
+int vec_of(const ConvArgs& a, int is_bf16) {
+  return a.D % 4 == 0 && a.ldx % 4 == 0 && reinterpret_cast<uintptr_t>(a.x) % (is_bf16 ? 8u : 16u) == 0 ? 4 : 1;
 }
 
 // Tokens of a strip: long strips re-read fewer rows, short ones keep the card
-// busy on short inputs.  At most 64 (64K tokens x 4096 channels: 215 us, 32
-// 231, 128 215; gradients of 32K x 2048: 127 us, 32 134, 128 127), fewer below
-// 256K threads (8191 packed tokens x 4352 channels: 34.6 us; 128K threads 37.9,
-// 512K 40.1) or, backward, 128K (4096 tokens x 2048: 28.7 us; 64K threads 32.1,
-// 256K 29.1).
+// busy on short inputs.  Forward at most 128 (64K tokens x 4096 channels: 196
+// us, 64 203), fewer below 256K threads (16384 x 4096: 45 us; 512K 53; 128K
+// is as good).  Backward at most 64 (32K x 2048: 111 us; 32 116, 128 150), fewer
+// below 128K threads (4096 x 4352: 40 us; 64K 60, 256K 44).
 int fwd_strip(long long rows, int cg) {
-  int part = 64;
+  int part = 128;
   while (part > kFwdRows && rows * cg / part < 256LL * 1024) part >>= 1;
   return part;
 }
@@ -318,16 +328,24 @@ hipError_t state_go(const ConvArgs& a, const SeqTab& s, hipStream_t st) {
                      st, a, s, CG);
   return hipGetLastError();
 }
-template <typename T, int VE>
+// Sequences of a token step's thread: more where enough threads are left (256
+// x 4352 channels: 4.4 us; one sequence 4.9, four 4.45; 1024 x 4352: four 11.6,
+// two 12.8, one 14.3; 64 x 4352: one 2.5, two 2.6).
+template <typename T, int W>
 hipError_t step_go(const ConvArgs& a, int B, hipStream_t st) {
-  const unsigned CG = (unsigned)(a.D / VE);
-  const unsigned long long n = (unsigned long long)B * CG;
-  if (n > 0x7fffffffULL) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)((n + kConvThreads - 1) / kConvThreads));
-  if (a.W == 2) hipLaunchKernelGGL((conv_step_kernel<T, 2, VE>), grid, dim3(kConvThreads), 0, st, a, (unsigned)B, CG);
-  else if (a.W == 3) hipLaunchKernelGGL((conv_step_kernel<T, 3, VE>), grid, dim3(kConvThreads), 0, st, a, (unsigned)B, CG);
-  else hipLaunchKernelGGL((conv_step_kernel<T, 4, VE>), grid, dim3(kConvThreads), 0, st, a, (unsigned)B, CG);
+  const long long all = (long long)B * a.D;
+  const int S = all < (1 << 19) ? 1 : all < (1 << 21) ? 2 : 4;
+  const long long n = ((long long)B + S - 1) / S * a.D;
+  if (n > 0x7fffffffLL) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)((n + kConvThreads - 1) / kConvThreads)), th(kConvThreads);
+  if (S == 1) hipLaunchKernelGGL((conv_step_kernel<T, W, 1>), grid, th, 0, st, a, (unsigned)B);
+  else if (S == 2) hipLaunchKernelGGL((conv_step_kernel<T, W, 2>), grid, th, 0, st, a, (unsigned)B);
+  else hipLaunchKernelGGL((conv_step_kernel<T, W, 4>), grid, th, 0, st, a, (unsigned)B);
   return hipGetLastError();
+}
+template <typename T>
+hipError_t step_type(const ConvArgs& a, int B, hipStream_t st) {
+  return a.W == 2 ? step_go<T, 2>(a, B, st) : a.W == 3 ? step_go<T, 3>(a, B, st) : step_go<T, 4>(a, B, st);
 }
 // Work-groups along the items of a launch (partial rows it writes).
 unsigned bwd_groups(unsigned items, unsigned LC) {
@@ -406,7 +424,7 @@ hipError_t launch_sum_rows(const float* part, size_t nrows, unsigned n0, unsigne
 }
 
 hipError_t launch_conv_fwd(int is_bf16, const ConvArgs& a, const int* cu, int N, int B, int T, hipStream_t st) {
-  const int ve = vec_of(a), part = fwd_strip((long long)B * T, a.D / ve), end = cu ? N : B;
+  const int ve = vec_of(a, is_bf16), part = fwd_strip((long long)B * T, a.D / ve), end = cu ? N : B;
   // a state replaced in place is written by a launch of its own where another
   // strip still has to read the old one
   const bool later = a.st && a.st == a.s0 && T > part;
@@ -419,11 +437,11 @@ hipError_t launch_conv_fwd(int is_bf16, const ConvArgs& a, const int* cu, int N,
       if (s.items < 0) return hipErrorInvalidConfiguration;
       hipError_t e;
       if (pass) {
-        if (is_bf16) e = ve == 8 ? state_go<bf16, 8>(b, s, st) : state_go<bf16, 1>(b, s, st);
-        else e = ve == 8 ? state_go<float, 8>(b, s, st) : state_go<float, 1>(b, s, st);
+        if (is_bf16) e = ve == 4 ? state_go<bf16, 4>(b, s, st) : state_go<bf16, 1>(b, s, st);
+        else e = ve == 4 ? state_go<float, 4>(b, s, st) : state_go<float, 1>(b, s, st);
       } else {
-        if (is_bf16) e = ve == 8 ? fwd_go<bf16, 8>(b, s, st) : fwd_go<bf16, 1>(b, s, st);
-        else e = ve == 8 ? fwd_go<float, 8>(b, s, st) : fwd_go<float, 1>(b, s, st);
+        if (is_bf16) e = ve == 4 ? fwd_go<bf16, 4>(b, s, st) : fwd_go<bf16, 1>(b, s, st);
+        else e = ve == 4 ? fwd_go<float, 4>(b, s, st) : fwd_go<float, 1>(b, s, st);
       }
       if (e != hipSuccess) return e;
     }
@@ -432,15 +450,13 @@ hipError_t launch_conv_fwd(int is_bf16, const ConvArgs& a, const int* cu, int N,
 }
 
 hipError_t launch_conv_step(int is_bf16, const ConvArgs& a, int B, hipStream_t st) {
-  const int ve = vec_of(a);
-  if (is_bf16) return ve == 8 ? step_go<bf16, 8>(a, B, st) : step_go<bf16, 1>(a, B, st);
-  return ve == 8 ? step_go<float, 8>(a, B, st) : step_go<float, 1>(a, B, st);
+  return is_bf16 ? step_type<bf16>(a, B, st) : step_type<float>(a, B, st);
 }
 
 size_t conv_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D, int W) {
   // the larger of the two channel widths' needs: x's stride decides at the call
   size_t most = 0;
-  for (int ve : {8, 1}) {
+  for (int ve : {4, 1}) {
     if (D % ve) continue;
     const int cg = D / ve, part = bwd_strip((long long)B * T, cg);
     const size_t items = (is_packed ? (size_t)T / part + N : (size_t)B * (((size_t)T + part - 1) / part));
@@ -454,7 +470,7 @@ size_t conv_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D, int W
 }
 
 hipError_t launch_conv_bwd(int is_bf16, const ConvBwdArgs& a, const int* cu, int N, int B, int T, hipStream_t st) {
-  const int ve = vec_of(a.f), part = bwd_strip((long long)B * T, a.f.D / ve), end = cu ? N : B;
+  const int ve = vec_of(a.f, is_bf16), part = bwd_strip((long long)B * T, a.f.D / ve), end = cu ? N : B;
   size_t rows = 0;
   for (int n = 0; n < end;) {
     SeqTab s;
@@ -464,9 +480,9 @@ hipError_t launch_conv_bwd(int is_bf16, const ConvBwdArgs& a, const int* cu, int
     b.part = a.part + rows * (size_t)(a.f.W + 1) * a.f.D;
     unsigned r = 0;
     hipError_t e;
-    if (!is_bf16) e = ve == 8 ? bwd_go<float, float, 8>(b, s, &r, st) : bwd_go<float, float, 1>(b, s, &r, st);
-    else if (a.dy_bf16) e = ve == 8 ? bwd_go<bf16, bf16, 8>(b, s, &r, st) : bwd_go<bf16, bf16, 1>(b, s, &r, st);
-    else e = ve == 8 ? bwd_go<bf16, float, 8>(b, s, &r, st) : bwd_go<bf16, float, 1>(b, s, &r, st);
+    if (!is_bf16) e = ve == 4 ? bwd_go<float, float, 4>(b, s, &r, st) : bwd_go<float, float, 1>(b, s, &r, st);
+    else if (a.dy_bf16) e = ve == 4 ? bwd_go<bf16, bf16, 4>(b, s, &r, st) : bwd_go<bf16, bf16, 1>(b, s, &r, st);
+    else e = ve == 4 ? bwd_go<bf16, float, 4>(b, s, &r, st) : bwd_go<bf16, float, 1>(b, s, &r, st);
     if (e != hipSuccess) return e;
     rows += r;
   }
