@@ -451,10 +451,13 @@ def _rows(t, name, lead, inner):
     return t.data_ptr(), ld
 
 
-def _dense(t, name, shape, dtype):
-    """Pointer of a contiguous tensor of this shape and type (None passes)."""
+def _dense(t, name, shape, dtype, dev=None):
+    """Pointer of a contiguous tensor of this shape and type, and on device dev
+    if given (None passes)."""
     if t is None:
         return None
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -491,11 +494,11 @@ def _packed(cu_seqlens, B, T):
     return arr, n
 
 
-def _given(out, shape, dtype, dev, name):
-    """`out` checked, or a new tensor."""
+def _given(out, like, name):
+    """`out` checked, or a new tensor of like's shape, type and device."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _dense(out, name, shape, dtype)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
+    _dense(out, name, like.shape, like.dtype, like.device)
     return out
 
 
@@ -520,7 +523,7 @@ def conv_fwd(x, w, bias=None, s0=None, *, silu=True, cu_seqlens=None, final_stat
     px, ld = _rows(x, "x", (B, T), (D,))
     arr, N = _packed(cu_seqlens, B, T)
     _same_device(x.device, w=w, bias=bias, s0=s0, st=st, out=out)
-    y = _given(out, (B, T, D), x.dtype, x.device, "out")
+    y = _given(out, x, "out")
     if final_state and st is None:
         st = torch.empty((N, W - 1, D), dtype=x.dtype, device=x.device)
     _call(x.device, "kda_conv_fwd", px, ld, _dense(w, "w", (D, W), torch.float32), _dense(bias, "bias", (D,), torch.float32),
@@ -536,11 +539,11 @@ def conv_step(x, w, bias, state, *, silu=True, state_out=None, out=None):
     B, D = x.shape
     W = w.shape[-1]
     px, ld = _rows(x, "x", (B,), (D,))
-    _same_device(x.device, w=w, bias=bias, state=state, state_out=state_out, out=out)
-    y = _given(out, (B, D), x.dtype, x.device, "out")
+    dev, st = x.device, (B, W - 1, D)
+    y = _given(out, x, "out")
     so = state if state_out is None else state_out
-    _call(x.device, "kda_conv_step", px, ld, _dense(w, "w", (D, W), torch.float32), _dense(bias, "bias", (D,), torch.float32),
-          _dense(state, "state", (B, W - 1, D), x.dtype), _dense(so, "state_out", (B, W - 1, D), x.dtype), y.data_ptr(),
+    _call(dev, "kda_conv_step", px, ld, _dense(w, "w", (D, W), torch.float32, dev), _dense(bias, "bias", (D,), torch.float32, dev),
+          _dense(state, "state", st, x.dtype, dev), _dense(so, "state_out", st, x.dtype, dev), y.data_ptr(),
           KDA_CONV_SILU if silu else 0, _dtype_code(x), B, D, W)
     return y
 
@@ -587,9 +590,11 @@ def _qk_setup(q, k, cos, sin, pos, pos0, mode, interleaved):
     if cos is not None and cos.dim() != 2:
         raise ValueError(f"cos must be [n_pos, rot/2], got {list(cos.shape)}")
     rot, n_pos = (0, 0) if cos is None else (2 * cos.shape[1], cos.shape[0])
-    cos = _dense(cos, "cos", (n_pos, rot // 2), torch.float32)
-    sin = _dense(sin, "sin", (n_pos, rot // 2), torch.float32)
-    pos = _dense(pos, "pos", (B, T), torch.int32) if rot else None
+    dev = q.device
+    _same_device(dev, k=k)
+    cos = _dense(cos, "cos", (n_pos, rot // 2), torch.float32, dev)
+    sin = _dense(sin, "sin", (n_pos, rot // 2), torch.float32, dev)
+    pos = _dense(pos, "pos", (B, T), torch.int32, dev) if rot else None
     flags = (KDA_QK_RMS if mode == "rms" else 0) | (KDA_QK_INTERLEAVED if interleaved else 0)
     return (pq, ldq, pk, ldk), (cos, sin, pos, int(pos0), n_pos), (flags, _dtype_code(q), B, T, Hq, Hk, d, rot)
 
@@ -606,12 +611,11 @@ def qk_norm_rope(q, k, wq=None, wk=None, *, cos=None, sin=None, pos=None, pos0=0
     to write to, which may be contiguous q and k themselves."""
     rows, table, sizes = _qk_setup(q, k, cos, sin, pos, pos0, mode, interleaved)
     _, _, B, T, Hq, Hk, d, _ = sizes
-    _same_device(q.device, k=k, wq=wq, wk=wk, cos=cos, sin=sin, pos=pos)
+    dev = q.device
     qo, ko = (None, None) if out is None else out
-    qo = _given(qo, (B, T, Hq, d), q.dtype, q.device, "out[0]")
-    ko = None if k is None else _given(ko, (B, T, Hk, d), q.dtype, q.device, "out[1]")
-    _same_device(q.device, qo=qo, ko=ko)
-    _call(q.device, "kda_qk_norm_rope", *rows, _dense(wq, "wq", (d,), torch.float32), _dense(wk, "wk", (d,), torch.float32), *table,
+    qo = _given(qo, q, "out[0]")
+    ko = None if k is None else _given(ko, k, "out[1]")
+    _call(dev, "kda_qk_norm_rope", *rows, _dense(wq, "wq", (d,), torch.float32, dev), _dense(wk, "wk", (d,), torch.float32, dev), *table,
           float(eps), qo.data_ptr(), None if ko is None else ko.data_ptr(), *sizes)
     return qo, ko
 
@@ -634,7 +638,7 @@ def qk_norm_rope_bwd(q, k, dqo, dko, wq=None, wk=None, *, cos=None, sin=None, po
     nbytes = lib().kda_qk_bwd_workspace_bytes(B, T, Hq, Hk, d)
     wanted = out.get("dwq") is not None or out.get("dwk") is not None
     ws = _scratch(workspace, nbytes, dev, "kda_qk_bwd_workspace_bytes") if wanted else None
-    _same_device(dev, k=k, wq=wq, wk=wk, cos=cos, sin=sin, pos=pos, dqo=dqo, dko=dko, workspace=ws, **out)
+    _same_device(dev, wq=wq, wk=wk, dqo=dqo, dko=dko, workspace=ws, **out)
     _call(dev, "kda_qk_norm_rope_bwd", *rows, _dense(wq, "wq", (d,), torch.float32), _dense(wk, "wk", (d,), torch.float32), *table,
           float(eps), _dense(dqo, "dqo", (B, T, Hq, d), dqo.dtype), _dense(dko if k is not None else None, "dko", (B, T, Hk, d), dqo.dtype),
           _dtype_code(dqo), _dense(out["dq"], "dq", (B, T, Hq, d), q.dtype),
@@ -651,8 +655,9 @@ def _ssm_setup(x, dt, A, Bm, Cm, D, dt_bias, lead):
     for n, t in (("dt", dt), ("Bm", Bm), ("Cm", Cm)):
         if t.dtype != x.dtype:
             raise TypeError(f"{n} dtype {t.dtype} != x dtype {x.dtype}")
-    _same_device(x.device, dt=dt, A=A, Bm=Bm, Cm=Cm, D=D, dt_bias=dt_bias)
-    vec = lambda t, n: _dense(t, n, (H,), torch.float32)
+    dev = x.device
+    _same_device(dev, dt=dt, Bm=Bm, Cm=Cm)
+    vec = lambda t, n: _dense(t, n, (H,), torch.float32, dev)
     return (*_rows(x, "x", lead, (H, dv)), *_rows(dt, "dt", lead, (H,)), vec(A, "A"), *_rows(Bm, "Bm", lead, (G, dk)),
             *_rows(Cm, "Cm", lead, (G, dk)), vec(D, "D"), vec(dt_bias, "dt_bias")), G, dk
 
@@ -670,12 +675,12 @@ def ssm_fwd_chunked(x, dt, A, Bm, Cm, h0=None, *, D=None, dt_bias=None, softplus
     args, G, dk = _ssm_setup(x, dt, A, Bm, Cm, D, dt_bias, (B, T))
     arr, N = _packed(cu_seqlens, B, T)
     code, dev, st = _dtype_code(x), x.device, (N, H, dk, dv)
-    y = _given(out, (B, T, H, dv), x.dtype, dev, "out")
+    y = _given(out, x, "out")
     if final_state and ht is None:
         ht = torch.empty(st, dtype=torch.float32, device=dev)
     n = lib().kda_ssm_workspace_bytes(B, T, H, dk, dv, code)
     ws = _scratch(workspace, n, dev, "kda_ssm_workspace_bytes") if n else None
-    _same_device(dev, h0=h0, ht=ht, out=y, workspace=ws)
+    _same_device(dev, h0=h0, ht=ht, workspace=ws)
     _call(dev, "kda_ssm_fwd_chunked", *args, _dense(h0, "h0", st, torch.float32),
           _dense(ht if final_state else None, "ht", st, torch.float32), y.data_ptr(), KDA_SSM_SOFTPLUS if softplus else 0, code, B, T,
           H, G, dk, dv, arr, N, _ptr(ws), 0 if ws is None else ws.numel())
@@ -689,10 +694,10 @@ def ssm_step(x, dt, A, Bm, Cm, state, *, D=None, dt_bias=None, softplus=False, s
     B, H, dv = x.shape
     args, G, dk = _ssm_setup(x, dt, A, Bm, Cm, D, dt_bias, (B,))
     so = state if state_out is None else state_out
-    y = _given(out, (B, H, dv), x.dtype, x.device, "out")
-    _same_device(x.device, state=state, state_out=so, out=y)
-    _call(x.device, "kda_ssm_step", *args, _dense(state, "state", (B, H, dk, dv), torch.float32),
-          _dense(so, "state_out", (B, H, dk, dv), torch.float32), y.data_ptr(), KDA_SSM_SOFTPLUS if softplus else 0, _dtype_code(x), B,
+    y = _given(out, x, "out")
+    dev, st = x.device, (B, H, dk, dv)
+    _call(dev, "kda_ssm_step", *args, _dense(state, "state", st, torch.float32, dev),
+          _dense(so, "state_out", st, torch.float32, dev), y.data_ptr(), KDA_SSM_SOFTPLUS if softplus else 0, _dtype_code(x), B,
           H, G, dk, dv)
     return y
 
