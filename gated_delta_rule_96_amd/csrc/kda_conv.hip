@@ -11,9 +11,9 @@
 // Bound by HBM: every input once, every output once, 2W operations each.
 // One thread owns VE = 4 neighbouring channels (their weights are 16 bytes a
 // channel: with eight channels a thread a wave's weights lie in twice as many
-// cache lines per load) of a strip of tokens and walks it with the last W-1 rows in registers, eight
-// rows' loads in flight; only the W-1 rows before a strip are read twice
-// (from the caches).  All sums in fp32, one rounding to the output type.
+// cache lines per load) of a strip of tokens and walks it with the last W-1
+// rows in registers, eight rows' loads in flight; only the W-1 rows before a
+// strip are read twice (from the caches).  All sums in fp32, one rounding to the output type.
 // Measured (bf16): 65536 tokens x 4096 channels 196 us (5.5 TB/s; with eight
 // channels a thread 207); 8191 packed tokens x 4352 channels 30 us (4.7 TB/s,
 // rows of a wider tensor; 34); gradients of 32768 tokens x 2048 channels from

@@ -17,8 +17,8 @@
 // one token, so a token's table row is read once for all of them.  Rows are
 // in fp32 between the loads and the one rounding at the end.
 // Measured (bf16): 65536 tokens x 64 heads of 128 381 us (5.7 TB/s); gradients
-// of 32768 tokens x 32 heads 213 us (5.0 TB/s); a token for 256 sequences 15 us,
-// which is the call's time on the host.
+// of 32768 tokens x 32 heads 205 us (5.2 TB/s); a token for 256 sequences 5 us
+// (14 through the Python binding).
 #include "kda_rows.h"
 
 namespace kda {

@@ -557,7 +557,8 @@ hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a0, int dk, int dv, const 
 // ---------------------------------------------------------------------------
 // Single token.  Bound by the state, read once and written once: a thread
 // keeps four value columns of DK / RG rows in registers, all rows' loads
-// issued first; the sums over the state channels are joined through LDS.
+// issued first; the sums over the state channels are joined through LDS.  256
+// sequences x 32 heads of 128 x 128: 193 us (5.6 TB/s).
 namespace {
 
 constexpr int kStepThreads = 512;
