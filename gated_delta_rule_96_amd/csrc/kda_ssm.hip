@@ -31,8 +31,8 @@
 // work-groups.
 //
 // Measured (65536 tokens, 32 heads of 128 x 128, bf16): 618 us, 1.8 TB/s of
-// the inputs and outputs and 220 TFLOP/s of the products (kernel by kernel, at
-// the lower clock of a traced run: first pass 244, chaining 12, scan 491).
+// the inputs and outputs and 220 TFLOP/s of the products (traced kernel by
+// kernel: first pass 215, chaining 12, scan 415).
 // Neither rate binds: a chunk's 144 matrix instructions per state wave are 147
 // us of the scan's time at 2 GHz; the rest are their LDS operands, the exact
 // splits, the state's scaling and y's stores of the same four waves, one
@@ -229,8 +229,8 @@ __global__ __launch_bounds__(kSsmThreads) void ssm_chunk_kernel(const SsmArgs a,
 // into LDS, form chunk k + 1's M and chunk k + 2's step sizes, while the back
 // waves take chunk k's products with S, its y and the state's update.  One
 // barrier a chunk; the matrix instructions of one set cover the loads and
-// exponents of the other (64K tokens x 32 heads: this kernel 491 us; 628 with
-// four waves that do one thing after the other).
+// exponents of the other (64K tokens x 32 heads, the first calls of a process:
+// this kernel 491 us; 628 with four waves that do one thing after the other).
 constexpr int kPipeThreads = 2 * kSsmThreads;
 
 template <int DK, int DV>

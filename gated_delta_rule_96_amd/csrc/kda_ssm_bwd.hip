@@ -25,9 +25,9 @@
 //
 // A state and its gradient per chunk and head, written and read once (2 dk dv 4
 // bytes each way), are the bulk of the traffic beside the inputs.
-// Measured (4 x 8192 tokens, 16 heads of 128 x 128, one group, bf16): 897 us:
-// this kernel 529, sweeps that keep states 137 + 136 (0.54 GB written each, 3.9
-// TB/s), own sums of the parts 67 + 65, chaining 24, last sums 5.  This kernel
+// Measured (4 x 8192 tokens, 16 heads of 128 x 128, one group, bf16): 900 us:
+// this kernel 510, sweeps that keep states 130 + 131 (0.54 GB written each, 4.1
+// TB/s), own sums of the parts 59 + 62, chaining 23, last sums 5.  This kernel
 // reads 1.1 GB of states (2.1 TB/s); it is bound by waits: for the states,
 // which the registers only allow to be fetched two slabs of 32 columns ahead,
 // and at the four barriers of a head.

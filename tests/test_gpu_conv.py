@@ -133,6 +133,23 @@ def test_conv_step_continues_the_prompt(dtype, B, D, W, pad):
     assert np.array_equal(f64(state), st_ref)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,D,pad", [(64, 4352, 0), (255, 2061, 3), (257, 4352, 4128), (601, 3999, 1), (1, 40000, 0)])
+def test_conv_step_is_a_prompt_of_one_token(dtype, B, D, pad):
+    # from few channels and sequences to as many as a thread takes four sequences for
+    say(f"conv step {dtype} B={B} D={D} pad={pad}")
+    torch.manual_seed(18)
+    x = torch.randn(B, D + pad, device="cuda").to(dtype)[:, :D]
+    w, bias, state = torch.randn(D, 4, device="cuda"), torch.randn(D, device="cuda"), torch.randn(B, 3, D, device="cuda").to(dtype)
+    y, st = kda.conv_fwd(x[:, None], w, bias, state)
+    nxt = torch.full_like(state, float("nan"))
+    kept = state.clone()
+    got = kda.conv_step(x, w, bias, state, state_out=nxt)
+    assert torch.equal(got, y[:, 0]) and torch.equal(nxt, st) and torch.equal(state, kept)
+    again = kda.conv_step(x, w, bias, state)
+    assert torch.equal(again, got) and torch.equal(state, st)
+
+
 def grads_case(c, lens, silu, dst):
     cu, w, b = cuts(lens), f64(c["w"]), f64(c["bias"])
     W = w.shape[1]
