@@ -9,7 +9,7 @@ namespace kda {
 
 // N consecutive elements of type T as fp32, and back (RNE).  N = 8 or 4: one
 // or two 16-byte (or one 8-byte) accesses, the pointer aligned accordingly;
-// N = 1: one element.
+// N = 1: one element.  (Eight are read as fp32 only.)
 template <typename T, int N> struct Rows;
 template <typename T> struct Rows<T, 1> {
   static __device__ __forceinline__ void load(const T* p, float (&x)[1]) { x[0] = to_f32(*p); }
@@ -26,11 +26,6 @@ template <typename T> struct Rows<T, 4> {
   }
 };
 template <> struct Rows<bf16, 8> {
-  static __device__ __forceinline__ void load(const bf16* p, float (&x)[8]) {
-    const bf16x8 v = *reinterpret_cast<const bf16x8*>(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (float)v[i];
-  }
   static __device__ __forceinline__ void store(bf16* p, const float (&x)[8]) {
     bf16x8 v;
 #pragma unroll
