@@ -16,6 +16,8 @@ using kda::valid_dtype;
 namespace {
 
 constexpr int kMaxT = 1 << 30;
+// Heads are numbered in 32 bits, up to a wave's 32 beyond the last one.
+constexpr int kMaxHeads = 1 << 24;
 
 // A span of memory an argument covers.
 struct Span {
@@ -132,7 +134,7 @@ int check_qk(const void* q, long long ldq, const void* k, long long ldk, const f
              const float* sin, const int* pos, int pos0, int n_pos, float eps, int flags, int dtype, int B, int T, int Hq, int Hk,
              int d, int rot) {
   if (!valid_dtype(dtype)) return KDA_ERR_DTYPE;
-  if (B <= 0 || T <= 0 || T > kMaxT || Hq <= 0 || Hk < 0 || d <= 0 || rot < 0 || (flags & ~(KDA_QK_RMS | KDA_QK_INTERLEAVED)) ||
+  if (B <= 0 || T <= 0 || T > kMaxT || Hq <= 0 || Hq > kMaxHeads || Hk < 0 || Hk > kMaxHeads || d <= 0 || rot < 0 || (flags & ~(KDA_QK_RMS | KDA_QK_INTERLEAVED)) ||
       !(eps >= 0.f) || !size_ok(B, T, (long long)Hq + Hk, 8LL * d) || (long long)B * T > (1LL << 40))
     return KDA_ERR_SHAPE;
   if (d % 8 || d > 512 || rot % 8 || rot > d) return KDA_ERR_UNSUPPORTED;
@@ -197,7 +199,9 @@ int kda_qk_norm_rope(const void* q, long long ldq, const void* k, long long ldk,
 }
 
 size_t kda_qk_bwd_workspace_bytes(int B, int T, int Hq, int Hk, int d) {
-  if (B <= 0 || T <= 0 || T > kMaxT || Hq <= 0 || Hk < 0 || d <= 0 || d % 8 || d > 512 || (long long)B * T > (1LL << 40)) return 0;
+  if (B <= 0 || T <= 0 || T > kMaxT || Hq <= 0 || Hq > kMaxHeads || Hk < 0 || Hk > kMaxHeads || d <= 0 || d % 8 || d > 512 ||
+      !size_ok(B, T, (long long)Hq + Hk, 8LL * d) || (long long)B * T > (1LL << 40))
+    return 0;
   return kda::qk_bwd_workspace_bytes((long long)B * T, Hq, Hk, d);
 }
 

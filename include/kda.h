@@ -435,10 +435,10 @@ int kda_conv_bwd(const void* x, long long ldx, const float* w, const float* bias
  *   the first rot channels (a multiple of 8, 0..d) turn pairwise by the
  *   token's angles: (a,b) -> (a cos - b sin, b cos + a sin), pairs (i,
  *   i+rot/2), or neighbours (2i,2i+1) with flags & KDA_QK_INTERLEAVED.
- * q: rows [B,T,Hq,d], k: rows [B,T,Hk,d] (Hk = 0: no keys, k NULL), token
- * strides of 16 bytes' multiples.  cos, sin [n_pos, rot/2] fp32 (ignored for
- * rot = 0).  pos [B,T] int32 on the device, or NULL: token t of every
- * sequence is at pos0 + t.  A position outside [0, n_pos) reads nothing and
+ * q: rows [B,T,Hq,d], k: rows [B,T,Hk,d] (Hk = 0: no keys, k NULL; at most
+ * 2^24 heads each), token strides of 16 bytes' multiples.  cos, sin [n_pos,
+ * rot/2] fp32 (ignored for rot = 0).  pos [B,T] int32 on the device, or NULL:
+ * token t of every sequence is at pos0 + t.  A position outside [0, n_pos) reads nothing and
  * makes the rotated channels NaN.  q_out [B,T,Hq,d] and k_out of dtype may
  * be q and k themselves where those are contiguous.
  * With the sum norm, w NULL and rot 0 it is the row normalisation

@@ -172,3 +172,15 @@ def test_ssm_bwd_workspace_bytes():
     assert f(1, 640, 2, 1, 64, 64, 1, 50) >= f(1, 640, 2, 1, 64, 64, 1, 0)
     for bad in ((0, 1, 2, 1, 64, 64, 1, 0), (1, 1, 2, 3, 64, 64, 1, 0), (1, 1, 2, 1, 32, 64, 1, 0), (1, 1, 2, 1, 64, 64, 2, 0), (2, 1, 2, 1, 64, 64, 1, 3)):
         assert f(*bad) == 0
+
+
+@pytest.mark.parametrize("kw", [dict(Hq=(1 << 31) - 1, Hk=0, k=None, ko=None, d=8, rot=0), dict(Hq=1, Hk=(1 << 31) - 1, d=8, rot=0),
+                                dict(Hq=(1 << 24) + 1, Hk=0, k=None, ko=None, d=8, rot=0)])
+def test_qk_refuses_more_heads_than_it_numbers(kw):
+    # heads are numbered in 32 bits, up to a wave's 32 beyond the last one
+    one = dict(B=1, T=1, ldq=8 * kw["Hq"], ldk=8 * kw["Hk"], **kw)
+    assert call("kda_qk_norm_rope", QK, QK, **one) == 2
+    back = dict(one, dk=one.get("ko", QBWD["dk"]), dko=None if kw["Hk"] == 0 else QBWD["dko"])
+    back.pop("ko", None)
+    assert call("kda_qk_norm_rope_bwd", QBWD, QBWD, **back) == 2
+    assert kda.lib().kda_qk_bwd_workspace_bytes(1, 1, kw["Hq"], kw["Hk"], 8) == 0
