@@ -311,9 +311,7 @@ unsigned pow2_lanes(unsigned cg) {
 template <typename T, int VE>
 hipError_t fwd_go(const ConvArgs& a, const SeqTab& s, hipStream_t st) {
   const unsigned CG = (unsigned)(a.D / VE);
-  const unsigned long long n = (unsigned long long)s.items * CG;
-  if (n > 0x7fffffffULL) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)((n + kConvThreads - 1) / kConvThreads));
+  const dim3 grid(((unsigned)s.items * CG + kConvThreads - 1) / kConvThreads);
   if (a.W == 2) hipLaunchKernelGGL((conv_fwd_kernel<T, 2, VE>), grid, dim3(kConvThreads), 0, st, a, s, CG);
   else if (a.W == 3) hipLaunchKernelGGL((conv_fwd_kernel<T, 3, VE>), grid, dim3(kConvThreads), 0, st, a, s, CG);
   else hipLaunchKernelGGL((conv_fwd_kernel<T, 4, VE>), grid, dim3(kConvThreads), 0, st, a, s, CG);
@@ -322,10 +320,8 @@ hipError_t fwd_go(const ConvArgs& a, const SeqTab& s, hipStream_t st) {
 template <typename T, int VE>
 hipError_t state_go(const ConvArgs& a, const SeqTab& s, hipStream_t st) {
   const unsigned CG = (unsigned)(a.D / VE);
-  const unsigned long long n = (unsigned long long)s.items * CG;
-  if (n > 0x7fffffffULL) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((conv_state_kernel<T, VE>), dim3((unsigned)((n + kConvThreads - 1) / kConvThreads)), dim3(kConvThreads), 0,
-                     st, a, s, CG);
+  const dim3 grid(((unsigned)s.items * CG + kConvThreads - 1) / kConvThreads);
+  hipLaunchKernelGGL((conv_state_kernel<T, VE>), grid, dim3(kConvThreads), 0, st, a, s, CG);
   return hipGetLastError();
 }
 // Sequences of a token step's thread: more where enough threads are left (256
@@ -356,7 +352,6 @@ template <typename T, typename TG, int VE>
 hipError_t bwd_go(const ConvBwdArgs& a, const SeqTab& s, unsigned* rows, hipStream_t st) {
   const unsigned CG = (unsigned)(a.f.D / VE), LC = pow2_lanes(CG), cb = (CG + LC - 1) / LC;
   const unsigned ng = bwd_groups((unsigned)s.items, LC);
-  if ((unsigned long long)ng * cb > 0x7fffffffULL) return hipErrorInvalidConfiguration;
   const dim3 grid(ng * cb);
   if (a.f.W == 2) hipLaunchKernelGGL((conv_bwd_kernel<T, TG, 2, VE>), grid, dim3(kConvThreads), 0, st, a, s, CG, LC, cb);
   else if (a.f.W == 3) hipLaunchKernelGGL((conv_bwd_kernel<T, TG, 3, VE>), grid, dim3(kConvThreads), 0, st, a, s, CG, LC, cb);
@@ -375,8 +370,7 @@ int make_seq_tab(SeqTab& s, const int* cu, int N, int n0, int B, int T, int part
   if (!cu) {
     s.n = 0;
     s.parts = (T + part - 1) / part;
-    const long long items = (long long)B * s.parts;
-    s.items = items > 0x7fffffffLL ? -1 : (int)items;
+    s.items = B * s.parts;
     return B;
   }
   s.n = N - n0 < kMaxVarSeq ? N - n0 : kMaxVarSeq;
@@ -391,14 +385,29 @@ int make_seq_tab(SeqTab& s, const int* cu, int N, int n0, int B, int T, int part
     items += len > 0 ? (len + part - 1) / part : 1;
     chunks += len > 0 ? (len + kSeqChunk - 1) / kSeqChunk : 1;
   }
-  s.items = items > 0x7fffffffLL ? -1 : (int)items;
+  s.items = (int)items;
   return n0 + s.n;
 }
 
+bool seq_tabs_fit(const int* cu, int N, int B, int T, int part, long long most) {
+  if (!cu) return (long long)B * ((T + part - 1) / part) <= most;
+  if ((long long)T / part + N <= most) return true;
+  for (int n = 0; n < N;) {
+    long long items = 0;
+    for (const int end = N - n < kMaxVarSeq ? N : n + kMaxVarSeq; n < end; ++n) {
+      const long long len = cu[n + 1] - cu[n];
+      items += len > 0 ? (len + part - 1) / part : 1;
+    }
+    if (items > most) return false;
+  }
+  return true;
+}
+
+constexpr int kSumThreads = 1024;
 // out[c]: sum of column c of part [nrows][n0 + n1 + n2] over its rows, the
 // columns in three outputs.  A work-group takes 64 columns; its 16 waves take
 // every 16th row and are joined through LDS, always in the same order.
-__global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict__ part, size_t nrows, unsigned n0, unsigned n1,
+__global__ __launch_bounds__(kSumThreads) void sum_rows_kernel(const float* __restrict__ part, size_t nrows, unsigned n0, unsigned n1,
                                                         unsigned n2, float* __restrict__ out0, float* __restrict__ out1,
                                                         float* __restrict__ out2) {
   __shared__ double red[16][64];
@@ -419,12 +428,13 @@ __global__ __launch_bounds__(1024) void sum_rows_kernel(const float* __restrict_
 
 hipError_t launch_sum_rows(const float* part, size_t nrows, unsigned n0, unsigned n1, unsigned n2, float* out0, float* out1,
                            float* out2, hipStream_t st) {
-  hipLaunchKernelGGL(sum_rows_kernel, dim3((n0 + n1 + n2 + 63) / 64), dim3(1024), 0, st, part, nrows, n0, n1, n2, out0, out1, out2);
+  hipLaunchKernelGGL(sum_rows_kernel, dim3((n0 + n1 + n2 + 63) / 64), dim3(kSumThreads), 0, st, part, nrows, n0, n1, n2, out0, out1, out2);
   return hipGetLastError();
 }
 
 hipError_t launch_conv_fwd(int is_bf16, const ConvArgs& a, const int* cu, int N, int B, int T, hipStream_t st) {
   const int ve = vec_of(a, is_bf16), part = fwd_strip((long long)B * T, a.D / ve), end = cu ? N : B;
+  if (!seq_tabs_fit(cu, N, B, T, part, 0x7fffffffLL / (a.D / ve))) return hipErrorInvalidConfiguration;
   // a state replaced in place is written by a launch of its own where another
   // strip still has to read the old one
   const bool later = a.st && a.st == a.s0 && T > part;
@@ -433,8 +443,7 @@ hipError_t launch_conv_fwd(int is_bf16, const ConvArgs& a, const int* cu, int N,
     if (later && pass == 0) b.st = nullptr;
     for (int n = 0; n < end;) {
       SeqTab s;
-      n = make_seq_tab(s, cu, N, n, B, T, pass ? (T > 0 ? T : 1) : part);
-      if (s.items < 0) return hipErrorInvalidConfiguration;
+      n = make_seq_tab(s, cu, N, n, B, T, pass ? T : part);
       hipError_t e;
       if (pass) {
         if (is_bf16) e = ve == 4 ? state_go<bf16, 4>(b, s, st) : state_go<bf16, 1>(b, s, st);
@@ -471,11 +480,14 @@ size_t conv_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D, int W
 
 hipError_t launch_conv_bwd(int is_bf16, const ConvBwdArgs& a, const int* cu, int N, int B, int T, hipStream_t st) {
   const int ve = vec_of(a.f, is_bf16), part = bwd_strip((long long)B * T, a.f.D / ve), end = cu ? N : B;
+  const unsigned CG = (unsigned)(a.f.D / ve), LC = pow2_lanes(CG), cb = (CG + LC - 1) / LC;
+  if (!seq_tabs_fit(cu, N, B, T, part, max_groups(kConvThreads) / cb * (64 / LC * (kConvThreads / 64))) ||
+      ((long long)a.f.D * (a.f.W + 1) + 63) / 64 > max_groups(kSumThreads))
+    return hipErrorInvalidConfiguration;
   size_t rows = 0;
   for (int n = 0; n < end;) {
     SeqTab s;
     n = make_seq_tab(s, cu, N, n, B, T, part);
-    if (s.items < 0) return hipErrorInvalidConfiguration;
     ConvBwdArgs b = a;
     b.part = a.part + rows * (size_t)(a.f.W + 1) * a.f.D;
     unsigned r = 0;

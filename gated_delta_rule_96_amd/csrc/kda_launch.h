@@ -123,8 +123,13 @@ struct SeqTab {
 // The table of sequences n0 .. of a call, cut into parts of `part` tokens:
 // B sequences of T (cu == nullptr, one launch), or N packed ones from n0 on
 // (as many as one launch carries).  Returns the first sequence not covered.
-// items < 0: more items than a launch can number.
 int make_seq_tab(SeqTab& s, const int* cu, int N, int n0, int B, int T, int part);
+// Whether none of a call's tables has more than `most` items.
+bool seq_tabs_fit(const int* cu, int N, int B, int T, int part, long long most);
+// Work-groups of `threads` that one launch may have: a launch of 2^32 threads
+// or more runs only a part of them, without an error.  Sizes beyond it are
+// hipErrorInvalidConfiguration before a call's first launch.
+constexpr long long max_groups(int threads) { return 0xffffffffLL / threads; }
 
 // out[0][c], then out[1], out[2]: column sums of part [nrows][n0 + n1 + n2], in
 // a fixed order (any output may be null).

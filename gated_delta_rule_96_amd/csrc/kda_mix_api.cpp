@@ -51,9 +51,12 @@ int check_cu(const int* cu, int N, int B, int T) {
   return KDA_OK;
 }
 
-int hip_status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
+// (hipErrorInvalidConfiguration: sizes beyond a launch's, see max_groups)
+int hip_status(hipError_t e) {
+  return e == hipSuccess ? KDA_OK : e == hipErrorInvalidConfiguration ? KDA_ERR_SHAPE : KDA_ERR_HIP;
+}
 
-// Sizes and strides of the convolution's x; `N`: sequences.
+// Sizes and strides of the convolution's x.
 int check_conv(const void* x, long long ldx, const float* w, const float* bias, int flags, int dtype, int B, int T, int D, int W) {
   if (!valid_dtype(dtype)) return KDA_ERR_DTYPE;
   if (B <= 0 || T <= 0 || T > kMaxT || D <= 0 || ldx < D || (flags & ~KDA_CONV_SILU) || !size_ok(B, T, ldx, 8))

@@ -136,10 +136,10 @@ __device__ __forceinline__ Heads task_heads(long long task, unsigned per, unsign
 }
 
 template <typename T, int L, bool kInter>
-__global__ __launch_bounds__(kQkThreads) void qk_fwd_kernel(const QkArgs a, unsigned per, unsigned tq, long long tasks) {
+__global__ __launch_bounds__(kQkThreads) void qk_fwd_kernel(const QkArgs a, unsigned per, unsigned tq, long long first, long long tasks) {
   constexpr int G = 64 / L, NH = G * kQkRows;
   const int lane = threadIdx.x & 63, c = lane & (L - 1), grp = lane / L;
-  const long long task = (long long)blockIdx.x * (kQkThreads / 64) + (threadIdx.x >> 6);
+  const long long task = first + (long long)blockIdx.x * (kQkThreads / 64) + (threadIdx.x >> 6);
   if (task >= tasks) return;
   const Heads hs = task_heads(task, per, tq, NH);
   const LanePlace p = lane_place<kInter>(a, c);
@@ -290,16 +290,20 @@ unsigned bwd_groups(long long tasks) {
 template <typename T, bool kInter>
 hipError_t fwd_go(const QkArgs& a, hipStream_t st) {
   const Tasks t = qk_tasks(a.tokens, a.H[0], a.H[1], a.d, kQkRows);
-  const long long blocks = (t.n + kQkThreads / 64 - 1) / (kQkThreads / 64);
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)blocks), th(kQkThreads);
-  switch (row_lanes(a.d)) {
-    case 8: hipLaunchKernelGGL((qk_fwd_kernel<T, 8, kInter>), grid, th, 0, st, a, t.per, t.tq, t.n); break;
-    case 16: hipLaunchKernelGGL((qk_fwd_kernel<T, 16, kInter>), grid, th, 0, st, a, t.per, t.tq, t.n); break;
-    case 32: hipLaunchKernelGGL((qk_fwd_kernel<T, 32, kInter>), grid, th, 0, st, a, t.per, t.tq, t.n); break;
-    default: hipLaunchKernelGGL((qk_fwd_kernel<T, 64, kInter>), grid, th, 0, st, a, t.per, t.tq, t.n); break;
+  constexpr int kWaves = kQkThreads / 64;
+  for (long long first = 0; first < t.n; first += max_groups(kQkThreads) * kWaves) {   // (launches of one call)
+    const long long left = (t.n - first + kWaves - 1) / kWaves;
+    const dim3 grid((unsigned)(left < max_groups(kQkThreads) ? left : max_groups(kQkThreads))), th(kQkThreads);
+    switch (row_lanes(a.d)) {
+      case 8: hipLaunchKernelGGL((qk_fwd_kernel<T, 8, kInter>), grid, th, 0, st, a, t.per, t.tq, first, t.n); break;
+      case 16: hipLaunchKernelGGL((qk_fwd_kernel<T, 16, kInter>), grid, th, 0, st, a, t.per, t.tq, first, t.n); break;
+      case 32: hipLaunchKernelGGL((qk_fwd_kernel<T, 32, kInter>), grid, th, 0, st, a, t.per, t.tq, first, t.n); break;
+      default: hipLaunchKernelGGL((qk_fwd_kernel<T, 64, kInter>), grid, th, 0, st, a, t.per, t.tq, first, t.n); break;
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 template <typename T, typename TG, bool kInter>
 hipError_t bwd_go(const QkArgs& a, unsigned groups, hipStream_t st) {

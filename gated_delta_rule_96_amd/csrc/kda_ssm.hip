@@ -457,8 +457,7 @@ __global__ __launch_bounds__(kPipeThreads, 2) void ssm_pipe_kernel(const SsmArgs
 
 template <typename T, int DK, int DV>
 hipError_t fwd_go(const SsmArgs& a, const SeqTab& s, int seqs, bool split, hipStream_t st) {
-  dim3 grid;
-  if (!item_head_grid(s.items, a.H, grid)) return hipErrorInvalidConfiguration;
+  const dim3 grid = item_head_grid(s.items, a.H);
   if (split) {
     SweepArgs w{};
     w.f = a;
@@ -524,6 +523,7 @@ hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a0, int dk, int dv, const 
                           hipStream_t st) {
   const long long tokens = (long long)B * T;
   const int part = ssm_part_of(a0.H, kScanWgs, cu, N, B, T), end = cu ? N : B;
+  if (!seq_tabs_fit(cu, N, B, T, part, most_items(a0.H))) return hipErrorInvalidConfiguration;
   SsmArgs a = a0;
   a.seg = static_cast<float*>(workspace);
   const size_t states = kSubs * ssm_slots(tokens, a.H, kScanWgs) * (size_t)dk * dv;
@@ -533,7 +533,6 @@ hipError_t launch_ssm_fwd(int is_bf16, const SsmArgs& a0, int dk, int dv, const 
     SeqTab s;
     const int n0 = n;
     n = make_seq_tab(s, cu, N, n, B, T, part);
-    if (s.items < 0) return hipErrorInvalidConfiguration;
     const bool split = s.items > n - n0;   // some sequence has more than one part
     hipError_t e;
 #define KDA_SSM_GO(T_, K_, V_) e = fwd_go<T_, K_, V_>(a, s, n - n0, split, st)
@@ -620,6 +619,7 @@ hipError_t step_go(const SsmArgs& a, int dk, int dv, int B, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_ssm_step(int is_bf16, const SsmArgs& a, int dk, int dv, int B, hipStream_t st) {
+  if ((long long)B * a.H > max_groups(kStepThreads)) return hipErrorInvalidConfiguration;
   return is_bf16 ? step_go<bf16>(a, dk, dv, B, st) : step_go<float>(a, dk, dv, B, st);
 }
 

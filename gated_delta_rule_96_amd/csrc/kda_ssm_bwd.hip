@@ -492,7 +492,6 @@ hipError_t bwd_go(const SsmBwdArgs& b, const BwdLayout& L, const int* cu, int N,
     const int n0 = n;
     n = make_seq_tab(s, cu, N, n0, B, Tn, part);
     make_seq_tab(sc, cu, N, n0, B, Tn, kQ);
-    if (s.items < 0 || sc.items < 0) return hipErrorInvalidConfiguration;
     const bool split = s.items > n - n0;
     const size_t at = done * (size_t)b.f.H;
     float* S = reinterpret_cast<float*>(ws + L.S) + at * (DK * DV);
@@ -529,15 +528,14 @@ hipError_t bwd_go(const SsmBwdArgs& b, const BwdLayout& L, const int* cu, int N,
     a.S = S;
     a.dS = dS;
     a.part = reinterpret_cast<float*>(ws + L.part) + at * 3;
-    const long long blocks = (long long)sc.items * b.f.G * a.shares;
-    if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((ssm_bwd_kernel<T, DK, DV>), dim3((unsigned)blocks), dim3(kBwdThreads), 0, st, a, sc);
+    const dim3 grid((unsigned)sc.items * (unsigned)(b.f.G * a.shares));
+    hipLaunchKernelGGL((ssm_bwd_kernel<T, DK, DV>), grid, dim3(kBwdThreads), 0, st, a, sc);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     done += (size_t)sc.items;
   }
   if (a.shares > 1) {
     const size_t n8 = (size_t)tokens * b.f.G * DK / 8;
-    if (2 * n8 / 256 + 1 > 0x7fffffffULL) return hipErrorInvalidConfiguration;
+    // (several shares: fewer than 256 chunks)
     hipLaunchKernelGGL((ssm_shares_kernel<T>), dim3((unsigned)((2 * n8 + 255) / 256)), dim3(256), 0, st, a.dBp, a.dCp, (T*)b.dB, (T*)b.dC,
                        n8, a.shares);
     const hipError_t e = hipGetLastError();
@@ -563,6 +561,8 @@ size_t ssm_bwd_workspace_bytes(int is_packed, int N, int B, int T, int H, int G,
 
 hipError_t launch_ssm_bwd(int is_bf16, const SsmBwdArgs& a, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
                           hipStream_t st) {
+  // parts are longer than chunks, and a chunk has at most one work-group a head
+  if (!seq_tabs_fit(cu, N, B, T, kQ, most_items(a.f.H))) return hipErrorInvalidConfiguration;
   const BwdLayout L = bwd_layout(cu != nullptr, N, B, T, a.f.H, a.f.G, dk, dv);
   char* ws = static_cast<char*>(workspace);
   return is_bf16 ? bwd_dims<bf16>(a, dk, dv, L, cu, N, B, T, ws, st) : bwd_dims<float>(a, dk, dv, L, cu, N, B, T, ws, st);

@@ -486,11 +486,9 @@ __device__ __forceinline__ bool item_head(int items, int H, ItemHead& w) {
   w.h = (int)(id - (unsigned)w.item * (unsigned)H);
   return true;
 }
-inline bool item_head_grid(int items, int H, dim3& grid) {
-  const long long n = ((long long)items * H + 7) / 8 * 8;
-  if (n > 0x7fffffffLL) return false;
-  grid = dim3((unsigned)n);
-  return true;
-}
+inline dim3 item_head_grid(int items, int H) { return dim3(((unsigned)items * (unsigned)H + 7) / 8 * 8); }
+// Items of a launch at most: 512 threads for each (item, head) (scan and
+// gradients, or two sweep work-groups of 256).
+inline long long most_items(int H) { return (max_groups(512) - 7) / H; }
 
 }  // namespace kda

@@ -223,8 +223,7 @@ __global__ __launch_bounds__(256) void ssm_chain_kernel(const SweepArgs a, const
 
 template <typename T, int DK, int DV, bool kRev, bool kKeep, bool kLow>
 hipError_t launch_sweep(const SweepArgs& a, const SeqTab& s, hipStream_t st) {
-  dim3 grid;
-  if (s.items > 0x7fffffff / 2 || !item_head_grid(s.items * (kKeep ? 1 : a.subs), a.f.H, grid)) return hipErrorInvalidConfiguration;
+  const dim3 grid = item_head_grid(s.items * (kKeep ? 1 : a.subs), a.f.H);
   if constexpr (sizeof(T) == 2)
     hipLaunchKernelGGL((ssm_sweep_kernel<DK, DV, kRev, kKeep, kLow>), grid, dim3(kSsmThreads), 0, st, a, s);
   else
@@ -232,10 +231,10 @@ hipError_t launch_sweep(const SweepArgs& a, const SeqTab& s, hipStream_t st) {
   return hipGetLastError();
 }
 inline hipError_t launch_chain(const SweepArgs& a, const SeqTab& s, int seqs, int sd, bool rev, hipStream_t st) {
-  const long long blocks = (long long)seqs * a.f.H * (sd / 4 / 256);
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidConfiguration;
-  if (rev) hipLaunchKernelGGL(ssm_chain_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, st, a, s, sd / 4);
-  else hipLaunchKernelGGL(ssm_chain_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, st, a, s, sd / 4);
+  // (a sequence is cut only where a launch's sequences have fewer than 2^16 heads together)
+  const dim3 grid((unsigned)seqs * (unsigned)a.f.H * (unsigned)(sd / 4 / 256));
+  if (rev) hipLaunchKernelGGL(ssm_chain_kernel<true>, grid, dim3(256), 0, st, a, s, sd / 4);
+  else hipLaunchKernelGGL(ssm_chain_kernel<false>, grid, dim3(256), 0, st, a, s, sd / 4);
   return hipGetLastError();
 }
 

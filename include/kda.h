@@ -384,8 +384,12 @@ int kda_bwd_chunked(const void* q, const void* k, const void* v, const void* g, 
  *     kda_fwd_chunked_varlen (B = 1; empty sequences allowed); NULL: B
  *     sequences of T tokens, N ignored.  States are then [B, ...] instead of
  *     [N, ...].  Up to 128 sequences run in one launch, more in several.
- *   - T at most 2^30.  No call allocates or synchronises; results do not
- *     depend on how the work is split (no atomics).
+ *   - T at most 2^30.  Sizes beyond one launch (2^32 threads) are
+ *     KDA_ERR_SHAPE: the scan with 2^23 (sequence, head) pairs or more, the
+ *     convolution with 2^31 or more sequences x channels, its gradients with
+ *     2^28 or more weights and biases together.
+ *   - No call allocates or synchronises; results do not depend on how the
+ *     work is split (no atomics).
  */
 
 /*

@@ -184,3 +184,29 @@ def test_qk_refuses_more_heads_than_it_numbers(kw):
     back.pop("ko", None)
     assert call("kda_qk_norm_rope_bwd", QBWD, QBWD, **back) == 2
     assert kda.lib().kda_qk_bwd_workspace_bytes(1, 1, kw["Hq"], kw["Hk"], 8) == 0
+
+
+FAR = [(i + 1) << 45 for i in range(14)]   # addresses with room for hundreds of gigabytes
+
+
+def far(base):
+    """The base call with its pointers far apart."""
+    return {n: FAR[A.index(v)] if v in A else v for n, v in base.items()}
+
+
+def test_sizes_beyond_a_launch_are_refused():
+    # a launch of 2^32 threads runs only a part of them: refused as a size,
+    # before anything is enqueued
+    many, none = (1 << 31) - 1, dict(h0=None, ht=None, dk=64, dv=64, H=1, G=1, ldx=64, lddt=1, ldb=64, ldc=64)
+    assert call("kda_conv_fwd", CONV, far(CONV), B=many, T=1, D=3, ldx=3, s0=None, st=None) == 2
+    assert call("kda_conv_step", STEP, far(STEP), B=many, D=9, ldx=9) == 2
+    one = dict(B=1, T=1, D=60_000_000, ldx=60_000_000, s0=None, dst=None, ds0=None, wsb=1 << 44)
+    assert call("kda_conv_bwd", CBWD, far(CBWD), **one) == 2                                         # (the sums of dw)
+    assert call("kda_conv_bwd", CBWD, far(CBWD), **dict(one, B=many, D=7, ldx=7)) == 2
+    assert call("kda_ssm_fwd_chunked", SSM_ORDER, far(SSM), Bn=1 << 23, T=1, **none) == 2
+    assert call("kda_ssm_step", list(SSTEP), far(SSTEP), Bn=1 << 23, **dict(none, h0=FAR[12], ht=FAR[12])) == 2
+    back = {n: v for n, v in none.items() if n != "ht"}
+    assert call("kda_ssm_bwd_chunked", list(SBWD), far(SBWD), Bn=1 << 23, T=1, wsb=1 << 44, **back) == 2
+    cu = (ctypes.c_int * 301)(*[0] * 300, 1000)
+    wide = dict(none, H=1 << 18, ldx=1 << 24, lddt=1 << 18)   # 128 sequences a launch of too many heads
+    assert call("kda_ssm_fwd_chunked", SSM_ORDER, far(SSM), Bn=1, T=1000, cu=cu, N=300, **wide, wsb=1 << 44) == 2

@@ -197,3 +197,14 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for a, b in zip(got, (qo, ko, *out.values())):
             assert torch.equal(a, b)
+
+
+def test_more_tokens_than_one_launch_holds():
+    # 70 million tokens of one head: more waves than a launch's 2^32 threads
+    T, d = 70_000_003, 8
+    say(f"qk norm T={T} Hq=1 d={d}")
+    q = torch.randn(1, T, 1, d, device="cuda", dtype=torch.bfloat16)
+    whole, _ = kda.qk_norm_rope(q, None, mode="rms")
+    for a, b in ((0, 30_000_000), (30_000_000, 60_000_000), (60_000_000, T)):
+        part, _ = kda.qk_norm_rope(q[:, a:b], None, mode="rms")
+        assert torch.equal(whole[:, a:b], part)
