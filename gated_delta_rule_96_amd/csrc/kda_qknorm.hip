@@ -225,8 +225,9 @@ __global__ __launch_bounds__(kQkThreads) void qk_bwd_kernel(const QkArgs a, unsi
       }
       sq = lane_sum<L>(sq);
       dot = lane_sum<L>(dot);
-      // dx = r (w dn - (x r) (sum w dn x) r / d): no power of r alone
-      const float rn = 1.0f / sqrtf(sq + a.eps);
+      // dx = r (w dn - (x r) (sum w dn x) r / d): no power of r alone.  A lane
+      // group without a head adds nothing to s (with eps = 0 its r is infinite)
+      const float rn = h < H ? 1.0f / sqrtf(sq + a.eps) : 0.f;
       const float k = dot * rn * inv;
       float o[8];
 #pragma unroll

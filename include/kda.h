@@ -445,6 +445,7 @@ int kda_conv_bwd(const void* x, long long ldx, const float* w, const float* bias
  * token t of every sequence is at pos0 + t.  A position outside [0, n_pos) reads nothing and
  * makes the rotated channels NaN.  q_out [B,T,Hq,d] and k_out of dtype may
  * be q and k themselves where those are contiguous.
+ * eps may be 0: a row of zeros is then NaN (0 / 0).
  * With the sum norm, w NULL and rot 0 it is the row normalisation
  * kda_fwd_chunked_layer fuses.
  * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides, pos0 + T > n_pos

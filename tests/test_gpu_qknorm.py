@@ -208,3 +208,28 @@ def test_more_tokens_than_one_launch_holds():
     for a, b in ((0, 30_000_000), (30_000_000, 60_000_000), (60_000_000, T)):
         part, _ = kda.qk_norm_rope(q[:, a:b], None, mode="rms")
         assert torch.equal(whole[:, a:b], part)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("mode", ["l2", "rms"])
+@pytest.mark.parametrize("Hq,Hk,d,rot", [(4, 2, 128, 64), (1, 1, 64, 0), (3, 5, 96, 96), (9, 8, 128, 0), (1, 3, 512, 16)])
+def test_weight_gradients_without_an_epsilon(dtype, mode, Hq, Hk, d, rot):
+    # eps = 0 on rows that are not zero: lanes that hold no head add nothing to
+    # the weights' gradients.  Tolerances as above (no epsilon enters them).
+    say(f"qk bwd eps=0 {dtype} {mode} Hq={Hq} Hk={Hk} d={d} rot={rot}")
+    B, T, rms = 2, 5, mode == "rms"
+    c = make(B, T, Hq, Hk, d, rot, dtype, 27)
+    cos, sin = table(c)
+    kw = dict(cos=c["cos"], sin=c["sin"], pos=c["pos"], mode=mode, eps=0.0)
+    qo, ko = kda.qk_norm_rope(c["q"], c["k"], c["wq"], c["wk"], **kw)
+    g = kda.qk_norm_rope_bwd(c["q"], c["k"], c["dq"], c["dk"], c["wq"], c["wk"], **kw)
+    torch.cuda.synchronize()
+    for n, out, H in (("q", qo, Hq), ("k", ko, Hk)):
+        x, w, dy = f64(c[n]).reshape(B * T, H, d), f64(c["w" + n]), f64(c["d" + n]).reshape(B * T, H, d)
+        want, size = mix.qk_fwd(x, w, cos, sin, rms, False, 0.0), pair_size(mix.qk_fwd(x, w, None, None, rms, False, 0.0), rot, False)
+        check(n, out.reshape(B * T, H, d), want, 18 * U * size, dtype)
+        dx, dw = mix.qk_bwd(x, w, cos, sin, dy, rms, False, 0.0)
+        r, gs = mix._rinv(x, rms, 0.0), pair_size(dy, rot, False)
+        sq = (gs * np.abs(w) * np.abs(x)).sum(-1, keepdims=True) / (d if rms else 1)
+        check("dw" + n, g["dw" + n], dw, (25 + 40 + B * T * H / 1024) * U * (gs * np.abs(x) * r).sum((0, 1)), torch.float32)
+        check("d" + n, g["d" + n].reshape(B * T, H, d), dx, 30 * U * (gs * np.abs(w) * r + np.abs(x) * r ** 3 * sq), dtype)
