@@ -229,3 +229,46 @@ def test_refusals_of_the_binding():
         kda.ssm_fwd_chunked(c["x"][None], c["dt"][None], c["A"], c["B"][None], c["C"][None, :7])
     with pytest.raises(kda.KDAError):
         kda.ssm_fwd_chunked(c["x"][None, ..., :32].contiguous(), c["dt"][None], c["A"], c["B"][None], c["C"][None])
+
+
+def reset_case(dtype, big, soft, seed):
+    """Small steps with two resetting tokens (a huge step, x = 0) in mid-chunk."""
+    c = make([200], 2, 1, 64, 128, dtype, seed, soft=False, rate=2.0)
+    c["A"].fill_(-16.0)
+    c["dt"].copy_(0.005 * torch.rand(c["dt"].shape, device="cuda") + 0.002)
+    if soft:   # the raw values whose Softplus the steps are
+        c["dt"].copy_(torch.log(torch.expm1(c["dt"].float())))
+        c["soft"] = True
+    for t in (80, 150):
+        c["dt"][t] = big
+        c["x"][t] = 0
+        if big > 1e30:   # (their product with B would be out of range)
+            c["B"][t] = 0
+    return c
+
+
+def reset_check(c, dtype):
+    # As at the head of the file, without the term for 32-bit decay sums: a
+    # step's exponent |e| costs its own rounding alone, 0.54 u at most.
+    y_ref, h_ref, size, zt = mix.ssm_seq(f64(c["x"]), f64(c["dt"]), f64(c["A"]), f64(c["B"]), f64(c["C"]), f64(c["h0"])[0], f64(c["D"]), None, c["soft"])
+    k = (250 + 4 * 4) * U
+    ty, th = size * (k + (2 ** -8 * 1.01 if dtype == torch.bfloat16 else 0)), zt * k
+    y, ht = call(c, [200])
+    state, ys = c["h0"].clone(), []
+    for t in range(200):
+        ys.append(kda.ssm_step(c["x"][t:t + 1], c["dt"][t:t + 1], c["A"], c["B"][t:t + 1], c["C"][t:t + 1], state, D=c["D"], softplus=c["soft"]))
+    torch.cuda.synchronize()
+    check("step", torch.cat(ys), y_ref, ty, dtype)
+    check("state", state[0], h_ref, th, torch.float32)
+    check("ht", ht[0], h_ref, th, torch.float32)
+    check("y", y[0], y_ref, ty, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("soft", [False, True])
+@pytest.mark.parametrize("big", [2.0 ** 13, 2.0 ** 17, 2.0 ** 20])
+def test_small_steps_behind_a_reset(dtype, soft, big):
+    # exp(dt A) of a huge step leaves nothing of the state; the tokens behind it
+    # in the chunk keep their own small decays
+    say(f"ssm reset {dtype} dt={big} soft={soft}")
+    reset_check(reset_case(dtype, big, soft, 39), dtype)
