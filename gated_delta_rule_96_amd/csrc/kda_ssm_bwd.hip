@@ -67,9 +67,10 @@ struct BwdLds {
   union {
     T x[kQ * PV];
     struct {   // when x has been used up: sums of the waves
-      float u[DK / 16][kQ], v[DK / 16][kQ], col[4][kQ], row[2][kQ], diag[kQ], qd[kQ], g[kBwdWaves];
+      float u[DK / 16][kQ], v[DK / 16][kQ], diag[kQ], qd[kQ], g[kBwdWaves];
     } s;
   };
+  double col[4][kQ], row[2][kQ];   // R's sums over 16 rows i, and over two column tiles j
   T dy[kQ * PV];
   T m[kQ * PM];              // E dt Qm, then E P: [i][j]
   // dS rounded to T, [state channel][value column] (fp32: read from memory
@@ -81,15 +82,16 @@ struct BwdLds {
 };
 
 // Sum over the 16 lanes of a row of lanes, by lane permutations.
-__device__ __forceinline__ float sum16(float x) {
-  x += dpp_f<0xB1>(x);    // quad_perm [1,0,3,2]
-  x += dpp_f<0x4E>(x);    // quad_perm [2,3,0,1]
-  x += dpp_f<0x141>(x);   // row_half_mirror
-  x += dpp_f<0x140>(x);   // row_mirror
+__device__ __forceinline__ double sum16(double x) {
+  x += dpp_zero<0xB1>(x);    // quad_perm [1,0,3,2]
+  x += dpp_zero<0x4E>(x);    // quad_perm [2,3,0,1]
+  x += dpp_zero<0x141>(x);   // row_half_mirror
+  x += dpp_zero<0x140>(x);   // row_mirror
   return x;
 }
 // Sum over the four lane groups that hold one column of a tile.
-__device__ __forceinline__ float sum_groups(float x) {
+template <typename F>
+__device__ __forceinline__ F sum_groups(F x) {
   x += __shfl_xor(x, 16);
   x += __shfl_xor(x, 32);
   return x;
@@ -200,9 +202,11 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
     if (h + 1 < h1) fetch(h + 1);
     __syncthreads();
 
-    // half strip of Qm, and from it R's sums, E dt Qm (to LDS) and E P (kept)
-    float row = 0.f, diag = 0.f, qd = 0.f;
-    f32x4 col[2];
+    // half strip of Qm, and from it R's sums, E dt Qm (to LDS) and E P (kept).
+    // A token's decay gradient is a difference of R's row and column sums: both
+    // in 64 bits, or their roundings do not cancel and dt_t times them is dA
+    double row = 0.0;
+    float diag = 0.f, qd = 0.f;
     V4<T> ep[2];
     {
       Slab<T> ys[DV / 32];
@@ -212,7 +216,6 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         const int jt = 2 * jh + q;
-        col[q] = zero4();
         ep[q] = narrow4<T>(zero4());
         if (jt > (is | 1)) continue;   // tile is + 1 of an even strip: zeros complete its slab
         f32x4 nn = zero4(), mm = zero4();
@@ -222,6 +225,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
           for (int k = 0; k < DV / 32; ++k) acc = mma(slab_any(sm.x, PV, 16 * jt, 32 * k, ln), ys[k], acc);
           const int j = 16 * jt + 4 * g;
           const f32x4 dj = load4(sm.dt + j);
+          double col[4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const bool in = j + r <= i_own, on = j + r == i_own;
@@ -233,22 +237,23 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
             if (on) {
               diag = rr;
               qd = acc[r];
-            } else {
-              row = fmaf(rr, dj[r], row);
-              col[q][r] = rr;
             }
+            col[r] = on ? 0.0 : (double)rr;
+            row = fma(col[r], (double)dj[r], row);
+            col[r] = sum16(col[r]);
+          }
+          if (l16 == 0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sm.col[is][j + r] = col[r];
           }
         }
         ep[q] = narrow4<T>(mm);
         store4(m_own + 16 * jt + 4 * g, narrow4<T>(nn));
       }
       row = sum_groups(row);
+      if (g == 0) sm.row[jh][i_own] = row;
       diag = sum_groups(diag);   // one lane of a column holds it
       qd = sum_groups(qd);
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) col[q][r] = sum16(col[q][r]);
     }
 
     // S dy and dS x (transposed: rows the wave's state channels)
@@ -306,15 +311,10 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
         sm.s.u[wave % KT][16 * (tk + t) + l16] = su[t];
         sm.s.v[wave % KT][16 * (tk + t) + l16] = sv[t];
       }
-      sm.s.row[jh][i_own] = row;
       if (jh == is / 2) {
         sm.s.diag[i_own] = diag;
         sm.s.qd[i_own] = qd;
       }
-    }
-    if (l16 == 0) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) store4(&sm.s.col[is][16 * (2 * jh + q) + 4 * g], col[q]);
     }
     if (lane == 0) sm.s.g[wave] = gs;
 
@@ -382,11 +382,11 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
       // a strip before token j's tile has no entry of column j
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (q >= lane >> 4) cs += (double)sm.s.col[q][lane];
+        if (q >= lane >> 4) cs += sm.col[q][lane];
 #pragma unroll
       for (int q = 0; q < kBwdWaves; ++q) gsum += (double)sm.s.g[q];
       const double dts = (double)sm.dt[lane], vd = v * dts;
-      const double net = ((double)sm.s.row[0][lane] + sm.s.row[1][lane]) + u - cs * dts - vd;
+      const double net = (sm.row[0][lane] + sm.row[1][lane]) + u - cs * dts - vd;
       const double incl = wave_scan(net);
       const double all = lane63(incl) + lane63(wave_scan(vd)) + (double)exp2_of(sm.cum[kQ - 1]) * gsum;
       const double da = all - (incl - net);

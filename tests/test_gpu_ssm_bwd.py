@@ -177,3 +177,41 @@ def test_gradient_by_differences_of_the_forward():
         # the central difference's own error: step^2 / 6 of the third derivative, below 1e-2 of the sum of the products' sizes here
         size = np.abs(f64(g[gn]).reshape(f64(v).shape) * f64(v)).sum()
         assert abs(got - want) <= 1e-2 * size, (n, got, want, size)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("big", [2.0 ** 13, 2.0 ** 20])
+def test_small_steps_behind_a_reset(dtype, big):
+    from test_gpu_ssm import reset_case
+    say(f"ssm bwd reset {dtype} dt={big}")
+    c = grads(reset_case(dtype, big, False, 47), [200])
+    g = run(c, [200])
+    torch.cuda.synchronize()
+    compare(c, g, oracle(c, [200]), [200], dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_token_sums_that_cancel(dtype):
+    # No decay (A = 0), steps of one, unit vectors as B and x: the products of a
+    # chunk are R_ij = C_i[j] dy_i[j], whole numbers of our choice.  Large ones
+    # cancel within rows and columns, and every sum is exact in 64 bits: dA =
+    # sum_ij R_ij (i - j) and ddt_j = sum_i R_ij come out to their own rounding.
+    say(f"ssm bwd cancelling sums {dtype}")
+    n, big = 64, 2.0 ** 13
+    r = np.random.default_rng(48)
+    C, dy = r.integers(-2, 3, (n, n)).astype(float), np.ones((n, n))
+    for i, j, s in ((20, 0, 1), (20, 8, -1), (28, 8, 1), (28, 0, -1), (45, 33, 1), (45, 38, -1), (47, 38, 1), (47, 33, -1), (60, 3, 1), (60, 40, -1),
+                    (62, 40, 1), (62, 3, -1)):
+        C[i, j], dy[i, j] = s * big, big
+    C, dy = np.tril(C), np.tril(dy)
+    one = lambda a: cast(a, dtype).cuda()
+    v = lambda a: cast(a, torch.float32).cuda()
+    e = np.eye(n)
+    g = kda.ssm_bwd_chunked(one(e[None, :, None]), one(np.ones((1, n, 1))), v(np.zeros(1)), one(e[None, :, None]), one(C[None, :, None]),
+                            one(dy[None, :, None]), dt_bias=v(np.zeros(1)))
+    torch.cuda.synchronize()
+    R, at = C * dy, np.arange(n)
+    ddt = R.sum(0)
+    check("dA", g["dA"], np.array([(R * (at[:, None] - at)).sum()]), 0.0, torch.float32)
+    check("ddt_bias", g["ddt_bias"], np.array([ddt.sum()]), 0.0, torch.float32)
+    check("ddt", g["ddt"][0, :, 0], ddt, 0.0, dtype)
