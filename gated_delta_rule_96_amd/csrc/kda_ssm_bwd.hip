@@ -190,6 +190,7 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
     StepSize s = step_size(raw, bias, f.softplus, a2);
     if (lane >= n) s = StepSize{0.f, 0.0};
     const float slope = f.softplus ? sigmoid_fast(raw + bias) : 1.f;
+    const bool cut = s.a == kNothing;   // nothing crosses this token
     const double cum = wave_scan(s.a), last = lane63(cum);
     __syncthreads();   // the head before is done with LDS
     rx.store(sm.x, tid);
@@ -389,7 +390,8 @@ __global__ __launch_bounds__(kBwdThreads, 2) void ssm_bwd_kernel(const ChunkBwd 
       const double net = (sm.row[0][lane] + sm.row[1][lane]) + u - cs * dts - vd;
       const double incl = wave_scan(net);
       const double all = lane63(incl) + lane63(wave_scan(vd)) + (double)exp2_of(sm.cum[kQ - 1]) * gsum;
-      const double da = all - (incl - net);
+      // (what is left of the sums at a cut is their rounding; dt_t is large there)
+      const double da = cut ? 0.0 : all - (incl - net);
       double d = ((double)f.A[h] * da + cs + sm.s.diag[lane] + v) * (double)sm.slope[lane];
       if (lane >= n) d = 0.0;
       if (lane < n) ((T*)b.ddt)[(tok + lane) * (size_t)f.H + h] = from_f32<T>((float)d);

@@ -62,16 +62,21 @@ __device__ __forceinline__ double lane63(double x) {
 __device__ __forceinline__ float exp2_of(double x) { return exp2_fast((float)x); }
 
 // A token's step size and its decay exponent dt A in log2 units (64 bits: sums
-// of many tokens keep the small differences between neighbours).
+// of many tokens keep the small differences between neighbours).  Exponents
+// below kNothing count as it: every factor across such a token is 0 in fp32
+// either way (a product of others that outweighs it is out of range itself),
+// and the sums of a chunk keep their places behind the point down to 2^-26.
 struct StepSize {
   float dt;
   double a;
 };
+constexpr double kNothing = -1048576.0;
 __device__ __forceinline__ StepSize step_size(float raw, float bias, int softplus, double a2) {
   StepSize s;
   const float v = raw + bias;
   s.dt = softplus ? softplus_f(v) : v;
   s.a = (double)s.dt * a2;
+  if (s.a < kNothing) s.a = kNothing;
   return s;
 }
 

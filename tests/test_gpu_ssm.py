@@ -272,3 +272,10 @@ def test_small_steps_behind_a_reset(dtype, soft, big):
     # in the chunk keep their own small decays
     say(f"ssm reset {dtype} dt={big} soft={soft}")
     reset_check(reset_case(dtype, big, soft, 39), dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("soft", [False, True])
+def test_small_steps_behind_a_reset_of_the_largest_step(dtype, soft):
+    say(f"ssm reset {dtype} dt=max soft={soft}")
+    reset_check(reset_case(dtype, torch.finfo(dtype).max, soft, 40), dtype)

@@ -215,3 +215,13 @@ def test_token_sums_that_cancel(dtype):
     check("dA", g["dA"], np.array([(R * (at[:, None] - at)).sum()]), 0.0, torch.float32)
     check("ddt_bias", g["ddt_bias"], np.array([ddt.sum()]), 0.0, torch.float32)
     check("ddt", g["ddt"][0, :, 0], ddt, 0.0, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_small_steps_behind_a_reset_of_the_largest_step(dtype):
+    from test_gpu_ssm import reset_case
+    say(f"ssm bwd reset {dtype} dt=max")
+    c = grads(reset_case(dtype, torch.finfo(dtype).max, False, 49), [200])
+    g = run(c, [200])
+    torch.cuda.synchronize()
+    compare(c, g, oracle(c, [200]), [200], dtype)
