@@ -281,10 +281,19 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
 }
 
 // Four channels a thread where every row starts on the size of four elements
-// (channels and the token stride a multiple of 4, x aligned); one channel
-// otherwise (16384 tokens x 4096 channels: 45 us; of rows 13 elements wider: 63).
+// (channels and the token stride a multiple of 4, all tensors aligned); one
+// channel otherwise (16384 tokens x 4096 channels: 45 us; of rows 13 elements
+// wider: 63).
+bool on_four(const void* p, int is_bf16) { return reinterpret_cast<uintptr_t>(p) % (is_bf16 ? 8u : 16u) == 0; }
 int vec_of(const ConvArgs& a, int is_bf16) {
-  return a.D % 4 == 0 && a.ldx % 4 == 0 && reinterpret_cast<uintptr_t>(a.x) % (is_bf16 ? 8u : 16u) == 0 ? 4 : 1;
+  return a.D % 4 == 0 && a.ldx % 4 == 0 && on_four(a.x, is_bf16) && on_four(a.s0, is_bf16) && on_four(a.st, is_bf16) &&
+                 on_four(a.y, is_bf16)
+             ? 4
+             : 1;
+}
+int vec_of(const ConvBwdArgs& a, int is_bf16) {
+  return on_four(a.dy, a.dy_bf16) && on_four(a.dst, is_bf16) && on_four(a.dx, is_bf16) && on_four(a.ds0, is_bf16) ? vec_of(a.f, is_bf16)
+                                                                                                              : 1;
 }
 
 // Tokens of a strip: long strips re-read fewer rows, short ones keep the card
@@ -463,7 +472,7 @@ hipError_t launch_conv_step(int is_bf16, const ConvArgs& a, int B, hipStream_t s
 }
 
 size_t conv_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D, int W) {
-  // the larger of the two channel widths' needs: x's stride decides at the call
+  // the larger of the two channel widths' needs: strides and alignment decide at the call
   size_t most = 0;
   for (int ve : {4, 1}) {
     if (D % ve) continue;
@@ -479,7 +488,7 @@ size_t conv_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D, int W
 }
 
 hipError_t launch_conv_bwd(int is_bf16, const ConvBwdArgs& a, const int* cu, int N, int B, int T, hipStream_t st) {
-  const int ve = vec_of(a.f, is_bf16), part = bwd_strip((long long)B * T, a.f.D / ve), end = cu ? N : B;
+  const int ve = vec_of(a, is_bf16), part = bwd_strip((long long)B * T, a.f.D / ve), end = cu ? N : B;
   const unsigned CG = (unsigned)(a.f.D / ve), LC = pow2_lanes(CG), cb = (CG + LC - 1) / LC;
   if (!seq_tabs_fit(cu, N, B, T, part, max_groups(kConvThreads) / cb * (64 / LC * (kConvThreads / 64))) ||
       ((long long)a.f.D * (a.f.W + 1) + 63) / 64 > max_groups(kSumThreads))

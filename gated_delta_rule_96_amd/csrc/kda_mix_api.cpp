@@ -68,6 +68,13 @@ int check_conv(const void* x, long long ldx, const float* w, const float* bias, 
   return KDA_OK;
 }
 
+// Tokens or states of D channels without gaps: from any element where rows of
+// D are no whole 16 bytes.
+bool conv_aligned(const void* p, int D, int dtype) {
+  const size_t esz = elem_size(dtype);
+  return reinterpret_cast<uintptr_t>(p) % ((size_t)D * esz % 16 == 0 ? 16 : esz) == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -77,7 +84,7 @@ int kda_conv_fwd(const void* x, long long ldx, const float* w, const float* bias
   int e = check_conv(x, ldx, w, bias, flags, dtype, B, T, D, W);
   if (e != KDA_OK) return e;
   if (!y) return KDA_ERR_NULL;
-  if (!aligned16(s0) || !aligned16(st) || !aligned16(y)) return KDA_ERR_ALIGN;
+  if (!conv_aligned(s0, D, dtype) || !conv_aligned(st, D, dtype) || !conv_aligned(y, D, dtype)) return KDA_ERR_ALIGN;
   if ((e = check_cu(cu_seqlens, N, B, T)) != KDA_OK) return e;
   const size_t esz = elem_size(dtype), rows = (size_t)B * T, ns = (size_t)(cu_seqlens ? N : B) * (W - 1) * D * esz;
   const Span in[] = {{x, rows_bytes(rows, ldx, D, esz)}, {s0, ns}, {w, (size_t)D * W * 4}, {bias, (size_t)D * 4}};
@@ -92,7 +99,7 @@ int kda_conv_step(const void* x, long long ldx, const float* w, const float* bia
   const int e = check_conv(x, ldx, w, bias, flags, dtype, B, 1, D, W);
   if (e != KDA_OK) return e;
   if (!state || !state_out || !y) return KDA_ERR_NULL;
-  if (!aligned16(state) || !aligned16(state_out) || !aligned16(y)) return KDA_ERR_ALIGN;
+  if (!conv_aligned(state, D, dtype) || !conv_aligned(state_out, D, dtype) || !conv_aligned(y, D, dtype)) return KDA_ERR_ALIGN;
   const size_t esz = elem_size(dtype), ns = (size_t)B * (W - 1) * D * esz;
   const Span in[] = {{x, rows_bytes(B, ldx, D, esz)}, {state, ns}, {w, (size_t)D * W * 4}, {bias, (size_t)D * 4}};
   const Span out[] = {{y, (size_t)B * D * esz}, {state_out, ns}};
@@ -113,8 +120,9 @@ int kda_conv_bwd(const void* x, long long ldx, const float* w, const float* bias
   if (e != KDA_OK) return e;
   if (!valid_dtype(dy_dtype) || (dtype == KDA_F32 && dy_dtype != KDA_F32)) return KDA_ERR_DTYPE;
   if (!dy || !dx || !dw) return KDA_ERR_NULL;
-  for (const void* p : {s0, dy, dst, (const void*)dx, (const void*)dw, (const void*)dbias, (const void*)ds0})
-    if (!aligned16(p)) return KDA_ERR_ALIGN;
+  for (const void* p : {s0, dst, (const void*)dx, (const void*)ds0})
+    if (!conv_aligned(p, D, dtype)) return KDA_ERR_ALIGN;
+  if (!conv_aligned(dy, D, dy_dtype) || !aligned16(dw) || !aligned16(dbias)) return KDA_ERR_ALIGN;
   if ((e = check_cu(cu_seqlens, N, B, T)) != KDA_OK) return e;
   const size_t need = kda_conv_bwd_workspace_bytes(B, T, D, W, cu_seqlens ? N : 0);
   if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;

@@ -397,7 +397,10 @@ int kda_bwd_chunked(const void* q, const void* k, const void* v, const void* g, 
  *   z[t,c] = bias[c] + sum_j w[c,j] x[t-(W-1-j),c];  y = z, or z Sigmoid(z)
  *   with flags & KDA_CONV_SILU.
  * x: rows [B,T,D] of dtype (any D; element alignment suffices; rows that
- * start on four elements are faster); w [D,W] fp32; bias [D] fp32 or NULL; s0 [N,W-1,D] of dtype:
+ * start on four elements are faster); w [D,W] fp32; bias [D] fp32 or NULL.
+ * Tokens and states without gaps (y, s0, st, and the gradients below) are
+ * 16-byte aligned where rows of D are whole 16 bytes, otherwise they may
+ * start on any element.  s0 [N,W-1,D] of dtype:
  * the W-1 tokens before each sequence, oldest first (NULL: zeros); st
  * [N,W-1,D] or NULL: receives the last W-1 tokens (older ones from s0); may
  * be s0 itself (in-place carry).  y [B,T,D] of dtype.

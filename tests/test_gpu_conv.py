@@ -260,3 +260,40 @@ def test_conv_binding_refusals():
         kda.conv_fwd(x, w, out=x)
     with pytest.raises(ValueError, match="workspace"):
         kda.conv_bwd(x, w, None, x, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,D,off", [(torch.float32, 13, 1), (torch.float32, 13, 13)] +
+                         [(torch.bfloat16, D, off) for D, off in ((13, 1), (13, 13), (12, 1), (12, 2), (12, 4), (36, 12))])
+def test_rows_of_ragged_width_from_any_element(dtype, D, off):
+    # states, outputs and gradients as slices of pools that start between two
+    # 16-byte places, where a row of D channels is no multiple of 16 bytes
+    say(f"conv unaligned {dtype} D={D} off={off}")
+    lens, W = [70, 0, 3], 4
+    c = make(lens, D, W, dtype, 14)
+    cu, x = cuts(lens), c["x"][None]
+    gtypes = [dtype] if dtype == torch.float32 else [dtype, torch.float32]
+
+    def shifted(t):
+        pool = torch.full((t.numel() + off + 8,), 7, dtype=t.dtype, device="cuda")
+        s = pool[off:off + t.numel()].view(t.shape)
+        s.copy_(t)
+        return s
+    y, st = kda.conv_fwd(x, c["w"], c["bias"], c["s0"], cu_seqlens=cu)
+    y2, st2 = kda.conv_fwd(shifted(x), c["w"], c["bias"], shifted(c["s0"]), cu_seqlens=cu, st=shifted(st), out=shifted(y))
+    assert torch.equal(y, y2) and torch.equal(st, st2)
+    one = x[0, :3].contiguous()
+    y1, s1 = kda.conv_step(one, c["w"], c["bias"], st.clone()), shifted(st)
+    assert torch.equal(kda.conv_step(shifted(one), c["w"], c["bias"], s1, out=shifted(y1)), y1)
+    for gt in gtypes:
+        if D * gt.itemsize % 16 == 0:
+            continue
+        dy = c["dy"][None].to(gt)
+        g = kda.conv_bwd(x, c["w"], c["bias"], dy, c["s0"], c["dst"], cu_seqlens=cu)
+        out = {n: shifted(t) if n in ("dx", "ds0") else torch.empty_like(t) for n, t in g.items()}
+        kda.conv_bwd(shifted(x), c["w"], c["bias"], shifted(dy), shifted(c["s0"]), shifted(c["dst"]), cu_seqlens=cu, out=out)
+        for n in g:   # (four channels a thread and one add in another order)
+            if n in ("dx", "ds0"):
+                assert torch.equal(g[n], out[n]), n
+        ref, tol = grads_case(dict(c, dy=dy[0]), lens, True, True)
+        check("dw", out["dw"], ref[1], tol[1], torch.float32)
+        check("dbias", out["dbias"], ref[2], tol[2], torch.float32)
