@@ -277,8 +277,13 @@ def fwd_chunked_layer(q, k, v, z, A, beta, h0=None, *, og=None, qk_l2norm=False,
     return o, (ht if final_state else None)
 
 
+_INT_MAX = (1 << 31) - 1   # sizes go to the library as C ints, which ctypes would wrap around
+
+
 def _cu_array(cu_seqlens):
     cu = [int(x) for x in cu_seqlens]
+    if cu and (max(cu) > _INT_MAX or min(cu) < -_INT_MAX):
+        raise ValueError("cu_seqlens must be in 32 bits")
     return (ctypes.c_int * len(cu))(*cu), len(cu) - 1
 
 
@@ -428,6 +433,8 @@ def _rows(t, name, lead, inner):
     of a wider tensor: inner elements contiguous, all tokens one distance apart."""
     if t.shape != lead + inner:
         raise ValueError(f"{name} must be {list(lead + inner)}, got {list(t.shape)}")
+    if t.numel() > _INT_MAX and max(t.shape) > _INT_MAX:
+        raise ValueError(f"{name}: a size is not in 32 bits: {list(t.shape)}")
     if not t.is_cuda:
         raise ValueError(f"{name} must live on the GPU")
     if t.is_contiguous():
@@ -579,6 +586,8 @@ def _qk_setup(q, k, cos, sin, pos, pos0, mode, interleaved):
     """Checked common arguments of the head norms: pointers, sizes and flags."""
     B, T, Hq, d = q.shape
     Hk = 0 if k is None else k.shape[2]
+    if not -_INT_MAX <= pos0 <= _INT_MAX or cos is not None and cos.numel() > _INT_MAX and cos.shape[0] > _INT_MAX:
+        raise ValueError("positions must be in 32 bits")
     if k is not None and k.dtype != q.dtype:
         raise TypeError(f"k dtype {k.dtype} != q dtype {q.dtype}")
     if mode not in ("l2", "rms"):

@@ -210,3 +210,21 @@ def test_sizes_beyond_a_launch_are_refused():
     cu = (ctypes.c_int * 301)(*[0] * 300, 1000)
     wide = dict(none, H=1 << 18, ldx=1 << 24, lddt=1 << 18)   # 128 sequences a launch of too many heads
     assert call("kda_ssm_fwd_chunked", SSM_ORDER, far(SSM), Bn=1, T=1000, cu=cu, N=300, **wide, wsb=1 << 44) == 2
+
+
+def test_binding_refuses_what_32_bits_do_not_hold():
+    # sizes and positions go to the library as 32-bit ints: none may wrap around
+    with pytest.raises(ValueError, match="32 bits"):
+        kda._packed([0, (1 << 32) + 4], 1, 4)
+    with pytest.raises(ValueError, match="32 bits"):
+        kda.varlen_snapshots([0, (1 << 32) + 640], 1)
+    x = torch.empty((1, (1 << 32) + 3, 8), dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="32 bits"):
+        kda._rows(x, "x", (1, (1 << 32) + 3), (8,))
+    q = torch.empty((1, 4, 1, 64), device="meta")
+    for kw in (dict(pos0=1 << 32), dict(pos0=-(1 << 31) - 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            kda.qk_norm_rope(q, None, cos=torch.empty((8, 8)), sin=torch.empty((8, 8)), **kw)
+    long = torch.empty(((1 << 32) + 8, 8), device="meta")
+    with pytest.raises(ValueError, match="32 bits"):
+        kda.qk_norm_rope(q, None, cos=long, sin=long)
