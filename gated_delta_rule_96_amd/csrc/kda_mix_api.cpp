@@ -109,7 +109,9 @@ int kda_conv_step(const void* x, long long ldx, const float* w, const float* bia
 }
 
 size_t kda_conv_bwd_workspace_bytes(int B, int T, int D, int W, int N) {
-  if (B <= 0 || T <= 0 || T > kMaxT || D <= 0 || W < 2 || W > 4 || N < 0 || (N > 0 && B != 1) || !size_ok(B, T, D, 8)) return 0;
+  if (B <= 0 || T <= 0 || T > kMaxT || D <= 0 || W < 2 || W > 4 || N < 0 || (N > 0 && B != 1) || !size_ok(B, T, D, 8) ||
+      (long long)D * (W + 1) > 0x7fffffffLL)
+    return 0;
   return kda::conv_bwd_workspace_bytes(N > 0, N, B, T, D, W);
 }
 
@@ -333,7 +335,8 @@ int kda_ssm_step(const void* x, long long ldx, const void* dt, long long lddt, c
 
 size_t kda_ssm_bwd_workspace_bytes(int B, int T, int H, int G, int dk, int dv, int dtype, int N) {
   if (!valid_dtype(dtype) || B <= 0 || T <= 0 || T > kMaxT || H <= 0 || G <= 0 || H % G || !kda::supported_d(dk) ||
-      !kda::supported_d(dv) || N < 0 || (N > 0 && B != 1) || !size_ok(B, T, H, 8LL * dk * dv) || (long long)B * T > (1LL << 40))
+      !kda::supported_d(dv) || N < 0 || (N > 0 && B != 1) || !size_ok(B, T, H, 8LL * dk * dv) || (long long)B * T > (1LL << 40) ||
+      (long long)N * H > 0x7fffffffLL)
     return 0;
   return kda::ssm_bwd_workspace_bytes(N > 0, N, B, T, H, G, dk, dv);
 }
@@ -357,7 +360,6 @@ int kda_ssm_bwd_chunked(const void* x, long long ldx, const void* dt, long long 
                         (const void*)dD, (const void*)ddt_bias, (const void*)dh0})
     if (!aligned16(p)) return KDA_ERR_ALIGN;
   if ((e = check_cu(cu_seqlens, N, B, T)) != KDA_OK) return e;
-  if (cu_seqlens && (long long)N * H > 0x7fffffffLL) return KDA_ERR_SHAPE;
   const size_t need = kda_ssm_bwd_workspace_bytes(B, T, H, G, dk, dv, dtype, cu_seqlens ? N : 0);
   if (need == 0) return KDA_ERR_SHAPE;
   if (!workspace || workspace_bytes < need) return KDA_ERR_WORKSPACE;

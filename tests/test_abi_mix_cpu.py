@@ -228,3 +228,11 @@ def test_binding_refuses_what_32_bits_do_not_hold():
     long = torch.empty(((1 << 32) + 8, 8), device="meta")
     with pytest.raises(ValueError, match="32 bits"):
         kda.qk_norm_rope(q, None, cos=long, sin=long)
+
+
+def test_workspace_sizes_of_absurd_calls_are_zero():
+    # sizes the calls refuse: 0, not a byte count that wrapped around
+    many = (1 << 31) - 1
+    L = kda.lib()
+    assert L.kda_ssm_bwd_workspace_bytes(1, 64, 1 << 18, 1, 128, 128, 1, many) == 0
+    assert L.kda_conv_bwd_workspace_bytes(1, 1, many, 4, many) == 0 and L.kda_conv_bwd_workspace_bytes(1, 1, many, 4, 0) == 0
