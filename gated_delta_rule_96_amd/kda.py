@@ -135,9 +135,10 @@ def _ptr(t):
 
 
 def _stream(device) -> int:
-    # (the handle itself: torch.cuda.current_stream() builds an object around
-    # it, 1.9 us of a single-token call's 12)
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    # (the handle itself where torch gives it: torch.cuda.current_stream()
+    # builds an object around it, 1.9 us of a single-token call's 12)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream(device).cuda_stream if raw is None else raw(device.index)
 
 
 def _check(status: int, where: str):

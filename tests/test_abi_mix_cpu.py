@@ -236,3 +236,13 @@ def test_workspace_sizes_of_absurd_calls_are_zero():
     L = kda.lib()
     assert L.kda_ssm_bwd_workspace_bytes(1, 64, 1 << 18, 1, 128, 128, 1, many) == 0
     assert L.kda_conv_bwd_workspace_bytes(1, 1, many, 4, many) == 0 and L.kda_conv_bwd_workspace_bytes(1, 1, many, 4, 0) == 0
+
+
+def test_stream_without_the_raw_handle(monkeypatch):
+    # a torch without the private accessor: the public stream's handle
+    class Stream:
+        cuda_stream = 1234
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d: asked.append(d) or Stream())
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert kda._stream(torch.device("cuda", 3)) == 1234 and asked == [torch.device("cuda", 3)]
