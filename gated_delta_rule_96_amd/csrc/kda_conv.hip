@@ -14,11 +14,12 @@
 // cache lines per load) of a strip of tokens and walks it with the last W-1
 // rows in registers, eight rows' loads in flight; only the W-1 rows before a
 // strip are read twice (from the caches).  All sums in fp32, one rounding to the output type.
-// Measured (bf16): 65536 tokens x 4096 channels 196 us (5.5 TB/s; with eight
-// channels a thread 207); 8191 packed tokens x 4352 channels 30 us (4.7 TB/s,
-// rows of a wider tensor; 34); gradients of 32768 tokens x 2048 channels from
-// fp32 dy 111 us (4.8 TB/s; 123); a token for 256 sequences x 4352 channels 4.4
-// us (4.0 TB/s), twice that through the Python binding.
+// Measured (bf16): 65536 tokens x 4096 channels 195 us (5.5 TB/s); 8191 packed
+// tokens x 4352 channels 30 us (4.7 TB/s, rows of a wider tensor); gradients of
+// 32768 tokens x 2048 channels from fp32 dy 114 us (4.7 TB/s); a token for 256
+// sequences x 4352 channels 4.5 us (3.9 TB/s), twice that through the Python
+// binding.  Eight channels a thread took 207, 34 and 123 us where four took
+// 199, 32 and 114.
 #include "kda_rows.h"
 
 namespace kda {
@@ -26,9 +27,9 @@ namespace kda {
 namespace {
 
 constexpr int kConvThreads = 256;
-// Rows loaded together: forward (64K tokens x 4096 channels: 203 us; four 217,
-// sixteen 220), and x and dy rows of the backward (32K x 2048: 111 us; four 151;
-// one as good, but 98 against 80 for fp32 inputs).
+// Rows loaded together: forward (64K tokens x 4096 channels: 203 us, 16K: 46;
+// four 214 and 46, sixteen 200 and 51), and x and dy rows of the backward (32K x
+// 2048: 115 us, 16K of fp32: 84; four 153 and 78, one 114 and 104).
 constexpr int kFwdRows = 8;
 constexpr int kBwdRows = 2;
 
@@ -282,8 +283,8 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
 
 // Four channels a thread where every row starts on the size of four elements
 // (channels and the token stride a multiple of 4, all tensors aligned); one
-// channel otherwise (16384 tokens x 4096 channels: 45 us; of rows 13 elements
-// wider: 63).
+// channel otherwise (16384 tokens x 4096 channels: 46 us; of rows 13 elements
+// wider: 67).
 bool on_four(const void* p, int is_bf16) { return reinterpret_cast<uintptr_t>(p) % (is_bf16 ? 8u : 16u) == 0; }
 int vec_of(const ConvArgs& a, int is_bf16) {
   return a.D % 4 == 0 && a.ldx % 4 == 0 && on_four(a.x, is_bf16) && on_four(a.s0, is_bf16) && on_four(a.st, is_bf16) &&
@@ -297,10 +298,10 @@ int vec_of(const ConvBwdArgs& a, int is_bf16) {
 }
 
 // Tokens of a strip: long strips re-read fewer rows, short ones keep the card
-// busy on short inputs.  Forward at most 128 (64K tokens x 4096 channels: 196
-// us, 64 203), fewer below 256K threads (16384 x 4096: 45 us; 512K 53; 128K
-// is as good).  Backward at most 64 (32K x 2048: 111 us; 32 116, 128 150), fewer
-// below 128K threads (4096 x 4352: 40 us; 64K 60, 256K 44).
+// busy on short inputs.  Forward at most 128 (64K tokens x 4096 channels: 203
+// us; 64 209), fewer below 256K threads (16384 x 4096: 46 us; 512K 55, 128K 54).
+// Backward at most 64 (32K x 2048: 115 us; 32 120, 128 152), fewer below 128K
+// threads (4096 x 4352: 42 us; 64K 62, 256K 46).
 int fwd_strip(long long rows, int cg) {
   int part = 128;
   while (part > kFwdRows && rows * cg / part < 256LL * 1024) part >>= 1;
@@ -334,8 +335,8 @@ hipError_t state_go(const ConvArgs& a, const SeqTab& s, hipStream_t st) {
   return hipGetLastError();
 }
 // Sequences of a token step's thread: more where enough threads are left (256
-// x 4352 channels: 4.4 us; one sequence 4.9, four 4.45; 1024 x 4352: four 11.6,
-// two 12.8, one 14.3; 64 x 4352: one 2.5, two 2.6).
+// x 4352 channels: two 4.5 us, one 4.9, four 4.5; 1024 x 4352: four 11.9, two
+// 12.7, one 14.0; 64 x 4352: one 2.5, two 2.7).
 template <typename T, int W>
 hipError_t step_go(const ConvArgs& a, int B, hipStream_t st) {
   const long long all = (long long)B * a.D;

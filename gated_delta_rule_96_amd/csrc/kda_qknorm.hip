@@ -16,9 +16,10 @@
 // lane traffic, the norm a sum over L lanes.  A wave takes 64/L x R heads of
 // one token, so a token's table row is read once for all of them.  Rows are
 // in fp32 between the loads and the one rounding at the end.
-// Measured (bf16): 65536 tokens x 64 heads of 128 381 us (5.7 TB/s); gradients
-// of 32768 tokens x 32 heads 205 us (5.2 TB/s); a token for 256 sequences 5 us
-// (14 through the Python binding).
+// Measured (bf16): 65536 tokens x 64 heads of 128 382 us (5.7 TB/s); gradients
+// of 32768 tokens x 32 heads 205 us (5.2 TB/s); a token for 256 sequences x 40
+// heads 4.5 us (14 through the Python binding): two memory trips one behind the
+// other, position and table, in a launch of a tenth of the card.
 #include "kda_rows.h"
 
 namespace kda {
@@ -26,13 +27,14 @@ namespace kda {
 namespace {
 
 constexpr int kQkThreads = 256;
-// Heads a lane group holds at once: forward (64K tokens x 64 heads of 128: 404
-// us; two 421, eight 430) and backward (32K tokens x 32 heads: 213 us; one 228,
-// four 262).
+// Heads a lane group holds at once: forward (64K tokens x 64 heads of 128: 370
+// us; two 382, eight 408; fewer heads would like fewer: 8 query heads and 1 key
+// head 92, two 70) and backward (32K tokens x 32 heads: 206 us; one 217, four
+// 244; 64K x 8 + 1 heads: 150; 145, 284).
 constexpr int kQkRows = 4, kBwdRows = 2;
 // Work-groups of the backward at most, each with a partial row of dw (same
-// case: 213 us; 768 224, 1536 243, 2048 219: these do not all run at once and
-// end unevenly).
+// cases: 206 and 150 us; 768 210 and 177, 1536 227 and 189, 2048 212 and 156:
+// more do not all run at once and end unevenly).
 constexpr int kBwdGroups = 1024;
 
 // Where a lane's eight channels are.

@@ -11,7 +11,8 @@
 //         M_ij = (C_i . B_j) exp(cum_i - cum_j) dt_j
 //   S_Q = exp(cum_Q) S_0 + sum_j exp(cum_Q - cum_j) dt_j B_j x_j^T
 // Every factor is exp of a difference that is <= 0 for A <= 0: nothing is
-// rescaled, any decay is in range.  Later tokens never reach an earlier one's
+// rescaled, any decay is in range (sums and differences of exponents in 48 bits
+// or more, see step_size and PipeLds).  Later tokens never reach an earlier one's
 // y, also not as 0 x inf or 0 x NaN.
 //
 // A work-group walks the chunks of one part of one sequence for one head with
@@ -30,9 +31,9 @@
 // twice; it keeps the chain of dependent chunks short without waits between
 // work-groups.
 //
-// Measured (65536 tokens, 32 heads of 128 x 128, bf16): 618 us, 1.8 TB/s of
+// Measured (65536 tokens, 32 heads of 128 x 128, bf16): 620 us, 1.8 TB/s of
 // the inputs and outputs and 220 TFLOP/s of the products (traced kernel by
-// kernel: first pass 215, chaining 12, scan 415).
+// kernel: first pass 206, chaining 11, scan 410).
 // Neither rate binds: a chunk's 144 matrix instructions per state wave are 147
 // us of the scan's time at 2 GHz; the rest are their LDS operands, the exact
 // splits, the state's scaling and y's stores of the same four waves, one
@@ -50,11 +51,11 @@ namespace kda {
 
 namespace {
 
-// One scan work-group per CU (64K tokens x 32 heads: 634 us; 128 in all 937,
-// 512 658).
+// One scan work-group per CU (64K tokens x 32 heads: 610 us, 16K of fp32: 692;
+// 128 in all 911 and 1210, 512 633 and 709).
 constexpr int kScanWgs = 256;
 // A part's own sum is formed in two shares: two sweep work-groups per CU (the
-// same tokens: 634 us; one share 664, four 643).
+// same tokens: 610 and 692 us; one share 641 and 716, four 619 and 704).
 constexpr int kSubs = 2;
 
 template <int DK, int DV>
@@ -229,8 +230,9 @@ __global__ __launch_bounds__(kSsmThreads) void ssm_chunk_kernel(const SsmArgs a,
 // into LDS, form chunk k + 1's M and chunk k + 2's step sizes, while the back
 // waves take chunk k's products with S, its y and the state's update.  One
 // barrier a chunk; the matrix instructions of one set cover the loads and
-// exponents of the other (64K tokens x 32 heads, the first calls of a process:
-// this kernel 491 us; 628 with four waves that do one thing after the other).
+// exponents of the other (64K tokens x 32 heads: 491 us for this kernel as first
+// written against 628 with four waves that do one thing after the other; 410
+// now).
 constexpr int kPipeThreads = 2 * kSsmThreads;
 
 template <int DK, int DV>
@@ -488,8 +490,9 @@ hipError_t fwd_go(const SsmArgs& a, const SeqTab& s, int seqs, bool split, hipSt
 
 int ssm_part(long long tokens, int H, int wgs) {
   // a part is at least four chunks, so that the extra pass and the chaining
-  // stay small beside it (1000 tokens x 32 heads: 42 us; at least two 46, eight
-  // 48), and a whole number of chunks for each of its shares
+  // stay small beside it (1000 tokens x 32 heads: 42 us; at least two 47, eight
+  // 48; 4 heads would like two: 30 against 27, fp32 85 against 53), and a whole
+  // number of chunks for each of its shares
   const long long want = (tokens * H + wgs - 1) / wgs, unit = (long long)kQ * kSubs;
   const long long part = (want + unit - 1) / unit * unit;
   return (int)(part < 256 ? 256 : part > (1 << 30) ? (1 << 30) : part);
@@ -500,9 +503,9 @@ int ssm_part(long long tokens, int H, int wgs) {
 // whole, and with it every other one; of up to 2 parts + 256 where the parts
 // would be more than the work-groups that run at once.  Whole against cut, us
 // (bf16, 32 heads, lengths behind the name of the work-groups' share of the
-// tokens): 256: 640 32 against 36, 1000 49 against 42; 1024: 1500 + 7 x 928 75
-// against 128, 2000 + 7 x 864 91 against 126; 2048: 3600 + 13 x 950 191
-// against 208.
+// tokens): 256: 640 33 against 35, 1000 47 against 42; 1024: 1500 + 7 x 928 77
+// against 130, 2000 + 7 x 864 94 against 128; 2048: 3600 + 13 x 950 198
+// against 212.
 int ssm_part_of(int H, int wgs, const int* cu, int N, int B, int T) {
   const int part = ssm_part((long long)B * T, H, wgs);
   long long longest = T, parts = 0;

@@ -25,10 +25,10 @@
 //
 // A state and its gradient per chunk and head, written and read once (2 dk dv 4
 // bytes each way), are the bulk of the traffic beside the inputs.
-// Measured (4 x 8192 tokens, 16 heads of 128 x 128, one group, bf16): 900 us:
-// this kernel 510, sweeps that keep states 130 + 131 (0.54 GB written each, 4.1
-// TB/s), own sums of the parts 59 + 62, chaining 23, last sums 5.  This kernel
-// reads 1.1 GB of states (2.1 TB/s); it is bound by waits: for the states,
+// Measured (4 x 8192 tokens, 16 heads of 128 x 128, one group, bf16): 870 us:
+// this kernel 474, sweeps that keep states 125 + 129 (0.54 GB written each, 4.2
+// TB/s), own sums of the parts 57 + 61, chaining 23, last sums 5.  This kernel
+// reads 1.1 GB of states (2.3 TB/s); it is bound by waits: for the states,
 // which the registers only allow to be fetched two slabs of 32 columns ahead,
 // and at the four barriers of a head.
 //
@@ -42,12 +42,12 @@ namespace kda {
 
 namespace {
 
-// Two sweep work-groups per CU (32K tokens x 16 heads: 895 us in all; one 960,
-// four 935).
+// Two sweep work-groups per CU (32K tokens x 16 heads: 885 us in all; one 954,
+// four 929).
 constexpr int kSweepWgs = 512;
 // Eight waves a chunk: with four, the sums over the heads and the products of
-// one head do not fit the registers (32K tokens x 16 heads: 1101 us in all,
-// with eight 1018).
+// one head do not fit the registers (32K tokens x 16 heads, as first written:
+// 1101 us in all, with eight 1018).
 constexpr int kBwdWaves = 8, kBwdThreads = 64 * kBwdWaves;
 
 struct ChunkBwd {
@@ -440,8 +440,8 @@ __global__ __launch_bounds__(256) void ssm_shares_kernel(const float* __restrict
 }
 
 // Work-groups a group's heads are split over: enough for about one per CU (1000
-// tokens x 32 heads: 127 us; for two per CU, the sums over the shares make it
-// 139).
+// tokens x 32 heads: 128 us; for two per CU, the sums over the shares make it
+// 140).
 int head_shares(long long chunks, int H, int G) {
   long long s = 1;
   while (s < H / G && chunks * G * s < 256) s *= 2;

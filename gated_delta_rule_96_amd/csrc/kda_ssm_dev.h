@@ -12,10 +12,12 @@ constexpr int kQ = kSeqChunk;   // tokens per chunk
 
 // Softplus(x) = log(1 + e^x) = max(x, 0) + log1p(u), u = e^-|x| in (0, 1], with
 // log1p(u) = 2 artanh(z), z = u / (2 + u) <= 1/3, by its series (the first
-// term left out is below 2e-9 of the sum): relative accuracy also for very
-// negative x, where the result is e^x.  e^-|x| as 2^(n + r) with the rounding
-// r of the product by log2(e) put back, so that large |x| costs no accuracy;
-// e^-|x| is zero from |x| = 200 on (also for infinities; NaN stays NaN).
+// term left out is below 2e-9 of the sum): relative accuracy also for
+// negative x, where the result is e^x, down to x = -87.3; below it e^x is not a
+// normal fp32 number and the result 0 (v_exp_f32 gives no smaller ones).
+// e^-|x| as 2^(n + r) with the rounding r of the product by log2(e) put back, so
+// that large |x| costs no accuracy; |x| counts as 200 at most, so that
+// infinities need no case of their own (NaN stays NaN).
 __device__ __forceinline__ float softplus_f(float x) {
   const float ax = fabsf(x), m = ax > 200.f ? -200.f : -ax;
   const float n = m * kLog2e;

@@ -126,9 +126,10 @@ __global__ __launch_bounds__(kSsmThreads) void ssm_sweep_f32_kernel(const SweepA
 // The same for bf16: the rows of the next chunk go straight into the other
 // half of LDS while this one's products run (one barrier a chunk), and the
 // four waves take turns at forming the next chunk's weights.  64K tokens x 32
-// heads of 128 x 128, own sums, the first calls of a process: 244 us (rows
-// through registers and two barriers: 289); the products are 98 us of it at 2 GHz (96 matrix instructions
-// a wave and chunk, two waves per SIMD), their splits and LDS operands the rest.
+// heads of 128 x 128, own sums: 206 us (as first written 244 against 289 with
+// rows through registers and two barriers); the products are 98 us of it at 2
+// GHz (96 matrix instructions a wave and chunk, two waves per SIMD), their
+// splits and LDS operands the rest.
 template <int DK, int DV, bool kRev, bool kKeep, bool kLow>
 __global__ __launch_bounds__(kSsmThreads, 2) void ssm_sweep_kernel(const SweepArgs a, const SeqTab sq) {
   typedef bf16 T;

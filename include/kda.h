@@ -388,8 +388,10 @@ int kda_bwd_chunked(const void* q, const void* k, const void* v, const void* g, 
  *     KDA_ERR_SHAPE: the scan with 2^23 (sequence, head) pairs or more, the
  *     convolution with 2^31 or more sequences x channels, its gradients with
  *     2^28 or more weights and biases together.
- *   - No call allocates or synchronises; results do not depend on how the
- *     work is split (no atomics).
+ *   - No call allocates or synchronises.  The same call gives the same bits
+ *     (no atomics).  Sums over tokens and states of the scan may differ in
+ *     their last places with what a sequence is batched or packed with, as
+ *     the sizes of the whole call decide where it is cut.
  */
 
 /*
@@ -495,7 +497,9 @@ int kda_qk_norm_rope_bwd(const void* q, long long ldq, const void* k, long long 
  * fp32 sums, one rounding).  Precondition: A finite; dt A <= 0 is the
  * intended range, larger values are computed as they are and may overflow.
  * A raw step size of -inf under the Softplus is a step of zero: the token
- * leaves the state alone.
+ * leaves the state alone (where its x and B are finite: 0 x NaN is NaN).  A
+ * step whose decay leaves nothing starts the state anew, up to the type's
+ * largest value (where dt B x is finite).
  * Conventions and errors as for the operators above, KDA_ERR_SHAPE also for
  * G not dividing H.
  */
