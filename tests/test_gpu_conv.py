@@ -297,3 +297,14 @@ def test_rows_of_ragged_width_from_any_element(dtype, D, off):
         ref, tol = grads_case(dict(c, dy=dy[0]), lens, True, True)
         check("dw", out["dw"], ref[1], tol[1], torch.float32)
         check("dbias", out["dbias"], ref[2], tol[2], torch.float32)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [64, 37])
+def test_in_place_states_of_more_sequences_than_a_launch_holds(dtype, D):
+    lens = [3] * 126 + [60, 0, 300] + [2, 0] * 60 + [70] + [1] * 10
+    c = make(lens, D, 4, dtype, 15)
+    want = kda.conv_fwd(c["x"][None], c["w"], c["bias"], c["s0"], cu_seqlens=cuts(lens))
+    state = c["s0"].clone()
+    y, _ = kda.conv_fwd(c["x"][None], c["w"], c["bias"], state, st=state, cu_seqlens=cuts(lens))
+    assert torch.equal(y, want[0]) and torch.equal(state, want[1])

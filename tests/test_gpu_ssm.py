@@ -279,3 +279,36 @@ def test_small_steps_behind_a_reset(dtype, soft, big):
 def test_small_steps_behind_a_reset_of_the_largest_step(dtype, soft):
     say(f"ssm reset {dtype} dt=max soft={soft}")
     reset_check(reset_case(dtype, torch.finfo(dtype).max, soft, 40), dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("big", [2.0 ** 17, "max"])
+def test_resets_in_a_sequence_of_several_parts(dtype, big):
+    # parts of 256 tokens: a reset inside a part, on its first and on its last token
+    say(f"ssm reset parts {dtype} dt={big}")
+    T = 1300
+    c = make([T], 2, 1, 64, 64, dtype, 50, soft=False, rate=2.0)
+    c["A"].fill_(-16.0)
+    c["dt"].copy_(0.005 * torch.rand(c["dt"].shape, device="cuda") + 0.002)
+    for t in (100, 256, 767, 1090):
+        c["dt"][t] = torch.finfo(dtype).max if big == "max" else big
+        c["x"][t] = 0
+        c["B"][t] = 0
+    y_ref, h_ref, size, zt = mix.ssm_seq(f64(c["x"]), f64(c["dt"]), f64(c["A"]), f64(c["B"]), f64(c["C"]), f64(c["h0"])[0], f64(c["D"]), None, False)
+    k = (250 + 4 * (T // 64 + 1)) * U
+    y, ht = call(c, [T])
+    torch.cuda.synchronize()
+    check("ht", ht[0], h_ref, zt * k, torch.float32)
+    check("y", y[0], y_ref, size * (k + (2 ** -8 * 1.01 if dtype == torch.bfloat16 else 0)), dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_in_place_states_of_more_sequences_than_a_launch_holds(dtype):
+    # 260 sequences, three launches, some cut into parts
+    lens = [3] * 126 + [600, 0, 300] + [2, 0] * 60 + [700] + [1] * 10
+    say(f"ssm in place {dtype} N={len(lens)}")
+    c = make(lens, 2, 1, 64, 64, dtype, 51, rate=2.0)
+    want = call(c, lens)
+    state = c["h0"].clone()
+    y, ht = call(dict(c, h0=state), lens, ht=state)
+    assert ht.data_ptr() == state.data_ptr() and torch.equal(y, want[0]) and torch.equal(state, want[1])
