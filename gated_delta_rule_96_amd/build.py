@@ -24,7 +24,8 @@ BUILD = PKG / "_build"
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["kda_api.cpp", "kda_mix_api.cpp", "kda_decay.hip", "kda_chunk.hip", "kda_decode.hip", "kda_bwd.hip", "kda_noalloc.hip",
-           "kda_conv.hip", "kda_qknorm.hip", "kda_ssm.hip", "kda_ssm_bwd.hip"]
+           "kda_conv.hip", "kda_qknorm.hip", "kda_ssm.hip", "kda_ssm_bwd.hip", "kda_block_api.cpp", "kda_rmsnorm.hip",
+           "kda_gemm8.hip", "kda_lru.hip", "kda_lru_bwd.hip"]
 
 COMMON = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -224,4 +224,63 @@ size_t ssm_bwd_workspace_bytes(int is_packed, int N, int B, int T, int H, int G,
 hipError_t launch_ssm_bwd(int is_bf16, const SsmBwdArgs& a, int dk, int dv, const int* cu, int N, int B, int T, void* workspace,
                           hipStream_t stream);
 
+// Norm of the residual stream with the residual's addition: see kda_rmsnorm.hip.
+struct NormArgs {
+  const void* x;         // rows: the addend (forward), h (backward)
+  long long ldx;
+  const void* res;       // forward: rows of the stream or null; backward: dh, contiguous, or null
+  long long ldr;
+  const float* w;        // [D] or null
+  void* sum;             // forward: h, contiguous
+  void* y;               // forward: the norm (8-bit with scale); backward: dx
+  float* scale;          // forward: [rows][blocks of 128], or null
+  const void* dy;        // backward
+  float* part;           // backward workspace, or null
+  long long rows;
+  int D;
+  float eps;
+};
+hipError_t launch_norm_fwd(int is_bf16, int sum_bf16, const NormArgs& a, hipStream_t stream);
+size_t norm_bwd_workspace_bytes(long long rows, int D);
+hipError_t launch_norm_bwd(int is_bf16, int dy_bf16, const NormArgs& a, float* dw, hipStream_t stream);
+
+// Product of 8-bit rows and weights with scales by blocks: see kda_gemm8.hip.
+struct Gemm8Args {
+  const unsigned char* a;   // rows [M][K]
+  long long lda;
+  const float* sa;          // rows [M][KB]
+  long long lsa;
+  const unsigned char* w;   // [N][K]
+  const float* sw;          // [NB][KB]
+  void* c;                  // [M][N]
+  long long M;
+  int N, K;
+};
+hipError_t launch_gemm8(int out_bf16, const Gemm8Args& g, hipStream_t stream);
+
+// Gated linear recurrence, one state a channel: see kda_lru.hip, kda_lru_bwd.hip.
+struct LruArgs {
+  const void *x, *r, *i;             // rows [tokens][D]; i may be null
+  long long ldx, ldr, ldi;
+  const float* c;                    // [D] or null
+  const float* h0;                   // [N][D] or null
+  float* ht;                         // [N][D] or null
+  void* y;                           // [tokens][D]
+  int unit, D;
+};
+size_t lru_workspace_bytes(int is_packed, int N, int B, int T, int D);
+hipError_t launch_lru_fwd(int is_bf16, const LruArgs& a, const int* cu, int N, int B, int T, void* workspace, hipStream_t stream);
+// One token per sequence: state h0 -> ht (may be the same).
+hipError_t launch_lru_step(int is_bf16, const LruArgs& a, int B, hipStream_t stream);
+struct LruBwdArgs {
+  LruArgs f;                         // ht and y unused
+  const void* dy;                    // [tokens][D]
+  const float* dht;                  // [N][D] or null
+  void *dx, *dr, *di;                // [tokens][D]; di null without i
+  float* dc;                         // [D] or null
+  float* dh0;                        // [N][D] or null
+};
+size_t lru_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D);
+hipError_t launch_lru_bwd(int is_bf16, const LruBwdArgs& a, const int* cu, int N, int B, int T, void* workspace, hipStream_t stream);
+
 }  // namespace kda

@@ -1,0 +1,284 @@
+// Gradients of the gated linear recurrence (kda_lru_dev.h has the forward's
+// formulas).  With l_t = dL/dh_t and e_t = a_t l_t what a token hands to the one
+// before it:
+//   l_t = dy_t + e_{t+1}  (e behind the last token: dht),  dh0 = e_1
+//   dx = l m s,   di = l m x s (1 - s),   s = Sigmoid(i)
+//   dg = a (l h_{t-1} - l s x a / m)      (the second term with unit only)
+//   dr = dg g (1 - Sigmoid(r)),  dc = -sum dg Sigmoid(r)   (dr = dg without c)
+// A part of a sequence (as in the forward) takes e from the right by
+// e -> P e + K with K = sum_t P_t dy_t, P_t the product of its a up to t.
+// Where m = 0 (a decay of exactly 1) its derivative counts as 0.
+//
+// Three launches: every part's P, H, K; the states and the e that enter the
+// parts; the gradients.  The last walks the parts from the end, so that what
+// the first read last is still in the cache.
+#include "kda_lru_dev.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kWaves = 8;
+template <typename T> struct RunOf { static constexpr int R = 16; };   // tokens of a wave's run
+template <> struct RunOf<float> { static constexpr int R = 8; };
+template <typename T> constexpr int part_of() { return kWaves * RunOf<T>::R; }
+
+// A run's rows as loaded.
+template <typename T, int NC, int R> struct BwdRun {
+  LruPack<T, NC> x[R], r[R], i[R], dy[R];
+};
+template <typename T, int NC, int R>
+__device__ __forceinline__ void load_rows(const LruBwdArgs& b, const SeqPart& p, const LruLane& l, int t, BwdRun<T, NC, R>& w) {
+  typedef LruPack<T, NC> Pk;
+  if (t >= p.t1) return;
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const size_t row = p.start + (size_t)min(t + k, p.t1 - 1);
+    w.x[k] = *reinterpret_cast<const Pk*>((const T*)b.f.x + row * (size_t)b.f.ldx + l.cl);
+    w.r[k] = *reinterpret_cast<const Pk*>((const T*)b.f.r + row * (size_t)b.f.ldr + l.cl);
+    if (b.f.i) w.i[k] = *reinterpret_cast<const Pk*>((const T*)b.f.i + row * (size_t)b.f.ldi + l.cl);
+    w.dy[k] = *reinterpret_cast<const Pk*>((const T*)b.dy + row * (size_t)b.f.D + l.cl);
+  }
+}
+
+// a and u of a run, and its P, H and K.  Tokens past the part's end leave
+// everything as it is (a = 1, u = 0, dy = 0).
+template <typename T, int NC, int R>
+__device__ __forceinline__ void run_sums(const LruMode& md, const float (&c)[NC], const BwdRun<T, NC, R>& w, int n, float (&a)[R][NC], float (&u)[R][NC],
+                                         float (&P)[NC], float (&H)[NC], float (&K)[NC]) {
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    P[j] = 1.f;
+    H[j] = K[j] = 0.f;
+  }
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      a[k][j] = 1.f;
+      u[k][j] = 0.f;
+      if (k < n) {
+        lru_gates<T>(md, c[j], to_f32(w.x[k].v[j]), to_f32(w.r[k].v[j]), md.igate ? to_f32(w.i[k].v[j]) : 0.f, a[k][j], u[k][j]);
+        P[j] *= a[k][j];
+        H[j] = fmaf(a[k][j], H[j], u[k][j]);
+        K[j] = fmaf(P[j], to_f32(w.dy[k].v[j]), K[j]);
+      }
+    }
+}
+
+// seg [items][3][D]: P, H, K of every part.
+template <typename T, int NC>
+__global__ __launch_bounds__(64 * kWaves) void lru_bwd_part_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, float* seg) {
+  constexpr int R = RunOf<T>::R;
+  __shared__ float red[3][kWaves][64 * NC];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = b.f.D;
+  const unsigned item = blockIdx.x / slices;
+  const LruLane l = lru_lane<NC>((int)(blockIdx.x - item * slices), D);
+  const SeqPart p = seq_part(s, (int)item);
+  const int t = p.t0 + wave * R;
+  BwdRun<T, NC, R> w;
+  load_rows<T, NC, R>(b, p, l, t, w);
+  float a[R][NC], u[R][NC], c[NC], P[NC], H[NC], K[NC];
+  lru_coef<NC>(b.f, l, c);
+  run_sums<T, NC, R>(lru_mode(b.f), c, w, p.t1 - t, a, u, P, H, K);
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    red[0][wave][lane * NC + j] = P[j];
+    red[1][wave][lane * NC + j] = H[j];
+    red[2][wave][lane * NC + j] = K[j];
+  }
+  __syncthreads();
+  if (wave || !l.live) return;
+#pragma unroll
+  for (int q = 1; q < kWaves; ++q)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const float f = red[0][q][lane * NC + j];
+      K[j] = fmaf(P[j], red[2][q][lane * NC + j], K[j]);
+      H[j] = fmaf(f, H[j], red[1][q][lane * NC + j]);
+      P[j] *= f;
+    }
+  float* to = seg + (size_t)item * 3 * D + l.c;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    to[j] = P[j];
+    to[D + j] = H[j];
+    to[2 * D + j] = K[j];
+  }
+}
+
+// What enters a sequence's parts: states over H, e from the right over K.
+__global__ __launch_bounds__(64) void lru_bwd_chain_kernel(const LruBwdArgs b, const SeqTab s, float* seg) {
+  const int D = b.f.D, blocks = (D + 63) / 64, li = blockIdx.x / blocks, c = (blockIdx.x - li * blocks) * 64 + threadIdx.x;
+  if (c >= D) return;
+  const int n = s.n0 + li;
+  const int i0 = s.n ? s.cc[li] : li * s.parts, i1 = s.n ? s.cc[li + 1] : i0 + s.parts;
+  float h = b.f.h0 ? b.f.h0[(size_t)n * D + c] : 0.f;
+#pragma unroll 8
+  for (int i = i0; i < i1; ++i) {
+    float* at = seg + (size_t)i * 3 * D + c;
+    const float P = at[0], H = at[D];
+    at[D] = h;
+    h = fmaf(P, h, H);
+  }
+  float e = b.dht ? b.dht[(size_t)n * D + c] : 0.f;
+#pragma unroll 8
+  for (int i = i1 - 1; i >= i0; --i) {
+    float* at = seg + (size_t)i * 3 * D + c;
+    const float P = at[0], K = at[2 * D];
+    at[2 * D] = e;
+    e = fmaf(P, e, K);
+  }
+  if (b.dh0) b.dh0[(size_t)n * D + c] = e;
+}
+
+// Gradients.  dcp [items][D]: every part's sum of dg Sigmoid(r), or null.
+template <typename T, int NC>
+__global__ __launch_bounds__(64 * kWaves) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
+  constexpr int R = RunOf<T>::R;
+  typedef LruPack<T, NC> Pk;
+  __shared__ float red[3][kWaves][64 * NC];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = b.f.D;
+  const unsigned id = gridDim.x - 1 - blockIdx.x, item = id / slices;
+  const LruLane l = lru_lane<NC>((int)(id - item * slices), D);
+  const SeqPart p = seq_part(s, (int)item);
+  const int t = p.t0 + wave * R, n = p.t1 - t;
+  const LruMode md = lru_mode(b.f);
+  BwdRun<T, NC, R> w;
+  load_rows<T, NC, R>(b, p, l, t, w);
+  float a[R][NC], u[R][NC], c[NC], P[NC], H[NC], K[NC], h[NC], e[NC], sum[NC];
+  lru_coef<NC>(b.f, l, c);
+  const float* from = seg + (size_t)item * 3 * D + l.cl;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    h[j] = from[D + j];
+    e[j] = from[2 * D + j];
+    sum[j] = 0.f;
+  }
+  run_sums<T, NC, R>(md, c, w, n, a, u, P, H, K);
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    red[0][wave][lane * NC + j] = P[j];
+    red[1][wave][lane * NC + j] = H[j];
+    red[2][wave][lane * NC + j] = K[j];
+  }
+  __syncthreads();
+  for (int q = 0; q < wave; ++q)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) h[j] = fmaf(red[0][q][lane * NC + j], h[j], red[1][q][lane * NC + j]);
+  for (int q = kWaves - 1; q > wave; --q)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) e[j] = fmaf(red[0][q][lane * NC + j], e[j], red[2][q][lane * NC + j]);
+  // u becomes the state before its token
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const float before = h[j];
+      h[j] = fmaf(a[k][j], h[j], u[k][j]);
+      u[k][j] = before;
+    }
+#pragma unroll
+  for (int k = R - 1; k >= 0; --k) {
+    if (k >= n) continue;
+    Pk dx, dr, di;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      const float x = to_f32(w.x[k].v[j]), r = to_f32(w.r[k].v[j]), av = a[k][j];
+      float sr = 1.f, tr = 1.f, g = r, si = 1.f, ti = 0.f, m = 1.f, im = 0.f;   // t: 1 - Sigmoid
+      if (md.gate) {
+        const float q = exp2_fast(-r * kLog2e);
+        sr = __builtin_amdgcn_rcpf(1.f + q);
+        tr = q > 1.f ? 1.f - sr : q * sr;
+        g = -c[j] * sr;
+      }
+      if (md.igate) {
+        const float q = exp2_fast(-to_f32(w.i[k].v[j]) * kLog2e);
+        si = __builtin_amdgcn_rcpf(1.f + q);
+        ti = q > 1.f ? 1.f - si : q * si;
+      }
+      if (md.unit) {
+        float unused;
+        m = __builtin_amdgcn_sqrtf(one_minus_decay<T>(g, unused) * (1.f + av));
+        im = m > 0.f ? __builtin_amdgcn_rcpf(m) : 0.f;
+      }
+      const float lt = to_f32(w.dy[k].v[j]) + e[j], lm = lt * m * si, ls = lt * si * x;
+      const float dg = av * (lt * u[k][j] - ls * av * im);
+      dx.v[j] = from_f32<T>(lm);
+      di.v[j] = from_f32<T>(lm * x * ti);
+      dr.v[j] = from_f32<T>(md.gate ? dg * g * tr : dg);
+      sum[j] = fmaf(dg, sr, sum[j]);
+      e[j] = av * lt;
+    }
+    if (l.live) {
+      const size_t at = (p.start + (size_t)(t + k)) * D + l.c;
+      *reinterpret_cast<Pk*>((T*)b.dx + at) = dx;
+      *reinterpret_cast<Pk*>((T*)b.dr + at) = dr;
+      if (md.igate) *reinterpret_cast<Pk*>((T*)b.di + at) = di;
+    }
+  }
+  if (!dcp) return;
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < NC; ++j) red[0][wave][lane * NC + j] = sum[j];
+  __syncthreads();
+  if (wave || !l.live) return;
+#pragma unroll
+  for (int q = 1; q < kWaves; ++q)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) sum[j] += red[0][q][lane * NC + j];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) dcp[(size_t)item * D + l.c + j] = -sum[j];
+}
+
+bool pairs(const LruBwdArgs& b, size_t esz) {
+  const LruArgs& a = b.f;
+  if (a.D % 2 || a.ldx % 2 || a.ldr % 2 || (a.i && a.ldi % 2)) return false;
+  for (const void* p : {a.x, a.r, a.i, b.dy, (const void*)b.dx, (const void*)b.dr, (const void*)b.di})
+    if (reinterpret_cast<uintptr_t>(p) % (2 * esz)) return false;
+  return true;
+}
+
+size_t all_items(int is_packed, int N, int B, int T, int part) {
+  return is_packed ? (size_t)T / part + (size_t)N : (size_t)B * (((size_t)T + part - 1) / part);
+}
+
+template <typename T, int NC>
+hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, float* ws, hipStream_t st) {
+  constexpr int kPart = part_of<T>();
+  const int D = b.f.D;
+  const unsigned slices = (unsigned)((D + 64 * NC - 1) / (64 * NC));
+  if (!seq_tabs_fit(cu, N, B, T_, kPart, max_groups(64 * kWaves) / slices)) return hipErrorInvalidConfiguration;
+  float* dcp = b.dc ? ws : nullptr;
+  float* seg = ws + all_items(cu != nullptr, N, B, T_, kPart) * D;
+  size_t rows = 0;
+  const int end = cu ? N : B;
+  for (int n = 0; n < end;) {
+    SeqTab s;
+    n = make_seq_tab(s, cu, N, n, B, T_, kPart);
+    const int seqs = s.n ? s.n : B;
+    const dim3 grid((unsigned)s.items * slices), th(64 * kWaves);
+    hipLaunchKernelGGL((lru_bwd_part_kernel<T, NC>), grid, th, 0, st, b, s, slices, seg);
+    hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)((D + 63) / 64) * (unsigned)seqs), dim3(64), 0, st, b, s, seg);
+    hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC>), grid, th, 0, st, b, s, slices, seg, dcp ? dcp + rows * D : nullptr);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    rows += s.items;
+  }
+  return dcp ? launch_sum_rows(dcp, rows, (unsigned)D, 0, 0, b.dc, nullptr, nullptr, st) : hipSuccess;
+}
+
+}  // namespace
+
+size_t lru_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D) {
+  // the shorter parts of fp32 inputs need more
+  return (all_items(is_packed, N, B, T, part_of<float>()) * 4 * D * sizeof(float) + 255) & ~(size_t)255;
+}
+
+hipError_t launch_lru_bwd(int is_bf16, const LruBwdArgs& b, const int* cu, int N, int B, int T, void* workspace, hipStream_t st) {
+  float* ws = static_cast<float*>(workspace);
+  if (is_bf16) return pairs(b, 2) ? bwd_go<bf16, 2>(b, cu, N, B, T, ws, st) : bwd_go<bf16, 1>(b, cu, N, B, T, ws, st);
+  return pairs(b, 4) ? bwd_go<float, 2>(b, cu, N, B, T, ws, st) : bwd_go<float, 1>(b, cu, N, B, T, ws, st);
+}
+
+}  // namespace kda

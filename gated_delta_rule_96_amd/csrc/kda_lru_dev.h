@@ -1,0 +1,78 @@
+// Gated linear recurrence with one state a channel: its gates, and the tiles
+// of tokens and channels that the forward (kda_lru.hip) and the gradients
+// (kda_lru_bwd.hip) share.
+//
+//   g_t = -c Sigmoid(r_t), or r_t itself;   a_t = e^{g_t}
+//   m_t = sqrt(1 - a_t^2), or 1;            u_t = m_t Sigmoid(i_t) x_t
+//   h_t = a_t h_{t-1} + u_t,                y_t = h_t
+// Over a run of tokens the state moves by h -> P h + H with P the product of
+// the run's a and H its own state from zero; runs join by
+// (P, H) then (P', H') = (P P', P' H + H').
+#pragma once
+#include "kda_rows.h"
+
+namespace kda {
+
+template <typename T, int NC> struct alignas(sizeof(T) * NC) LruPack {   // NC channels of a token as loaded
+  T v[NC];
+};
+
+// a = e^g, g <= 0, by way of d = 1 - a from the series of 1 - e^g where g is
+// small: a is then within half a unit of its last place to either side (the
+// exponential instruction's error has a bias, which a state that remembers
+// thousands of tokens adds up), and 1 - a^2 = d (1 + a) loses nothing near
+// a = 1.  Four terms below 2^-4 (bf16 inputs: what is left out is 2^-23 of d),
+// eight below 2^-1 (2^-26).
+template <typename T> __device__ __forceinline__ float one_minus_decay(float g, float& a) {
+  constexpr bool kShort = sizeof(T) == 2;
+  float s = kShort ? 1.f / 24 : 1.f / 40320;
+  if (!kShort) {
+    s = fmaf(g, s, 1.f / 5040);
+    s = fmaf(g, s, 1.f / 720);
+    s = fmaf(g, s, 1.f / 120);
+    s = fmaf(g, s, 1.f / 24);
+  }
+  s = fmaf(g, s, 1.f / 6);
+  s = fmaf(g, s, 0.5f);
+  s = -g * fmaf(g, s, 1.f);
+  const float e = exp2_fast(g * kLog2e);
+  const bool near = g > (kShort ? -0.0625f : -0.5f);
+  a = near ? 1.f - s : e;
+  return near ? s : 1.f - e;
+}
+
+// What a call is made of, the same for all lanes.
+struct LruMode {
+  bool gate, igate, unit;
+};
+__device__ __forceinline__ LruMode lru_mode(const LruArgs& a) { return LruMode{a.c != nullptr, a.i != nullptr, a.unit != 0}; }
+
+// a and u of one channel of a token (c: the channel's coefficient).
+template <typename T>
+__device__ __forceinline__ void lru_gates(const LruMode& md, float c, float x, float r, float i, float& a, float& u) {
+  const float g = md.gate ? -c * sigmoid_fast(r) : r;
+  const float d = one_minus_decay<T>(g, a);
+  u = md.igate ? x * sigmoid_fast(i) : x;
+  if (md.unit) u *= __builtin_amdgcn_sqrtf(d * (1.f + a));
+}
+
+// Channels of a wave's lane: NC neighbours from c on; lanes past D do the last
+// ones' loads and store nothing.
+struct LruLane {
+  int c, cl;   // channel, channel to load from
+  bool live;
+};
+template <int NC> __device__ __forceinline__ LruLane lru_lane(int slice, int D) {
+  LruLane l;
+  l.c = (slice * 64 + (int)(threadIdx.x & 63)) * NC;
+  l.live = l.c < D;
+  l.cl = l.live ? l.c : 0;
+  return l;
+}
+
+template <int NC> __device__ __forceinline__ void lru_coef(const LruArgs& a, const LruLane& l, float (&c)[NC]) {
+#pragma unroll
+  for (int k = 0; k < NC; ++k) c[k] = a.c ? a.c[l.cl + k] : 0.f;
+}
+
+}  // namespace kda

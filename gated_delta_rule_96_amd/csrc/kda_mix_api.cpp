@@ -8,53 +8,20 @@
 #include "kda_launch.h"
 
 using kda::aligned16;
+using kda::check_cu;
 using kda::elem_size;
-using kda::overlap;
+using kda::hip_status;
+using kda::kMaxT;
+using kda::rows_bytes;
 using kda::size_ok;
+using kda::Span;
+using kda::spans_apart;
 using kda::valid_dtype;
 
 namespace {
 
-constexpr int kMaxT = 1 << 30;
 // Heads are numbered in 32 bits, up to a wave's 32 beyond the last one.
 constexpr int kMaxHeads = 1 << 24;
-
-// A span of memory an argument covers.
-struct Span {
-  const void* p;
-  size_t n;
-};
-// Whether an output overlaps an input or another output; an output that
-// starts where inputs[same] starts and covers the same bytes is that input
-// replaced in place (same < 0: never).
-template <int NI, int NO>
-bool spans_apart(const Span (&in)[NI], const Span (&out)[NO], const int (&same)[NO]) {
-  for (int o = 0; o < NO; ++o) {
-    for (int i = 0; i < NI; ++i) {
-      if (i == same[o] && in[i].p == out[o].p && in[i].n == out[o].n) continue;
-      if (overlap(in[i].p, in[i].n, out[o].p, out[o].n)) return false;
-    }
-    for (int k = 0; k < o; ++k)
-      if (overlap(out[k].p, out[k].n, out[o].p, out[o].n)) return false;
-  }
-  return true;
-}
-// Bytes from the first to the last element of `rows` rows of n elements, ld
-// apart.
-size_t rows_bytes(size_t rows, long long ld, size_t n, size_t esz) { return ((rows - 1) * (size_t)ld + n) * esz; }
-
-int check_cu(const int* cu, int N, int B, int T) {
-  if (!cu) return KDA_OK;
-  if (B != 1 || N <= 0 || cu[0] != 0 || cu[N] != T) return KDA_ERR_SHAPE;
-  for (int i = 0; i < N; ++i)
-    if (cu[i + 1] < cu[i]) return KDA_ERR_SHAPE;
-  return KDA_OK;
-}
-
-// (hipErrorInvalidConfiguration: sizes beyond a launch's, see max_groups)
-int hip_status(hipError_t e) {
-  return e == hipSuccess ? KDA_OK : e == hipErrorInvalidConfiguration ? KDA_ERR_SHAPE : KDA_ERR_HIP;
-}
 
 // Sizes and strides of the convolution's x.
 int check_conv(const void* x, long long ldx, const float* w, const float* bias, int flags, int dtype, int B, int T, int D, int W) {

@@ -1,0 +1,290 @@
+// Root-mean-square norm of the residual stream with the residual's addition,
+// its output in the input's type or in 8 bits with scales, and its gradients.
+//
+// A row is one token, D channels:
+//   h = x + res, rounded to the stream's type (h = x without a residual)
+//   n = w h r,  r = 1 / sqrt(mean(h^2) + eps)
+//   y = n, or q = e4m3(n / s) with one s = max |n| / 448 for every 128 channels
+// The norm is that of the rounded h, so that the backward, which has h in
+// hand, differentiates what the forward computed.
+// Backward, u = h r:  dx = r (w dy - u mean(w dy u)) + dh;  dw = sum dy u.
+//
+// Bound by HBM: one pass, every row read and written once.  A row is held in
+// registers by one wave (up to 2048 channels), four or sixteen, eight
+// neighbouring channels a lane, so 16 lanes hold the 128 channels of a scale
+// and its maximum stays inside a DPP row.  All arithmetic is fp32 up to the
+// one rounding of each output.
+#include "kda_rows.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kE4m3Max = 448.f;
+// A block whose largest |n| is below this has scale 1 and zeros (448 / max
+// would overflow below 2^-119).
+constexpr float kBlockMin = 0x1p-100f;
+
+template <typename T> struct Raw8;   // eight channels as loaded
+template <> struct Raw8<bf16> {
+  bf16x8 v;
+  __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const bf16x8*>(p); }
+  __device__ __forceinline__ float at(int i) const { return (float)v[i]; }
+};
+template <> struct Raw8<float> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = load4(p);
+    b = load4(p + 4);
+  }
+  __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i] : b[i - 4]; }
+};
+
+// Sum over a wave's 64 lanes, in every lane.
+__device__ __forceinline__ float wave_sum(float x) {
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) x += __shfl_xor(x, off);
+  return x;
+}
+
+// Largest x >= 0 of each 16 lanes, in all of them.
+__device__ __forceinline__ float max16(float x) {
+  x = fmaxf(x, dpp_f<0xB1>(x));    // quad_perm [1,0,3,2]
+  x = fmaxf(x, dpp_f<0x4E>(x));    // quad_perm [2,3,0,1]
+  x = fmaxf(x, dpp_f<0x141>(x));   // row_half_mirror
+  return fmaxf(x, dpp_f<0x140>(x));   // row_mirror
+}
+
+// Sums over the W waves that share a row.  `red` has two sets of slots, used
+// by turns, so one barrier a row is enough: a wave overwrites a set only
+// behind the next row's barrier, which every wave passes after its reads.
+template <int W, int N>
+__device__ __forceinline__ void row_sum(float (&s)[N], float (*red)[N][W], int turn, int wave) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = wave_sum(s[k]);
+  if (W == 1) return;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[turn][k][wave] = s[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    s[k] = 0.f;
+#pragma unroll
+    for (int q = 0; q < W; ++q) s[k] += red[turn][k][q];
+  }
+}
+
+// Vector j of a lane: channels 8 (j 64 W + lane) .. + 7 (lane of the W waves).
+template <int W> __device__ __forceinline__ int channel(int j, int lane) { return 8 * (j * (64 * W) + lane); }
+
+template <int NV, int W> __device__ __forceinline__ void load_weights(const float* w, int D, int lane, float (&wv)[NV][8]) {
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = channel<W>(j, lane);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wv[j][i] = 1.f;
+    if (w && c < D) Rows<float, 8>::load(w + c, wv[j]);
+  }
+}
+
+// T: type of x and of y; TH: type of the stream (res and h).
+template <typename T, typename TH, bool kRes, bool kFp8, int NV, int W>
+__global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_fwd_kernel(const NormArgs a, long long groups) {
+  __shared__ float red[2][1][W];
+  constexpr int kPer = W >= 4 ? 1 : kThreads / 64;   // rows a work-group holds at once
+  const int lane = W == 1 ? (threadIdx.x & 63) : threadIdx.x, wave = threadIdx.x >> 6, D = a.D;
+  const float inv = 1.f / (float)D;
+  float w[NV][8];
+  load_weights<NV, W>(a.w, D, lane, w);
+  int turn = 0;
+  for (long long m = (long long)blockIdx.x * kPer + (W == 1 ? wave : 0); m < a.rows; m += groups * kPer, turn ^= 1) {
+    Raw8<T> x[NV];
+    Raw8<TH> r[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = channel<W>(j, lane);
+      if (c < D) {
+        x[j].load((const T*)a.x + m * a.ldx + c);
+        if (kRes) r[j].load((const TH*)a.res + m * a.ldr + c);
+      }
+    }
+    float h[NV][8], sq[1] = {0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = channel<W>(j, lane);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = 0.f;
+      if (c < D) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] = kRes ? to_f32(from_f32<TH>(x[j].at(i) + r[j].at(i))) : x[j].at(i);
+        if (kRes) Rows<TH, 8>::store((TH*)a.sum + m * D + c, h[j]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sq[0] = fmaf(h[j][i] * inv, h[j][i], sq[0]);
+    }
+    row_sum<W, 1>(sq, red, turn, wave);
+    const float rn = 1.f / sqrtf(sq[0] + a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = channel<W>(j, lane);
+      float n[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n[i] = h[j][i] * rn * w[j][i];
+      if (kFp8) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(n[i]));
+        top = max16(top);   // (lanes past D hold zeros)
+        const bool live = top >= kBlockMin;
+        const float q = live ? kE4m3Max / top : 1.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = live || n[i] != n[i] ? n[i] * q : 0.f;
+        int lo = __builtin_amdgcn_cvt_pk_fp8_f32(n[0], n[1], 0, false);
+        lo = __builtin_amdgcn_cvt_pk_fp8_f32(n[2], n[3], lo, true);
+        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(n[4], n[5], 0, false);
+        hi = __builtin_amdgcn_cvt_pk_fp8_f32(n[6], n[7], hi, true);
+        if (c < D) {
+          *reinterpret_cast<int2*>((unsigned char*)a.y + m * D + c) = make_int2(lo, hi);
+          if ((lane & 15) == 0) a.scale[m * ((D + 127) / 128) + (c >> 7)] = live ? top / kE4m3Max : 1.f;
+        }
+      } else if (c < D) {
+        Rows<T, 8>::store((T*)a.y + m * D + c, n);
+      }
+    }
+  }
+}
+
+// Gradients.  T: type of h, dh and dx; TG: type of dy.  Each row holder (one
+// wave, or a work-group) walks its rows and keeps the sums of dw of its
+// channels; they are a partial row of the workspace.
+template <typename T, typename TG, int NV, int W>
+__global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_bwd_kernel(const NormArgs a, long long groups) {
+  __shared__ float red[2][2][W];
+  constexpr int kPer = W >= 4 ? 1 : kThreads / 64;
+  const int lane = W == 1 ? (threadIdx.x & 63) : threadIdx.x, wave = threadIdx.x >> 6, D = a.D;
+  const float inv = 1.f / (float)D;
+  float w[NV][8], dw[NV][8];
+  load_weights<NV, W>(a.w, D, lane, w);
+#pragma unroll
+  for (int j = 0; j < NV; ++j)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
+  const long long holder = (long long)blockIdx.x * kPer + (W == 1 ? wave : 0);
+  int turn = 0;
+  for (long long m = holder; m < a.rows; m += groups * kPer, turn ^= 1) {
+    Raw8<T> h[NV], s[NV];
+    Raw8<TG> g[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = channel<W>(j, lane);
+      if (c < D) {
+        h[j].load((const T*)a.x + m * a.ldx + c);
+        g[j].load((const TG*)a.dy + m * D + c);
+        if (a.res) s[j].load((const T*)a.res + m * D + c);
+      }
+    }
+    float sum[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (channel<W>(j, lane) < D)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = h[j].at(i) * inv;
+          sum[0] = fmaf(v, h[j].at(i), sum[0]);
+          sum[1] = fmaf(g[j].at(i) * w[j][i], v, sum[1]);
+        }
+    row_sum<W, 2>(sum, red, turn, wave);
+    // dx = r (w dy - u mean(w dy h) r): no power of r alone
+    const float rn = 1.f / sqrtf(sum[0] + a.eps), k = sum[1] * rn;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = channel<W>(j, lane);
+      if (c >= D) continue;
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float u = h[j].at(i) * rn, gy = g[j].at(i);
+        dw[j][i] = fmaf(gy, u, dw[j][i]);
+        o[i] = rn * (gy * w[j][i] - u * k);
+        if (a.res) o[i] += s[j].at(i);
+      }
+      Rows<T, 8>::store((T*)a.y + m * D + c, o);
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = channel<W>(j, lane);
+    if (c < D) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<f32x4*>(a.part + holder * D + c + 4 * q) = f32x4{dw[j][4 * q], dw[j][4 * q + 1], dw[j][4 * q + 2], dw[j][4 * q + 3]};
+    }
+  }
+}
+
+// Work-groups at most.
+constexpr int kFwdGroups = 2048, kBwdGroups = 512;
+
+// Waves that hold a row of D channels.
+int row_waves(int D) { return D <= 2048 ? 1 : D <= 8192 ? 4 : 16; }
+unsigned norm_groups(long long rows, int D, int most) {
+  const int per = row_waves(D) >= 4 ? 1 : kThreads / 64;
+  const long long g = (rows + per - 1) / per;
+  return (unsigned)(g < most ? g : most);
+}
+long long part_rows(long long rows, int D) {
+  return (long long)norm_groups(rows, D, kBwdGroups) * (row_waves(D) >= 4 ? 1 : kThreads / 64);
+}
+
+// The instance for rows of D channels.
+#define KDA_NORM_BY_WIDTH(kernel, ...)                                                                           \
+  do {                                                                                                           \
+    const dim3 grid(groups), th(row_waves(a.D) == 16 ? 1024 : kThreads);                                         \
+    if (a.D <= 512) hipLaunchKernelGGL((kernel<__VA_ARGS__, 1, 1>), grid, th, 0, st, a, (long long)groups);      \
+    else if (a.D <= 1024) hipLaunchKernelGGL((kernel<__VA_ARGS__, 2, 1>), grid, th, 0, st, a, (long long)groups); \
+    else if (a.D <= 2048) hipLaunchKernelGGL((kernel<__VA_ARGS__, 4, 1>), grid, th, 0, st, a, (long long)groups); \
+    else if (a.D <= 4096) hipLaunchKernelGGL((kernel<__VA_ARGS__, 2, 4>), grid, th, 0, st, a, (long long)groups); \
+    else if (a.D <= 8192) hipLaunchKernelGGL((kernel<__VA_ARGS__, 4, 4>), grid, th, 0, st, a, (long long)groups); \
+    else hipLaunchKernelGGL((kernel<__VA_ARGS__, 2, 16>), grid, th, 0, st, a, (long long)groups);                 \
+    return hipGetLastError();                                                                                    \
+  } while (0)
+
+template <typename T, typename TH, bool kRes, bool kFp8>
+hipError_t fwd_go(const NormArgs& a, hipStream_t st) {
+  const unsigned groups = norm_groups(a.rows, a.D, kFwdGroups);
+  KDA_NORM_BY_WIDTH(norm_fwd_kernel, T, TH, kRes, kFp8);
+}
+template <typename T, typename TH, bool kRes>
+hipError_t fwd_out(const NormArgs& a, hipStream_t st) {
+  return a.scale ? fwd_go<T, TH, kRes, true>(a, st) : fwd_go<T, TH, kRes, false>(a, st);
+}
+template <typename T, typename TG>
+hipError_t bwd_go(const NormArgs& a, hipStream_t st) {
+  const unsigned groups = norm_groups(a.rows, a.D, kBwdGroups);
+  KDA_NORM_BY_WIDTH(norm_bwd_kernel, T, TG);
+}
+
+}  // namespace
+
+hipError_t launch_norm_fwd(int is_bf16, int sum_bf16, const NormArgs& a, hipStream_t st) {
+  if (!a.res) return is_bf16 ? fwd_out<bf16, bf16, false>(a, st) : fwd_out<float, float, false>(a, st);
+  if (!is_bf16) return fwd_out<float, float, true>(a, st);
+  return sum_bf16 ? fwd_out<bf16, bf16, true>(a, st) : fwd_out<bf16, float, true>(a, st);
+}
+
+size_t norm_bwd_workspace_bytes(long long rows, int D) {
+  return ((size_t)part_rows(rows, D) * D * sizeof(float) + 255) & ~(size_t)255;
+}
+
+hipError_t launch_norm_bwd(int is_bf16, int dy_bf16, const NormArgs& a, float* dw, hipStream_t st) {
+  hipError_t e;
+  if (is_bf16) e = dy_bf16 ? bwd_go<bf16, bf16>(a, st) : bwd_go<bf16, float>(a, st);
+  else e = dy_bf16 ? bwd_go<float, bf16>(a, st) : bwd_go<float, float>(a, st);
+  if (e != hipSuccess || !a.part) return e;
+  return launch_sum_rows(a.part, (size_t)part_rows(a.rows, a.D), (unsigned)a.D, 0, 0, dw, nullptr, nullptr, st);
+}
+
+}  // namespace kda

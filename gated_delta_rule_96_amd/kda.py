@@ -28,6 +28,7 @@ KDA_LAYER_QK_L2NORM = 1
 KDA_CONV_SILU = 1
 KDA_QK_RMS, KDA_QK_INTERLEAVED = 1, 2
 KDA_SSM_SOFTPLUS = 1
+KDA_LRU_UNIT = 1
 CHUNK = 64
 GMIN = -5.0
 
@@ -98,6 +99,15 @@ def lib() -> ctypes.CDLL:
                 ("kda_ssm_fwd_chunked", I, [P, LL, P, LL, P, P, LL, P, LL, P, P, P, P, P] + [I] * 8 + [P, I, P, S, P]),
                 ("kda_ssm_step", I, [P, LL, P, LL, P, P, LL, P, LL, P, P, P, P, P] + [I] * 7 + [P]),
                 ("kda_ssm_bwd_workspace_bytes", S, [I] * 8),
+                ("kda_add_rms_norm", I, [P, LL, P, LL, I, P, F, P, P, P, I, LL, I, P]),
+                ("kda_add_rms_norm_bwd_workspace_bytes", S, [LL, I]),
+                ("kda_add_rms_norm_bwd", I, [P, LL, P, F, P, I, P, P, P, I, LL, I, P, S, P]),
+                ("kda_gemm_fp8", I, [P, LL, P, LL, P, P, P, I, LL, I, I, P]),
+                ("kda_lru_workspace_bytes", S, [I] * 4),
+                ("kda_lru_fwd", I, [P, LL, P, LL, P, LL, P, P, P, P, I, I, I, I, I, P, I, P, S, P]),
+                ("kda_lru_step", I, [P, LL, P, LL, P, LL, P, P, P, P, I, I, I, I, P]),
+                ("kda_lru_bwd_workspace_bytes", S, [I] * 4),
+                ("kda_lru_bwd", I, [P, LL, P, LL, P, LL] + [P] * 9 + [I] * 5 + [P, I, P, S, P]),
                 ("kda_ssm_bwd_chunked", I, [P, LL, P, LL, P, P, LL, P, LL] + [P] * 13 + [I] * 8 + [P, I, P, S, P])):
             getattr(L, name).restype = res
             getattr(L, name).argtypes = args
@@ -735,6 +745,166 @@ def ssm_bwd_chunked(x, dt, A, Bm, Cm, dy, h0=None, dht=None, *, D=None, dt_bias=
     _call(dev, "kda_ssm_bwd_chunked", *args, _dense(h0, "h0", st, torch.float32), _dense(dy, "dy", (B, T, H, dv), x.dtype),
           _dense(dht, "dht", st, torch.float32), p["dx"], p["ddt"], p["dA"], p["dB"], p["dC"], p["dD"], p["ddt_bias"], p["dh0"],
           KDA_SSM_SOFTPLUS if softplus else 0, code, B, T, H, G, dk, dv, arr, N, _ptr(ws), ws.numel())
+    return out
+
+
+# ---------------------------------------------------------------- a recurrent block's norm, projection and recurrence
+def _flat_rows(t, name, D):
+    """Pointer, row stride and leading sizes of rows [..., D]: one or two
+    leading dimensions, as for _rows."""
+    lead = tuple(t.shape[:-1])
+    if len(lead) not in (1, 2) or t.shape[-1] != D:
+        raise ValueError(f"{name} must be [rows, {D}] or [B, T, {D}], got {list(t.shape)}")
+    p, ld = _rows(t, name, lead, (D,))
+    return p, ld, lead
+
+
+def add_rms_norm(x, res=None, w=None, *, eps=1e-6, fp8=False, out=None, scale_out=None, sum_out=None):
+    """y, h = add_rms_norm(x, res, w): norm of the residual stream with the
+    residual's addition (kda_add_rms_norm), h = x + res in res's type (x's, or
+    fp32 for a stream kept in 32 bits; None: h = x, returned as None), y =
+    w h / sqrt(mean h^2 + eps) in x's type.  x, res [rows,D] or [B,T,D] (bf16 or
+    fp32, may be slices of wider tensors); w [D] fp32 or None.  sum_out may be
+    a contiguous res itself.  fp8: y is the pair (y8, scale): y8 in
+    torch.float8_e4m3fn, scale [..., ceil(D/128)] fp32 with n = y8 scale."""
+    D = x.shape[-1]
+    px, ldx, lead = _flat_rows(x, "x", D)
+    dev, dt, rows = x.device, _dtype_code(x), math.prod(lead)
+    pr, ldr, rdt = None, 0, dt
+    if res is not None:
+        if res.shape != x.shape:
+            raise ValueError(f"res must be {list(x.shape)}, got {list(res.shape)}")
+        pr, ldr, _ = _flat_rows(res, "res", D)
+        rdt = _dtype_code(res)
+        sum_out = _given(sum_out, res, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs res")
+    ot = torch.float8_e4m3fn if fp8 else x.dtype
+    if out is None:
+        out = torch.empty(x.shape, dtype=ot, device=dev)
+    if fp8 and scale_out is None:
+        scale_out = torch.empty((*lead, (D + 127) // 128), dtype=torch.float32, device=dev)
+    _same_device(dev, res=res)
+    _call(dev, "kda_add_rms_norm", px, ldx, pr, ldr, rdt, _dense(w, "w", (D,), torch.float32, dev), float(eps),
+          None if res is None else sum_out.data_ptr(), _dense(out, "out", x.shape, ot, dev),
+          _dense(scale_out, "scale_out", (*lead, (D + 127) // 128), torch.float32, dev) if fp8 else None, dt, rows, D)
+    return ((out, scale_out) if fp8 else out), (None if res is None else sum_out)
+
+
+def add_rms_norm_bwd(h, w, dy, dh=None, *, eps=1e-6, want_dw=None, workspace=None, out=None):
+    """Gradients of add_rms_norm (kda_add_rms_norm_bwd) from h [rows,D] or
+    [B,T,D] (the sum it returned, or its x), dy (bf16 or fp32) and dh (h's type,
+    the gradient that reaches h past the norm, or None): a dict of dx (h's type;
+    the gradient of x and of res) and dw [D] fp32 (None without w; want_dw=True:
+    that of a weight of ones).  `out` may supply that dict; its dx may be dh."""
+    D = h.shape[-1]
+    ph, ldh, lead = _flat_rows(h, "h", D)
+    dev, rows = h.device, math.prod(lead)
+    if out is None:
+        wanted = w is not None if want_dw is None else want_dw
+        out = {"dx": torch.empty(h.shape, dtype=h.dtype, device=dev), "dw": torch.empty(D, dtype=torch.float32, device=dev) if wanted else None}
+    ws = None
+    if out.get("dw") is not None:
+        ws = _scratch(workspace, lib().kda_add_rms_norm_bwd_workspace_bytes(rows, D), dev, "kda_add_rms_norm_bwd_workspace_bytes")
+    _same_device(dev, workspace=ws)
+    _call(dev, "kda_add_rms_norm_bwd", ph, ldh, _dense(w, "w", (D,), torch.float32, dev), float(eps), _dense(dy, "dy", h.shape, dy.dtype, dev),
+          _dtype_code(dy), _dense(dh, "dh", h.shape, h.dtype, dev), _dense(out["dx"], "dx", h.shape, h.dtype, dev),
+          _dense(out.get("dw"), "dw", (D,), torch.float32, dev), _dtype_code(h), rows, D, _ptr(ws), 0 if ws is None else ws.numel())
+    return out
+
+
+def gemm_fp8(a, sa, w, sw, *, out_dtype=torch.bfloat16, out=None):
+    """c = gemm_fp8(a, sa, w, sw): product of 8-bit rows a [M,K] or [B,T,K] and
+    weights w [N,K] (torch.float8_e4m3fn; a may be a slice of a wider tensor)
+    with fp32 scales sa [..., ceil(K/128)] and sw [ceil(N/128), ceil(K/128)]
+    (kda_gemm_fp8): c [..., N] of out_dtype (bf16 or fp32), sums in fp32."""
+    for n, t in (("a", a), ("w", w)):
+        if t.dtype != torch.float8_e4m3fn:
+            raise TypeError(f"{n} must be torch.float8_e4m3fn, got {t.dtype}")
+    if sa.dtype != torch.float32:
+        raise TypeError(f"sa must be torch.float32, got {sa.dtype}")
+    N, K = w.shape
+    kb = (K + 127) // 128
+    pa, lda, lead = _flat_rows(a, "a", K)
+    ps, lsa = _rows(sa, "sa", lead, (kb,))
+    dev = a.device
+    _same_device(dev, sa=sa)
+    if out is None:
+        out = torch.empty((*lead, N), dtype=out_dtype, device=dev)
+    _call(dev, "kda_gemm_fp8", pa, lda, ps, lsa, _dense(w, "w", (N, K), torch.float8_e4m3fn, dev),
+          _dense(sw, "sw", ((N + 127) // 128, kb), torch.float32, dev), _dense(out, "out", (*lead, N), out.dtype, dev), _dtype_code(out),
+          math.prod(lead), N, K)
+    return out
+
+
+def _lru_setup(x, r, i, c, lead):
+    """Checked inputs of the gated linear recurrence: (x .. c of the C call)."""
+    D = x.shape[-1]
+    for n, t in (("r", r), ("i", i)):
+        if t is not None and t.dtype != x.dtype:
+            raise TypeError(f"{n} dtype {t.dtype} != x dtype {x.dtype}")
+    dev = x.device
+    _same_device(dev, r=r, i=i)
+    return (*_rows(x, "x", lead, (D,)), *_rows(r, "r", lead, (D,)), *((None, 0) if i is None else _rows(i, "i", lead, (D,))),
+            _dense(c, "c", (D,), torch.float32, dev))
+
+
+def lru_fwd(x, r, i=None, c=None, h0=None, *, unit=True, cu_seqlens=None, final_state=True, ht=None, workspace=None, out=None):
+    """y, ht = lru_fwd(x, r, i, c, h0): gated linear recurrence with one state a
+    channel (kda_lru_fwd), h_t = exp(g) h_{t-1} + m Sigmoid(i) x, y = h, with
+    g = -c Sigmoid(r) (c None: r is the log-decay itself), m = sqrt(1 - exp(2 g))
+    (unit=False: 1).  x, r, i [B,T,D] (bf16 or fp32, may be slices of wider
+    tensors; i None: no input gate); c [D] fp32; h0 / ht [N,D] fp32 of the N = B
+    sequences, or of those cu_seqlens (host ints) cuts the packed axis into; ht
+    may be h0 itself."""
+    B, T, D = x.shape
+    args = _lru_setup(x, r, i, c, (B, T))
+    arr, N = _packed(cu_seqlens, B, T)
+    dev, st = x.device, (N, D)
+    y = _given(out, x, "out")
+    if final_state and ht is None:
+        ht = torch.empty(st, dtype=torch.float32, device=dev)
+    ws = _scratch(workspace, lib().kda_lru_workspace_bytes(B, T, D, N if arr is not None else 0), dev, "kda_lru_workspace_bytes")
+    _same_device(dev, workspace=ws)
+    _call(dev, "kda_lru_fwd", *args, _dense(h0, "h0", st, torch.float32, dev), _dense(ht if final_state else None, "ht", st, torch.float32, dev),
+          y.data_ptr(), KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, T, D, arr, N, _ptr(ws), ws.numel())
+    return y, (ht if final_state else None)
+
+
+def lru_step(x, r, i, c, state, *, unit=True, state_out=None, out=None):
+    """y = lru_step(x, r, i, c, state): one token x, r, i [B,D] per sequence
+    (kda_lru_step); state [B,D] fp32 moves on in place, or into state_out (the
+    old state is then kept)."""
+    B, D = x.shape
+    args = _lru_setup(x, r, i, c, (B,))
+    dev, st = x.device, (B, D)
+    so = state if state_out is None else state_out
+    y = _given(out, x, "out")
+    _call(dev, "kda_lru_step", *args, _dense(state, "state", st, torch.float32, dev), _dense(so, "state_out", st, torch.float32, dev),
+          y.data_ptr(), KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, D)
+    return y
+
+
+def lru_bwd(x, r, i, c, dy, h0=None, dht=None, *, unit=True, cu_seqlens=None, workspace=None, out=None):
+    """Gradients of lru_fwd (kda_lru_bwd) from dy [B,T,D] (x's type) and dht
+    [N,D] fp32 (gradient of ht, or None): a dict of dx, dr, di (x's type; di
+    None without i), dc [D] fp32 (None without c) and dh0 [N,D] fp32 (None
+    without h0).  `out` may supply that dict to be filled in place."""
+    B, T, D = x.shape
+    args = _lru_setup(x, r, i, c, (B, T))
+    arr, N = _packed(cu_seqlens, B, T)
+    dev, st = x.device, (N, D)
+    if out is None:
+        out = {n: torch.empty((B, T, D), dtype=x.dtype, device=dev) if t is not None else None for n, t in (("dx", x), ("dr", r), ("di", i))}
+        out["dc"] = torch.empty(D, dtype=torch.float32, device=dev) if c is not None else None
+        out["dh0"] = torch.empty(st, dtype=torch.float32, device=dev) if h0 is not None else None
+    ws = _scratch(workspace, lib().kda_lru_bwd_workspace_bytes(B, T, D, N if arr is not None else 0), dev, "kda_lru_bwd_workspace_bytes")
+    _same_device(dev, workspace=ws)
+    p = {n: _dense(out.get(n), n, (B, T, D), x.dtype, dev) for n in ("dx", "dr", "di")}
+    _call(dev, "kda_lru_bwd", *args, _dense(h0, "h0", st, torch.float32, dev), _dense(dy, "dy", (B, T, D), x.dtype, dev),
+          _dense(dht, "dht", st, torch.float32, dev), p["dx"], p["dr"], p["di"], _dense(out.get("dc"), "dc", (D,), torch.float32, dev),
+          _dense(out.get("dh0"), "dh0", st, torch.float32, dev), KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, T, D, arr, N, _ptr(ws),
+          ws.numel())
     return out
 
 

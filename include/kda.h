@@ -543,6 +543,117 @@ int kda_ssm_bwd_chunked(const void* x, long long ldx, const void* dt, long long 
                         float* ddt_bias, float* dh0, int flags, int dtype, int B, int T, int H, int G, int dk, int dv,
                         const int* cu_seqlens, int N, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The operators of a recurrent block in front of and beside the mixers above:
+ * the norm of the residual stream, the projection of its rows in 8 bits, and
+ * the gated linear recurrence with one state a channel.  Conventions as for
+ * the operators around the recurrence (rows with a stride, fp32 parameters,
+ * outputs apart from inputs, no atomics: the same call gives the same bits).
+ */
+
+/*
+ * Norm of the residual stream with the residual's addition:
+ *   h = x + res, rounded to res_dtype (res NULL: h = x)
+ *   n = w h / sqrt(mean(h^2) + eps), of the rounded h
+ * x: `rows` rows of D channels of dtype, ldx apart; res: rows of res_dtype
+ * (dtype, or KDA_F32: a stream kept in 32 bits), ldr apart; sum [rows,D] of
+ * res_dtype receives h and may be res itself where ldr = D (res NULL: not
+ * used); w [D] fp32 or NULL (ones).
+ * scale NULL: y [rows,D] of dtype receives n.  Otherwise y receives n in 8
+ * bits (e4m3, one byte each) and scale [rows, ceil(D/128)] fp32 one scale for
+ * every 128 channels: s = max |n| / 448, y = e4m3(n / s), nearest with ties to
+ * even.  A block whose largest |n| is below 2^-100 has s = 1 and zeros.  NaN
+ * stays NaN; the largest value is taken over the others.
+ * eps may be 0: a row of zeros is then NaN.
+ * D a multiple of 8, at most 16384; row strides in multiples of 16 bytes.
+ * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides, eps), KDA_ERR_DTYPE,
+ *         KDA_ERR_ALIGN, KDA_ERR_UNSUPPORTED (D), KDA_ERR_OVERLAP, KDA_ERR_HIP.
+ */
+int kda_add_rms_norm(const void* x, long long ldx, const void* res, long long ldr, int res_dtype, const float* w, float eps,
+                     void* sum, void* y, float* scale, int dtype, long long rows, int D, void* stream);
+
+/*
+ * Gradients of kda_add_rms_norm (with y of a dtype, not of 8 bits): from h
+ * rows [rows,D] of dtype (the stream's type), dy [rows,D] of dy_dtype and dh
+ * [rows,D] of dtype (the gradient that reaches h past the norm; NULL: none):
+ * dx [rows,D] of dtype, the gradient of x and of res alike, which may be dh
+ * itself; dw [D] fp32 (NULL: not wanted; given also for a NULL w, as the
+ * gradient of a weight of ones).  workspace: as for kda_conv_bwd, not read
+ * without dw (may be NULL then).  Errors as above, KDA_ERR_WORKSPACE.
+ */
+size_t kda_add_rms_norm_bwd_workspace_bytes(long long rows, int D);
+int kda_add_rms_norm_bwd(const void* h, long long ldh, const float* w, float eps, const void* dy, int dy_dtype, const void* dh,
+                         void* dx, float* dw, int dtype, long long rows, int D, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * Product of 8-bit rows and 8-bit weights (e4m3) with fp32 scales, one for
+ * every 128 channels of a row and for every 128 x 128 tile of the weights:
+ *   c[m,n] = sum_kb sa[m,kb] sw[n/128,kb] sum_{k in block kb} a[m,k] w[n,k]
+ * a: rows [M,K], lda bytes apart (a multiple of 16); sa: rows [M,ceil(K/128)]
+ * fp32, lsa apart; w [N,K]; sw [ceil(N/128), ceil(K/128)] fp32; c [M,N] of
+ * c_dtype.  K a multiple of 16, K and lda at most 2^24; M, N any (the last
+ * blocks may be shorter).
+ * KDA_BF16: a block's 128 products are summed by the 8-bit matrix instruction
+ * (off by 1.4e-5 of the sum's rms), blocks in fp32.  KDA_F32: all sums in fp32
+ * at half that rate.  One rounding.  What is not finite in a row of a
+ * or sa stays in that row of c, in a row of w in that column.
+ * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides), KDA_ERR_DTYPE,
+ *         KDA_ERR_ALIGN, KDA_ERR_UNSUPPORTED (K), KDA_ERR_OVERLAP, KDA_ERR_HIP.
+ */
+int kda_gemm_fp8(const void* a, long long lda, const float* sa, long long lsa, const void* w, const float* sw, void* c,
+                 int c_dtype, long long M, int N, int K, void* stream);
+
+/*
+ * Gated linear recurrence with one state a channel:
+ *   g_t = -c Sigmoid(r_t), or r_t itself with c NULL (a log-decay)
+ *   h_t = exp(g_t) h_{t-1} + m_t Sigmoid(i_t) x_t      (i NULL: no input gate)
+ *   m_t = sqrt(1 - exp(2 g_t)) with flags & KDA_LRU_UNIT, otherwise 1
+ *   y_t = h_t
+ * x, r, i: rows [B,T,D] of dtype (any D; element alignment suffices; rows
+ * that start on two elements are faster); c [D] fp32 >= 0.  h0 [N,D] fp32
+ * (NULL: zero), ht [N,D] (NULL: not wanted) the states behind the sequences,
+ * may be h0 itself.  y [B,T,D] of dtype.  Tokens and states without gaps (y,
+ * h0, ht, and the gradients below) are 16-byte aligned where rows of D are
+ * whole 16 bytes, otherwise they may start on any element.
+ * Precondition: g <= 0 (a positive log-decay is computed as it is and may
+ * overflow; its m is NaN).  g = -inf starts the state anew (where it is
+ * finite).  A value that is not finite stays in its channel and reaches
+ * its own and later tokens of its sequence only.
+ * workspace: kda_lru_workspace_bytes (0 for invalid sizes; N = 0 for a
+ * batch), 256-byte aligned, contents ignored on entry; calls that share one
+ * must not overlap on the device.
+ * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides, cu_seqlens, flags),
+ *         KDA_ERR_DTYPE, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE, KDA_ERR_OVERLAP,
+ *         KDA_ERR_HIP.
+ */
+#define KDA_LRU_UNIT 1
+size_t kda_lru_workspace_bytes(int B, int T, int D, int N);
+int kda_lru_fwd(const void* x, long long ldx, const void* r, long long ldr, const void* i, long long ldi, const float* c,
+                const float* h0, float* ht, void* y, int flags, int dtype, int B, int T, int D, const int* cu_seqlens, int N,
+                void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token per sequence: x, r, i rows [B,D], state [B,D] fp32 read, state_out
+ * (which may be state itself) written, y [B,D].  Errors as kda_lru_fwd. */
+int kda_lru_step(const void* x, long long ldx, const void* r, long long ldr, const void* i, long long ldi, const float* c,
+                 const float* state, float* state_out, void* y, int flags, int dtype, int B, int D, void* stream);
+
+/*
+ * Gradients of kda_lru_fwd from dy [B,T,D] of dtype and dht [N,D] fp32 (NULL:
+ * none): dx, dr [B,T,D] and di (given with i, and only then) of dtype, dc [D]
+ * (NULL: not wanted; only with c) and dh0 [N,D] (NULL: not wanted) fp32, all
+ * contiguous and overwritten.  The states are recomputed inside `workspace`
+ * (kda_lru_bwd_workspace_bytes; contents ignored on entry).  Where m_t = 0 (a
+ * decay of exactly 1) its derivative counts as 0.  A value that is not finite
+ * stays in its channel and its sequence.  Errors as kda_lru_fwd.
+ */
+size_t kda_lru_bwd_workspace_bytes(int B, int T, int D, int N);
+int kda_lru_bwd(const void* x, long long ldx, const void* r, long long ldr, const void* i, long long ldi, const float* c,
+                const float* h0, const void* dy, const float* dht, void* dx, void* dr, void* di, float* dc, float* dh0,
+                int flags, int dtype, int B, int T, int D, const int* cu_seqlens, int N, void* workspace,
+                size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

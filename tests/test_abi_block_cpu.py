@@ -1,0 +1,139 @@
+"""Argument checks of a recurrent block's operators (norm of the residual
+stream, product of 8-bit rows, gated linear recurrence): every bad call is
+refused before anything is enqueued, so these run without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from gated_delta_rule_96_amd import kda
+
+# 16-byte aligned addresses far apart, never dereferenced: a check fails first
+A = [(i + 1) << 40 for i in range(14)]
+
+
+def call(name, base, **kw):
+    return getattr(kda.lib(), name)(*{**base, **kw}.values())
+
+
+NORM = dict(x=A[0], ldx=256, res=A[1], ldr=256, rt=1, w=A[2], eps=1e-6, sum=A[3], y=A[4], scale=A[5], dtype=1, rows=10, D=256, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), 1), (dict(y=None), 1), (dict(sum=None), 1),
+    (dict(rows=0), 2), (dict(rows=1 << 41), 2), (dict(D=0), 2), (dict(ldx=248), 2), (dict(ldr=8), 2), (dict(eps=-1.0), 2), (dict(eps=float("nan")), 2),
+    (dict(dtype=2), 3), (dict(rt=7), 3), (dict(dtype=0, rt=1), 3),
+    (dict(x=A[0] + 8), 4), (dict(ldx=260), 4), (dict(ldr=260), 4), (dict(w=A[2] + 4), 4), (dict(y=A[4] + 8), 4), (dict(scale=A[5] + 4), 4),
+    (dict(D=12, ldx=16), 5), (dict(D=16392, ldx=16392, ldr=16392), 5),
+    (dict(y=A[0]), 10), (dict(sum=A[1] + 512), 10), (dict(sum=A[1], ldr=512), 10), (dict(scale=A[4]), 10), (dict(y=A[1]), 10), (dict(sum=A[0]), 10),
+    (dict(scale=A[2]), 10),
+])
+def test_norm_refuses(kw, code):
+    assert call("kda_add_rms_norm", NORM, **kw) == code
+
+
+NBWD = dict(h=A[0], ldh=256, w=A[1], eps=1e-6, dy=A[2], gt=1, dh=A[3], dx=A[4], dw=A[5], dtype=1, rows=10, D=256, ws=A[6], wsb=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(h=None), 1), (dict(dy=None), 1), (dict(dx=None), 1), (dict(rows=-1), 2), (dict(ldh=128), 2), (dict(gt=2), 3), (dict(dy=A[2] + 8), 4),
+    (dict(ws=A[6] + 16), 4), (dict(D=20, ldh=24), 5), (dict(ws=None), 6), (dict(wsb=64), 6),
+    (dict(dx=A[0]), 10), (dict(dx=A[2]), 10), (dict(dx=A[3] + 16), 10), (dict(dw=A[1]), 10), (dict(dx=A[6]), 10),
+])
+def test_norm_bwd_refuses(kw, code):
+    assert call("kda_add_rms_norm_bwd", NBWD, **kw) == code
+
+
+def test_norm_workspace_bytes():
+    f = kda.lib().kda_add_rms_norm_bwd_workspace_bytes
+    assert f(1000, 4096) > 0 and f(1000, 4096) % 256 == 0
+    for bad in ((0, 64), (10, 0), (10, 12), (10, 16392), (1 << 41, 64)):
+        assert f(*bad) == 0
+
+
+GEMM = dict(a=A[0], lda=320, sa=A[1], lsa=3, w=A[2], sw=A[3], c=A[4], ct=1, M=7, N=200, K=320, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(a=None), 1), (dict(sa=None), 1), (dict(w=None), 1), (dict(sw=None), 1), (dict(c=None), 1),
+    (dict(M=0), 2), (dict(N=0), 2), (dict(K=0), 2), (dict(lda=304), 2), (dict(lsa=2), 2), (dict(K=(1 << 24) + 16, lda=1 << 25, lsa=1 << 20), 2),
+    (dict(lda=(1 << 24) + 16), 2), (dict(M=1 << 41), 2), (dict(N=(1 << 30) + 1), 2),
+    (dict(ct=4), 3), (dict(a=A[0] + 8), 4), (dict(lda=328), 4), (dict(w=A[2] + 8), 4), (dict(c=A[4] + 8), 4), (dict(sa=A[1] + 2), 4), (dict(sw=A[3] + 1), 4),
+    (dict(K=312), 5), (dict(K=8, lda=16), 5),
+    (dict(c=A[0]), 10), (dict(c=A[2] + 64), 10), (dict(c=A[1]), 10), (dict(c=A[3]), 10),
+])
+def test_gemm_refuses(kw, code):
+    assert call("kda_gemm_fp8", GEMM, **kw) == code
+
+
+LRU = dict(x=A[0], ldx=64, r=A[1], ldr=64, i=A[2], ldi=64, c=A[3], h0=A[4], ht=A[5], y=A[6], flags=1, dtype=1, B=2, T=10, D=64, cu=None, N=0,
+           ws=A[7], wsb=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), 1), (dict(r=None), 1), (dict(y=None), 1),
+    (dict(B=0), 2), (dict(T=0), 2), (dict(T=(1 << 30) + 1), 2), (dict(D=0), 2), (dict(ldx=63), 2), (dict(ldi=1), 2), (dict(flags=2), 2),
+    (dict(dtype=2), 3), (dict(x=A[0] + 1), 4), (dict(c=A[3] + 4), 4), (dict(ht=A[5] + 4), 4), (dict(y=A[6] + 8), 4), (dict(ws=A[7] + 16), 4),
+    (dict(ws=None), 6), (dict(wsb=16), 6),
+    (dict(y=A[0]), 10), (dict(y=A[2] + 64), 10), (dict(ht=A[4] + 16), 10), (dict(ht=A[6]), 10), (dict(y=A[7]), 10), (dict(ht=A[3]), 10),
+])
+def test_lru_refuses(kw, code):
+    assert call("kda_lru_fwd", LRU, **kw) == code
+
+
+def test_lru_refuses_bad_sequences():
+    cu = lambda *v: (ctypes.c_int * len(v))(*v)
+    for c, n, b in ((cu(0, 6, 5), 2, 1), (cu(1, 10), 1, 1), (cu(0, 9), 1, 1), (cu(0, 10), 0, 1), (cu(0, 10), 1, 2)):
+        assert call("kda_lru_fwd", LRU, cu=c, N=n, B=b) == 2
+
+
+STEP = dict(x=A[0], ldx=64, r=A[1], ldr=64, i=None, ldi=0, c=None, state=A[4], so=A[4], y=A[6], flags=0, dtype=0, B=2, D=64, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [(dict(state=None), 1), (dict(so=None), 1), (dict(B=0), 2), (dict(dtype=9), 3), (dict(so=A[4] + 4), 4),
+                                     (dict(so=A[4] + 16), 10), (dict(y=A[0]), 10), (dict(y=A[1]), 10)])
+def test_lru_step_refuses(kw, code):
+    assert call("kda_lru_step", STEP, **kw) == code
+
+
+LBWD = dict(x=A[0], ldx=64, r=A[1], ldr=64, i=A[2], ldi=64, c=A[3], h0=A[4], dy=A[5], dht=A[6], dx=A[7], dr=A[8], di=A[9], dc=A[10], dh0=A[11],
+            flags=1, dtype=1, B=2, T=10, D=64, cu=None, N=0, ws=A[12], wsb=1 << 30, stream=None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dy=None), 1), (dict(dx=None), 1), (dict(dr=None), 1), (dict(di=None), 1), (dict(i=None), 1), (dict(c=None), 1), (dict(T=-1), 2),
+    (dict(dy=A[5] + 4), 4), (dict(dc=A[10] + 4), 4), (dict(ws=A[12] + 64), 4), (dict(ws=None), 6), (dict(wsb=16), 6),
+    (dict(dx=A[5]), 10), (dict(dr=A[1]), 10), (dict(dh0=A[6]), 10), (dict(dc=A[11]), 10), (dict(di=A[12]), 10), (dict(dx=A[8]), 10),
+])
+def test_lru_bwd_refuses(kw, code):
+    assert call("kda_lru_bwd", LBWD, **kw) == code
+
+
+def test_lru_workspace_bytes():
+    L = kda.lib()
+    for f in (L.kda_lru_workspace_bytes, L.kda_lru_bwd_workspace_bytes):
+        assert f(2, 1000, 64, 0) > 0 and f(2, 1000, 64, 0) % 256 == 0
+        assert f(1, 100, 64, 300) >= f(1, 100, 64, 0)
+        for bad in ((0, 1, 1, 0), (1, 0, 1, 0), (1, 1, 0, 0), (2, 1, 1, 3), (1, 1, 1, -1), (1, (1 << 30) + 1, 1, 0)):
+            assert f(*bad) == 0
+
+
+def test_binding_checks_before_the_library():
+    z = torch.zeros
+    f8 = lambda *s: z(*s).to(torch.float8_e4m3fn)
+    with pytest.raises(ValueError, match="GPU"):
+        kda.add_rms_norm(z(4, 64))
+    with pytest.raises(ValueError, match="rows"):
+        kda.add_rms_norm(z(64))
+    with pytest.raises(TypeError, match="float8"):
+        kda.gemm_fp8(z(4, 64), z(4, 1), f8(8, 64), z(1, 1))
+    with pytest.raises(TypeError, match="sa must be"):
+        kda.gemm_fp8(f8(4, 64), z(4, 1).double(), f8(8, 64), z(1, 1))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.gemm_fp8(f8(4, 64), z(4, 1), f8(8, 64), z(1, 1))
+    with pytest.raises(ValueError, match="GPU"):
+        kda.lru_fwd(z(1, 4, 8), z(1, 4, 8))
+    with pytest.raises(TypeError, match="r dtype"):
+        kda.lru_fwd(z(1, 4, 8), z(1, 4, 8).bfloat16())
+    with pytest.raises(ValueError, match="GPU"):
+        kda.lru_step(z(4, 8), z(4, 8), None, None, z(4, 8))
