@@ -3,9 +3,8 @@
 //
 // A wave holds R tokens of 64 NC channels in registers, a work-group kWaves
 // runs of them, one behind the other: a part of a sequence.  Its (P, H) are
-// joined over the waves in LDS.  Sequences of several parts run in three
-// launches: every part's (P, H), the states that enter the parts, and the
-// outputs.
+// joined over the waves in LDS.  Every input is read once: the parts of a
+// sequence hand their states on inside the one launch.
 #include "kda_lru_dev.h"
 
 namespace kda {
@@ -13,6 +12,7 @@ namespace kda {
 namespace {
 
 constexpr int kWaves = 8, kR = 16, kPart = kWaves * kR;
+constexpr int kBack = 4;   // parts that a part looks back over
 
 // a and u of a wave's run of R tokens from token t on; tokens past the part's
 // end leave the state as it is.
@@ -62,69 +62,63 @@ __device__ __forceinline__ void run_sum(const float (&a)[R][NC], const float (&u
     }
 }
 
-// (P, H) of every part: to seg [items][2][D].
-template <typename T, int NC>
-__global__ __launch_bounds__(64 * kWaves) void lru_part_kernel(const LruArgs g, const SeqTab s, unsigned slices, float* seg) {
-  __shared__ float red[2][kWaves][64 * NC];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const unsigned item = blockIdx.x / slices;
-  const LruLane l = lru_lane<NC>((int)(blockIdx.x - item * slices), g.D);
-  const SeqPart p = seq_part(s, (int)item);
-  float a[kR][NC], u[kR][NC], P[NC], H[NC];
-  load_run<T, NC, kR>(g, p, l, p.t0 + wave * kR, a, u);
-  run_sum<NC, kR>(a, u, P, H);
+// What a part hands to the parts behind it, a word pair or word a channel in
+// the workspace: `own` its (P, H), `into` the state behind it.  A word is valid
+// once it is not all ones (a fill that every call does first), so that a word is
+// its own flag: relaxed accesses at device scope are enough, and nothing is
+// ordered by fences, which would write back the caches.
+struct Words {
+  unsigned* ticket;             // parts and slices given out so far
+  unsigned long long* own;      // [items][D]
+  unsigned* into;               // [items][D]
+};
+constexpr unsigned kNone = 0xffffffffu;
+// Bits of x as a word: a NaN of all ones becomes the usual one.
+__device__ __forceinline__ unsigned word_of(float x) {
+  const unsigned b = __float_as_uint(x);
+  return b == kNone ? 0x7fc00000u : b;
+}
+__device__ __forceinline__ Words words_at(void* ws, size_t n) {
+  Words w;
+  w.ticket = static_cast<unsigned*>(ws);
+  w.own = reinterpret_cast<unsigned long long*>(w.ticket + 64);
+  w.into = reinterpret_cast<unsigned*>(w.own + n);
+  return w;
+}
+__global__ __launch_bounds__(256) void lru_fill_kernel(unsigned* ws, size_t n) {   // n words of ones behind the ticket
+  const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at == 0) ws[0] = 0;
+  for (size_t i = at; i < n; i += (size_t)gridDim.x * 1024)
 #pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    red[0][wave][lane * NC + j] = P[j];
-    red[1][wave][lane * NC + j] = H[j];
-  }
-  __syncthreads();
-  if (wave || !l.live) return;
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w)
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const float q = red[0][w][lane * NC + j];
-      H[j] = fmaf(q, H[j], red[1][w][lane * NC + j]);
-      P[j] *= q;
-    }
-  float* to = seg + (size_t)item * 2 * g.D + l.c;
-#pragma unroll
-  for (int j = 0; j < NC; ++j) {
-    to[j] = P[j];
-    to[g.D + j] = H[j];
-  }
+    for (int k = 0; k < 4; ++k)
+      if (i + k < n) ws[64 + i + k] = kNone;
 }
 
-// The states that enter a sequence's parts, over their H; and its final state.
-__global__ __launch_bounds__(64) void lru_chain_kernel(const LruArgs g, const SeqTab s, float* seg) {
-  const int blocks = (g.D + 63) / 64, li = blockIdx.x / blocks, c = (blockIdx.x - li * blocks) * 64 + threadIdx.x;
-  if (c >= g.D) return;
-  const int n = s.n0 + li;
-  const int i0 = s.n ? s.cc[li] : li * s.parts, i1 = s.n ? s.cc[li + 1] : i0 + s.parts;
-  float h = g.h0 ? g.h0[(size_t)n * g.D + c] : 0.f;
-#pragma unroll 8
-  for (int i = i0; i < i1; ++i) {
-    float* at = seg + (size_t)i * 2 * g.D + c;
-    const float P = at[0], H = at[g.D];
-    at[g.D] = h;
-    h = fmaf(P, h, H);
-  }
-  if (g.ht) g.ht[(size_t)n * g.D + c] = h;
-}
-
-// Outputs.  seg null: every sequence is one part.
-template <typename T, int NC>
-__global__ __launch_bounds__(64 * kWaves) void lru_out_kernel(const LruArgs g, const SeqTab s, unsigned slices, const float* seg) {
+// Outputs.  kChain: sequences of several parts.  Each work-group takes the
+// next (part, slice) by a ticket and waits for parts before its own only, all
+// of which have lower tickets: the lowest ticket that is not done waits for
+// nothing, so every wait ends, however many work-groups run at once.  The
+// first wave joins its part's runs, publishes them, and goes back through the
+// parts before until one has its state published.
+template <typename T, int NC, bool kChain>
+__global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g, const SeqTab s, unsigned slices, void* ws) {
   __shared__ float red[2][kWaves][64 * NC];
+  __shared__ float carry[64 * NC];
+  __shared__ unsigned given;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const unsigned item = blockIdx.x / slices;
-  const LruLane l = lru_lane<NC>((int)(blockIdx.x - item * slices), g.D);
+  unsigned id = blockIdx.x;
+  const Words w = words_at(ws, (size_t)s.items * g.D);
+  if (kChain) {
+    if (threadIdx.x == 0) given = __hip_atomic_fetch_add(w.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    id = given;
+  }
+  unsigned item = id / slices;
+  const LruLane l = lru_lane<NC>((int)(id - item * slices), g.D);
+  // (equal sequences take turns, so that their chains run side by side)
+  if (kChain && s.n == 0) item = item % (unsigned)(s.items / s.parts) * s.parts + item / (unsigned)(s.items / s.parts);
   const SeqPart p = seq_part(s, (int)item);
   float a[kR][NC], u[kR][NC], P[NC], H[NC], h[NC];
-  const float* from = seg ? seg + (size_t)item * 2 * g.D + g.D : g.h0 ? g.h0 + (size_t)p.n * g.D : nullptr;
-#pragma unroll
-  for (int j = 0; j < NC; ++j) h[j] = from ? from[l.cl + j] : 0.f;
   load_run<T, NC, kR>(g, p, l, p.t0 + wave * kR, a, u);
   run_sum<NC, kR>(a, u, P, H);
 #pragma unroll
@@ -133,10 +127,81 @@ __global__ __launch_bounds__(64 * kWaves) void lru_out_kernel(const LruArgs g, c
     red[1][wave][lane * NC + j] = H[j];
   }
   __syncthreads();
-  for (int w = 0; w < wave; ++w)
+  if (wave == 0) {
 #pragma unroll
-    for (int j = 0; j < NC; ++j) h[j] = fmaf(red[0][w][lane * NC + j], h[j], red[1][w][lane * NC + j]);
+    for (int q = 1; q < kWaves; ++q)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        const float f = red[0][q][lane * NC + j];
+        H[j] = fmaf(f, H[j], red[1][q][lane * NC + j]);
+        P[j] *= f;
+      }
+    if (!kChain || p.first) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) h[j] = g.h0 ? g.h0[(size_t)p.n * g.D + l.cl + j] : 0.f;
+    } else {
+      const size_t at = (size_t)item * g.D + l.cl;
+      if (!p.last && l.live)
+#pragma unroll
+        for (int j = 0; j < NC; ++j)
+          __hip_atomic_store(w.own + at + j, (unsigned long long)word_of(H[j]) << 32 | word_of(P[j]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      // From the nearest of the last kBack parts whose state is there, if the
+      // (P, H) of those in between are: the state is carried over them one by one,
+      // as each of them does, so that the bits do not depend on which was found.
+      const int parts_before = p.t0 / kPart;
+      unsigned in[kBack][NC];
+      unsigned long long ow[kBack][NC];
+      int found = 0;
+      for (;;) {
+#pragma unroll
+        for (int d = 0; d < kBack; ++d) {
+          const size_t from = at - (size_t)min(d + 1, parts_before) * g.D;   // (the first part publishes its state only)
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            in[d][j] = __hip_atomic_load(w.into + from + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            ow[d][j] = __hip_atomic_load(w.own + from + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          }
+        }
+        bool open = true;
+#pragma unroll
+        for (int d = 0; d < kBack; ++d) {
+          bool got = true, has = true;
+#pragma unroll
+          for (int j = 0; j < NC; ++j) {
+            got &= in[d][j] != kNone;
+            has &= ow[d][j] != ~0ull;
+          }
+          if (open && !found && __all(got || !l.live)) found = d + 1;
+          open = open && __all(has || !l.live);
+        }
+        if (found) break;
+        __builtin_amdgcn_s_sleep(1);
+      }
+#pragma unroll
+      for (int d = kBack - 1; d >= 0; --d)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          if (d + 1 == found) h[j] = __uint_as_float(in[d][j]);
+          else if (d + 1 < found) h[j] = fmaf(__uint_as_float((unsigned)ow[d][j]), h[j], __uint_as_float((unsigned)(ow[d][j] >> 32)));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      carry[lane * NC + j] = h[j];
+      const float end = fmaf(P[j], h[j], H[j]);
+      if (!l.live) continue;
+      if (kChain && !p.last)
+        __hip_atomic_store(w.into + (size_t)item * g.D + l.c + j, word_of(end), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (p.last && g.ht) g.ht[(size_t)p.n * g.D + l.c + j] = end;
+    }
+  }
+  __syncthreads();
   if (!l.live) return;
+#pragma unroll
+  for (int j = 0; j < NC; ++j) h[j] = carry[lane * NC + j];
+  for (int q = 0; q < wave; ++q)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) h[j] = fmaf(red[0][q][lane * NC + j], h[j], red[1][q][lane * NC + j]);
   const int t = p.t0 + wave * kR;
 #pragma unroll
   for (int k = 0; k < kR; ++k) {
@@ -148,9 +213,6 @@ __global__ __launch_bounds__(64 * kWaves) void lru_out_kernel(const LruArgs g, c
     }
     if (t + k < p.t1) *reinterpret_cast<LruPack<T, NC>*>((T*)g.y + (p.start + (size_t)(t + k)) * g.D + l.c) = o;
   }
-  if (!seg && g.ht && wave == kWaves - 1)
-#pragma unroll
-    for (int j = 0; j < NC; ++j) g.ht[(size_t)p.n * g.D + l.c + j] = h[j];
 }
 
 // One token per sequence.
@@ -187,21 +249,21 @@ bool pairs(const LruArgs& a, size_t esz) {
 }
 
 template <typename T, int NC>
-hipError_t fwd_go(const LruArgs& a, const int* cu, int N, int B, int T_, float* seg, hipStream_t st) {
+hipError_t fwd_go(const LruArgs& a, const int* cu, int N, int B, int T_, void* ws, hipStream_t st) {
   const unsigned slices = (unsigned)((a.D + 64 * NC - 1) / (64 * NC));
   if (!seq_tabs_fit(cu, N, B, T_, kPart, max_groups(64 * kWaves) / slices)) return hipErrorInvalidConfiguration;
   const int end = cu ? N : B;
   for (int n = 0; n < end;) {
     SeqTab s;
     n = make_seq_tab(s, cu, N, n, B, T_, kPart);
-    const int seqs = s.n ? s.n : B;
-    const bool one = s.items == seqs;   // no sequence has a second part
     const dim3 grid((unsigned)s.items * slices), th(64 * kWaves);
-    if (!one) {
-      hipLaunchKernelGGL((lru_part_kernel<T, NC>), grid, th, 0, st, a, s, slices, seg);
-      hipLaunchKernelGGL(lru_chain_kernel, dim3((unsigned)(a.D + 63) / 64 * seqs), dim3(64), 0, st, a, s, seg);
+    if (s.items == (s.n ? s.n : B)) {   // no sequence has a second part
+      hipLaunchKernelGGL((lru_out_kernel<T, NC, false>), grid, th, 0, st, a, s, slices, ws);
+    } else {
+      const size_t words = (size_t)s.items * a.D * 3, groups = (words + 1023) / 1024;
+      hipLaunchKernelGGL(lru_fill_kernel, dim3((unsigned)(groups < 4096 ? groups : 4096)), dim3(256), 0, st, static_cast<unsigned*>(ws), words);
+      hipLaunchKernelGGL((lru_out_kernel<T, NC, true>), grid, th, 0, st, a, s, slices, ws);
     }
-    hipLaunchKernelGGL((lru_out_kernel<T, NC>), grid, th, 0, st, a, s, slices, one ? nullptr : seg);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -221,13 +283,12 @@ hipError_t step_go(const LruArgs& a, int B, hipStream_t st) {
 
 size_t lru_workspace_bytes(int is_packed, int N, int B, int T, int D) {
   const size_t items = is_packed ? (size_t)T / kPart + (size_t)N : (size_t)B * (((size_t)T + kPart - 1) / kPart);
-  return (items * 2 * D * sizeof(float) + 255) & ~(size_t)255;
+  return (256 + items * 3 * D * sizeof(float) + 255) & ~(size_t)255;
 }
 
 hipError_t launch_lru_fwd(int is_bf16, const LruArgs& a, const int* cu, int N, int B, int T, void* workspace, hipStream_t st) {
-  float* seg = static_cast<float*>(workspace);
-  if (is_bf16) return pairs(a, 2) ? fwd_go<bf16, 2>(a, cu, N, B, T, seg, st) : fwd_go<bf16, 1>(a, cu, N, B, T, seg, st);
-  return pairs(a, 4) ? fwd_go<float, 2>(a, cu, N, B, T, seg, st) : fwd_go<float, 1>(a, cu, N, B, T, seg, st);
+  if (is_bf16) return pairs(a, 2) ? fwd_go<bf16, 2>(a, cu, N, B, T, workspace, st) : fwd_go<bf16, 1>(a, cu, N, B, T, workspace, st);
+  return pairs(a, 4) ? fwd_go<float, 2>(a, cu, N, B, T, workspace, st) : fwd_go<float, 1>(a, cu, N, B, T, workspace, st);
 }
 
 hipError_t launch_lru_step(int is_bf16, const LruArgs& a, int B, hipStream_t st) {
