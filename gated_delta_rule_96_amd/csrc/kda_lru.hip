@@ -14,35 +14,51 @@ namespace {
 constexpr int kWaves = 8, kR = 16, kPart = kWaves * kR;
 constexpr int kBack = 4;   // parts that a part looks back over
 
-// a and u of a wave's run of R tokens from token t on; tokens past the part's
-// end leave the state as it is.
-template <typename T, int NC, int R>
+// a and u of a wave's run of R tokens from token t on (the same for all
+// lanes); tokens past the part's end leave the state as it is.
+template <typename T, int NC, int R, bool kFull>
 __device__ __forceinline__ void load_run(const LruArgs& g, const SeqPart& p, const LruLane& l, int t, float (&a)[R][NC], float (&u)[R][NC]) {
   typedef LruPack<T, NC> Pk;
-  const LruMode md = lru_mode(g);
-  Pk x[R], r[R], i[R];
-  if (t < p.t1) {
+  const int n = p.t1 - t;
+  if (n <= 0) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const size_t row = p.start + (size_t)min(t + k, p.t1 - 1);
-      x[k] = *reinterpret_cast<const Pk*>((const T*)g.x + row * (size_t)g.ldx + l.cl);
-      r[k] = *reinterpret_cast<const Pk*>((const T*)g.r + row * (size_t)g.ldr + l.cl);
-      if (md.igate) i[k] = *reinterpret_cast<const Pk*>((const T*)g.i + row * (size_t)g.ldi + l.cl);
-    }
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        a[k][j] = 1.f;
+        u[k][j] = 0.f;
+      }
+    return;
   }
   float c[NC];
   lru_coef<NC>(g, l, c);
+  Pk x[R], r[R], i[R];
+  const size_t row = p.start + (size_t)t;
+  const T *px = (const T*)g.x + row * (size_t)g.ldx, *pr = (const T*)g.r + row * (size_t)g.ldr, *pi = (const T*)g.i + row * (size_t)g.ldi;
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-#pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      a[k][j] = 1.f;
-      u[k][j] = 0.f;
-    }
-    if (t + k < p.t1)
-#pragma unroll
-      for (int j = 0; j < NC; ++j) lru_gates<T>(md, c[j], to_f32(x[k].v[j]), to_f32(r[k].v[j]), md.igate ? to_f32(i[k].v[j]) : 0.f, a[k][j], u[k][j]);
+    const int q = min(k, n - 1);
+    x[k] = *reinterpret_cast<const Pk*>(px + q * g.ldx + l.cl);
+    r[k] = *reinterpret_cast<const Pk*>(pr + q * g.ldr + l.cl);
   }
+  if (kFull || g.i)
+#pragma unroll
+    for (int k = 0; k < R; ++k) i[k] = *reinterpret_cast<const Pk*>(pi + min(k, n - 1) * g.ldi + l.cl);
+  const LruMode md = lru_mode<kFull>(g);
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int j = 0; j < NC; ++j)
+      lru_gate<T>(md, c[j], to_f32(x[k].v[j]), to_f32(r[k].v[j]), md.igate ? to_f32(i[k].v[j]) : 0.f, a[k][j], u[k][j]);
+  if (n < R)
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (k >= n)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+          a[k][j] = 1.f;
+          u[k][j] = 0.f;
+        }
 }
 
 // P and H of a run.
@@ -100,18 +116,18 @@ __global__ __launch_bounds__(256) void lru_fill_kernel(unsigned* ws, size_t n) {
 // nothing, so every wait ends, however many work-groups run at once.  The
 // first wave joins its part's runs, publishes them, and goes back through the
 // parts before until one has its state published.
-template <typename T, int NC, bool kChain>
+template <typename T, int NC, bool kChain, bool kFull>
 __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g, const SeqTab s, unsigned slices, void* ws) {
   __shared__ float red[2][kWaves][64 * NC];
   __shared__ float carry[64 * NC];
   __shared__ unsigned given;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   unsigned id = blockIdx.x;
   const Words w = words_at(ws, (size_t)s.items * g.D);
   if (kChain) {
     if (threadIdx.x == 0) given = __hip_atomic_fetch_add(w.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
-    id = given;
+    id = __builtin_amdgcn_readfirstlane(given);
   }
   unsigned item = id / slices;
   const LruLane l = lru_lane<NC>((int)(id - item * slices), g.D);
@@ -119,7 +135,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
   if (kChain && s.n == 0) item = item % (unsigned)(s.items / s.parts) * s.parts + item / (unsigned)(s.items / s.parts);
   const SeqPart p = seq_part(s, (int)item);
   float a[kR][NC], u[kR][NC], P[NC], H[NC], h[NC];
-  load_run<T, NC, kR>(g, p, l, p.t0 + wave * kR, a, u);
+  load_run<T, NC, kR, kFull>(g, p, l, p.t0 + wave * kR, a, u);
   run_sum<NC, kR>(a, u, P, H);
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
@@ -203,6 +219,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
 #pragma unroll
     for (int j = 0; j < NC; ++j) h[j] = fmaf(red[0][q][lane * NC + j], h[j], red[1][q][lane * NC + j]);
   const int t = p.t0 + wave * kR;
+  T* y = (T*)g.y + (p.start + (size_t)t) * g.D;
 #pragma unroll
   for (int k = 0; k < kR; ++k) {
     LruPack<T, NC> o;
@@ -211,7 +228,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
       h[j] = fmaf(a[k][j], h[j], u[k][j]);
       o.v[j] = from_f32<T>(h[j]);
     }
-    if (t + k < p.t1) *reinterpret_cast<LruPack<T, NC>*>((T*)g.y + (p.start + (size_t)(t + k)) * g.D + l.c) = o;
+    if (t + k < p.t1) *reinterpret_cast<LruPack<T, NC>*>(y + (long long)k * g.D + l.c) = o;
   }
 }
 
@@ -222,17 +239,22 @@ __global__ __launch_bounds__(256) void lru_step_kernel(const LruArgs g, unsigned
   if (n >= B) return;
   const int ch = (int)(id - n * CG) * NC;
   typedef LruPack<T, NC> Pk;
-  const LruMode md = lru_mode(g);
-  const Pk x = *reinterpret_cast<const Pk*>((const T*)g.x + n * (size_t)g.ldx + ch), r = *reinterpret_cast<const Pk*>((const T*)g.r + n * (size_t)g.ldr + ch);
-  Pk i = x, o;
-  if (md.igate) i = *reinterpret_cast<const Pk*>((const T*)g.i + n * (size_t)g.ldi + ch);
+  float c[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) c[j] = g.c ? g.c[ch + j] : 0.f;
+  Pk x, r, i, o;
+  x = *reinterpret_cast<const Pk*>((const T*)g.x + n * (size_t)g.ldx + ch);
+  r = *reinterpret_cast<const Pk*>((const T*)g.r + n * (size_t)g.ldr + ch);
+  i = x;
+  if (g.i) i = *reinterpret_cast<const Pk*>((const T*)g.i + n * (size_t)g.ldi + ch);
   const size_t at = (size_t)n * g.D + ch;
   const LruPack<float, NC> h0 = *reinterpret_cast<const LruPack<float, NC>*>(g.h0 + at);
   LruPack<float, NC> ht;
+  const LruMode md = lru_mode<false>(g);
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     float a, u;
-    lru_gates<T>(md, g.c ? g.c[ch + j] : 0.f, to_f32(x.v[j]), to_f32(r.v[j]), to_f32(i.v[j]), a, u);
+    lru_gate<T>(md, c[j], to_f32(x.v[j]), to_f32(r.v[j]), to_f32(i.v[j]), a, u);
     ht.v[j] = fmaf(a, h0.v[j], u);
     o.v[j] = from_f32<T>(ht.v[j]);
   }
@@ -248,7 +270,7 @@ bool pairs(const LruArgs& a, size_t esz) {
   return true;
 }
 
-template <typename T, int NC>
+template <typename T, int NC, bool kFull>
 hipError_t fwd_go(const LruArgs& a, const int* cu, int N, int B, int T_, void* ws, hipStream_t st) {
   const unsigned slices = (unsigned)((a.D + 64 * NC - 1) / (64 * NC));
   if (!seq_tabs_fit(cu, N, B, T_, kPart, max_groups(64 * kWaves) / slices)) return hipErrorInvalidConfiguration;
@@ -258,16 +280,22 @@ hipError_t fwd_go(const LruArgs& a, const int* cu, int N, int B, int T_, void* w
     n = make_seq_tab(s, cu, N, n, B, T_, kPart);
     const dim3 grid((unsigned)s.items * slices), th(64 * kWaves);
     if (s.items == (s.n ? s.n : B)) {   // no sequence has a second part
-      hipLaunchKernelGGL((lru_out_kernel<T, NC, false>), grid, th, 0, st, a, s, slices, ws);
+      hipLaunchKernelGGL((lru_out_kernel<T, NC, false, kFull>), grid, th, 0, st, a, s, slices, ws);
     } else {
       const size_t words = (size_t)s.items * a.D * 3, groups = (words + 1023) / 1024;
       hipLaunchKernelGGL(lru_fill_kernel, dim3((unsigned)(groups < 4096 ? groups : 4096)), dim3(256), 0, st, static_cast<unsigned*>(ws), words);
-      hipLaunchKernelGGL((lru_out_kernel<T, NC, true>), grid, th, 0, st, a, s, slices, ws);
+      hipLaunchKernelGGL((lru_out_kernel<T, NC, true, kFull>), grid, th, 0, st, a, s, slices, ws);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
+}
+
+template <typename T>
+hipError_t fwd_type(const LruArgs& a, const int* cu, int N, int B, int T_, void* ws, hipStream_t st) {
+  if (pairs(a, sizeof(T))) return lru_full(a) ? fwd_go<T, 2, true>(a, cu, N, B, T_, ws, st) : fwd_go<T, 2, false>(a, cu, N, B, T_, ws, st);
+  return lru_full(a) ? fwd_go<T, 1, true>(a, cu, N, B, T_, ws, st) : fwd_go<T, 1, false>(a, cu, N, B, T_, ws, st);
 }
 
 template <typename T, int NC>
@@ -287,8 +315,8 @@ size_t lru_workspace_bytes(int is_packed, int N, int B, int T, int D) {
 }
 
 hipError_t launch_lru_fwd(int is_bf16, const LruArgs& a, const int* cu, int N, int B, int T, void* workspace, hipStream_t st) {
-  if (is_bf16) return pairs(a, 2) ? fwd_go<bf16, 2>(a, cu, N, B, T, workspace, st) : fwd_go<bf16, 1>(a, cu, N, B, T, workspace, st);
-  return pairs(a, 4) ? fwd_go<float, 2>(a, cu, N, B, T, workspace, st) : fwd_go<float, 1>(a, cu, N, B, T, workspace, st);
+  if (is_bf16) return fwd_type<bf16>(a, cu, N, B, T, workspace, st);
+  return fwd_type<float>(a, cu, N, B, T, workspace, st);
 }
 
 hipError_t launch_lru_step(int is_bf16, const LruArgs& a, int B, hipStream_t st) {

@@ -27,18 +27,24 @@ template <typename T> constexpr int part_of() { return kWaves * RunOf<T>::R; }
 template <typename T, int NC, int R> struct BwdRun {
   LruPack<T, NC> x[R], r[R], i[R], dy[R];
 };
-template <typename T, int NC, int R>
+template <typename T, int NC, int R, bool kFull>
 __device__ __forceinline__ void load_rows(const LruBwdArgs& b, const SeqPart& p, const LruLane& l, int t, BwdRun<T, NC, R>& w) {
   typedef LruPack<T, NC> Pk;
-  if (t >= p.t1) return;
+  const int n = p.t1 - t;
+  if (n <= 0) return;
+  const size_t row = p.start + (size_t)t;
+  const T *px = (const T*)b.f.x + row * (size_t)b.f.ldx, *pr = (const T*)b.f.r + row * (size_t)b.f.ldr;
+  const T *pi = (const T*)b.f.i + row * (size_t)b.f.ldi, *pd = (const T*)b.dy + row * (size_t)b.f.D;
 #pragma unroll
   for (int k = 0; k < R; ++k) {
-    const size_t row = p.start + (size_t)min(t + k, p.t1 - 1);
-    w.x[k] = *reinterpret_cast<const Pk*>((const T*)b.f.x + row * (size_t)b.f.ldx + l.cl);
-    w.r[k] = *reinterpret_cast<const Pk*>((const T*)b.f.r + row * (size_t)b.f.ldr + l.cl);
-    if (b.f.i) w.i[k] = *reinterpret_cast<const Pk*>((const T*)b.f.i + row * (size_t)b.f.ldi + l.cl);
-    w.dy[k] = *reinterpret_cast<const Pk*>((const T*)b.dy + row * (size_t)b.f.D + l.cl);
+    const int q = min(k, n - 1);
+    w.x[k] = *reinterpret_cast<const Pk*>(px + q * b.f.ldx + l.cl);
+    w.r[k] = *reinterpret_cast<const Pk*>(pr + q * b.f.ldr + l.cl);
+    w.dy[k] = *reinterpret_cast<const Pk*>(pd + (long long)q * b.f.D + l.cl);
   }
+  if (kFull || b.f.i)
+#pragma unroll
+    for (int k = 0; k < R; ++k) w.i[k] = *reinterpret_cast<const Pk*>(pi + min(k, n - 1) * b.f.ldi + l.cl);
 }
 
 // a and u of a run, and its P, H and K.  Tokens past the part's end leave
@@ -51,36 +57,42 @@ __device__ __forceinline__ void run_sums(const LruMode& md, const float (&c)[NC]
     P[j] = 1.f;
     H[j] = K[j] = 0.f;
   }
+  if (n > 0)
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        lru_gate<T>(md, c[j], to_f32(w.x[k].v[j]), to_f32(w.r[k].v[j]), md.igate ? to_f32(w.i[k].v[j]) : 0.f, a[k][j], u[k][j]);
 #pragma unroll
   for (int k = 0; k < R; ++k)
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      a[k][j] = 1.f;
-      u[k][j] = 0.f;
       if (k < n) {
-        lru_gates<T>(md, c[j], to_f32(w.x[k].v[j]), to_f32(w.r[k].v[j]), md.igate ? to_f32(w.i[k].v[j]) : 0.f, a[k][j], u[k][j]);
         P[j] *= a[k][j];
         H[j] = fmaf(a[k][j], H[j], u[k][j]);
         K[j] = fmaf(P[j], to_f32(w.dy[k].v[j]), K[j]);
+      } else {
+        a[k][j] = 1.f;
+        u[k][j] = 0.f;
       }
     }
 }
 
 // seg [items][3][D]: P, H, K of every part.
-template <typename T, int NC>
+template <typename T, int NC, bool kFull>
 __global__ __launch_bounds__(64 * kWaves) void lru_bwd_part_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, float* seg) {
   constexpr int R = RunOf<T>::R;
   __shared__ float red[3][kWaves][64 * NC];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = b.f.D;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, D = b.f.D;
   const unsigned item = blockIdx.x / slices;
   const LruLane l = lru_lane<NC>((int)(blockIdx.x - item * slices), D);
   const SeqPart p = seq_part(s, (int)item);
   const int t = p.t0 + wave * R;
   BwdRun<T, NC, R> w;
-  load_rows<T, NC, R>(b, p, l, t, w);
+  load_rows<T, NC, R, kFull>(b, p, l, t, w);
   float a[R][NC], u[R][NC], c[NC], P[NC], H[NC], K[NC];
   lru_coef<NC>(b.f, l, c);
-  run_sums<T, NC, R>(lru_mode(b.f), c, w, p.t1 - t, a, u, P, H, K);
+  run_sums<T, NC, R>(lru_mode<kFull>(b.f), c, w, p.t1 - t, a, u, P, H, K);
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     red[0][wave][lane * NC + j] = P[j];
@@ -133,21 +145,21 @@ __global__ __launch_bounds__(64) void lru_bwd_chain_kernel(const LruBwdArgs b, c
 }
 
 // Gradients.  dcp [items][D]: every part's sum of dg Sigmoid(r), or null.
-template <typename T, int NC>
+template <typename T, int NC, bool kFull>
 __global__ __launch_bounds__(64 * kWaves) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
   constexpr int R = RunOf<T>::R;
   typedef LruPack<T, NC> Pk;
   __shared__ float red[3][kWaves][64 * NC];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, D = b.f.D;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, D = b.f.D;
   const unsigned id = gridDim.x - 1 - blockIdx.x, item = id / slices;
   const LruLane l = lru_lane<NC>((int)(id - item * slices), D);
   const SeqPart p = seq_part(s, (int)item);
   const int t = p.t0 + wave * R, n = p.t1 - t;
-  const LruMode md = lru_mode(b.f);
   BwdRun<T, NC, R> w;
-  load_rows<T, NC, R>(b, p, l, t, w);
+  load_rows<T, NC, R, kFull>(b, p, l, t, w);
   float a[R][NC], u[R][NC], c[NC], P[NC], H[NC], K[NC], h[NC], e[NC], sum[NC];
   lru_coef<NC>(b.f, l, c);
+  const LruMode md = lru_mode<kFull>(b.f);
   const float* from = seg + (size_t)item * 3 * D + l.cl;
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
@@ -243,7 +255,7 @@ size_t all_items(int is_packed, int N, int B, int T, int part) {
   return is_packed ? (size_t)T / part + (size_t)N : (size_t)B * (((size_t)T + part - 1) / part);
 }
 
-template <typename T, int NC>
+template <typename T, int NC, bool kFull>
 hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, float* ws, hipStream_t st) {
   constexpr int kPart = part_of<T>();
   const int D = b.f.D;
@@ -258,14 +270,20 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
     n = make_seq_tab(s, cu, N, n, B, T_, kPart);
     const int seqs = s.n ? s.n : B;
     const dim3 grid((unsigned)s.items * slices), th(64 * kWaves);
-    hipLaunchKernelGGL((lru_bwd_part_kernel<T, NC>), grid, th, 0, st, b, s, slices, seg);
+    hipLaunchKernelGGL((lru_bwd_part_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg);
     hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)((D + 63) / 64) * (unsigned)seqs), dim3(64), 0, st, b, s, seg);
-    hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC>), grid, th, 0, st, b, s, slices, seg, dcp ? dcp + rows * D : nullptr);
+    hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg, dcp ? dcp + rows * D : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     rows += s.items;
   }
   return dcp ? launch_sum_rows(dcp, rows, (unsigned)D, 0, 0, b.dc, nullptr, nullptr, st) : hipSuccess;
+}
+
+template <typename T>
+hipError_t bwd_type(const LruBwdArgs& b, const int* cu, int N, int B, int T_, float* ws, hipStream_t st) {
+  if (pairs(b, sizeof(T))) return lru_full(b.f) ? bwd_go<T, 2, true>(b, cu, N, B, T_, ws, st) : bwd_go<T, 2, false>(b, cu, N, B, T_, ws, st);
+  return lru_full(b.f) ? bwd_go<T, 1, true>(b, cu, N, B, T_, ws, st) : bwd_go<T, 1, false>(b, cu, N, B, T_, ws, st);
 }
 
 }  // namespace
@@ -277,8 +295,7 @@ size_t lru_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D) {
 
 hipError_t launch_lru_bwd(int is_bf16, const LruBwdArgs& b, const int* cu, int N, int B, int T, void* workspace, hipStream_t st) {
   float* ws = static_cast<float*>(workspace);
-  if (is_bf16) return pairs(b, 2) ? bwd_go<bf16, 2>(b, cu, N, B, T, ws, st) : bwd_go<bf16, 1>(b, cu, N, B, T, ws, st);
-  return pairs(b, 4) ? bwd_go<float, 2>(b, cu, N, B, T, ws, st) : bwd_go<float, 1>(b, cu, N, B, T, ws, st);
+  return is_bf16 ? bwd_type<bf16>(b, cu, N, B, T, ws, st) : bwd_type<float>(b, cu, N, B, T, ws, st);
 }
 
 }  // namespace kda

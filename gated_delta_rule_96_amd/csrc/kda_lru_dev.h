@@ -23,7 +23,8 @@ template <typename T, int NC> struct alignas(sizeof(T) * NC) LruPack {   // NC c
 // thousands of tokens adds up), and 1 - a^2 = d (1 + a) loses nothing near
 // a = 1.  Four terms below 2^-4 (bf16 inputs: what is left out is 2^-23 of d),
 // eight below 2^-1 (2^-26).
-template <typename T> __device__ __forceinline__ float one_minus_decay(float g, float& a) {
+template <typename T> constexpr float lru_near() { return sizeof(T) == 2 ? 0.0625f : 0.5f; }
+template <typename T> __device__ __forceinline__ float one_minus_decay_near(float g) {
   constexpr bool kShort = sizeof(T) == 2;
   float s = kShort ? 1.f / 24 : 1.f / 40320;
   if (!kShort) {
@@ -34,22 +35,34 @@ template <typename T> __device__ __forceinline__ float one_minus_decay(float g, 
   }
   s = fmaf(g, s, 1.f / 6);
   s = fmaf(g, s, 0.5f);
-  s = -g * fmaf(g, s, 1.f);
-  const float e = exp2_fast(g * kLog2e);
-  const bool near = g > (kShort ? -0.0625f : -0.5f);
-  a = near ? 1.f - s : e;
-  return near ? s : 1.f - e;
+  return -g * fmaf(g, s, 1.f);
+}
+// The exponential is taken only where some lane of the wave needs it.
+template <typename T> __device__ __forceinline__ float one_minus_decay(float g, float& a) {
+  float d = one_minus_decay_near<T>(g);
+  a = 1.f - d;
+  const bool far = !(g > -lru_near<T>());
+  if (__any(far)) {
+    const float e = exp2_fast(g * kLog2e);
+    a = far ? e : a;
+    d = far ? 1.f - e : d;
+  }
+  return d;
 }
 
-// What a call is made of, the same for all lanes.
+// What a call is made of.  kFull: both gates and the unit factor, known when
+// the kernel is compiled.
 struct LruMode {
   bool gate, igate, unit;
 };
-__device__ __forceinline__ LruMode lru_mode(const LruArgs& a) { return LruMode{a.c != nullptr, a.i != nullptr, a.unit != 0}; }
+template <bool kFull> __device__ __forceinline__ LruMode lru_mode(const LruArgs& a) {
+  return kFull ? LruMode{true, true, true} : LruMode{a.c != nullptr, a.i != nullptr, a.unit != 0};
+}
+inline bool lru_full(const LruArgs& a) { return a.c && a.i && a.unit; }
 
 // a and u of one channel of a token (c: the channel's coefficient).
 template <typename T>
-__device__ __forceinline__ void lru_gates(const LruMode& md, float c, float x, float r, float i, float& a, float& u) {
+__device__ __forceinline__ void lru_gate(const LruMode md, float c, float x, float r, float i, float& a, float& u) {
   const float g = md.gate ? -c * sigmoid_fast(r) : r;
   const float d = one_minus_decay<T>(g, a);
   u = md.igate ? x * sigmoid_fast(i) : x;
