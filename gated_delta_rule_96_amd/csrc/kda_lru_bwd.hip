@@ -19,8 +19,7 @@ namespace kda {
 namespace {
 
 constexpr int kWaves = 8;
-template <typename T> struct RunOf { static constexpr int R = 16; };   // tokens of a wave's run
-template <> struct RunOf<float> { static constexpr int R = 8; };
+template <typename T> struct RunOf { static constexpr int R = 8; };   // tokens of a wave's run
 template <typename T> constexpr int part_of() { return kWaves * RunOf<T>::R; }
 
 // A run's rows as loaded.
@@ -47,8 +46,20 @@ __device__ __forceinline__ void load_rows(const LruBwdArgs& b, const SeqPart& p,
     for (int k = 0; k < R; ++k) w.i[k] = *reinterpret_cast<const Pk*>(pi + min(k, n - 1) * b.f.ldi + l.cl);
 }
 
-// a and u of a run, and its P, H and K.  Tokens past the part's end leave
-// everything as it is (a = 1, u = 0, dy = 0).
+// Hides that the rows are still the same ones: what the first walk made of them
+// is then made again in the second instead of being kept (and spilled).
+template <typename Pk> __device__ __forceinline__ void hide(Pk& v) {
+  if constexpr (sizeof(Pk) % 4 == 0) {
+    unsigned w[sizeof(Pk) / 4];
+    __builtin_memcpy(w, &v, sizeof(Pk));
+#pragma unroll
+    for (unsigned k = 0; k < sizeof(Pk) / 4; ++k) asm volatile("" : "+v"(w[k]));
+    __builtin_memcpy(&v, w, sizeof(Pk));
+  }
+}
+
+// a and u of a run of n tokens, and its P, H and K.  Tokens past the part's
+// end leave everything as it is (a = 1, u = 0, dy = 0).
 template <typename T, int NC, int R>
 __device__ __forceinline__ void run_sums(const LruMode& md, const float (&c)[NC], const BwdRun<T, NC, R>& w, int n, float (&a)[R][NC], float (&u)[R][NC],
                                          float (&P)[NC], float (&H)[NC], float (&K)[NC]) {
@@ -57,30 +68,26 @@ __device__ __forceinline__ void run_sums(const LruMode& md, const float (&c)[NC]
     P[j] = 1.f;
     H[j] = K[j] = 0.f;
   }
-  if (n > 0)
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-#pragma unroll
-      for (int j = 0; j < NC; ++j)
-        lru_gate<T>(md, c[j], to_f32(w.x[k].v[j]), to_f32(w.r[k].v[j]), md.igate ? to_f32(w.i[k].v[j]) : 0.f, a[k][j], u[k][j]);
+  if (n <= 0) return;
 #pragma unroll
   for (int k = 0; k < R; ++k)
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      if (k < n) {
-        P[j] *= a[k][j];
-        H[j] = fmaf(a[k][j], H[j], u[k][j]);
-        K[j] = fmaf(P[j], to_f32(w.dy[k].v[j]), K[j]);
-      } else {
+      lru_gate<T>(md, c[j], to_f32(w.x[k].v[j]), to_f32(w.r[k].v[j]), md.igate ? to_f32(w.i[k].v[j]) : 0.f, a[k][j], u[k][j]);
+      float d = to_f32(w.dy[k].v[j]);
+      if (k >= n) {
         a[k][j] = 1.f;
-        u[k][j] = 0.f;
+        u[k][j] = d = 0.f;
       }
+      P[j] *= a[k][j];
+      H[j] = fmaf(a[k][j], H[j], u[k][j]);
+      K[j] = fmaf(P[j], d, K[j]);
     }
 }
 
 // seg [items][3][D]: P, H, K of every part.
 template <typename T, int NC, bool kFull>
-__global__ __launch_bounds__(64 * kWaves) void lru_bwd_part_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, float* seg) {
+__global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_part_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, float* seg) {
   constexpr int R = RunOf<T>::R;
   __shared__ float red[3][kWaves][64 * NC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, D = b.f.D;
@@ -119,34 +126,56 @@ __global__ __launch_bounds__(64 * kWaves) void lru_bwd_part_kernel(const LruBwdA
   }
 }
 
-// What enters a sequence's parts: states over H, e from the right over K.
-__global__ __launch_bounds__(64) void lru_bwd_chain_kernel(const LruBwdArgs b, const SeqTab s, float* seg) {
-  const int D = b.f.D, blocks = (D + 63) / 64, li = blockIdx.x / blocks, c = (blockIdx.x - li * blocks) * 64 + threadIdx.x;
-  if (c >= D) return;
-  const int n = s.n0 + li;
+// What enters a sequence's parts: states over H, e from the right over K.  The
+// 16 waves of a work-group each take a run of the parts of 64 channels, join
+// their runs in LDS and walk them again.
+constexpr int kChainWaves = 16;
+__global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const LruBwdArgs b, const SeqTab s, float* seg) {
+  __shared__ float red[3][kChainWaves][64];
+  const int D = b.f.D, blocks = (D + 63) / 64, li = blockIdx.x / blocks, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c0 = (blockIdx.x - li * blocks) * 64 + lane;
+  const bool live = c0 < D;
+  const int c = live ? c0 : 0, n = s.n0 + li;
   const int i0 = s.n ? s.cc[li] : li * s.parts, i1 = s.n ? s.cc[li + 1] : i0 + s.parts;
-  float h = b.f.h0 ? b.f.h0[(size_t)n * D + c] : 0.f;
-#pragma unroll 8
-  for (int i = i0; i < i1; ++i) {
-    float* at = seg + (size_t)i * 3 * D + c;
-    const float P = at[0], H = at[D];
-    at[D] = h;
-    h = fmaf(P, h, H);
+  const int per = (i1 - i0 + kChainWaves - 1) / kChainWaves, lo = min(i0 + wave * per, i1), hi = min(lo + per, i1);
+  float* at = seg + c;
+  float P = 1.f, H = 0.f, K = 0.f;
+#pragma unroll 4
+  for (int i = lo; i < hi; ++i) {
+    const float* q = at + (size_t)i * 3 * D;
+    const float p = q[0];
+    H = fmaf(p, H, q[D]);
+    K = fmaf(P, q[2 * D], K);
+    P *= p;
   }
-  float e = b.dht ? b.dht[(size_t)n * D + c] : 0.f;
-#pragma unroll 8
-  for (int i = i1 - 1; i >= i0; --i) {
-    float* at = seg + (size_t)i * 3 * D + c;
-    const float P = at[0], K = at[2 * D];
-    at[2 * D] = e;
-    e = fmaf(P, e, K);
+  red[0][wave][lane] = P;
+  red[1][wave][lane] = H;
+  red[2][wave][lane] = K;
+  __syncthreads();
+  float h = b.f.h0 ? b.f.h0[(size_t)n * D + c] : 0.f, e = b.dht ? b.dht[(size_t)n * D + c] : 0.f;
+  for (int q = 0; q < wave; ++q) h = fmaf(red[0][q][lane], h, red[1][q][lane]);
+  for (int q = kChainWaves - 1; q > wave; --q) e = fmaf(red[0][q][lane], e, red[2][q][lane]);
+  if (!live) return;
+#pragma unroll 4
+  for (int i = lo; i < hi; ++i) {
+    float* q = at + (size_t)i * 3 * D;
+    const float p = q[0], v = q[D];
+    q[D] = h;
+    h = fmaf(p, h, v);
   }
-  if (b.dh0) b.dh0[(size_t)n * D + c] = e;
+#pragma unroll 4
+  for (int i = hi - 1; i >= lo; --i) {
+    float* q = at + (size_t)i * 3 * D;
+    const float p = q[0], v = q[2 * D];
+    q[2 * D] = e;
+    e = fmaf(p, e, v);
+  }
+  if (b.dh0 && wave == 0) b.dh0[(size_t)n * D + c] = e;
 }
 
 // Gradients.  dcp [items][D]: every part's sum of dg Sigmoid(r), or null.
 template <typename T, int NC, bool kFull>
-__global__ __launch_bounds__(64 * kWaves) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
+__global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
   constexpr int R = RunOf<T>::R;
   typedef LruPack<T, NC> Pk;
   __shared__ float red[3][kWaves][64 * NC];
@@ -182,6 +211,7 @@ __global__ __launch_bounds__(64 * kWaves) void lru_bwd_out_kernel(const LruBwdAr
 #pragma unroll
     for (int j = 0; j < NC; ++j) e[j] = fmaf(red[0][q][lane * NC + j], e[j], red[2][q][lane * NC + j]);
   // u becomes the state before its token
+  if (n > 0)
 #pragma unroll
   for (int k = 0; k < R; ++k)
 #pragma unroll
@@ -190,6 +220,12 @@ __global__ __launch_bounds__(64 * kWaves) void lru_bwd_out_kernel(const LruBwdAr
       h[j] = fmaf(a[k][j], h[j], u[k][j]);
       u[k][j] = before;
     }
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    hide(w.x[k]);
+    hide(w.r[k]);
+    hide(w.i[k]);
+  }
 #pragma unroll
   for (int k = R - 1; k >= 0; --k) {
     if (k >= n) continue;
@@ -271,7 +307,7 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
     const int seqs = s.n ? s.n : B;
     const dim3 grid((unsigned)s.items * slices), th(64 * kWaves);
     hipLaunchKernelGGL((lru_bwd_part_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg);
-    hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)((D + 63) / 64) * (unsigned)seqs), dim3(64), 0, st, b, s, seg);
+    hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)((D + 63) / 64) * (unsigned)seqs), dim3(64 * kChainWaves), 0, st, b, s, seg);
     hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg, dcp ? dcp + rows * D : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
