@@ -5,6 +5,7 @@
 //   dx = l m s,   di = l m x s (1 - s),   s = Sigmoid(i)
 //   dg = a (l h_{t-1} - l s x a / m)      (the second term with unit only)
 //   dr = dg g (1 - Sigmoid(r)),  dc = -sum dg Sigmoid(r)   (dr = dg without c)
+// (1 - Sigmoid in fp32: off by 3 x 2^-24 of 1, not of itself.)
 // A part of a sequence (as in the forward) takes e from the right by
 // e -> P e + K with K = sum_t P_t dy_t, P_t the product of its a up to t.
 // Where m = 0 (a decay of exactly 1) its derivative counts as 0.
@@ -18,7 +19,7 @@ namespace kda {
 
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 4;
 template <typename T> struct RunOf { static constexpr int R = 8; };   // tokens of a wave's run
 template <typename T> constexpr int part_of() { return kWaves * RunOf<T>::R; }
 
@@ -46,23 +47,11 @@ __device__ __forceinline__ void load_rows(const LruBwdArgs& b, const SeqPart& p,
     for (int k = 0; k < R; ++k) w.i[k] = *reinterpret_cast<const Pk*>(pi + min(k, n - 1) * b.f.ldi + l.cl);
 }
 
-// Hides that the rows are still the same ones: what the first walk made of them
-// is then made again in the second instead of being kept (and spilled).
-template <typename Pk> __device__ __forceinline__ void hide(Pk& v) {
-  if constexpr (sizeof(Pk) % 4 == 0) {
-    unsigned w[sizeof(Pk) / 4];
-    __builtin_memcpy(w, &v, sizeof(Pk));
-#pragma unroll
-    for (unsigned k = 0; k < sizeof(Pk) / 4; ++k) asm volatile("" : "+v"(w[k]));
-    __builtin_memcpy(&v, w, sizeof(Pk));
-  }
-}
-
-// a and u of a run of n tokens, and its P, H and K.  Tokens past the part's
-// end leave everything as it is (a = 1, u = 0, dy = 0).
-template <typename T, int NC, int R>
-__device__ __forceinline__ void run_sums(const LruMode& md, const float (&c)[NC], const BwdRun<T, NC, R>& w, int n, float (&a)[R][NC], float (&u)[R][NC],
-                                         float (&P)[NC], float (&H)[NC], float (&K)[NC]) {
+// P, H and K of a run of n tokens from its tokens' a, u and dy, which `gate`
+// gives.  Tokens past the part's end leave everything as it is (a = 1, u = 0,
+// dy = 0).
+template <typename T, int NC, int R, typename F>
+__device__ __forceinline__ void run_sums(const BwdRun<T, NC, R>& w, int n, float (&P)[NC], float (&H)[NC], float (&K)[NC], F gate) {
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     P[j] = 1.f;
@@ -73,14 +62,14 @@ __device__ __forceinline__ void run_sums(const LruMode& md, const float (&c)[NC]
   for (int k = 0; k < R; ++k)
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      lru_gate<T>(md, c[j], to_f32(w.x[k].v[j]), to_f32(w.r[k].v[j]), md.igate ? to_f32(w.i[k].v[j]) : 0.f, a[k][j], u[k][j]);
-      float d = to_f32(w.dy[k].v[j]);
+      float a, u, d = to_f32(w.dy[k].v[j]);
+      gate(k, j, a, u);
       if (k >= n) {
-        a[k][j] = 1.f;
-        u[k][j] = d = 0.f;
+        a = 1.f;
+        u = d = 0.f;
       }
-      P[j] *= a[k][j];
-      H[j] = fmaf(a[k][j], H[j], u[k][j]);
+      P[j] *= a;
+      H[j] = fmaf(a, H[j], u);
       K[j] = fmaf(P[j], d, K[j]);
     }
 }
@@ -97,9 +86,12 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_part_kernel(const LruB
   const int t = p.t0 + wave * R;
   BwdRun<T, NC, R> w;
   load_rows<T, NC, R, kFull>(b, p, l, t, w);
-  float a[R][NC], u[R][NC], c[NC], P[NC], H[NC], K[NC];
+  float c[NC], P[NC], H[NC], K[NC];
   lru_coef<NC>(b.f, l, c);
-  run_sums<T, NC, R>(lru_mode<kFull>(b.f), c, w, p.t1 - t, a, u, P, H, K);
+  const LruMode md = lru_mode<kFull>(b.f);
+  run_sums<T, NC, R>(w, p.t1 - t, P, H, K, [&](int k, int j, float& a, float& u) {
+    lru_gate<T>(md, c[j], to_f32(w.x[k].v[j]), to_f32(w.r[k].v[j]), md.igate ? to_f32(w.i[k].v[j]) : 0.f, a, u);
+  });
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     red[0][wave][lane * NC + j] = P[j];
@@ -175,7 +167,7 @@ __global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const L
 
 // Gradients.  dcp [items][D]: every part's sum of dg Sigmoid(r), or null.
 template <typename T, int NC, bool kFull>
-__global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
+__global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
   constexpr int R = RunOf<T>::R;
   typedef LruPack<T, NC> Pk;
   __shared__ float red[3][kWaves][64 * NC];
@@ -186,7 +178,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_out_kernel(const LruBw
   const int t = p.t0 + wave * R, n = p.t1 - t;
   BwdRun<T, NC, R> w;
   load_rows<T, NC, R, kFull>(b, p, l, t, w);
-  float a[R][NC], u[R][NC], c[NC], P[NC], H[NC], K[NC], h[NC], e[NC], sum[NC];
+  // of every token: a, u (later the state before it), Sigmoid(r), Sigmoid(i), m
+  // and 1/m; the second walk has them from the first
+  float a[R][NC], u[R][NC], sr[R][NC], si[R][NC], m[R][NC], im[R][NC], c[NC], P[NC], H[NC], K[NC], h[NC], e[NC], sum[NC];
   lru_coef<NC>(b.f, l, c);
   const LruMode md = lru_mode<kFull>(b.f);
   const float* from = seg + (size_t)item * 3 * D + l.cl;
@@ -196,7 +190,21 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_out_kernel(const LruBw
     e[j] = from[2 * D + j];
     sum[j] = 0.f;
   }
-  run_sums<T, NC, R>(md, c, w, n, a, u, P, H, K);
+  run_sums<T, NC, R>(w, n, P, H, K, [&](int k, int j, float& av, float& uv) {
+    const float r = to_f32(w.r[k].v[j]);
+    sr[k][j] = md.gate ? sigmoid_fast(r) : 1.f;
+    si[k][j] = md.igate ? sigmoid_fast(to_f32(w.i[k].v[j])) : 1.f;
+    const float d = one_minus_decay<T>(md.gate ? -c[j] * sr[k][j] : r, av);
+    m[k][j] = im[k][j] = 1.f;
+    if (md.unit) {
+      const float q = d * (1.f + av);
+      im[k][j] = __builtin_fabsf(q) < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q);
+      m[k][j] = q * im[k][j];
+    }
+    uv = to_f32(w.x[k].v[j]) * si[k][j] * m[k][j];
+    a[k][j] = av;
+    u[k][j] = uv;
+  });
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     red[0][wave][lane * NC + j] = P[j];
@@ -210,53 +218,29 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_out_kernel(const LruBw
   for (int q = kWaves - 1; q > wave; --q)
 #pragma unroll
     for (int j = 0; j < NC; ++j) e[j] = fmaf(red[0][q][lane * NC + j], e[j], red[2][q][lane * NC + j]);
-  // u becomes the state before its token
   if (n > 0)
 #pragma unroll
-  for (int k = 0; k < R; ++k)
+    for (int k = 0; k < R; ++k)
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      const float before = h[j];
-      h[j] = fmaf(a[k][j], h[j], u[k][j]);
-      u[k][j] = before;
-    }
-#pragma unroll
-  for (int k = 0; k < R; ++k) {
-    hide(w.x[k]);
-    hide(w.r[k]);
-    hide(w.i[k]);
-  }
+      for (int j = 0; j < NC; ++j) {
+        const float before = h[j];
+        h[j] = fmaf(a[k][j], h[j], u[k][j]);
+        u[k][j] = before;
+      }
 #pragma unroll
   for (int k = R - 1; k >= 0; --k) {
     if (k >= n) continue;
     Pk dx, dr, di;
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const float x = to_f32(w.x[k].v[j]), r = to_f32(w.r[k].v[j]), av = a[k][j];
-      float sr = 1.f, tr = 1.f, g = r, si = 1.f, ti = 0.f, m = 1.f, im = 0.f;   // t: 1 - Sigmoid
-      if (md.gate) {
-        const float q = exp2_fast(-r * kLog2e);
-        sr = __builtin_amdgcn_rcpf(1.f + q);
-        tr = q > 1.f ? 1.f - sr : q * sr;
-        g = -c[j] * sr;
-      }
-      if (md.igate) {
-        const float q = exp2_fast(-to_f32(w.i[k].v[j]) * kLog2e);
-        si = __builtin_amdgcn_rcpf(1.f + q);
-        ti = q > 1.f ? 1.f - si : q * si;
-      }
-      if (md.unit) {
-        float unused;
-        m = __builtin_amdgcn_sqrtf(one_minus_decay<T>(g, unused) * (1.f + av));
-        im = m > 0.f ? __builtin_amdgcn_rcpf(m) : 0.f;
-      }
-      const float lt = to_f32(w.dy[k].v[j]) + e[j], lm = lt * m * si, ls = lt * si * x;
-      const float dg = av * (lt * u[k][j] - ls * av * im);
-      dx.v[j] = from_f32<T>(lm);
-      di.v[j] = from_f32<T>(lm * x * ti);
-      dr.v[j] = from_f32<T>(md.gate ? dg * g * tr : dg);
-      sum[j] = fmaf(dg, sr, sum[j]);
-      e[j] = av * lt;
+      const float x = to_f32(w.x[k].v[j]), s = si[k][j], lt = to_f32(w.dy[k].v[j]) + e[j];
+      e[j] = a[k][j] * lt;
+      const float gx = lt * m[k][j] * s;
+      const float dg = e[j] * (md.unit ? fmaf(-a[k][j], x * s * im[k][j], u[k][j]) : u[k][j]);
+      dx.v[j] = from_f32<T>(gx);
+      di.v[j] = from_f32<T>(gx * x * (1.f - s));
+      dr.v[j] = from_f32<T>(md.gate ? dg * (-c[j] * sr[k][j]) * (1.f - sr[k][j]) : dg);
+      sum[j] = fmaf(dg, sr[k][j], sum[j]);
     }
     if (l.live) {
       const size_t at = (p.start + (size_t)(t + k)) * D + l.c;

@@ -9,7 +9,9 @@ the error of h_t is at most E_t = a E_{t-1} + (4 + 8 |g|) u a H_{t-1} + 40 u |u_
 + 2 u H_t with H_t = a H_{t-1} + |u_t|, and likewise F_t for l_t = dL/dh_t with
 L_t = |dy_t| + a L_{t+1}.  Products of them add, 100 u for their gates; each
 output then rounds by h = finfo.eps / 2.  dc sums at most 16 tokens of a run and
-8 runs in fp32 (24 u), parts in 64 bits.
+8 runs in fp32 (24 u), parts in 64 bits.  1 - Sigmoid is a difference: the
+Sigmoid is off by 2 u of itself at most and the difference rounds by u / 2, 3 u
+together, of 1 and not of the difference.
 """
 import numpy as np
 import pytest
@@ -105,11 +107,11 @@ def oracle(k, lens, unit, back=False):
         tg = a * (Fl * np.abs(before) + L * Eb + 100 * U * L * Hb) + back2 * (Fl + 100 * U * L)
         sg = np.abs(g) * block.sigmoid(-s[1]) if c is not None else np.ones_like(g)
         size = L * (a * Hb + back2)
-        for name, v in (("dx", dx), ("tdx", tx), ("dr", dr), ("tdr", (tg + 20 * U * size) * sg), ("dh0", dh0), ("tdh0", F)):
+        for name, v in (("dx", dx), ("tdx", tx), ("dr", dr), ("tdr", (tg + 20 * U * size) * sg + (3 * U * size * np.abs(g) if c is not None else 0.0)), ("dh0", dh0), ("tdh0", F)):
             out[name].append(v)
         if i is not None:
             out["di"].append(di)
-            out["tdi"].append((tx + 20 * U * L * ms) * np.abs(s[0]) * block.sigmoid(-s[2]))
+            out["tdi"].append(((tx + 20 * U * L * ms) * block.sigmoid(-s[2]) + 3 * U * L * ms) * np.abs(s[0]))
         if c is not None:
             sr = block.sigmoid(s[1])
             dc += dcn
