@@ -25,9 +25,9 @@ constexpr int kMaxNormD = 16384;
 // Channels of the recurrence and outputs of the product are numbered in 32
 // bits, a tile beyond the last.
 constexpr int kMaxWidth = 1 << 30;
-// Bytes between two rows of the product's operands: a tile of 256 rows is
-// addressed in 32 bits.
-constexpr int kMaxStride8 = 1 << 24;
+// Bytes between two rows of the product's operands, and scales between two
+// rows': a tile of 256 rows is addressed in 32 bits.
+constexpr int kMaxStride8 = 1 << 24, kMaxScaleStride = 1 << 20;
 
 int check_norm(long long rows, int D, float eps) {
   if (rows <= 0 || rows > kMaxRows || D <= 0 || !(eps >= 0.f)) return KDA_ERR_SHAPE;
@@ -89,7 +89,7 @@ int kda_gemm_fp8(const void* a, long long lda, const float* sa, long long lsa, c
   if (M <= 0 || M > kMaxRows || N <= 0 || N > kMaxWidth || K <= 0 || K > kMaxStride8 || lda > kMaxStride8) return KDA_ERR_SHAPE;
   if (K % 16) return KDA_ERR_UNSUPPORTED;
   const int KB = (K + 127) / 128;
-  if (lda < K || lsa < KB || !size_ok(M, lda, 8, 1) || !size_ok(M, lsa, 8, 1) || !size_ok(M, N, 8, 1)) return KDA_ERR_SHAPE;
+  if (lda < K || lsa < KB || lsa > kMaxScaleStride || !size_ok(M, lda, 8, 1) || !size_ok(M, lsa, 8, 1) || !size_ok(M, N, 8, 1)) return KDA_ERR_SHAPE;
   if (!a || !sa || !w || !sw || !c) return KDA_ERR_NULL;
   if (!aligned16(a) || (M > 1 && lda % 16) || !aligned16(w) || !aligned16(c)) return KDA_ERR_ALIGN;
   if ((reinterpret_cast<uintptr_t>(sa) & 3u) || (reinterpret_cast<uintptr_t>(sw) & 3u)) return KDA_ERR_ALIGN;

@@ -85,9 +85,9 @@ template <typename T, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8Args g, unsigned tm, unsigned tn) {
   constexpr int kThreads = 64 * WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int LA = BM * 8 / kThreads, LB = BN * 8 / kThreads;   // 16-byte pieces a thread stages
-  static_assert(BN / WN <= 128 && BM <= 256 && BN <= 256 && BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0, "tile");
+  static_assert(kThreads % 128 == 0 && BN / WN <= 128 && BM <= 256 && BN <= 256 && BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0, "tile");
   extern __shared__ u8 smem[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave % WM, wn = wave / WM, r = lane & 15, grp = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave % WM, wn = wave / WM, r = lane & 15, grp = lane >> 4;
   // tiles of one XCD (work-groups b, b + 8, ..) are neighbours: runs of eight
   // tile rows share a column of weights in its L2
   const unsigned tiles = tm * tn, per = (tiles + 7) / 8;
@@ -115,32 +115,26 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
   // Pieces past K re-read the row's first block; the products left out are made
   // zero on a's side (what is read of w there is w's own row: no new NaN).
   auto stage = [&](int kb) {
-    u8* base = smem + (kb & 1) * (BM + BN) * 128;
-    const unsigned k = (unsigned)kb * 128;
-    const bool tail = kb * 128 + 128 > g.K;
+    u8* base = smem + (kb & 1) * (BM + BN) * 128 + wave * 1024;
+    const size_t k = (size_t)kb * 128;
+    if (kb * 128 + 128 <= g.K) {
 #pragma unroll
-    for (int i = 0; i < LA; ++i) {
-      unsigned o = oa[i] + k;
-      if (tail) {
-        const int s = i * kThreads + tid, c = ((s & 7) ^ ((s >> 4) & 7)) * 16;
-        if ((int)k + c >= g.K) o = oa[i] - c;
-      }
-      __builtin_amdgcn_global_load_lds((GlbP)(ga + o), (LdsP)(base + (i * kThreads + wave * 64) * 16), 16, 0, 0);
-    }
-    base += BM * 128;
+      for (int i = 0; i < LA; ++i) __builtin_amdgcn_global_load_lds((GlbP)(ga + k + oa[i]), (LdsP)(base + i * kThreads * 16), 16, 0, 0);
 #pragma unroll
-    for (int i = 0; i < LB; ++i) {
-      unsigned o = ob[i] + k;
-      if (tail) {
-        const int s = i * kThreads + tid, c = ((s & 7) ^ ((s >> 4) & 7)) * 16;
-        if ((int)k + c >= g.K) o = ob[i] - c;
-      }
-      __builtin_amdgcn_global_load_lds((GlbP)(gw + o), (LdsP)(base + (i * kThreads + wave * 64) * 16), 16, 0, 0);
+      for (int i = 0; i < LB; ++i) __builtin_amdgcn_global_load_lds((GlbP)(gw + k + ob[i]), (LdsP)(base + BM * 128 + i * kThreads * 16), 16, 0, 0);
+    } else {
+      const int c = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;   // (the same piece of every row this thread stages)
+      const size_t kc = (int)k + c < g.K ? k : (size_t)0 - c;
+#pragma unroll
+      for (int i = 0; i < LA; ++i) __builtin_amdgcn_global_load_lds((GlbP)(ga + kc + oa[i]), (LdsP)(base + i * kThreads * 16), 16, 0, 0);
+#pragma unroll
+      for (int i = 0; i < LB; ++i) __builtin_amdgcn_global_load_lds((GlbP)(gw + kc + ob[i]), (LdsP)(base + BM * 128 + i * kThreads * 16), 16, 0, 0);
     }
   };
-  const float* sa[MT];
+  const float* gsa = g.sa + m0 * g.lsa;
+  unsigned os[MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) sa[i] = g.sa + (m0 + min(wm * (BM / WM) + i * 16 + r, rows - 1)) * g.lsa;
+  for (int i = 0; i < MT; ++i) os[i] = (unsigned)min(wm * (BM / WM) + i * 16 + r, rows - 1) * (unsigned)g.lsa;
   const float* sw = g.sw + (size_t)min((n0 + wn * (BN / WN)) / 128, (g.N - 1) / 128) * KB;
 
   // where this lane's pieces grp and grp + 4 of row r of a 16-row tile are
@@ -161,7 +155,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
   // use before would wait for the step's tiles as well
   float an[MT], wnx = sw[0];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) an[i] = sa[i][0];
+  for (int i = 0; i < MT; ++i) an[i] = gsa[os[i]];
   stage(0);
   for (int kb = 0; kb < KB; ++kb) {
     // this wave's pieces of step kb are in LDS (a barrier alone does not wait
@@ -174,7 +168,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
     if (kb + 1 < KB) {
       wnx = sw[kb + 1];
 #pragma unroll
-      for (int i = 0; i < MT; ++i) an[i] = sa[i][kb + 1];
+      for (int i = 0; i < MT; ++i) an[i] = (gsa + kb + 1)[os[i]];
       stage(kb + 1);
     }
     const u8* ta = smem + (kb & 1) * (BM + BN) * 128 + wm * (BM / WM) * 128;
@@ -203,12 +197,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
         if (i == 0 && j + 1 < NT) wb[(j + 1) & 1] = frag(tb + (j + 1) * 2048);
         p[q % 3] = mma128(wb[j & 1], xa[i]);
       }
+      __builtin_amdgcn_sched_barrier(0);   // (the compiler would put the fmas in front)
       if (q >= 2) {
         const int j = (q - 2) / MT, i = (q - 2) % MT;
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][i][e] = fmaf(p[(q - 2) % 3][e], f[i], acc[j][i][e]);
       }
-      __builtin_amdgcn_sched_barrier(0);   // (the compiler would put the fmas right behind their product)
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 #pragma unroll

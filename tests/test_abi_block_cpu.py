@@ -57,7 +57,7 @@ GEMM = dict(a=A[0], lda=320, sa=A[1], lsa=3, w=A[2], sw=A[3], c=A[4], ct=1, M=7,
 @pytest.mark.parametrize("kw,code", [
     (dict(a=None), 1), (dict(sa=None), 1), (dict(w=None), 1), (dict(sw=None), 1), (dict(c=None), 1),
     (dict(M=0), 2), (dict(N=0), 2), (dict(K=0), 2), (dict(lda=304), 2), (dict(lsa=2), 2), (dict(K=(1 << 24) + 16, lda=1 << 25, lsa=1 << 20), 2),
-    (dict(lda=(1 << 24) + 16), 2), (dict(M=1 << 41), 2), (dict(N=(1 << 30) + 1), 2),
+    (dict(lda=(1 << 24) + 16), 2), (dict(lsa=(1 << 20) + 1), 2), (dict(M=1 << 41), 2), (dict(N=(1 << 30) + 1), 2),
     (dict(ct=4), 3), (dict(a=A[0] + 8), 4), (dict(lda=328), 4), (dict(w=A[2] + 8), 4), (dict(c=A[4] + 8), 4), (dict(sa=A[1] + 2), 4), (dict(sw=A[3] + 1), 4),
     (dict(K=312), 5), (dict(K=8, lda=16), 5),
     (dict(c=A[0]), 10), (dict(c=A[2] + 64), 10), (dict(c=A[1]), 10), (dict(c=A[3]), 10),
