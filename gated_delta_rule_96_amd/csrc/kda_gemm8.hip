@@ -8,6 +8,10 @@
 // The weights are the MFMA's left operand, so that a lane holds four
 // neighbouring outputs of one row (an 8- or 16-byte store) and needs one scale
 // per 16 rows instead of four.
+// Measured: 8192 x 12288 x 4096 402 us (2.05 PFLOP/s; a library's product of
+// such operands with one scale each 338), 256 rows 22, one row 11.  Of the
+// large tile's time the matrix instructions take 45%; the fmas that join
+// blocks, the LDS reads and the loads to LDS share the rest.
 #include "kda_rows.h"
 
 namespace kda {
@@ -79,9 +83,9 @@ template <typename T> __device__ __forceinline__ void store_out(const Gemm8Args&
 __device__ __forceinline__ int lds_piece(int r, int p) { return r * 128 + ((p ^ ((r >> 1) & 7)) << 4); }
 
 
-// Work-group tile BM x BN, WM x WN waves; `left` reduction indices of a step
-// are inside K (128 but for the last).
-template <typename T, int BM, int BN, int WM, int WN>
+// Work-group tile BM x BN, WM x WN waves, S steps in LDS: step kb's loads are
+// issued S - 1 steps before it.
+template <typename T, int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8Args g, unsigned tm, unsigned tn) {
   constexpr int kThreads = 64 * WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int LA = BM * 8 / kThreads, LB = BN * 8 / kThreads;   // 16-byte pieces a thread stages
@@ -112,29 +116,37 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
     const int s = i * kThreads + tid, row = s >> 3;
     ob[i] = (unsigned)min(row, cols - 1) * (unsigned)g.K + ((s & 7) ^ ((row >> 1) & 7)) * 16;
   }
-  // Pieces past K re-read the row's first block; the products left out are made
+  // Offsets reach 256 strides at most.  Pieces past K re-read the row's first block; the products left out are made
   // zero on a's side (what is read of w there is w's own row: no new NaN).
-  auto stage = [&](int kb) {
-    u8* base = smem + (kb & 1) * (BM + BN) * 128 + wave * 1024;
-    const size_t k = (size_t)kb * 128;
-    if (kb * 128 + 128 <= g.K) {
+  // (a thread stages the same piece of every row it stages)
+  const int ck = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;
+  auto step_offset = [&](int kb) { return (unsigned)(kb * 128 + ck < g.K ? kb * 128 : -ck); };
+  auto stage = [&](int n, int kb, unsigned k) {   // the n-th of a thread's LA + LB pieces of step kb
+    u8* base = smem + kb % S * ((BM + BN) * 128) + wave * 1024;
+    if (n < LA) __builtin_amdgcn_global_load_lds((GlbP)(ga + (oa[n < LA ? n : 0] + k)), (LdsP)(base + n * kThreads * 16), 16, 0, 0);
+    else __builtin_amdgcn_global_load_lds((GlbP)(gw + (ob[n < LA ? 0 : n - LA] + k)), (LdsP)(base + BM * 128 + (n - LA) * kThreads * 16), 16, 0, 0);
+  };
+  // The rows' scales go through LDS four steps at a time, one row a thread: a
+  // scale a lane straight from memory touched a cache line a row in every step
+  // (8192 x 12288 x 4096: 524 us).
+  constexpr int kSc = S * (BM + BN) * 128;   // their place in LDS: two sets of [BM][4]
+  static_assert(kThreads >= BM, "a thread a row");
+  const bool sc4 = (KB & 3) == 0 && (g.lsa & 3) == 0 && (reinterpret_cast<uintptr_t>(g.sa) & 15) == 0;
+  const float* gsa = g.sa + m0 * g.lsa;
+  const unsigned os = (unsigned)min(tid, rows - 1) * (unsigned)g.lsa;
+  auto stage_scales = [&](int kq) {   // of steps 4 kq .. 4 kq + 3
+    if (wave * 64 >= BM) return;
+    u8* base = smem + kSc + (kq & 1) * (BM * 16);
+    if (sc4) {
+      __builtin_amdgcn_global_load_lds((GlbP)(gsa + 4 * kq + os), (LdsP)(base + wave * 1024), 16, 0, 0);
+    } else {   // set kq as [4][BM]
 #pragma unroll
-      for (int i = 0; i < LA; ++i) __builtin_amdgcn_global_load_lds((GlbP)(ga + k + oa[i]), (LdsP)(base + i * kThreads * 16), 16, 0, 0);
-#pragma unroll
-      for (int i = 0; i < LB; ++i) __builtin_amdgcn_global_load_lds((GlbP)(gw + k + ob[i]), (LdsP)(base + BM * 128 + i * kThreads * 16), 16, 0, 0);
-    } else {
-      const int c = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;   // (the same piece of every row this thread stages)
-      const size_t kc = (int)k + c < g.K ? k : (size_t)0 - c;
-#pragma unroll
-      for (int i = 0; i < LA; ++i) __builtin_amdgcn_global_load_lds((GlbP)(ga + kc + oa[i]), (LdsP)(base + i * kThreads * 16), 16, 0, 0);
-#pragma unroll
-      for (int i = 0; i < LB; ++i) __builtin_amdgcn_global_load_lds((GlbP)(gw + kc + ob[i]), (LdsP)(base + BM * 128 + i * kThreads * 16), 16, 0, 0);
+      for (int e = 0; e < 4; ++e)
+        __builtin_amdgcn_global_load_lds((GlbP)(gsa + min(4 * kq + e, KB - 1) + os), (LdsP)(base + e * (BM * 4) + wave * 256), 4, 0, 0);
     }
   };
-  const float* gsa = g.sa + m0 * g.lsa;
-  unsigned os[MT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) os[i] = (unsigned)min(wm * (BM / WM) + i * 16 + r, rows - 1) * (unsigned)g.lsa;
+  const int row_at = sc4 ? 16 : 4, step_at = sc4 ? 4 : BM * 4;   // bytes between rows, between steps
+  const u8* sc = smem + kSc + (wm * (BM / WM) + r) * row_at;
   const float* sw = g.sw + (size_t)min((n0 + wn * (BN / WN)) / 128, (g.N - 1) / 128) * KB;
 
   // where this lane's pieces grp and grp + 4 of row r of a 16-row tile are
@@ -151,28 +163,35 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
   for (int j = 0; j < NT; ++j)
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[j][i] = zero4();
-  // scales of the coming step as loaded: multiplied behind the next wait, as a
-  // use before would wait for the step's tiles as well
-  float an[MT], wnx = sw[0];
+  stage_scales(0);
 #pragma unroll
-  for (int i = 0; i < MT; ++i) an[i] = gsa[os[i]];
-  stage(0);
+  for (int kb = 0; kb < S - 1; ++kb) {
+    const unsigned k = step_offset(min(kb, KB - 1));
+#pragma unroll
+    for (int n = 0; n < LA + LB; ++n) stage(n, kb, k);
+  }
+  float ws64 = 0.f;
   for (int kb = 0; kb < KB; ++kb) {
-    // this wave's pieces of step kb are in LDS (a barrier alone does not wait
-    // for loads to LDS), and every wave has read what it needs of step kb - 1
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+    // This wave's pieces of step kb are in LDS (a barrier alone does not wait
+    // for loads to LDS): behind them are at least those of S - 2 steps.  Every
+    // wave has read what it needs of step kb - 1.
+    // (A fence in front of the barrier would wait for all loads in flight.)
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * (LA + LB)) : "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if ((kb & 63) == 0) {
+      ws64 = sw[min(kb + lane, KB - 1)];   // a lane a step
+      asm volatile("" : "+v"(ws64));       // (waited for here, not in every step)
+    }
+    const float ws = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws64), kb & 63));
     float f[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) f[i] = an[i] * wnx;
-    if (kb + 1 < KB) {
-      wnx = sw[kb + 1];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) an[i] = (gsa + kb + 1)[os[i]];
-      stage(kb + 1);
-    }
-    const u8* ta = smem + (kb & 1) * (BM + BN) * 128 + wm * (BM / WM) * 128;
-    const u8* tb = smem + (kb & 1) * (BM + BN) * 128 + (BM + wn * (BN / WN)) * 128;
+    for (int i = 0; i < MT; ++i)
+      f[i] = ws * *reinterpret_cast<const float*>(sc + ((kb >> 2) & 1) * (BM * 16) + (kb & 3) * step_at + i * 16 * row_at);
+    const unsigned kn = step_offset(min(kb + S - 1, KB - 1));   // (behind the last step its blocks again, unused)
+    if ((kb & 3) == 0 && kb + 4 < KB) stage_scales((kb >> 2) + 1);
+    const u8* ta = smem + kb % S * ((BM + BN) * 128) + wm * (BM / WM) * 128;
+    const u8* tb = ta + (BM - wm * (BM / WM) + wn * (BN / WN)) * 128;
     Frag<T> xa[MT];
     if (kb * 128 + 128 <= g.K) {
 #pragma unroll
@@ -196,6 +215,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
         const int j = q / MT, i = q % MT;
         if (i == 0 && j + 1 < NT) wb[(j + 1) & 1] = frag(tb + (j + 1) * 2048);
         p[q % 3] = mma128(wb[j & 1], xa[i]);
+        // the coming loads one by one between the first products: issued at once
+        // they hold the wave until the cache has taken them (480 us), spread over
+        // all products the last ones come late (490; 451 like this)
+        constexpr int kEach = (LA + LB + NT * MT - 1) / (NT * MT);
+#pragma unroll
+        for (int n = q * kEach; n < (q + 1) * kEach && n < LA + LB; ++n) stage(n, kb + S - 1, kn);
       }
       __builtin_amdgcn_sched_barrier(0);   // (the compiler would put the fmas in front)
       if (q >= 2) {
@@ -206,6 +231,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
       __builtin_amdgcn_sched_barrier(0);
     }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load to LDS outlives the work-group
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int row = wm * (BM / WM) + i * 16 + r;
@@ -216,78 +242,112 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
 }
 
 // ---------------------------------------------------------------- few rows
-// Up to 16 MT rows: bound by the weights' bytes.  A work-group takes 16
-// outputs of every row; its waves take every WK-th block of K straight from
-// memory and are joined through LDS.
-template <typename T, int MT, int WK>
+// Up to 16 rows: bound by the weights' bytes.  A work-group takes 16 NT outputs
+// of every row; its WK waves take every WK-th block of K straight from memory
+// and are joined through LDS.
+template <typename T, int NT, int WK>
 __global__ __launch_bounds__(64 * WK) void gemm8_rows_kernel(const Gemm8Args g) {
-  __shared__ f32x4 part[WK][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, grp = lane >> 4;
-  const int n0 = blockIdx.x * 16, KB = (g.K + 127) / 128;
-  const u8* pw = g.w + (size_t)min(n0 + r, g.N - 1) * g.K;
+  __shared__ f32x4 part[WK][NT][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, grp = lane >> 4;
+  const int n0 = blockIdx.x * (16 * NT), KB = (g.K + 127) / 128, cols = min(16 * NT, g.N - n0), m = min(r, (int)g.M - 1);
+  const u8* gw = g.w + (size_t)n0 * g.K;
   const float* sw = g.sw + (size_t)(n0 / 128) * KB;
-  const u8* pa[MT];
-  const float* sa[MT];
-  f32x4 acc[MT];
+  unsigned ow[NT];   // (rows past the last re-read that one)
 #pragma unroll
-  for (int i = 0; i < MT; ++i) {
-    const long long m = min((long long)(i * 16 + r), g.M - 1);
-    pa[i] = g.a + m * g.lda;
-    sa[i] = g.sa + m * g.lsa;
-    acc[i] = zero4();
-  }
+  for (int j = 0; j < NT; ++j) ow[j] = (unsigned)min(j * 16 + r, cols - 1) * (unsigned)g.K + grp * 16;
+  const unsigned oa = (unsigned)m * (unsigned)g.lda + grp * 16, os = (unsigned)m * (unsigned)g.lsa;
+  f32x4 acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = zero4();
   for (int kb = wave; kb < KB; kb += WK) {
-    const int k0 = kb * 128 + grp * 16, k1 = k0 + 64;
+    const unsigned k = (unsigned)kb * 128;
+    const bool in0 = (int)k + grp * 16 < g.K, in1 = (int)k + grp * 16 + 64 < g.K;
     const i32x4 z{0, 0, 0, 0};
-    const i32x4 w0 = k0 < g.K ? *reinterpret_cast<const i32x4*>(pw + k0) : z, w1 = k1 < g.K ? *reinterpret_cast<const i32x4*>(pw + k1) : z;
-    Frag<T> wb, xa;
-    wb.set(w0, w1);
-    const float s = sw[kb];
+    Frag<T> wb[NT], xa;
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const i32x4 a0 = k0 < g.K ? *reinterpret_cast<const i32x4*>(pa[i] + k0) : z, a1 = k1 < g.K ? *reinterpret_cast<const i32x4*>(pa[i] + k1) : z;
-      xa.set(a0, a1);
-      const f32x4 p = mma128(wb, xa);
-      const float f = sa[i][kb] * s;
+    for (int j = 0; j < NT; ++j)
+      wb[j].set(in0 ? *reinterpret_cast<const i32x4*>(gw + (ow[j] + k)) : z, in1 ? *reinterpret_cast<const i32x4*>(gw + (ow[j] + k + 64)) : z);
+    xa.set(in0 ? *reinterpret_cast<const i32x4*>(g.a + (oa + k)) : z, in1 ? *reinterpret_cast<const i32x4*>(g.a + (oa + k + 64)) : z);
+    const float f = g.sa[os + (unsigned)kb] * sw[kb];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(p[e], f, acc[i][e]);
+    for (int j = 0; j < NT; ++j) {
+      const f32x4 p = mma128(wb[j], xa);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] = fmaf(p[e], f, acc[j][e]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+  for (int j = 0; j < NT; ++j) part[wave][j][lane] = acc[j];
   __syncthreads();
-  for (int i = wave; i < MT; i += WK) {
-    const long long m = i * 16 + r;
-    f32x4 v = part[0][i][lane];
+  for (int j = wave; j < NT; j += WK) {
+    f32x4 v = part[0][j][lane];
 #pragma unroll
-    for (int q = 1; q < WK; ++q) v += part[q][i][lane];
-    if (m < g.M) store_out<T>(g, m, n0 + 4 * grp, v);
+    for (int k = 1; k < WK; ++k) v += part[k][j][lane];
+    if (r < g.M) store_out<T>(g, r, n0 + j * 16 + 4 * grp, v);
   }
 }
 
-template <typename T, int BM, int BN, int WM, int WN>
+template <typename T, int BM, int BN, int WM, int WN, int S>
 hipError_t tile_go(const Gemm8Args& g, hipStream_t st) {
-  constexpr int kThreads = 64 * WM * WN, kLds = 2 * (BM + BN) * 128;
+  constexpr int kThreads = 64 * WM * WN, kLds = S * (BM + BN) * 128 + 2 * BM * 16;
+  static_assert(kLds <= 160 * 1024, "LDS");
   const long long tm = (g.M + BM - 1) / BM, tn = (g.N + BN - 1) / BN, n = (tm * tn + 7) / 8 * 8;
   if (n > max_groups(kThreads)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm8_tile_kernel<T, BM, BN, WM, WN>), dim3((unsigned)n), dim3(kThreads), kLds, st, g, (unsigned)tm, (unsigned)tn);
+  hipLaunchKernelGGL((gemm8_tile_kernel<T, BM, BN, WM, WN, S>), dim3((unsigned)n), dim3(kThreads), kLds, st, g, (unsigned)tm, (unsigned)tn);
   return hipGetLastError();
 }
 
-template <typename T, int MT, int WK>
+template <typename T, int NT, int WK>
 hipError_t rows_go(const Gemm8Args& g, hipStream_t st) {
-  if ((g.N + 15) / 16 > max_groups(64 * WK)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm8_rows_kernel<T, MT, WK>), dim3((unsigned)((g.N + 15) / 16)), dim3(64 * WK), 0, st, g);
+  const long long n = (g.N + 16 * NT - 1) / (16 * NT);
+  if (n > max_groups(64 * WK)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((gemm8_rows_kernel<T, NT, WK>), dim3((unsigned)n), dim3(64 * WK), 0, st, g);
   return hipGetLastError();
 }
+
+// Tiles by the time of a round of one work-group a CU (two of 64 x 64), us for
+// K = 4096, as {first round of at most 256 tiles, any round}: what a shape
+// takes is its rounds times that.  Measured, 4096 outputs: 512 rows 64 x 64 18,
+// 128 x 128 23; 1024 rows 34 and 25; 2048 rows 128 x 128 47, 256 x 128 41; 8192
+// rows 256 x 128 160, 256 x 256 133.  fp32 outputs: 30 and 41, 55 and 45, 83 and
+// 66; 256 x 256 does not fit the registers there.
+struct TileTime {
+  int bm, bn, slots;
+  float first, round;
+};
+template <typename T> struct TileTimes;
+template <> struct TileTimes<bf16> {
+  static constexpr TileTime t[4] = {{64, 64, 512, 13.5f, 17.8f}, {128, 128, 256, 24.5f, 24.5f}, {256, 128, 256, 41.f, 41.f}, {256, 256, 256, 67.f, 67.f}};
+};
+template <> struct TileTimes<float> {
+  static constexpr TileTime t[3] = {{64, 64, 512, 21.f, 30.f}, {128, 128, 256, 43.f, 43.f}, {256, 128, 256, 65.f, 65.f}};
+};
 
 template <typename T>
 hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
-  if (g.M <= 16) return rows_go<T, 1, 4>(g, st);
-  if (g.M <= 32) return rows_go<T, 2, 4>(g, st);
-  if (g.M <= 64) return rows_go<T, 4, 4>(g, st);
-  if ((g.M + 255) / 256 * ((g.N + 255) / 256) >= 192) return tile_go<T, 256, 256, 4, 2>(g, st);
-  return tile_go<T, 128, 128, 2, 2>(g, st);
+  // Few rows: 64 outputs a work-group where those are enough for half the card
+  // (12288 outputs: 12.3 us, 16 outputs 14.5), else 16 (4096 outputs: 9.0 and
+  // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 15.3, two row sets here 17.6.
+  if (g.M <= 16) return g.N >= 8192 ? rows_go<T, 4, 16>(g, st) : rows_go<T, 1, 8>(g, st);
+  int best = 0, i = 0;
+  float least = 0.f;
+  for (const TileTime& t : TileTimes<T>::t) {
+    const long long n = ((g.M + t.bm - 1) / t.bm) * ((g.N + t.bn - 1) / t.bn);
+    const float us = n <= 256 ? t.first : (float)((n + t.slots - 1) / t.slots) * t.round;
+    if (i == 0 || us < least) {
+      best = i;
+      least = us;
+    }
+    ++i;
+  }
+  switch (best) {
+    case 0: return tile_go<T, 64, 64, 2, 2, 4>(g, st);
+    case 1: return tile_go<T, 128, 128, 4, 2, 3>(g, st);
+    case 2: return tile_go<T, 256, 128, 4, 2, 3>(g, st);
+    default: break;
+  }
+  if constexpr (sizeof(T) == 2) return tile_go<T, 256, 256, 4, 2, 2>(g, st);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
