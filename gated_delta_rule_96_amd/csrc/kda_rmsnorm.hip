@@ -225,8 +225,14 @@ __global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_bwd_kernel(con
   }
 }
 
-// Work-groups at most.
-constexpr int kFwdGroups = 2048, kBwdGroups = 512;
+// Work-groups at most.  Forward: a row (four, of up to 2048 channels) each, as
+// the next row's loads then come from another work-group while this one sums
+// (64K rows of 4096 to 8 bits: 328 us; 8192 work-groups 356, 2048 386); rows of
+// sixteen waves leave no room for another and walk on (8192 rows of 16384: 169;
+// a row each 176).  Backward, where each keeps a partial row of dw (64K rows of
+// 4096: 380 us; 1024 448, 256 460).
+constexpr int kBwdGroups = 512;
+int fwd_groups(int D) { return D <= 8192 ? 1 << 20 : 2048; }
 
 // Waves that hold a row of D channels.
 int row_waves(int D) { return D <= 2048 ? 1 : D <= 8192 ? 4 : 16; }
@@ -254,7 +260,7 @@ long long part_rows(long long rows, int D) {
 
 template <typename T, typename TH, bool kRes, bool kFp8>
 hipError_t fwd_go(const NormArgs& a, hipStream_t st) {
-  const unsigned groups = norm_groups(a.rows, a.D, kFwdGroups);
+  const unsigned groups = norm_groups(a.rows, a.D, fwd_groups(a.D));
   KDA_NORM_BY_WIDTH(norm_fwd_kernel, T, TH, kRes, kFp8);
 }
 template <typename T, typename TH, bool kRes>

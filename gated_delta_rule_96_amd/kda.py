@@ -752,11 +752,28 @@ def ssm_bwd_chunked(x, dt, A, Bm, Cm, dy, h0=None, dht=None, *, D=None, dt_bias=
 def _flat_rows(t, name, D):
     """Pointer, row stride and leading sizes of rows [..., D]: one or two
     leading dimensions, as for _rows."""
-    lead = tuple(t.shape[:-1])
-    if len(lead) not in (1, 2) or t.shape[-1] != D:
-        raise ValueError(f"{name} must be [rows, {D}] or [B, T, {D}], got {list(t.shape)}")
-    p, ld = _rows(t, name, lead, (D,))
+    shape = t.shape
+    if not 2 <= len(shape) <= 3 or shape[-1] != D:
+        raise ValueError(f"{name} must be [rows, {D}] or [B, T, {D}], got {list(shape)}")
+    lead = shape[:-1]
+    if D <= _INT_MAX and t.is_cuda and t.is_contiguous():
+        return t.data_ptr(), D, lead
+    p, ld = _rows(t, name, tuple(lead), (D,))
     return p, ld, lead
+
+
+def _rows_beside(t, name, x, dev, shape):
+    """Pointer and token stride of an input of x's (checked) shape, type and
+    device, or of None."""
+    if t is None:
+        return None, 0
+    if t.dtype is not x.dtype:
+        raise TypeError(f"{name} dtype {t.dtype} != x dtype {x.dtype}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, not on {dev}")
+    if t.shape == shape and t.is_contiguous():
+        return t.data_ptr(), shape[-1]
+    return _rows(t, name, tuple(shape[:-1]), (shape[-1],))
 
 
 def add_rms_norm(x, res=None, w=None, *, eps=1e-6, fp8=False, out=None, scale_out=None, sum_out=None):
@@ -767,27 +784,34 @@ def add_rms_norm(x, res=None, w=None, *, eps=1e-6, fp8=False, out=None, scale_ou
     fp32, may be slices of wider tensors); w [D] fp32 or None.  sum_out may be
     a contiguous res itself.  fp8: y is the pair (y8, scale): y8 in
     torch.float8_e4m3fn, scale [..., ceil(D/128)] fp32 with n = y8 scale."""
-    D = x.shape[-1]
+    shape = x.shape
+    D = shape[-1]
     px, ldx, lead = _flat_rows(x, "x", D)
-    dev, dt, rows = x.device, _dtype_code(x), math.prod(lead)
-    pr, ldr, rdt = None, 0, dt
+    dev, dt = x.device, _dtype_code(x)
+    pr, ldr, rdt, ph = None, 0, dt, None
     if res is not None:
-        if res.shape != x.shape:
-            raise ValueError(f"res must be {list(x.shape)}, got {list(res.shape)}")
+        if res.shape != shape:
+            raise ValueError(f"res must be {list(shape)}, got {list(res.shape)}")
+        if res.device != dev:
+            raise ValueError(f"res is on {res.device}, not on {dev}")
         pr, ldr, _ = _flat_rows(res, "res", D)
         rdt = _dtype_code(res)
         sum_out = _given(sum_out, res, "sum_out")
+        ph = sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out needs res")
-    ot = torch.float8_e4m3fn if fp8 else x.dtype
-    if out is None:
-        out = torch.empty(x.shape, dtype=ot, device=dev)
-    if fp8 and scale_out is None:
-        scale_out = torch.empty((*lead, (D + 127) // 128), dtype=torch.float32, device=dev)
-    _same_device(dev, res=res)
-    _call(dev, "kda_add_rms_norm", px, ldx, pr, ldr, rdt, _dense(w, "w", (D,), torch.float32, dev), float(eps),
-          None if res is None else sum_out.data_ptr(), _dense(out, "out", x.shape, ot, dev),
-          _dense(scale_out, "scale_out", (*lead, (D + 127) // 128), torch.float32, dev) if fp8 else None, dt, rows, D)
+    ps = None
+    if fp8:
+        if out is None:
+            out = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+        kb = (*lead, (D + 127) // 128)
+        scale_out = torch.empty(kb, dtype=torch.float32, device=dev) if scale_out is None else scale_out
+        ps = _dense(scale_out, "scale_out", kb, torch.float32, dev)
+        py = _dense(out, "out", shape, torch.float8_e4m3fn, dev)
+    else:
+        out = _given(out, x, "out")
+        py = out.data_ptr()
+    _call(dev, "kda_add_rms_norm", px, ldx, pr, ldr, rdt, _dense(w, "w", (D,), torch.float32, dev), eps, ph, py, ps, dt, math.prod(lead), D)
     return ((out, scale_out) if fp8 else out), (None if res is None else sum_out)
 
 
@@ -837,16 +861,12 @@ def gemm_fp8(a, sa, w, sw, *, out_dtype=torch.bfloat16, out=None):
     return out
 
 
-def _lru_setup(x, r, i, c, lead):
+def _lru_setup(x, r, i, c):
     """Checked inputs of the gated linear recurrence: (x .. c of the C call)."""
-    D = x.shape[-1]
-    for n, t in (("r", r), ("i", i)):
-        if t is not None and t.dtype != x.dtype:
-            raise TypeError(f"{n} dtype {t.dtype} != x dtype {x.dtype}")
-    dev = x.device
-    _same_device(dev, r=r, i=i)
-    return (*_rows(x, "x", lead, (D,)), *_rows(r, "r", lead, (D,)), *((None, 0) if i is None else _rows(i, "i", lead, (D,))),
-            _dense(c, "c", (D,), torch.float32, dev))
+    shape, dev = x.shape, x.device
+    D = shape[-1]
+    pr, pi = _rows_beside(r, "r", x, dev, shape), _rows_beside(i, "i", x, dev, shape)
+    return (*_rows(x, "x", tuple(shape[:-1]), (D,)), *pr, *pi, _dense(c, "c", (D,), torch.float32, dev))
 
 
 def lru_fwd(x, r, i=None, c=None, h0=None, *, unit=True, cu_seqlens=None, final_state=True, ht=None, workspace=None, out=None):
@@ -858,7 +878,7 @@ def lru_fwd(x, r, i=None, c=None, h0=None, *, unit=True, cu_seqlens=None, final_
     sequences, or of those cu_seqlens (host ints) cuts the packed axis into; ht
     may be h0 itself."""
     B, T, D = x.shape
-    args = _lru_setup(x, r, i, c, (B, T))
+    args = _lru_setup(x, r, i, c)
     arr, N = _packed(cu_seqlens, B, T)
     dev, st = x.device, (N, D)
     y = _given(out, x, "out")
@@ -876,7 +896,7 @@ def lru_step(x, r, i, c, state, *, unit=True, state_out=None, out=None):
     (kda_lru_step); state [B,D] fp32 moves on in place, or into state_out (the
     old state is then kept)."""
     B, D = x.shape
-    args = _lru_setup(x, r, i, c, (B,))
+    args = _lru_setup(x, r, i, c)
     dev, st = x.device, (B, D)
     so = state if state_out is None else state_out
     y = _given(out, x, "out")
@@ -891,7 +911,7 @@ def lru_bwd(x, r, i, c, dy, h0=None, dht=None, *, unit=True, cu_seqlens=None, wo
     None without i), dc [D] fp32 (None without c) and dh0 [N,D] fp32 (None
     without h0).  `out` may supply that dict to be filled in place."""
     B, T, D = x.shape
-    args = _lru_setup(x, r, i, c, (B, T))
+    args = _lru_setup(x, r, i, c)
     arr, N = _packed(cu_seqlens, B, T)
     dev, st = x.device, (N, D)
     if out is None:
