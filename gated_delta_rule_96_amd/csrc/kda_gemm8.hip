@@ -83,9 +83,10 @@ template <typename T> __device__ __forceinline__ void store_out(const Gemm8Args&
 __device__ __forceinline__ int lds_piece(int r, int p) { return r * 128 + ((p ^ ((r >> 1) & 7)) << 4); }
 
 
-// Work-group tile BM x BN, WM x WN waves, S steps in LDS: step kb's loads are
-// issued S - 1 steps before it.
-template <typename T, int BM, int BN, int WM, int WN, int S>
+// Work-group tile BM x BN, WM x WN waves, S sets of U steps in LDS (a step: one
+// block of 128 reduction indices): a set's loads are issued S - 1 sets before
+// it, and the waves meet once a set.
+template <typename T, int BM, int BN, int WM, int WN, int S, int U>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8Args g, unsigned tm, unsigned tn) {
   constexpr int kThreads = 64 * WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int LA = BM * 8 / kThreads, LB = BN * 8 / kThreads;   // 16-byte pieces a thread stages
@@ -122,14 +123,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
   const int ck = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;
   auto step_offset = [&](int kb) { return (unsigned)(kb * 128 + ck < g.K ? kb * 128 : -ck); };
   auto stage = [&](int n, int kb, unsigned k) {   // the n-th of a thread's LA + LB pieces of step kb
-    u8* base = smem + kb % S * ((BM + BN) * 128) + wave * 1024;
+    u8* base = smem + kb % (S * U) * ((BM + BN) * 128) + wave * 1024;
     if (n < LA) __builtin_amdgcn_global_load_lds((GlbP)(ga + (oa[n < LA ? n : 0] + k)), (LdsP)(base + n * kThreads * 16), 16, 0, 0);
     else __builtin_amdgcn_global_load_lds((GlbP)(gw + (ob[n < LA ? 0 : n - LA] + k)), (LdsP)(base + BM * 128 + (n - LA) * kThreads * 16), 16, 0, 0);
   };
   // The rows' scales go through LDS four steps at a time, one row a thread: a
   // scale a lane straight from memory touched a cache line a row in every step
   // (8192 x 12288 x 4096: 524 us).
-  constexpr int kSc = S * (BM + BN) * 128;   // their place in LDS: two sets of [BM][4]
+  constexpr int kSc = S * U * (BM + BN) * 128;   // their place in LDS: two sets of [BM][4]
   static_assert(kThreads >= BM, "a thread a row");
   const bool sc4 = (KB & 3) == 0 && (g.lsa & 3) == 0 && (reinterpret_cast<uintptr_t>(g.sa) & 15) == 0;
   const float* gsa = g.sa + m0 * g.lsa;
@@ -165,70 +166,75 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
     for (int i = 0; i < MT; ++i) acc[j][i] = zero4();
   stage_scales(0);
 #pragma unroll
-  for (int kb = 0; kb < S - 1; ++kb) {
+  for (int kb = 0; kb < (S - 1) * U; ++kb) {
     const unsigned k = step_offset(min(kb, KB - 1));
 #pragma unroll
     for (int n = 0; n < LA + LB; ++n) stage(n, kb, k);
   }
   float ws64 = 0.f;
-  for (int kb = 0; kb < KB; ++kb) {
-    // This wave's pieces of step kb are in LDS (a barrier alone does not wait
-    // for loads to LDS): behind them are at least those of S - 2 steps.  Every
-    // wave has read what it needs of step kb - 1.
+  for (int k0 = 0; k0 < KB; k0 += U) {
+    // This wave's pieces of these steps are in LDS (a barrier alone does not
+    // wait for loads to LDS): behind them are at least those of S - 2 sets.
+    // Every wave has read what it needs of the set before.
     // (A fence in front of the barrier would wait for all loads in flight.)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * (LA + LB)) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * U * (LA + LB)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if ((kb & 63) == 0) {
-      ws64 = sw[min(kb + lane, KB - 1)];   // a lane a step
+    if ((k0 & 63) == 0) {
+      ws64 = sw[min(k0 + lane, KB - 1)];   // a lane a step
       asm volatile("" : "+v"(ws64));       // (waited for here, not in every step)
     }
-    const float ws = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws64), kb & 63));
-    float f[MT];
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-      f[i] = ws * *reinterpret_cast<const float*>(sc + ((kb >> 2) & 1) * (BM * 16) + (kb & 3) * step_at + i * 16 * row_at);
-    const unsigned kn = step_offset(min(kb + S - 1, KB - 1));   // (behind the last step its blocks again, unused)
-    if ((kb & 3) == 0 && kb + 4 < KB) stage_scales((kb >> 2) + 1);
-    const u8* ta = smem + kb % S * ((BM + BN) * 128) + wm * (BM / WM) * 128;
-    const u8* tb = ta + (BM - wm * (BM / WM) + wn * (BN / WN)) * 128;
-    Frag<T> xa[MT];
-    if (kb * 128 + 128 <= g.K) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) xa[i] = frag(ta + i * 2048);
-    } else {
-      const int left = g.K - kb * 128;
-      const i32x4 z{0, 0, 0, 0};
+    for (int u = 0; u < U; ++u) {
+      const int kb = k0 + u;
+      if (U > 1 && kb >= KB) break;
+      const float ws = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws64), kb & 63));
+      float f[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
-        xa[i].set(grp * 16 < left ? *reinterpret_cast<const i32x4*>(ta + i * 2048 + lo) : z,
-                  grp * 16 + 64 < left ? *reinterpret_cast<const i32x4*>(ta + i * 2048 + hi) : z);
-    }
-    // Product q's result joins its sum two products later: its latency passes
-    // behind them.
-    Frag<T> wb[2];
-    wb[0] = frag(tb);
-    f32x4 p[3];
+        f[i] = ws * *reinterpret_cast<const float*>(sc + ((kb >> 2) & 1) * (BM * 16) + (kb & 3) * step_at + i * 16 * row_at);
+      const unsigned kn = step_offset(min(kb + (S - 1) * U, KB - 1));   // (behind the last step its blocks again, unused)
+      if (u == 0 && (kb & 3) == 0 && kb + 4 < KB) stage_scales((kb >> 2) + 1);
+      const u8* ta = smem + kb % (S * U) * ((BM + BN) * 128) + wm * (BM / WM) * 128;
+      const u8* tb = ta + (BM - wm * (BM / WM) + wn * (BN / WN)) * 128;
+      Frag<T> xa[MT];
+      if (kb * 128 + 128 <= g.K) {
 #pragma unroll
-    for (int q = 0; q < NT * MT + 2; ++q) {
-      if (q < NT * MT) {
-        const int j = q / MT, i = q % MT;
-        if (i == 0 && j + 1 < NT) wb[(j + 1) & 1] = frag(tb + (j + 1) * 2048);
-        p[q % 3] = mma128(wb[j & 1], xa[i]);
-        // the coming loads one by one between the first products: issued at once
-        // they hold the wave until the cache has taken them (480 us), spread over
-        // all products the last ones come late (490; 451 like this)
-        constexpr int kEach = (LA + LB + NT * MT - 1) / (NT * MT);
+        for (int i = 0; i < MT; ++i) xa[i] = frag(ta + i * 2048);
+      } else {
+        const int left = g.K - kb * 128;
+        const i32x4 z{0, 0, 0, 0};
 #pragma unroll
-        for (int n = q * kEach; n < (q + 1) * kEach && n < LA + LB; ++n) stage(n, kb + S - 1, kn);
+        for (int i = 0; i < MT; ++i)
+          xa[i].set(grp * 16 < left ? *reinterpret_cast<const i32x4*>(ta + i * 2048 + lo) : z,
+                    grp * 16 + 64 < left ? *reinterpret_cast<const i32x4*>(ta + i * 2048 + hi) : z);
       }
-      __builtin_amdgcn_sched_barrier(0);   // (the compiler would put the fmas in front)
-      if (q >= 2) {
-        const int j = (q - 2) / MT, i = (q - 2) % MT;
+      // Product q's result joins its sum two products later: its latency passes
+      // behind them.
+      Frag<T> wb[2];
+      wb[0] = frag(tb);
+      f32x4 p[3];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][i][e] = fmaf(p[(q - 2) % 3][e], f[i], acc[j][i][e]);
+      for (int q = 0; q < NT * MT + 2; ++q) {
+        if (q < NT * MT) {
+          const int j = q / MT, i = q % MT;
+          if (i == 0 && j + 1 < NT) wb[(j + 1) & 1] = frag(tb + (j + 1) * 2048);
+          p[q % 3] = mma128(wb[j & 1], xa[i]);
+          // the coming loads one by one between the first products: issued at once
+          // they hold the wave until the cache has taken them (480 us), spread over
+          // all products the last ones come late (490; 451 like this)
+          constexpr int kEach = (LA + LB + NT * MT - 1) / (NT * MT);
+#pragma unroll
+          for (int n = q * kEach; n < (q + 1) * kEach && n < LA + LB; ++n) stage(n, kb + (S - 1) * U, kn);
+        }
+        __builtin_amdgcn_sched_barrier(0);   // (the compiler would put the fmas in front)
+        if (q >= 2) {
+          const int j = (q - 2) / MT, i = (q - 2) % MT;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][i][e] = fmaf(p[(q - 2) % 3][e], f[i], acc[j][i][e]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load to LDS outlives the work-group
@@ -287,13 +293,13 @@ __global__ __launch_bounds__(64 * WK) void gemm8_rows_kernel(const Gemm8Args g) 
   }
 }
 
-template <typename T, int BM, int BN, int WM, int WN, int S>
+template <typename T, int BM, int BN, int WM, int WN, int S, int U>
 hipError_t tile_go(const Gemm8Args& g, hipStream_t st) {
-  constexpr int kThreads = 64 * WM * WN, kLds = S * (BM + BN) * 128 + 2 * BM * 16;
-  static_assert(kLds <= 160 * 1024, "LDS");
+  constexpr int kThreads = 64 * WM * WN, kLds = S * U * (BM + BN) * 128 + 2 * BM * 16;
+  static_assert(kLds <= 160 * 1024 && (U == 1 || U == 2 || U == 4), "LDS, sets of scales");
   const long long tm = (g.M + BM - 1) / BM, tn = (g.N + BN - 1) / BN, n = (tm * tn + 7) / 8 * 8;
   if (n > max_groups(kThreads)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm8_tile_kernel<T, BM, BN, WM, WN, S>), dim3((unsigned)n), dim3(kThreads), kLds, st, g, (unsigned)tm, (unsigned)tn);
+  hipLaunchKernelGGL((gemm8_tile_kernel<T, BM, BN, WM, WN, S, U>), dim3((unsigned)n), dim3(kThreads), kLds, st, g, (unsigned)tm, (unsigned)tn);
   return hipGetLastError();
 }
 
@@ -305,48 +311,45 @@ hipError_t rows_go(const Gemm8Args& g, hipStream_t st) {
   return hipGetLastError();
 }
 
-// Tiles by the time of a round of one work-group a CU (two of 64 x 64), us for
-// K = 4096, as {first round of at most 256 tiles, any round}: what a shape
-// takes is its rounds times that.  Measured, 4096 outputs: 512 rows 64 x 64 18,
-// 128 x 128 23; 1024 rows 34 and 25; 2048 rows 128 x 128 47, 256 x 128 41; 8192
-// rows 256 x 128 160, 256 x 256 133.  fp32 outputs: 30 and 41, 55 and 45, 83 and
-// 66; 256 x 256 does not fit the registers there.
+// Tiles by the time of a round of 256 work-groups, one a CU, us for K = 4096:
+// what a shape takes is its rounds times that.  Measured, 4096 outputs, bf16:
+// 256 rows 64 x 64 12.4, 128 x 64 15.4; 512 rows 128 x 64 16.3, 64 x 64 22.8; 1024
+// rows 128 x 128 24.3, 128 x 64 29.8; 2048 rows 128 x 256 39.5, 128 x 128 45.9;
+// 8192 rows 256 x 256 131, 128 x 256 148.  fp32: 20 and 25, 28 and 40, 41 and 51,
+// 64 and 78; 256 x 256 does not fit the registers there.  Two steps a set help
+// the small tiles (64 x 64: 12.4, one step a set 13.7), whose steps are short
+// beside the meeting of the waves.
 struct TileTime {
-  int bm, bn, slots;
-  float first, round;
+  int bm, bn;
+  float bf16_us, f32_us;
 };
-template <typename T> struct TileTimes;
-template <> struct TileTimes<bf16> {
-  static constexpr TileTime t[4] = {{64, 64, 512, 13.5f, 17.8f}, {128, 128, 256, 24.5f, 24.5f}, {256, 128, 256, 41.f, 41.f}, {256, 256, 256, 67.f, 67.f}};
-};
-template <> struct TileTimes<float> {
-  static constexpr TileTime t[3] = {{64, 64, 512, 21.f, 30.f}, {128, 128, 256, 43.f, 43.f}, {256, 128, 256, 65.f, 65.f}};
-};
+constexpr TileTime kTiles[5] = {{64, 64, 12.4f, 20.f}, {128, 64, 16.2f, 27.f}, {128, 128, 24.4f, 41.f}, {128, 256, 39.5f, 62.f}, {256, 256, 66.f, 0.f}};
 
 template <typename T>
 hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
   // Few rows: 64 outputs a work-group where those are enough for half the card
   // (12288 outputs: 12.3 us, 16 outputs 14.5), else 16 (4096 outputs: 9.0 and
-  // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 15.3, two row sets here 17.6.
+  // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 14.3, two row sets here 17.6.
   if (g.M <= 16) return g.N >= 8192 ? rows_go<T, 4, 16>(g, st) : rows_go<T, 1, 8>(g, st);
-  int best = 0, i = 0;
+  int best = 0;
   float least = 0.f;
-  for (const TileTime& t : TileTimes<T>::t) {
+  for (int i = 0; i < (sizeof(T) == 2 ? 5 : 4); ++i) {
+    const TileTime& t = kTiles[i];
     const long long n = ((g.M + t.bm - 1) / t.bm) * ((g.N + t.bn - 1) / t.bn);
-    const float us = n <= 256 ? t.first : (float)((n + t.slots - 1) / t.slots) * t.round;
+    const float us = (float)((n + 255) / 256) * (sizeof(T) == 2 ? t.bf16_us : t.f32_us);
     if (i == 0 || us < least) {
       best = i;
       least = us;
     }
-    ++i;
   }
   switch (best) {
-    case 0: return tile_go<T, 64, 64, 2, 2, 4>(g, st);
-    case 1: return tile_go<T, 128, 128, 4, 2, 3>(g, st);
-    case 2: return tile_go<T, 256, 128, 4, 2, 3>(g, st);
+    case 0: return tile_go<T, 64, 64, 4, 2, 3, 2>(g, st);
+    case 1: return tile_go<T, 128, 64, 4, 2, 3, 2>(g, st);
+    case 2: return tile_go<T, 128, 128, 4, 2, 3, 1>(g, st);
+    case 3: return tile_go<T, 128, 256, 2, 4, 3, 1>(g, st);
     default: break;
   }
-  if constexpr (sizeof(T) == 2) return tile_go<T, 256, 256, 4, 2, 2>(g, st);
+  if constexpr (sizeof(T) == 2) return tile_go<T, 256, 256, 4, 2, 2, 1>(g, st);
   return hipErrorInvalidValue;
 }
 
