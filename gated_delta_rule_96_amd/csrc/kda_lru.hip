@@ -38,18 +38,18 @@ __device__ __forceinline__ void load_run(const LruArgs& g, const SeqPart& p, con
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     const int q = min(k, n - 1);
-    x[k] = *reinterpret_cast<const Pk*>(px + q * g.ldx + l.cl);
-    r[k] = *reinterpret_cast<const Pk*>(pr + q * g.ldr + l.cl);
+    x[k] = lru_load<Pk>(px + q * g.ldx, l.cl);
+    r[k] = lru_load<Pk>(pr + q * g.ldr, l.cl);
   }
   if (kFull || g.i)
 #pragma unroll
-    for (int k = 0; k < R; ++k) i[k] = *reinterpret_cast<const Pk*>(pi + min(k, n - 1) * g.ldi + l.cl);
+    for (int k = 0; k < R; ++k) i[k] = lru_load<Pk>(pi + min(k, n - 1) * g.ldi, l.cl);
   const LruMode md = lru_mode<kFull>(g);
 #pragma unroll
   for (int k = 0; k < R; ++k)
 #pragma unroll
     for (int j = 0; j < NC; ++j)
-      lru_gate<T>(md, c[j], to_f32(x[k].v[j]), to_f32(r[k].v[j]), md.igate ? to_f32(i[k].v[j]) : 0.f, a[k][j], u[k][j]);
+      lru_gate<T>(md, c[j], x[k].at(j), r[k].at(j), md.igate ? i[k].at(j) : 0.f, a[k][j], u[k][j]);
   if (n < R)
 #pragma unroll
     for (int k = 0; k < R; ++k)
@@ -224,11 +224,9 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
   for (int k = 0; k < kR; ++k) {
     LruPack<T, NC> o;
 #pragma unroll
-    for (int j = 0; j < NC; ++j) {
-      h[j] = fmaf(a[k][j], h[j], u[k][j]);
-      o.v[j] = from_f32<T>(h[j]);
-    }
-    if (t + k < p.t1) *reinterpret_cast<LruPack<T, NC>*>(y + (long long)k * g.D + l.c) = o;
+    for (int j = 0; j < NC; ++j) h[j] = fmaf(a[k][j], h[j], u[k][j]);
+    o.set(h);
+    if (t + k < p.t1) lru_store(y + (long long)k * g.D, l.c, o);
   }
 }
 
@@ -254,10 +252,10 @@ __global__ __launch_bounds__(256) void lru_step_kernel(const LruArgs g, unsigned
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
     float a, u;
-    lru_gate<T>(md, c[j], to_f32(x.v[j]), to_f32(r.v[j]), to_f32(i.v[j]), a, u);
+    lru_gate<T>(md, c[j], x.at(j), r.at(j), i.at(j), a, u);
     ht.v[j] = fmaf(a, h0.v[j], u);
-    o.v[j] = from_f32<T>(ht.v[j]);
   }
+  o.set(ht.v);
   *reinterpret_cast<Pk*>((T*)g.y + at) = o;
   *reinterpret_cast<LruPack<float, NC>*>(g.ht + at) = ht;
 }

@@ -38,18 +38,28 @@ __device__ __forceinline__ void load_rows(const LruBwdArgs& b, const SeqPart& p,
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     const int q = min(k, n - 1);
-    w.x[k] = *reinterpret_cast<const Pk*>(px + q * b.f.ldx + l.cl);
-    w.r[k] = *reinterpret_cast<const Pk*>(pr + q * b.f.ldr + l.cl);
-    w.dy[k] = *reinterpret_cast<const Pk*>(pd + (long long)q * b.f.D + l.cl);
+    w.x[k] = lru_load<Pk>(px + q * b.f.ldx, l.cl);
+    w.r[k] = lru_load<Pk>(pr + q * b.f.ldr, l.cl);
+    w.dy[k] = lru_load<Pk>(pd + (long long)q * b.f.D, l.cl);
   }
   if (kFull || b.f.i)
 #pragma unroll
-    for (int k = 0; k < R; ++k) w.i[k] = *reinterpret_cast<const Pk*>(pi + min(k, n - 1) * b.f.ldi + l.cl);
+    for (int k = 0; k < R; ++k) w.i[k] = lru_load<Pk>(pi + min(k, n - 1) * b.f.ldi, l.cl);
+  if (n < R) {   // tokens past the part's end: a = 1, u = 0, dy = 0
+    const float open = b.f.c ? -__builtin_inff() : 0.f;
+#pragma unroll
+    for (int k = 1; k < R; ++k)
+      if (k >= n) {
+        w.x[k].fill(0.f);
+        w.i[k].fill(0.f);
+        w.dy[k].fill(0.f);
+        w.r[k].fill(open);
+      }
+  }
 }
 
 // P, H and K of a run of n tokens from its tokens' a, u and dy, which `gate`
-// gives.  Tokens past the part's end leave everything as it is (a = 1, u = 0,
-// dy = 0).
+// gives.
 template <typename T, int NC, int R, typename F>
 __device__ __forceinline__ void run_sums(const BwdRun<T, NC, R>& w, int n, float (&P)[NC], float (&H)[NC], float (&K)[NC], F gate) {
 #pragma unroll
@@ -62,15 +72,12 @@ __device__ __forceinline__ void run_sums(const BwdRun<T, NC, R>& w, int n, float
   for (int k = 0; k < R; ++k)
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      float a, u, d = to_f32(w.dy[k].v[j]);
+      float a, u;
+      const float d = w.dy[k].at(j);
       gate(k, j, a, u);
-      if (k >= n) {
-        a = 1.f;
-        u = d = 0.f;
-      }
-      P[j] *= a;
-      H[j] = fmaf(a, H[j], u);
-      K[j] = fmaf(P[j], d, K[j]);
+      P[j] = k ? P[j] * a : a;
+      H[j] = k ? fmaf(a, H[j], u) : u;
+      K[j] = k ? fmaf(P[j], d, K[j]) : a * d;
     }
 }
 
@@ -90,7 +97,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_part_kernel(const LruB
   lru_coef<NC>(b.f, l, c);
   const LruMode md = lru_mode<kFull>(b.f);
   run_sums<T, NC, R>(w, p.t1 - t, P, H, K, [&](int k, int j, float& a, float& u) {
-    lru_gate<T>(md, c[j], to_f32(w.x[k].v[j]), to_f32(w.r[k].v[j]), md.igate ? to_f32(w.i[k].v[j]) : 0.f, a, u);
+    lru_gate<T>(md, c[j], w.x[k].at(j), w.r[k].at(j), md.igate ? w.i[k].at(j) : 0.f, a, u);
   });
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
@@ -191,9 +198,9 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBw
     sum[j] = 0.f;
   }
   run_sums<T, NC, R>(w, n, P, H, K, [&](int k, int j, float& av, float& uv) {
-    const float r = to_f32(w.r[k].v[j]);
+    const float r = w.r[k].at(j);
     sr[k][j] = md.gate ? sigmoid_fast(r) : 1.f;
-    si[k][j] = md.igate ? sigmoid_fast(to_f32(w.i[k].v[j])) : 1.f;
+    si[k][j] = md.igate ? sigmoid_fast(w.i[k].at(j)) : 1.f;
     const float d = one_minus_decay<T>(md.gate ? -c[j] * sr[k][j] : r, av);
     m[k][j] = im[k][j] = 1.f;
     if (md.unit) {
@@ -201,7 +208,7 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBw
       im[k][j] = __builtin_fabsf(q) < 0x1p-126f ? 0.f : __builtin_amdgcn_rsqf(q);
       m[k][j] = q * im[k][j];
     }
-    uv = to_f32(w.x[k].v[j]) * si[k][j] * m[k][j];
+    uv = w.x[k].at(j) * si[k][j] * m[k][j];
     a[k][j] = av;
     u[k][j] = uv;
   });
@@ -230,23 +237,29 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBw
 #pragma unroll
   for (int k = R - 1; k >= 0; --k) {
     if (k >= n) continue;
-    Pk dx, dr, di;
+    float dx[NC], dr[NC], di[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
-      const float x = to_f32(w.x[k].v[j]), s = si[k][j], lt = to_f32(w.dy[k].v[j]) + e[j];
+      const float x = w.x[k].at(j), s = si[k][j], lt = w.dy[k].at(j) + e[j];
       e[j] = a[k][j] * lt;
       const float gx = lt * m[k][j] * s;
       const float dg = e[j] * (md.unit ? fmaf(-a[k][j], x * s * im[k][j], u[k][j]) : u[k][j]);
-      dx.v[j] = from_f32<T>(gx);
-      di.v[j] = from_f32<T>(gx * x * (1.f - s));
-      dr.v[j] = from_f32<T>(md.gate ? dg * (-c[j] * sr[k][j]) * (1.f - sr[k][j]) : dg);
+      dx[j] = gx;
+      di[j] = gx * x * (1.f - s);
+      dr[j] = md.gate ? dg * (-c[j] * sr[k][j]) * (1.f - sr[k][j]) : dg;
       sum[j] = fmaf(dg, sr[k][j], sum[j]);
     }
     if (l.live) {
-      const size_t at = (p.start + (size_t)(t + k)) * D + l.c;
-      *reinterpret_cast<Pk*>((T*)b.dx + at) = dx;
-      *reinterpret_cast<Pk*>((T*)b.dr + at) = dr;
-      if (md.igate) *reinterpret_cast<Pk*>((T*)b.di + at) = di;
+      const size_t row = (p.start + (size_t)(t + k)) * D;
+      Pk o;
+      o.set(dx);
+      lru_store((T*)b.dx + row, l.c, o);
+      o.set(dr);
+      lru_store((T*)b.dr + row, l.c, o);
+      if (md.igate) {
+        o.set(di);
+        lru_store((T*)b.di + row, l.c, o);
+      }
     }
   }
   if (!dcp) return;

@@ -13,8 +13,28 @@
 
 namespace kda {
 
-template <typename T, int NC> struct alignas(sizeof(T) * NC) LruPack {   // NC channels of a token as loaded
+// NC channels of a token as they lie in memory.
+template <typename T, int NC> struct alignas(sizeof(T) * NC) LruPack {
   T v[NC];
+  __device__ __forceinline__ float at(int j) const { return to_f32(v[j]); }
+  __device__ __forceinline__ void fill(float x) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) v[j] = from_f32<T>(x);
+  }
+  __device__ __forceinline__ void set(const float (&x)[NC]) {
+#pragma unroll
+    for (int j = 0; j < NC; ++j) v[j] = from_f32<T>(x[j]);
+  }
+};
+// (two bf16 as one word: as halves they are taken apart wherever paths meet)
+template <> struct alignas(4) LruPack<bf16, 2> {
+  unsigned w;
+  __device__ __forceinline__ float at(int j) const { return __uint_as_float(j ? w & 0xffff0000u : w << 16); }
+  __device__ __forceinline__ void fill(float x) { set({x, x}); }
+  __device__ __forceinline__ void set(const float (&x)[2]) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    w = __builtin_bit_cast(unsigned, bf16x2{(bf16)x[0], (bf16)x[1]});
+  }
 };
 
 // a = e^g, g <= 0, by way of d = 1 - a from the series of 1 - e^g where g is
@@ -81,6 +101,14 @@ template <int NC> __device__ __forceinline__ LruLane lru_lane(int slice, int D) 
   l.live = l.c < D;
   l.cl = l.live ? l.c : 0;
   return l;
+}
+// A lane's channels of a row that starts at `row` for all lanes: a scalar
+// address and 32 bits of bytes a lane.
+template <typename Pk, typename T> __device__ __forceinline__ Pk lru_load(const T* row, int c) {
+  return *reinterpret_cast<const Pk*>(reinterpret_cast<const char*>(row) + (unsigned)c * (unsigned)sizeof(T));
+}
+template <typename Pk, typename T> __device__ __forceinline__ void lru_store(T* row, int c, const Pk& v) {
+  *reinterpret_cast<Pk*>(reinterpret_cast<char*>(row) + (unsigned)c * (unsigned)sizeof(T)) = v;
 }
 
 template <int NC> __device__ __forceinline__ void lru_coef(const LruArgs& a, const LruLane& l, float (&c)[NC]) {

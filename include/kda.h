@@ -612,7 +612,7 @@ int kda_gemm_fp8(const void* a, long long lda, const float* sa, long long lsa, c
  *   m_t = sqrt(1 - exp(2 g_t)) with flags & KDA_LRU_UNIT, otherwise 1
  *   y_t = h_t
  * x, r, i: rows [B,T,D] of dtype (any D; element alignment suffices; rows
- * that start on two elements are faster); c [D] fp32 >= 0.  h0 [N,D] fp32
+ * that start on two elements are faster); c [D] fp32 >= 0, finite.  h0 [N,D] fp32
  * (NULL: zero), ht [N,D] (NULL: not wanted) the states behind the sequences,
  * may be h0 itself.  y [B,T,D] of dtype.  Tokens and states without gaps (y,
  * h0, ht, and the gradients below) are 16-byte aligned where rows of D are
