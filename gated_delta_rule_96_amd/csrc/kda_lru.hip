@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kWaves = 8, kR = 16, kPart = kWaves * kR;
 constexpr int kBack = 4;   // parts that a part looks back over
+constexpr int kPolls = 1 << 21;   // of a wait, a few seconds
 
 // a and u of a wave's run of R tokens from token t on (the same for all
 // lanes); tokens past the part's end leave the state as it is.
@@ -128,6 +129,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
     if (threadIdx.x == 0) given = __hip_atomic_fetch_add(w.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     id = __builtin_amdgcn_readfirstlane(given);
+    if (id >= gridDim.x) return;
   }
   unsigned item = id / slices;
   const LruLane l = lru_lane<NC>((int)(id - item * slices), g.D);
@@ -168,7 +170,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
       unsigned in[kBack][NC];
       unsigned long long ow[kBack][NC];
       int found = 0;
-      for (;;) {
+      for (int poll = 0;; ++poll) {
 #pragma unroll
         for (int d = 0; d < kBack; ++d) {
           const size_t from = at - (size_t)min(d + 1, parts_before) * g.D;   // (the first part publishes its state only)
@@ -190,9 +192,12 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
           if (open && !found && __all(got || !l.live)) found = d + 1;
           open = open && __all(has || !l.live);
         }
-        if (found) break;
+        if (found || poll == kPolls) break;
         __builtin_amdgcn_s_sleep(1);
       }
+      if (!found)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) h[j] = __builtin_nanf("");
 #pragma unroll
       for (int d = kBack - 1; d >= 0; --d)
 #pragma unroll
@@ -260,9 +265,10 @@ __global__ __launch_bounds__(256) void lru_step_kernel(const LruArgs g, unsigned
   *reinterpret_cast<LruPack<float, NC>*>(g.ht + at) = ht;
 }
 
-// Whether rows may be read and written two channels at a time.
+// Whether rows and states may be read and written two channels at a time.
 bool pairs(const LruArgs& a, size_t esz) {
-  if (a.D % 2 || a.ldx % 2 || a.ldr % 2 || (a.i && a.ldi % 2)) return false;
+  if (a.D % 2 || a.ldx % 2 || a.ldr % 2 || (a.i && a.ldi % 2) || reinterpret_cast<uintptr_t>(a.h0) % 8 || reinterpret_cast<uintptr_t>(a.ht) % 8)
+    return false;
   for (const void* p : {a.x, a.r, a.i, (const void*)a.y})
     if (reinterpret_cast<uintptr_t>(p) % (2 * esz)) return false;
   return true;

@@ -10,9 +10,10 @@
 // e -> P e + K with K = sum_t P_t dy_t, P_t the product of its a up to t.
 // Where m = 0 (a decay of exactly 1) its derivative counts as 0.
 //
-// Three launches: every part's P, H, K; the states and the e that enter the
-// parts; the gradients.  The last walks the parts from the end, so that what
-// the first read last is still in the cache.
+// Three launches where a sequence has several parts (one otherwise): every
+// part's P, H, K; the states and the e that enter the parts; the gradients.  The
+// last walks the parts from the end, so that what the first read last is still
+// in the cache.
 #include "kda_lru_dev.h"
 
 namespace kda {
@@ -172,7 +173,8 @@ __global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const L
   if (b.dh0 && wave == 0) b.dh0[(size_t)n * D + c] = e;
 }
 
-// Gradients.  dcp [items][D]: every part's sum of dg Sigmoid(r), or null.
+// Gradients.  seg null: every sequence is one part.  dcp [items][D]: every
+// part's -sum of dg Sigmoid(r), or null.
 template <typename T, int NC, bool kFull>
 __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
   constexpr int R = RunOf<T>::R;
@@ -190,11 +192,15 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBw
   float a[R][NC], u[R][NC], sr[R][NC], si[R][NC], m[R][NC], im[R][NC], c[NC], P[NC], H[NC], K[NC], h[NC], e[NC], sum[NC];
   lru_coef<NC>(b.f, l, c);
   const LruMode md = lru_mode<kFull>(b.f);
-  const float* from = seg + (size_t)item * 3 * D + l.cl;
+  const float *from = b.f.h0 ? b.f.h0 + (size_t)p.n * D : nullptr, *back = b.dht ? b.dht + (size_t)p.n * D : nullptr;
+  if (seg) {
+    from = seg + ((size_t)item * 3 + 1) * D;
+    back = from + D;
+  }
 #pragma unroll
   for (int j = 0; j < NC; ++j) {
-    h[j] = from[D + j];
-    e[j] = from[2 * D + j];
+    h[j] = from ? from[l.cl + j] : 0.f;
+    e[j] = back ? back[l.cl + j] : 0.f;
     sum[j] = 0.f;
   }
   run_sums<T, NC, R>(w, n, P, H, K, [&](int k, int j, float& av, float& uv) {
@@ -262,6 +268,9 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBw
       }
     }
   }
+  if (!seg && b.dh0 && wave == 0 && l.live)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) b.dh0[(size_t)p.n * D + l.c + j] = e[j];
   if (!dcp) return;
   __syncthreads();
 #pragma unroll
@@ -294,6 +303,8 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
   const int D = b.f.D;
   const unsigned slices = (unsigned)((D + 64 * NC - 1) / (64 * NC));
   if (!seq_tabs_fit(cu, N, B, T_, kPart, max_groups(64 * kWaves) / slices)) return hipErrorInvalidConfiguration;
+  if (!cu && T_ > kPart && (long long)B * ((D + 63) / 64) > max_groups(64 * kChainWaves)) return hipErrorInvalidConfiguration;
+  if (cu && (long long)kMaxVarSeq * ((D + 63) / 64) > max_groups(64 * kChainWaves)) return hipErrorInvalidConfiguration;
   float* dcp = b.dc ? ws : nullptr;
   float* seg = ws + all_items(cu != nullptr, N, B, T_, kPart) * D;
   size_t rows = 0;
@@ -303,9 +314,12 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
     n = make_seq_tab(s, cu, N, n, B, T_, kPart);
     const int seqs = s.n ? s.n : B;
     const dim3 grid((unsigned)s.items * slices), th(64 * kWaves);
-    hipLaunchKernelGGL((lru_bwd_part_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg);
-    hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)((D + 63) / 64) * (unsigned)seqs), dim3(64 * kChainWaves), 0, st, b, s, seg);
-    hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg, dcp ? dcp + rows * D : nullptr);
+    const bool one = s.items == seqs;   // no sequence has a second part
+    if (!one) {
+      hipLaunchKernelGGL((lru_bwd_part_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg);
+      hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)((D + 63) / 64) * (unsigned)seqs), dim3(64 * kChainWaves), 0, st, b, s, seg);
+    }
+    hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, one ? nullptr : seg, dcp ? dcp + rows * D : nullptr);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     rows += s.items;

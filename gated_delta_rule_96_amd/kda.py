@@ -848,6 +848,8 @@ def gemm_fp8(a, sa, w, sw, *, out_dtype=torch.bfloat16, out=None):
     if sa.dtype != torch.float32:
         raise TypeError(f"sa must be torch.float32, got {sa.dtype}")
     N, K = w.shape
+    if N > _INT_MAX or K > _INT_MAX:
+        raise ValueError(f"w: a size is not in 32 bits: {list(w.shape)}")
     kb = (K + 127) // 128
     pa, lda, lead = _flat_rows(a, "a", K)
     ps, lsa = _rows(sa, "sa", lead, (kb,))
