@@ -39,12 +39,12 @@ __device__ __forceinline__ void load_run(const LruArgs& g, const SeqPart& p, con
 #pragma unroll
   for (int k = 0; k < R; ++k) {
     const int q = min(k, n - 1);
-    x[k] = lru_load<Pk>(px + q * g.ldx, l.cl);
-    r[k] = lru_load<Pk>(pr + q * g.ldr, l.cl);
+    x[k] = *reinterpret_cast<const Pk*>(px + q * g.ldx + l.cl);
+    r[k] = *reinterpret_cast<const Pk*>(pr + q * g.ldr + l.cl);
   }
   if (kFull || g.i)
 #pragma unroll
-    for (int k = 0; k < R; ++k) i[k] = lru_load<Pk>(pi + min(k, n - 1) * g.ldi, l.cl);
+    for (int k = 0; k < R; ++k) i[k] = *reinterpret_cast<const Pk*>(pi + min(k, n - 1) * g.ldi + l.cl);
   const LruMode md = lru_mode<kFull>(g);
 #pragma unroll
   for (int k = 0; k < R; ++k)
@@ -231,7 +231,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
 #pragma unroll
     for (int j = 0; j < NC; ++j) h[j] = fmaf(a[k][j], h[j], u[k][j]);
     o.set(h);
-    if (t + k < p.t1) lru_store(y + (long long)k * g.D, l.c, o);
+    if (t + k < p.t1) *reinterpret_cast<LruPack<T, NC>*>(y + (long long)k * g.D + l.c) = o;
   }
 }
 

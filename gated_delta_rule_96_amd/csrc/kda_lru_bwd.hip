@@ -26,11 +26,11 @@ template <typename T> constexpr int part_of() { return kWaves * RunOf<T>::R; }
 
 // A run's rows as loaded.
 template <typename T, int NC, int R> struct BwdRun {
-  LruPack<T, NC> x[R], r[R], i[R], dy[R];
+  LruPack<T, NC, true> x[R], r[R], i[R], dy[R];
 };
 template <typename T, int NC, int R, bool kFull>
 __device__ __forceinline__ void load_rows(const LruBwdArgs& b, const SeqPart& p, const LruLane& l, int t, BwdRun<T, NC, R>& w) {
-  typedef LruPack<T, NC> Pk;
+  typedef LruPack<T, NC, true> Pk;
   const int n = p.t1 - t;
   if (n <= 0) return;
   const size_t row = p.start + (size_t)t;
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const L
 template <typename T, int NC, bool kFull>
 __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
   constexpr int R = RunOf<T>::R;
-  typedef LruPack<T, NC> Pk;
+  typedef LruPack<T, NC, true> Pk;
   __shared__ float red[3][kWaves][64 * NC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, D = b.f.D;
   const unsigned id = gridDim.x - 1 - blockIdx.x, item = id / slices;

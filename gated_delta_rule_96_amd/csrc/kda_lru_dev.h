@@ -13,8 +13,11 @@
 
 namespace kda {
 
-// NC channels of a token as they lie in memory.
-template <typename T, int NC> struct alignas(sizeof(T) * NC) LruPack {
+// NC channels of a token as they lie in memory.  kWord: two bf16 as one word.
+// Where paths meet between load and use, as in the gradients, halves are taken
+// apart there (32K x 2048 348 us, as words 336); the forward, which uses them in
+// place, is slower with words (64K x 4096 427 us, as halves 419).
+template <typename T, int NC, bool kWord = false> struct alignas(sizeof(T) * NC) LruPack {
   T v[NC];
   __device__ __forceinline__ float at(int j) const { return to_f32(v[j]); }
   __device__ __forceinline__ void fill(float x) {
@@ -26,8 +29,7 @@ template <typename T, int NC> struct alignas(sizeof(T) * NC) LruPack {
     for (int j = 0; j < NC; ++j) v[j] = from_f32<T>(x[j]);
   }
 };
-// (two bf16 as one word: as halves they are taken apart wherever paths meet)
-template <> struct alignas(4) LruPack<bf16, 2> {
+template <> struct alignas(4) LruPack<bf16, 2, true> {
   unsigned w;
   __device__ __forceinline__ float at(int j) const { return __uint_as_float(j ? w & 0xffff0000u : w << 16); }
   __device__ __forceinline__ void fill(float x) { set({x, x}); }
