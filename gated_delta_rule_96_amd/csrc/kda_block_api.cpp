@@ -96,7 +96,7 @@ int kda_gemm_fp8(const void* a, long long lda, const float* sa, long long lsa, c
   const Span in[] = {{a, rows_bytes(M, lda, K, 1)}, {sa, rows_bytes(M, lsa, KB, 4)}, {w, (size_t)N * K}, {sw, (size_t)((N + 127) / 128) * KB * 4}};
   const Span out[] = {{c, (size_t)M * N * elem_size(c_dtype)}};
   if (!spans_apart(in, out, {-1})) return KDA_ERR_OVERLAP;
-  const kda::Gemm8Args g{static_cast<const unsigned char*>(a), lda, sa, lsa, static_cast<const unsigned char*>(w), sw, c, M, N, K};
+  const kda::Gemm8Args g{static_cast<const unsigned char*>(a), lda, sa, lsa, static_cast<const unsigned char*>(w), sw, c, M, N, N, K};
   return hip_status(kda::launch_gemm8(c_dtype == KDA_BF16, g, static_cast<hipStream_t>(stream)));
 }
 

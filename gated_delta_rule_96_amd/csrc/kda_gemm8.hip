@@ -8,8 +8,8 @@
 // The weights are the MFMA's left operand, so that a lane holds four
 // neighbouring outputs of one row (an 8- or 16-byte store) and needs one scale
 // per 16 rows instead of four.
-// Measured: 8192 x 12288 x 4096 402 us (2.05 PFLOP/s; a library's product of
-// such operands with one scale each 338), 256 rows 22, one row 11.  Of the
+// Measured: 8192 x 12288 x 4096 391 us (2.11 PFLOP/s; a library's product of
+// such operands with one scale each 338), 8191 x 8480 x 4096 281, 256 rows 22, one row 11.  Of the
 // large tile's time the matrix instructions take 45%; the fmas that join
 // blocks, the LDS reads and the loads to LDS share the rest.
 #include "kda_rows.h"
@@ -66,8 +66,8 @@ __device__ __forceinline__ f32x4 mma128(const Frag<float>& a, const Frag<float>&
 }
 
 template <typename T> __device__ __forceinline__ void store_out(const Gemm8Args& g, long long m, int n, f32x4 v) {
-  T* p = (T*)g.c + m * g.N + n;
-  if ((g.N & 3) == 0) {   // n is a multiple of 4: all four inside, and aligned
+  T* p = (T*)g.c + m * g.ldc + n;
+  if ((g.ldc & 3) == 0) {   // (and with it N) n is a multiple of 4: all four inside, and aligned
     if (n < g.N) *reinterpret_cast<V4<T>*>(p) = narrow4<T>(v);
     return;
   }
@@ -325,24 +325,24 @@ struct TileTime {
 };
 constexpr TileTime kTiles[5] = {{64, 64, 12.4f, 20.f}, {128, 64, 16.2f, 27.f}, {128, 128, 24.4f, 41.f}, {128, 256, 39.5f, 62.f}, {256, 256, 66.f, 0.f}};
 
-template <typename T>
-hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
-  // Few rows: 64 outputs a work-group where those are enough for half the card
-  // (12288 outputs: 12.3 us, 16 outputs 14.5), else 16 (4096 outputs: 9.0 and
-  // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 14.3, two row sets here 17.6.
-  if (g.M <= 16) return g.N >= 8192 ? rows_go<T, 4, 16>(g, st) : rows_go<T, 1, 8>(g, st);
+template <typename T> float round_us(int i) { return sizeof(T) == 2 ? kTiles[i].bf16_us : kTiles[i].f32_us; }
+long long tiles_of(const TileTime& t, long long M, long long N) { return (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn); }
+
+// The tile that takes least for M x N, and its time.
+template <typename T> int best_tile(long long M, long long N, float& least) {
   int best = 0;
-  float least = 0.f;
   for (int i = 0; i < (sizeof(T) == 2 ? 5 : 4); ++i) {
-    const TileTime& t = kTiles[i];
-    const long long n = ((g.M + t.bm - 1) / t.bm) * ((g.N + t.bn - 1) / t.bn);
-    const float us = (float)((n + 255) / 256) * (sizeof(T) == 2 ? t.bf16_us : t.f32_us);
+    const float us = (float)((tiles_of(kTiles[i], M, N) + 255) / 256) * round_us<T>(i);
     if (i == 0 || us < least) {
       best = i;
       least = us;
     }
   }
-  switch (best) {
+  return best;
+}
+
+template <typename T> hipError_t tile_by(int i, const Gemm8Args& g, hipStream_t st) {
+  switch (i) {
     case 0: return tile_go<T, 64, 64, 4, 2, 3, 2>(g, st);
     case 1: return tile_go<T, 128, 64, 4, 2, 3, 2>(g, st);
     case 2: return tile_go<T, 128, 128, 4, 2, 3, 1>(g, st);
@@ -351,6 +351,45 @@ hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
   }
   if constexpr (sizeof(T) == 2) return tile_go<T, 256, 256, 4, 2, 2, 1>(g, st);
   return hipErrorInvalidValue;
+}
+
+template <typename T>
+hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
+  // Few rows: 64 outputs a work-group where those are enough for half the card
+  // (12288 outputs: 12.3 us, 16 outputs 14.5), else 16 (4096 outputs: 9.0 and
+  // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 14.3, two row sets here 17.6.
+  if (g.M <= 16) return g.N >= 8192 ? rows_go<T, 4, 16>(g, st) : rows_go<T, 1, 8>(g, st);
+  float one = 0.f;
+  int main_tile = best_tile<T>(g.M, g.N, one), rest_tile = 0;
+  // Where a last round would be mostly empty: whole rounds of one tile, and the
+  // columns that are left in a second launch (kGap us) with theirs
+  // (8191 x 8480 x 4096: 281 us; one launch 305).
+  constexpr float kGap = 4.f;
+  const float k = (float)g.K / 4096.f;
+  int cut = 0;
+  for (int i = 0; i < (sizeof(T) == 2 ? 5 : 4); ++i) {
+    const TileTime& t = kTiles[i];
+    const long long rows = (g.M + t.bm - 1) / t.bm, rounds = tiles_of(t, g.M, g.N) / 256, cols = rounds * 256 / rows * t.bn;
+    if (rounds == 0 || cols == 0 || cols >= g.N || cols % 128) continue;   // (scales are of 128 columns)
+    float rest;
+    const int r = best_tile<T>(g.M, g.N - cols, rest);
+    const float us = (float)rounds * round_us<T>(i) + rest + kGap / k;
+    if (us < one) {
+      one = us;
+      main_tile = i;
+      rest_tile = r;
+      cut = (int)cols;
+    }
+  }
+  if (!cut) return tile_by<T>(main_tile, g, st);
+  Gemm8Args a = g, b = g;
+  a.N = cut;
+  b.N = g.N - cut;
+  b.w += (size_t)cut * g.K;
+  b.sw += (size_t)(cut / 128) * ((g.K + 127) / 128);
+  b.c = static_cast<T*>(g.c) + cut;
+  const hipError_t e = tile_by<T>(main_tile, a, st);
+  return e != hipSuccess ? e : tile_by<T>(rest_tile, b, st);
 }
 
 }  // namespace

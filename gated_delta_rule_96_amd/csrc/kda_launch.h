@@ -252,8 +252,8 @@ struct Gemm8Args {
   long long lsa;
   const unsigned char* w;   // [N][K]
   const float* sw;          // [NB][KB]
-  void* c;                  // [M][N]
-  long long M;
+  void* c;                  // rows [M][N], ldc apart
+  long long M, ldc;
   int N, K;
 };
 hipError_t launch_gemm8(int out_bf16, const Gemm8Args& g, hipStream_t stream);

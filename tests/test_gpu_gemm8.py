@@ -58,7 +58,8 @@ def check(a, sa, w, sw, c):
 
 
 SIZES = [(1, 16, 16), (1, 1, 128), (3, 130, 144), (16, 200, 4096), (17, 129, 1040), (32, 64, 256), (33, 48, 640), (64, 500, 2048), (65, 300, 400),
-         (100, 128, 128), (128, 129, 16), (200, 1000, 1296), (257, 511, 512), (1000, 260, 272), (300, 4100, 384), (2100, 2050, 144), (4096, 3300, 208)]
+         (100, 128, 128), (128, 129, 16), (200, 1000, 1296), (257, 511, 512), (1000, 260, 272), (300, 4100, 384), (2100, 2050, 144), (4096, 3300, 208),
+         (2048, 8325, 1040)]   # (the last: whole rounds of one tile and the columns left in a second launch)
 
 
 @pytest.mark.parametrize("out", [BF, F32])
