@@ -9,9 +9,10 @@
 // neighbouring outputs of one row (an 8- or 16-byte store) and needs one scale
 // per 16 rows instead of four.
 // Measured: 8192 x 12288 x 4096 391 us (2.11 PFLOP/s; a library's product of
-// such operands with one scale each 338), 8191 x 8480 x 4096 281, 256 rows 22, one row 11.  Of the
-// large tile's time the matrix instructions take 45%; the fmas that join
-// blocks, the LDS reads and the loads to LDS share the rest.
+// such operands with one scale each 338), 8191 x 8480 x 4096 281, 256 rows of the
+// first 22.5, one row 11.  Of the large tile's time the matrix instructions take
+// 45%; the fmas that join blocks, the LDS reads and the loads to LDS share the
+// rest.
 #include "kda_rows.h"
 
 namespace kda {
@@ -22,8 +23,6 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(1))) const void* GlbP;
 typedef __attribute__((address_space(3))) void* LdsP;
-typedef unsigned char u8;
-
 typedef unsigned char u8;
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
@@ -82,7 +81,6 @@ template <typename T> __device__ __forceinline__ void store_out(const Gemm8Args&
 // different banks.
 __device__ __forceinline__ int lds_piece(int r, int p) { return r * 128 + ((p ^ ((r >> 1) & 7)) << 4); }
 
-
 // Work-group tile BM x BN, WM x WN waves, S sets of U steps in LDS (a step: one
 // block of 128 reduction indices): a set's loads are issued S - 1 sets before
 // it, and the waves meet once a set.
@@ -117,9 +115,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
     const int s = i * kThreads + tid, row = s >> 3;
     ob[i] = (unsigned)min(row, cols - 1) * (unsigned)g.K + ((s & 7) ^ ((row >> 1) & 7)) * 16;
   }
-  // Offsets reach 256 strides at most.  Pieces past K re-read the row's first block; the products left out are made
-  // zero on a's side (what is read of w there is w's own row: no new NaN).
-  // (a thread stages the same piece of every row it stages)
+  // Pieces past K re-read the row's first block; the products left out are
+  // made zero on a's side (what is read of w there is w's own row: no new NaN).
+  // (A thread stages the same piece of every row it stages.)
   const int ck = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;
   auto step_offset = [&](int kb) { return (unsigned)(kb * 128 + ck < g.K ? kb * 128 : -ck); };
   auto stage = [&](int n, int kb, unsigned k) {   // the n-th of a thread's LA + LB pieces of step kb
@@ -293,10 +291,11 @@ __global__ __launch_bounds__(64 * WK) void gemm8_rows_kernel(const Gemm8Args g) 
   }
 }
 
+constexpr int kTileThreads = 512;
 template <typename T, int BM, int BN, int WM, int WN, int S, int U>
 hipError_t tile_go(const Gemm8Args& g, hipStream_t st) {
   constexpr int kThreads = 64 * WM * WN, kLds = S * U * (BM + BN) * 128 + 2 * BM * 16;
-  static_assert(kLds <= 160 * 1024 && (U == 1 || U == 2 || U == 4), "LDS, sets of scales");
+  static_assert(kThreads == kTileThreads && kLds <= 160 * 1024 && (U == 1 || U == 2 || U == 4), "LDS, sets of scales");
   const long long tm = (g.M + BM - 1) / BM, tn = (g.N + BN - 1) / BN, n = (tm * tn + 7) / 8 * 8;
   if (n > max_groups(kThreads)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((gemm8_tile_kernel<T, BM, BN, WM, WN, S, U>), dim3((unsigned)n), dim3(kThreads), kLds, st, g, (unsigned)tm, (unsigned)tn);
@@ -328,12 +327,15 @@ constexpr TileTime kTiles[5] = {{64, 64, 12.4f, 20.f}, {128, 64, 16.2f, 27.f}, {
 template <typename T> float round_us(int i) { return sizeof(T) == 2 ? kTiles[i].bf16_us : kTiles[i].f32_us; }
 long long tiles_of(const TileTime& t, long long M, long long N) { return (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn); }
 
-// The tile that takes least for M x N, and its time.
+// The tile that takes least for M x N, and its time.  (Of more work-groups than
+// a launch may have: the largest only, which the launch refuses in its turn.)
 template <typename T> int best_tile(long long M, long long N, float& least) {
-  int best = 0;
-  for (int i = 0; i < (sizeof(T) == 2 ? 5 : 4); ++i) {
-    const float us = (float)((tiles_of(kTiles[i], M, N) + 255) / 256) * round_us<T>(i);
-    if (i == 0 || us < least) {
+  int best = sizeof(T) == 2 ? 4 : 3;
+  least = (float)((tiles_of(kTiles[best], M, N) + 255) / 256) * round_us<T>(best);
+  for (int i = 0; i < (sizeof(T) == 2 ? 4 : 3); ++i) {
+    const long long n = tiles_of(kTiles[i], M, N);
+    const float us = (float)((n + 255) / 256) * round_us<T>(i);
+    if (us < least && n <= max_groups(kTileThreads) - 8) {
       best = i;
       least = us;
     }
@@ -358,7 +360,8 @@ hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
   // Few rows: 64 outputs a work-group where those are enough for half the card
   // (12288 outputs: 12.3 us, 16 outputs 14.5), else 16 (4096 outputs: 9.0 and
   // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 14.3, two row sets here 17.6.
-  if (g.M <= 16) return g.N >= 8192 ? rows_go<T, 4, 16>(g, st) : rows_go<T, 1, 8>(g, st);
+  // (More outputs than a launch has work-groups for: tiles.)
+  if (g.M <= 16 && g.N <= 1 << 27) return g.N >= 8192 ? rows_go<T, 4, 16>(g, st) : rows_go<T, 1, 8>(g, st);
   float one = 0.f;
   int main_tile = best_tile<T>(g.M, g.N, one), rest_tile = 0;
   // Where a last round would be mostly empty: whole rounds of one tile, and the

@@ -5,6 +5,12 @@
 // runs of them, one behind the other: a part of a sequence.  Its (P, H) are
 // joined over the waves in LDS.  Every input is read once: the parts of a
 // sequence hand their states on inside the one launch.
+//
+// Bound by HBM: 65536 x 4096 bf16 419 us (8 bytes an element, 5.1 TB/s), 8191
+// packed tokens x 4096 fp32 119 us (4.5 TB/s); a token for each of 256 x 4096
+// channels is bound by the launch.  The tile: runs of 8, 24 or 32 tokens, 4 or 16
+// waves, four channels a lane, a look back over 2 or 8 parts were all slower or
+// the same.
 #include "kda_lru_dev.h"
 
 namespace kda {
@@ -103,12 +109,11 @@ __device__ __forceinline__ Words words_at(void* ws, size_t n) {
   return w;
 }
 __global__ __launch_bounds__(256) void lru_fill_kernel(unsigned* ws, size_t n) {   // n words of ones behind the ticket
-  const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (at == 0) ws[0] = 0;
-  for (size_t i = at; i < n; i += (size_t)gridDim.x * 1024)
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + k < n) ws[64 + i + k] = kNone;
+  typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+  const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x, step = (size_t)gridDim.x * 256;
+  if (id == 0) ws[0] = 0;
+  for (size_t q = id; q < n / 4; q += step) reinterpret_cast<u32x4*>(ws + 64)[q] = u32x4{kNone, kNone, kNone, kNone};
+  if (id < n % 4) ws[64 + n / 4 * 4 + id] = kNone;
 }
 
 // Outputs.  kChain: sequences of several parts.  Each work-group takes the
@@ -287,7 +292,7 @@ hipError_t fwd_go(const LruArgs& a, const int* cu, int N, int B, int T_, void* w
       hipLaunchKernelGGL((lru_out_kernel<T, NC, false, kFull>), grid, th, 0, st, a, s, slices, ws);
     } else {
       const size_t words = (size_t)s.items * a.D * 3, groups = (words + 1023) / 1024;
-      hipLaunchKernelGGL(lru_fill_kernel, dim3((unsigned)(groups < 4096 ? groups : 4096)), dim3(256), 0, st, static_cast<unsigned*>(ws), words);
+      hipLaunchKernelGGL(lru_fill_kernel, dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, st, static_cast<unsigned*>(ws), words);
       hipLaunchKernelGGL((lru_out_kernel<T, NC, true, kFull>), grid, th, 0, st, a, s, slices, ws);
     }
     const hipError_t e = hipGetLastError();

@@ -13,16 +13,26 @@
 // Three launches where a sequence has several parts (one otherwise): every
 // part's P, H, K; the states and the e that enter the parts; the gradients.  The
 // last walks the parts from the end, so that what the first read last is still
-// in the cache.
+// in the cache.  A single launch, as the forward's, would have to hold every
+// input between the state that comes from the left and the e from the right,
+// which the registers of the whole card cannot for more than a few thousand
+// tokens; so the inputs are read twice, and 22 bytes an element pass (bf16) where
+// the formulas need 14.
+//
+// Bound by HBM in both passes, in bf16 nearly as much by the exponentials and
+// roots (4 sequences of 8192 x 2048 with every gradient: sums 120 us, 4.4 TB/s;
+// chain 15; gradients 180, 5.2 TB/s; dc 7; 322 in all.  fp32: 200 and 325 us,
+// 5.3 and 5.8 TB/s).  The tile: runs of 8 in parts of 32 tokens 340 us, runs of 4
+// 358 to 362, parts of 64 375 (timed together).  One sequence behind the other,
+// so that the second pass finds its inputs in the last-level cache, 376 against
+// 344: the ends of the launches cost more than it gives.
 #include "kda_lru_dev.h"
 
 namespace kda {
 
 namespace {
 
-constexpr int kWaves = 4;
-template <typename T> struct RunOf { static constexpr int R = 8; };   // tokens of a wave's run
-template <typename T> constexpr int part_of() { return kWaves * RunOf<T>::R; }
+constexpr int kWaves = 4, kR = 8, kPart = kWaves * kR;   // kR tokens a wave's run
 
 // A run's rows as loaded.
 template <typename T, int NC, int R> struct BwdRun {
@@ -85,7 +95,7 @@ __device__ __forceinline__ void run_sums(const BwdRun<T, NC, R>& w, int n, float
 // seg [items][3][D]: P, H, K of every part.
 template <typename T, int NC, bool kFull>
 __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_part_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, float* seg) {
-  constexpr int R = RunOf<T>::R;
+  constexpr int R = kR;
   __shared__ float red[3][kWaves][64 * NC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, D = b.f.D;
   const unsigned item = blockIdx.x / slices;
@@ -177,7 +187,7 @@ __global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const L
 // part's -sum of dg Sigmoid(r), or null.
 template <typename T, int NC, bool kFull>
 __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
-  constexpr int R = RunOf<T>::R;
+  constexpr int R = kR;
   typedef LruPack<T, NC, true> Pk;
   __shared__ float red[3][kWaves][64 * NC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, D = b.f.D;
@@ -293,20 +303,19 @@ bool pairs(const LruBwdArgs& b, size_t esz) {
   return true;
 }
 
-size_t all_items(int is_packed, int N, int B, int T, int part) {
-  return is_packed ? (size_t)T / part + (size_t)N : (size_t)B * (((size_t)T + part - 1) / part);
+size_t all_items(int is_packed, int N, int B, int T) {
+  return is_packed ? (size_t)T / kPart + (size_t)N : (size_t)B * (((size_t)T + kPart - 1) / kPart);
 }
 
 template <typename T, int NC, bool kFull>
 hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, float* ws, hipStream_t st) {
-  constexpr int kPart = part_of<T>();
   const int D = b.f.D;
   const unsigned slices = (unsigned)((D + 64 * NC - 1) / (64 * NC));
   if (!seq_tabs_fit(cu, N, B, T_, kPart, max_groups(64 * kWaves) / slices)) return hipErrorInvalidConfiguration;
   if (!cu && T_ > kPart && (long long)B * ((D + 63) / 64) > max_groups(64 * kChainWaves)) return hipErrorInvalidConfiguration;
   if (cu && (long long)kMaxVarSeq * ((D + 63) / 64) > max_groups(64 * kChainWaves)) return hipErrorInvalidConfiguration;
   float* dcp = b.dc ? ws : nullptr;
-  float* seg = ws + all_items(cu != nullptr, N, B, T_, kPart) * D;
+  float* seg = ws + all_items(cu != nullptr, N, B, T_) * D;
   size_t rows = 0;
   const int end = cu ? N : B;
   for (int n = 0; n < end;) {
@@ -336,8 +345,7 @@ hipError_t bwd_type(const LruBwdArgs& b, const int* cu, int N, int B, int T_, fl
 }  // namespace
 
 size_t lru_bwd_workspace_bytes(int is_packed, int N, int B, int T, int D) {
-  // the shorter parts of fp32 inputs need more
-  return (all_items(is_packed, N, B, T, part_of<float>()) * 4 * D * sizeof(float) + 255) & ~(size_t)255;
+  return (all_items(is_packed, N, B, T) * 4 * D * sizeof(float) + 255) & ~(size_t)255;
 }
 
 hipError_t launch_lru_bwd(int is_bf16, const LruBwdArgs& b, const int* cu, int N, int B, int T, void* workspace, hipStream_t st) {
