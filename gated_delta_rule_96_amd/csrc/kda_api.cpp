@@ -27,7 +27,8 @@ const char* kda_status_str(int s) {
     case KDA_ERR_DTYPE: return "dtype is not KDA_F32 or KDA_BF16";
     case KDA_ERR_ALIGN: return "a tensor pointer is not 16-byte aligned";
     case KDA_ERR_UNSUPPORTED: return "unsupported dk/dv/chunk (dk, dv in {64,128}; chunk 64), convolution width (2..4), "
-                                     "head width or rotation (multiples of 8, heads to 512)";
+                                     "head width or rotation (multiples of 8, heads to 512), "
+                                     "norm width (a multiple of 8 to 16384), product K (a multiple of 16)";
     case KDA_ERR_WORKSPACE: return "workspace missing or smaller than kda_fwd_workspace_bytes";
     case KDA_ERR_RANGE: return "input value out of range (log-decay outside [gmin, 0], or gmin outside [-5, 0))";
     case KDA_ERR_HIP: return "HIP launch failed";

@@ -592,9 +592,10 @@ int kda_add_rms_norm_bwd(const void* h, long long ldh, const float* w, float eps
  * every 128 channels of a row and for every 128 x 128 tile of the weights:
  *   c[m,n] = sum_kb sa[m,kb] sw[n/128,kb] sum_{k in block kb} a[m,k] w[n,k]
  * a: rows [M,K], lda bytes apart (a multiple of 16); sa: rows [M,ceil(K/128)]
- * fp32, lsa (at most 2^20) apart; w [N,K]; sw [ceil(N/128), ceil(K/128)] fp32; c [M,N] of
- * c_dtype.  K a multiple of 16, K and lda at most 2^24; M, N any (the last
- * blocks may be shorter).
+ * fp32, lsa (at most 2^20) apart; w [N,K]; sw [ceil(N/128), ceil(K/128)]
+ * fp32; c [M,N] of c_dtype.  K a multiple of 16, K and lda at most 2^24; M, N
+ * any (the last blocks may be shorter) up to 2^23 tiles of 256 x 256 outputs,
+ * 128 x 256 in fp32.
  * KDA_BF16: a block's 128 products are summed by the 8-bit matrix instruction
  * (off by 1.4e-5 of the sum's rms), blocks in fp32.  KDA_F32: all sums in fp32
  * at half that rate.  One rounding.  What is not finite in a row of a

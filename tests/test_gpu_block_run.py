@@ -251,3 +251,34 @@ def test_long_cache_of_rows():
     torch.cuda.synchronize()
     # 2000 tokens of decay e^-1/2 and more forget everything before them
     assert torch.equal(y[0, -64:], tail[0, -64:])
+
+
+def test_more_work_than_the_usual_tiles_have_groups_for():
+    # the product: more outputs of one row than work-groups of 16 or 64 outputs,
+    # more rows than tiles of 64; the norm: more rows than one work-group each
+    one = torch.ones((1, 1), device="cuda")
+    N = (1 << 27) + 200
+    say(f"product 1 x {N} x 16")
+    w8 = torch.empty((N, 16), dtype=torch.uint8, device="cuda").fill_(56).view(F8)
+    w8[:300] = torch.randn((300, 16), device="cuda").to(F8)
+    w8[-300:] = torch.randn((300, 16), device="cuda").to(F8)
+    a8 = torch.randn((1, 16), device="cuda").to(F8)
+    sw = torch.rand(((N + 127) // 128, 1), device="cuda")
+    c = kda.gemm_fp8(a8, one, w8, sw)
+    cut = N // 128 * 128 - 128
+    assert torch.equal(c[:, cut:], kda.gemm_fp8(a8, one, w8[cut:], sw[cut // 128:])) and torch.equal(c[:, :256], kda.gemm_fp8(a8, one, w8[:256], sw[:2]))
+    del w8, c
+    M = (1 << 29) + 700
+    say(f"product {M} x 8 x 16")
+    a8 = torch.empty((M, 16), dtype=torch.uint8, device="cuda").fill_(56).view(F8)
+    a8[-900:] = torch.randn((900, 16), device="cuda").to(F8)
+    sa, w8 = torch.ones((M, 1), device="cuda"), torch.randn((8, 16), device="cuda").to(F8)
+    sa[-900:].uniform_()
+    c = kda.gemm_fp8(a8, sa, w8, one)
+    assert torch.equal(c[-900:], kda.gemm_fp8(a8[-900:], sa[-900:], w8, one)) and torch.equal(c[:900], kda.gemm_fp8(a8[:900], sa[:900], w8, one))
+    del a8, sa, c
+    R = (1 << 22) + 77
+    say(f"norm {R} x 8")
+    x = torch.randn((R, 8), dtype=BF, device="cuda")
+    y, _ = kda.add_rms_norm(x)
+    assert torch.equal(y[-900:], kda.add_rms_norm(x[-900:].contiguous())[0])
