@@ -144,6 +144,9 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _stream(device) -> int:
     # (the handle itself where torch gives it: torch.cuda.current_stream()
     # builds an object around it, 1.9 us of a single-token call's 12)
@@ -480,9 +483,9 @@ def _dense(t, name, shape, dtype, dev=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if not (t.is_cuda and t.is_contiguous()):
-        return _ptr(t)   # (says which)
-    return t.data_ptr()
+    if t.is_contiguous() and t.is_cuda:
+        return t.data_ptr()
+    return _ptr(t)   # (says which)
 
 
 def _same_device(dev, **tensors):
@@ -493,8 +496,11 @@ def _same_device(dev, **tensors):
 
 def _call(dev, name, *args):
     """Calls entry point `name` on dev's current stream (with dev the current device)."""
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        _check(getattr(lib(), name)(*args, _stream(dev)), name)
+    index = dev.index
+    if index is None or index == _current_device():
+        status = getattr(_lib or lib(), name)(*args, _stream(dev))
+        if status:
+            _check(status, name)
     else:
         with torch.cuda.device(dev):
             _check(getattr(lib(), name)(*args, _stream(dev)), name)
@@ -762,18 +768,18 @@ def _flat_rows(t, name, D):
     return p, ld, lead
 
 
-def _rows_beside(t, name, x, dev, shape):
+def _rows_beside(t, name, dtype, dev, shape, D):
     """Pointer and token stride of an input of x's (checked) shape, type and
     device, or of None."""
     if t is None:
         return None, 0
-    if t.dtype is not x.dtype:
-        raise TypeError(f"{name} dtype {t.dtype} != x dtype {x.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} dtype {t.dtype} != x dtype {dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, not on {dev}")
     if t.shape == shape and t.is_contiguous():
-        return t.data_ptr(), shape[-1]
-    return _rows(t, name, tuple(shape[:-1]), (shape[-1],))
+        return t.data_ptr(), D
+    return _rows(t, name, tuple(shape[:-1]), (D,))
 
 
 def add_rms_norm(x, res=None, w=None, *, eps=1e-6, fp8=False, out=None, scale_out=None, sum_out=None):
@@ -790,24 +796,28 @@ def add_rms_norm(x, res=None, w=None, *, eps=1e-6, fp8=False, out=None, scale_ou
     dev, dt = x.device, _dtype_code(x)
     pr, ldr, rdt, ph = None, 0, dt, None
     if res is not None:
-        if res.shape != shape:
-            raise ValueError(f"res must be {list(shape)}, got {list(res.shape)}")
-        if res.device != dev:
-            raise ValueError(f"res is on {res.device}, not on {dev}")
-        pr, ldr, _ = _flat_rows(res, "res", D)
+        pr, ldr = _rows_beside(res, "res", res.dtype, dev, shape, D)
         rdt = _dtype_code(res)
-        sum_out = _given(sum_out, res, "sum_out")
-        ph = sum_out.data_ptr()
+        if sum_out is None:
+            sum_out = torch.empty_like(res, memory_format=torch.contiguous_format)
+            ph = sum_out.data_ptr()
+        else:
+            ph = _dense(sum_out, "sum_out", shape, res.dtype, dev)
     elif sum_out is not None:
         raise ValueError("sum_out needs res")
     ps = None
     if fp8:
+        kb = (*lead, (D + 127) // 128)
         if out is None:
             out = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
-        kb = (*lead, (D + 127) // 128)
-        scale_out = torch.empty(kb, dtype=torch.float32, device=dev) if scale_out is None else scale_out
-        ps = _dense(scale_out, "scale_out", kb, torch.float32, dev)
-        py = _dense(out, "out", shape, torch.float8_e4m3fn, dev)
+            py = out.data_ptr()
+        else:
+            py = _dense(out, "out", shape, torch.float8_e4m3fn, dev)
+        if scale_out is None:
+            scale_out = torch.empty(kb, dtype=torch.float32, device=dev)
+            ps = scale_out.data_ptr()
+        else:
+            ps = _dense(scale_out, "scale_out", kb, torch.float32, dev)
     else:
         out = _given(out, x, "out")
         py = out.data_ptr()
@@ -826,7 +836,7 @@ def add_rms_norm_bwd(h, w, dy, dh=None, *, eps=1e-6, want_dw=None, workspace=Non
     dev, rows = h.device, math.prod(lead)
     if out is None:
         wanted = w is not None if want_dw is None else want_dw
-        out = {"dx": torch.empty(h.shape, dtype=h.dtype, device=dev), "dw": torch.empty(D, dtype=torch.float32, device=dev) if wanted else None}
+        out = {"dx": _given(None, h, "dx"), "dw": torch.empty(D, dtype=torch.float32, device=dev) if wanted else None}
     ws = None
     if out.get("dw") is not None:
         ws = _scratch(workspace, lib().kda_add_rms_norm_bwd_workspace_bytes(rows, D), dev, "kda_add_rms_norm_bwd_workspace_bytes")
@@ -865,10 +875,15 @@ def gemm_fp8(a, sa, w, sw, *, out_dtype=torch.bfloat16, out=None):
 
 def _lru_setup(x, r, i, c):
     """Checked inputs of the gated linear recurrence: (x .. c of the C call)."""
-    shape, dev = x.shape, x.device
+    shape, dev, dtype = x.shape, x.device, x.dtype
     D = shape[-1]
-    pr, pi = _rows_beside(r, "r", x, dev, shape), _rows_beside(i, "i", x, dev, shape)
-    return (*_rows(x, "x", tuple(shape[:-1]), (D,)), *pr, *pi, _dense(c, "c", (D,), torch.float32, dev))
+    pr, ldr = _rows_beside(r, "r", dtype, dev, shape, D)
+    pi, ldi = _rows_beside(i, "i", dtype, dev, shape, D)
+    if x.is_contiguous() and x.is_cuda and x.numel() <= _INT_MAX:
+        px, ldx = x.data_ptr(), D
+    else:
+        px, ldx = _rows(x, "x", tuple(shape[:-1]), (D,))
+    return px, ldx, pr, ldr, pi, ldi, _dense(c, "c", (D,), torch.float32, dev)
 
 
 def lru_fwd(x, r, i=None, c=None, h0=None, *, unit=True, cu_seqlens=None, final_state=True, ht=None, workspace=None, out=None):
@@ -884,12 +899,17 @@ def lru_fwd(x, r, i=None, c=None, h0=None, *, unit=True, cu_seqlens=None, final_
     arr, N = _packed(cu_seqlens, B, T)
     dev, st = x.device, (N, D)
     y = _given(out, x, "out")
-    if final_state and ht is None:
-        ht = torch.empty(st, dtype=torch.float32, device=dev)
+    pht = None
+    if final_state:
+        if ht is None:
+            ht = torch.empty(st, dtype=torch.float32, device=dev)
+            pht = ht.data_ptr()
+        else:
+            pht = _dense(ht, "ht", st, torch.float32, dev)
     ws = _scratch(workspace, lib().kda_lru_workspace_bytes(B, T, D, N if arr is not None else 0), dev, "kda_lru_workspace_bytes")
     _same_device(dev, workspace=ws)
-    _call(dev, "kda_lru_fwd", *args, _dense(h0, "h0", st, torch.float32, dev), _dense(ht if final_state else None, "ht", st, torch.float32, dev),
-          y.data_ptr(), KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, T, D, arr, N, _ptr(ws), ws.numel())
+    _call(dev, "kda_lru_fwd", *args, _dense(h0, "h0", st, torch.float32, dev), pht, y.data_ptr(),
+          KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, T, D, arr, N, _ptr(ws), ws.numel())
     return y, (ht if final_state else None)
 
 
@@ -897,13 +917,14 @@ def lru_step(x, r, i, c, state, *, unit=True, state_out=None, out=None):
     """y = lru_step(x, r, i, c, state): one token x, r, i [B,D] per sequence
     (kda_lru_step); state [B,D] fp32 moves on in place, or into state_out (the
     old state is then kept)."""
-    B, D = x.shape
+    st = x.shape
+    B, D = st
     args = _lru_setup(x, r, i, c)
-    dev, st = x.device, (B, D)
-    so = state if state_out is None else state_out
+    dev = x.device
+    ps = _dense(state, "state", st, torch.float32, dev)
+    po = ps if state_out is None else _dense(state_out, "state_out", st, torch.float32, dev)
     y = _given(out, x, "out")
-    _call(dev, "kda_lru_step", *args, _dense(state, "state", st, torch.float32, dev), _dense(so, "state_out", st, torch.float32, dev),
-          y.data_ptr(), KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, D)
+    _call(dev, "kda_lru_step", *args, ps, po, y.data_ptr(), KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, D)
     return y
 
 
@@ -917,7 +938,7 @@ def lru_bwd(x, r, i, c, dy, h0=None, dht=None, *, unit=True, cu_seqlens=None, wo
     arr, N = _packed(cu_seqlens, B, T)
     dev, st = x.device, (N, D)
     if out is None:
-        out = {n: torch.empty((B, T, D), dtype=x.dtype, device=dev) if t is not None else None for n, t in (("dx", x), ("dr", r), ("di", i))}
+        out = {n: _given(None, x, n) if t is not None else None for n, t in (("dx", x), ("dr", r), ("di", i))}
         out["dc"] = torch.empty(D, dtype=torch.float32, device=dev) if c is not None else None
         out["dh0"] = torch.empty(st, dtype=torch.float32, device=dev) if h0 is not None else None
     ws = _scratch(workspace, lib().kda_lru_bwd_workspace_bytes(B, T, D, N if arr is not None else 0), dev, "kda_lru_bwd_workspace_bytes")
