@@ -11,8 +11,11 @@
 // Measured: 8192 x 12288 x 4096 391 us (2.11 PFLOP/s; a library's product of
 // such operands with one scale each 338), 8191 x 8480 x 4096 281, 256 rows of the
 // first 22.5, one row 11.  Of the large tile's time the matrix instructions take
-// 45%; the fmas that join blocks, the LDS reads and the loads to LDS share the
-// rest.
+// 49%, and no single part binds it: without the loads to LDS it ran at 2.31
+// PFLOP/s, without its reads of the weights from LDS 2.31, without three in four of
+// the fmas that join blocks 2.15, with every load from the cache 2.18 (2.04 then).
+// The next step's first operands read behind the last products of a step: the
+// same.
 #include "kda_rows.h"
 
 namespace kda {
@@ -81,16 +84,22 @@ template <typename T> __device__ __forceinline__ void store_out(const Gemm8Args&
 // different banks.
 __device__ __forceinline__ int lds_piece(int r, int p) { return r * 128 + ((p ^ ((r >> 1) & 7)) << 4); }
 
-// Work-group tile BM x BN, WM x WN waves, S sets of U steps in LDS (a step: one
-// block of 128 reduction indices): a set's loads are issued S - 1 sets before
-// it, and the waves meet once a set.
-template <typename T, int BM, int BN, int WM, int WN, int S, int U>
-__global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8Args g, unsigned tm, unsigned tn) {
-  constexpr int kThreads = 64 * WM * WN, MT = BM / WM / 16, NT = BN / WN / 16;
+// Work-group tile BM x BN.  A step is one block of 128 reduction indices; R of
+// them are in LDS, in sets of U that the waves meet for: a step's loads are
+// issued R - U steps before it.  KG groups of WM x WN waves take a set's steps by
+// turns, with sums of their own that are joined through LDS at the end: fewer
+// waves read a step's operands, and larger pieces each (64 x 64 tiles, 8 waves for
+// every step against two groups of 4: 12.7 and 10.9 us for 64 x 4096 x 4096, 19.4
+// and 15.9 in fp32; 64 x 128: 16.6 and 15.0 for 512 x 4096 x 4096; with 128 x 128 two
+// groups leave no room for loads further ahead: 24.6 and 25.0).
+template <typename T, int BM, int BN, int WM, int WN, int KG, int R, int U>
+__global__ __launch_bounds__(64 * WM * WN * KG, 2) void gemm8_tile_kernel(const Gemm8Args g, unsigned tm, unsigned tn) {
+  constexpr int kThreads = 64 * WM * WN * KG, MT = BM / WM / 16, NT = BN / WN / 16;
   constexpr int LA = BM * 8 / kThreads, LB = BN * 8 / kThreads;   // 16-byte pieces a thread stages
   static_assert(kThreads % 128 == 0 && BN / WN <= 128 && BM <= 256 && BN <= 256 && BM * 8 % kThreads == 0 && BN * 8 % kThreads == 0, "tile");
   extern __shared__ u8 smem[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave % WM, wn = wave / WM, r = lane & 15, grp = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), r = lane & 15, grp = lane >> 4;
+  const int wm = wave % WM, wn = wave / WM % WN, kg = wave / (WM * WN);
   // tiles of one XCD (work-groups b, b + 8, ..) are neighbours: runs of eight
   // tile rows share a column of weights in its L2
   const unsigned tiles = tm * tn, per = (tiles + 7) / 8;
@@ -121,14 +130,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
   const int ck = ((tid & 7) ^ ((tid >> 4) & 7)) * 16;
   auto step_offset = [&](int kb) { return (unsigned)(kb * 128 + ck < g.K ? kb * 128 : -ck); };
   auto stage = [&](int n, int kb, unsigned k) {   // the n-th of a thread's LA + LB pieces of step kb
-    u8* base = smem + kb % (S * U) * ((BM + BN) * 128) + wave * 1024;
+    u8* base = smem + kb % R * ((BM + BN) * 128) + wave * 1024;
     if (n < LA) __builtin_amdgcn_global_load_lds((GlbP)(ga + (oa[n < LA ? n : 0] + k)), (LdsP)(base + n * kThreads * 16), 16, 0, 0);
     else __builtin_amdgcn_global_load_lds((GlbP)(gw + (ob[n < LA ? 0 : n - LA] + k)), (LdsP)(base + BM * 128 + (n - LA) * kThreads * 16), 16, 0, 0);
   };
   // The rows' scales go through LDS four steps at a time, one row a thread: a
   // scale a lane straight from memory touched a cache line a row in every step
   // (8192 x 12288 x 4096: 524 us).
-  constexpr int kSc = S * U * (BM + BN) * 128;   // their place in LDS: two sets of [BM][4]
+  constexpr int kSc = R * (BM + BN) * 128;   // their place in LDS: two sets of [BM][4]
   static_assert(kThreads >= BM, "a thread a row");
   const bool sc4 = (KB & 3) == 0 && (g.lsa & 3) == 0 && (reinterpret_cast<uintptr_t>(g.sa) & 15) == 0;
   const float* gsa = g.sa + m0 * g.lsa;
@@ -164,7 +173,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
     for (int i = 0; i < MT; ++i) acc[j][i] = zero4();
   stage_scales(0);
 #pragma unroll
-  for (int kb = 0; kb < (S - 1) * U; ++kb) {
+  for (int kb = 0; kb < R - U; ++kb) {
     const unsigned k = step_offset(min(kb, KB - 1));
 #pragma unroll
     for (int n = 0; n < LA + LB; ++n) stage(n, kb, k);
@@ -172,28 +181,30 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
   float ws64 = 0.f;
   for (int k0 = 0; k0 < KB; k0 += U) {
     // This wave's pieces of these steps are in LDS (a barrier alone does not
-    // wait for loads to LDS): behind them are at least those of S - 2 sets.
+    // wait for loads to LDS): behind them are at least those of R - 2 U steps.
     // Every wave has read what it needs of the set before.
     // (A fence in front of the barrier would wait for all loads in flight.)
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * U * (LA + LB)) : "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((R - 2 * U) * (LA + LB)) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if ((k0 & 63) == 0) {
       ws64 = sw[min(k0 + lane, KB - 1)];   // a lane a step
       asm volatile("" : "+v"(ws64));       // (waited for here, not in every step)
     }
+    if ((k0 & 3) == 0 && k0 + 4 < KB) stage_scales((k0 >> 2) + 1);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int kb = k0 + u;
+    for (int u = 0; u < U; u += KG) {
+      const int kb = k0 + u + kg;
       if (U > 1 && kb >= KB) break;
       const float ws = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, ws64), kb & 63));
       float f[MT];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
         f[i] = ws * *reinterpret_cast<const float*>(sc + ((kb >> 2) & 1) * (BM * 16) + (kb & 3) * step_at + i * 16 * row_at);
-      const unsigned kn = step_offset(min(kb + (S - 1) * U, KB - 1));   // (behind the last step its blocks again, unused)
-      if (u == 0 && (kb & 3) == 0 && kb + 4 < KB) stage_scales((kb >> 2) + 1);
-      const u8* ta = smem + kb % (S * U) * ((BM + BN) * 128) + wm * (BM / WM) * 128;
+      unsigned kn[KG];   // (behind the last step its blocks again, unused)
+#pragma unroll
+      for (int e = 0; e < KG; ++e) kn[e] = step_offset(min(k0 + u + e + R - U, KB - 1));
+      const u8* ta = smem + kb % R * ((BM + BN) * 128) + wm * (BM / WM) * 128;
       const u8* tb = ta + (BM - wm * (BM / WM) + wn * (BN / WN)) * 128;
       Frag<T> xa[MT];
       if (kb * 128 + 128 <= g.K) {
@@ -221,9 +232,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
           // the coming loads one by one between the first products: issued at once
           // they hold the wave until the cache has taken them (480 us), spread over
           // all products the last ones come late (490; 451 like this)
-          constexpr int kEach = (LA + LB + NT * MT - 1) / (NT * MT);
+          constexpr int kAll = KG * (LA + LB), kEach = (kAll + NT * MT - 1) / (NT * MT);
 #pragma unroll
-          for (int n = q * kEach; n < (q + 1) * kEach && n < LA + LB; ++n) stage(n, kb + (S - 1) * U, kn);
+          for (int n = q * kEach; n < (q + 1) * kEach && n < kAll; ++n)
+            stage(n % (LA + LB), k0 + u + n / (LA + LB) + R - U, kn[n / (LA + LB)]);
         }
         __builtin_amdgcn_sched_barrier(0);   // (the compiler would put the fmas in front)
         if (q >= 2) {
@@ -236,6 +248,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm8_tile_kernel(const Gemm8
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // no load to LDS outlives the work-group
+  if constexpr (KG > 1) {
+    static_assert((KG - 1) * BM * BN * 4 <= R * (BM + BN) * 128, "room for the sums");
+    f32x4* part = reinterpret_cast<f32x4*>(smem) + (wave % (WM * WN)) * (NT * MT * 64) + lane;
+    __syncthreads();
+    if (kg)
+#pragma unroll
+      for (int q = 0; q < NT * MT; ++q) part[(kg - 1) * (BM * BN / 4) + q * 64] = acc[q / MT][q % MT];
+    __syncthreads();
+    if (kg) return;
+#pragma unroll
+    for (int e = 0; e < KG - 1; ++e)
+#pragma unroll
+      for (int q = 0; q < NT * MT; ++q) acc[q / MT][q % MT] += part[e * (BM * BN / 4) + q * 64];
+  }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int row = wm * (BM / WM) + i * 16 + r;
@@ -292,13 +318,13 @@ __global__ __launch_bounds__(64 * WK) void gemm8_rows_kernel(const Gemm8Args g) 
 }
 
 constexpr int kTileThreads = 512;
-template <typename T, int BM, int BN, int WM, int WN, int S, int U>
+template <typename T, int BM, int BN, int WM, int WN, int KG, int R, int U>
 hipError_t tile_go(const Gemm8Args& g, hipStream_t st) {
-  constexpr int kThreads = 64 * WM * WN, kLds = S * U * (BM + BN) * 128 + 2 * BM * 16;
-  static_assert(kThreads == kTileThreads && kLds <= 160 * 1024 && (U == 1 || U == 2 || U == 4), "LDS, sets of scales");
+  constexpr int kThreads = 64 * WM * WN * KG, kLds = R * (BM + BN) * 128 + 2 * BM * 16;
+  static_assert(kThreads == kTileThreads && kLds <= 160 * 1024 && (U == 1 || U == 2 || U == 4) && U % KG == 0 && R >= 2 * U && R - 2 * U <= 4, "LDS, sets of scales");
   const long long tm = (g.M + BM - 1) / BM, tn = (g.N + BN - 1) / BN, n = (tm * tn + 7) / 8 * 8;
   if (n > max_groups(kThreads)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm8_tile_kernel<T, BM, BN, WM, WN, S, U>), dim3((unsigned)n), dim3(kThreads), kLds, st, g, (unsigned)tm, (unsigned)tn);
+  hipLaunchKernelGGL((gemm8_tile_kernel<T, BM, BN, WM, WN, KG, R, U>), dim3((unsigned)n), dim3(kThreads), kLds, st, g, (unsigned)tm, (unsigned)tn);
   return hipGetLastError();
 }
 
@@ -312,17 +338,16 @@ hipError_t rows_go(const Gemm8Args& g, hipStream_t st) {
 
 // Tiles by the time of a round of 256 work-groups, one a CU, us for K = 4096:
 // what a shape takes is its rounds times that.  Measured, 4096 outputs, bf16:
-// 256 rows 64 x 64 12.4, 128 x 64 15.4; 512 rows 128 x 64 16.3, 64 x 64 22.8; 1024
-// rows 128 x 128 24.3, 128 x 64 29.8; 2048 rows 128 x 256 39.5, 128 x 128 45.9;
-// 8192 rows 256 x 256 131, 128 x 256 148.  fp32: 20 and 25, 28 and 40, 41 and 51,
-// 64 and 78; 256 x 256 does not fit the registers there.  Two steps a set help
-// the small tiles (64 x 64: 12.4, one step a set 13.7), whose steps are short
-// beside the meeting of the waves.
+// 256 rows 64 x 64 11.2, 64 x 128 14.0; 512 rows 64 x 128 15.0, 64 x 64 20.5; 1024
+// rows 128 x 128 24.5, 64 x 128 28.5; 2048 rows 128 x 256 40, 128 x 128 47; 8192 rows
+// 256 x 256 131, 128 x 256 148.  fp32: 17 and 23, 24 and 30, 41 and 46, 64 and 78; 256
+// x 256 does not fit the registers there.  Two smaller work-groups a CU, each
+// with fewer steps in LDS, took 41 for 2048 rows in 128 x 128.
 struct TileTime {
   int bm, bn;
   float bf16_us, f32_us;
 };
-constexpr TileTime kTiles[5] = {{64, 64, 12.4f, 20.f}, {128, 64, 16.2f, 27.f}, {128, 128, 24.4f, 41.f}, {128, 256, 39.5f, 62.f}, {256, 256, 66.f, 0.f}};
+constexpr TileTime kTiles[5] = {{64, 64, 11.f, 16.5f}, {64, 128, 15.f, 24.f}, {128, 128, 24.3f, 41.f}, {128, 256, 39.5f, 62.f}, {256, 256, 66.f, 0.f}};
 
 template <typename T> float round_us(int i) { return sizeof(T) == 2 ? kTiles[i].bf16_us : kTiles[i].f32_us; }
 long long tiles_of(const TileTime& t, long long M, long long N) { return (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn); }
@@ -345,13 +370,13 @@ template <typename T> int best_tile(long long M, long long N, float& least) {
 
 template <typename T> hipError_t tile_by(int i, const Gemm8Args& g, hipStream_t st) {
   switch (i) {
-    case 0: return tile_go<T, 64, 64, 4, 2, 3, 2>(g, st);
-    case 1: return tile_go<T, 128, 64, 4, 2, 3, 2>(g, st);
-    case 2: return tile_go<T, 128, 128, 4, 2, 3, 1>(g, st);
-    case 3: return tile_go<T, 128, 256, 2, 4, 3, 1>(g, st);
+    case 0: return tile_go<T, 64, 64, 2, 2, 2, 6, 2>(g, st);
+    case 1: return tile_go<T, 64, 128, 2, 2, 2, 6, 2>(g, st);
+    case 2: return tile_go<T, 128, 128, 4, 2, 1, 4, 1>(g, st);
+    case 3: return tile_go<T, 128, 256, 2, 4, 1, 3, 1>(g, st);
     default: break;
   }
-  if constexpr (sizeof(T) == 2) return tile_go<T, 256, 256, 4, 2, 2, 1>(g, st);
+  if constexpr (sizeof(T) == 2) return tile_go<T, 256, 256, 4, 2, 1, 2, 1>(g, st);
   return hipErrorInvalidValue;
 }
 
@@ -359,7 +384,7 @@ template <typename T>
 hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
   // Few rows: 64 outputs a work-group where those are enough for half the card
   // (12288 outputs: 12.3 us, 16 outputs 14.5), else 16 (4096 outputs: 9.0 and
-  // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 14.3, two row sets here 17.6.
+  // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 14.6, two row sets here 17.6.
   // (More outputs than a launch has work-groups for: tiles.)
   if (g.M <= 16 && g.N <= 1 << 27) return g.N >= 8192 ? rows_go<T, 4, 16>(g, st) : rows_go<T, 1, 8>(g, st);
   float one = 0.f;
