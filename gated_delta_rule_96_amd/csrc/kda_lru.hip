@@ -18,7 +18,7 @@ namespace kda {
 namespace {
 
 constexpr int kWaves = 8, kR = 16, kPart = kWaves * kR;
-constexpr int kBack = 4;   // parts that a part looks back over
+constexpr int kBack = 4;   // parts that a wave looks back over
 constexpr int kPolls = 1 << 21;   // of a wait, a few seconds
 
 // a and u of a wave's run of R tokens from token t on (the same for all
@@ -116,14 +116,63 @@ __global__ __launch_bounds__(256) void lru_fill_kernel(unsigned* ws, size_t n) {
   if (id < n % 4) ws[64 + n / 4 * 4 + id] = kNone;
 }
 
-// Outputs.  kChain: sequences of several parts.  Each work-group takes the
-// next (part, slice) by a ticket and waits for parts before its own only, all
-// of which have lower tickets: the lowest ticket that is not done waits for
-// nothing, so every wait ends, however many work-groups run at once.  The
-// first wave joins its part's runs, publishes them, and goes back through the
-// parts before until one has its state published.
-template <typename T, int NC, bool kChain, bool kFull>
+// How a part gets the state in front of it.
+//   kOne: every sequence is one part
+//   kNear, kFar: it looks back over kBack parts, or its waves over kBack each
+enum LruWay { kOne, kNear, kFar };
+
+// What the parts d0 + 1 .. d0 + kBack before a part have published (bit d of the
+// result: part d0 + d + 1 its state; bit 8 + d: its own P and H).
+template <int NC> struct LruBack {
+  unsigned in[kBack][NC];
+  unsigned long long own[kBack][NC];
+};
+template <int NC> __device__ __forceinline__ unsigned look_back(const Words& w, size_t at, int D, int parts_before, int d0, bool live, LruBack<NC>& b) {
+#pragma unroll
+  for (int d = 0; d < kBack; ++d) {
+    const size_t from = at - (size_t)min(d0 + d + 1, parts_before) * D;   // (the first part publishes its state only)
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      b.in[d][j] = __hip_atomic_load(w.into + from + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      b.own[d][j] = __hip_atomic_load(w.own + from + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  unsigned bits = 0;
+#pragma unroll
+  for (int d = 0; d < kBack; ++d) {
+    bool got = true, has = true;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+      got &= b.in[d][j] != kNone;
+      has &= b.own[d][j] != ~0ull;
+    }
+    bits |= (__all(got || !live) ? 1u << d : 0u) | (__all(has || !live) ? 256u << d : 0u);
+  }
+  return bits;
+}
+// How many parts back the nearest state is, if the parts in between have their
+// own P and H there (else 0).
+__device__ __forceinline__ int found_back(unsigned got, unsigned has) {
+  if (!got) return 0;
+  const int d = __builtin_ctz(got);
+  const unsigned between = (1u << d) - 1;
+  return (has & between) == between ? d + 1 : 0;
+}
+// The state behind a part with own (P, H) from that in front of it.
+__device__ __forceinline__ float carry_over(unsigned long long own, float h) {
+  return fmaf(__uint_as_float((unsigned)own), h, __uint_as_float((unsigned)(own >> 32)));
+}
+
+// Outputs.  kNear and kFar: each work-group takes the next (part, slice) by a
+// ticket and waits for parts before its own only, all of which have lower
+// tickets: the lowest ticket that is not done waits for nothing, so every wait
+// ends, however many work-groups run at once.  A part publishes its own (P, H),
+// goes back to the nearest part that has its state published, if the (P, H) of
+// those in between are, and carries the state over them one by one, as each of
+// them does, so that the bits do not depend on which was found.
+template <typename T, int NC, LruWay kWay, bool kFull>
 __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g, const SeqTab s, unsigned slices, void* ws) {
+  constexpr bool kChain = kWay == kNear || kWay == kFar;
   __shared__ float red[2][kWaves][64 * NC];
   __shared__ float carry[64 * NC];
   __shared__ unsigned given;
@@ -150,6 +199,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
     red[1][wave][lane * NC + j] = H[j];
   }
   __syncthreads();
+  const size_t at = (size_t)item * g.D + l.cl;
   if (wave == 0) {
 #pragma unroll
     for (int q = 1; q < kWaves; ++q)
@@ -159,44 +209,21 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
         H[j] = fmaf(f, H[j], red[1][q][lane * NC + j]);
         P[j] *= f;
       }
-    if (!kChain || p.first) {
+    if (kChain && !p.first && !p.last && l.live)
 #pragma unroll
-      for (int j = 0; j < NC; ++j) h[j] = g.h0 ? g.h0[(size_t)p.n * g.D + l.cl + j] : 0.f;
-    } else {
-      const size_t at = (size_t)item * g.D + l.cl;
-      if (!p.last && l.live)
+      for (int j = 0; j < NC; ++j)
+        __hip_atomic_store(w.own + at + j, (unsigned long long)word_of(H[j]) << 32 | word_of(P[j]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (kWay == kOne || p.first) {
 #pragma unroll
-        for (int j = 0; j < NC; ++j)
-          __hip_atomic_store(w.own + at + j, (unsigned long long)word_of(H[j]) << 32 | word_of(P[j]), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      // From the nearest of the last kBack parts whose state is there, if the
-      // (P, H) of those in between are: the state is carried over them one by one,
-      // as each of them does, so that the bits do not depend on which was found.
-      const int parts_before = p.t0 / kPart;
-      unsigned in[kBack][NC];
-      unsigned long long ow[kBack][NC];
+    for (int j = 0; j < NC; ++j) h[j] = g.h0 ? g.h0[(size_t)p.n * g.D + l.cl + j] : 0.f;
+  } else if (kWay == kNear) {
+    if (wave == 0) {
+      LruBack<NC> b;
       int found = 0;
       for (int poll = 0;; ++poll) {
-#pragma unroll
-        for (int d = 0; d < kBack; ++d) {
-          const size_t from = at - (size_t)min(d + 1, parts_before) * g.D;   // (the first part publishes its state only)
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            in[d][j] = __hip_atomic_load(w.into + from + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            ow[d][j] = __hip_atomic_load(w.own + from + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          }
-        }
-        bool open = true;
-#pragma unroll
-        for (int d = 0; d < kBack; ++d) {
-          bool got = true, has = true;
-#pragma unroll
-          for (int j = 0; j < NC; ++j) {
-            got &= in[d][j] != kNone;
-            has &= ow[d][j] != ~0ull;
-          }
-          if (open && !found && __all(got || !l.live)) found = d + 1;
-          open = open && __all(has || !l.live);
-        }
+        const unsigned bits = look_back<NC>(w, at, g.D, p.t0 / kPart, 0, l.live, b);
+        found = found_back(bits & 255, bits >> 8);
         if (found || poll == kPolls) break;
         __builtin_amdgcn_s_sleep(1);
       }
@@ -207,22 +234,57 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
       for (int d = kBack - 1; d >= 0; --d)
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-          if (d + 1 == found) h[j] = __uint_as_float(in[d][j]);
-          else if (d + 1 < found) h[j] = fmaf(__uint_as_float((unsigned)ow[d][j]), h[j], __uint_as_float((unsigned)(ow[d][j] >> 32)));
+          if (d + 1 == found) h[j] = __uint_as_float(b.in[d][j]);
+          else if (d + 1 < found) h[j] = carry_over(b.own[d][j], h[j]);
         }
     }
+  } else if (kWay == kFar) {
+    __shared__ unsigned long long far[kWaves * kBack][64 * NC];
+    __shared__ unsigned seen[2][kWaves];
+    LruBack<NC> b;
+    int found = 0;
+    for (int poll = 0;; ++poll) {   // (two sets of bits by turns: one barrier a poll is enough)
+      const unsigned bits = look_back<NC>(w, at, g.D, p.t0 / kPart, wave * kBack, l.live, b);
+      if (lane == 0) seen[poll & 1][wave] = bits;
+      __syncthreads();
+      unsigned got = 0, has = 0;
+#pragma unroll
+      for (int q = 0; q < kWaves; ++q) {
+        const unsigned m = __builtin_amdgcn_readfirstlane(seen[poll & 1][q]);
+        got |= (m & 255) << (q * kBack);
+        has |= (m >> 8) << (q * kBack);
+      }
+      found = found_back(got, has);
+      if (found || poll == kPolls) break;
+      __builtin_amdgcn_s_sleep(1);
+    }
+#pragma unroll
+    for (int d = 0; d < kBack; ++d)
+      if (wave * kBack + d < found)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) far[wave * kBack + d][lane * NC + j] = wave * kBack + d + 1 == found ? b.in[d][j] : b.own[d][j];
+    __syncthreads();
+    if (wave == 0) {
+#pragma unroll
+      for (int j = 0; j < NC; ++j) h[j] = found ? __uint_as_float((unsigned)far[max(found, 1) - 1][lane * NC + j]) : __builtin_nanf("");
+#pragma unroll 4
+      for (int d = found - 2; d >= 0; --d)
+#pragma unroll
+        for (int j = 0; j < NC; ++j) h[j] = carry_over(far[d][lane * NC + j], h[j]);
+    }
+  }
+  if (wave == 0) {
 #pragma unroll
     for (int j = 0; j < NC; ++j) {
       carry[lane * NC + j] = h[j];
-      const float end = fmaf(P[j], h[j], H[j]);
+      const float behind = fmaf(P[j], h[j], H[j]);
       if (!l.live) continue;
       if (kChain && !p.last)
-        __hip_atomic_store(w.into + (size_t)item * g.D + l.c + j, word_of(end), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (p.last && g.ht) g.ht[(size_t)p.n * g.D + l.c + j] = end;
+        __hip_atomic_store(w.into + (size_t)item * g.D + l.c + j, word_of(behind), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (p.last && g.ht) g.ht[(size_t)p.n * g.D + l.c + j] = behind;
     }
   }
   __syncthreads();
-  if (!l.live) return;
 #pragma unroll
   for (int j = 0; j < NC; ++j) h[j] = carry[lane * NC + j];
   for (int q = 0; q < wave; ++q)
@@ -236,7 +298,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
 #pragma unroll
     for (int j = 0; j < NC; ++j) h[j] = fmaf(a[k][j], h[j], u[k][j]);
     o.set(h);
-    if (t + k < p.t1) *reinterpret_cast<LruPack<T, NC>*>(y + (long long)k * g.D + l.c) = o;
+    if (l.live && t + k < p.t1) *reinterpret_cast<LruPack<T, NC>*>(y + (long long)k * g.D + l.c) = o;
   }
 }
 
@@ -287,13 +349,18 @@ hipError_t fwd_go(const LruArgs& a, const int* cu, int N, int B, int T_, void* w
   for (int n = 0; n < end;) {
     SeqTab s;
     n = make_seq_tab(s, cu, N, n, B, T_, kPart);
+    const unsigned seqs = (unsigned)(s.n ? s.n : B);
     const dim3 grid((unsigned)s.items * slices), th(64 * kWaves);
-    if (s.items == (s.n ? s.n : B)) {   // no sequence has a second part
-      hipLaunchKernelGGL((lru_out_kernel<T, NC, false, kFull>), grid, th, 0, st, a, s, slices, ws);
+    if ((unsigned)s.items == seqs) {   // no sequence has a second part
+      hipLaunchKernelGGL((lru_out_kernel<T, NC, kOne, kFull>), grid, th, 0, st, a, s, slices, ws);
     } else {
       const size_t words = (size_t)s.items * a.D * 3, groups = (words + 1023) / 1024;
       hipLaunchKernelGGL(lru_fill_kernel, dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, st, static_cast<unsigned*>(ws), words);
-      hipLaunchKernelGGL((lru_out_kernel<T, NC, true, kFull>), grid, th, 0, st, a, s, slices, ws);
+      // Few chains at once wait for their states, hop by hop (65536 tokens of 512
+      // channels: 87 us by kFar, 167 by kNear; 1024: 157 and 180); with many the
+      // words read count (2048: 269 and 244; 4096: 492 and 425).
+      if (seqs * slices <= 8) hipLaunchKernelGGL((lru_out_kernel<T, NC, kFar, kFull>), grid, th, 0, st, a, s, slices, ws);
+      else hipLaunchKernelGGL((lru_out_kernel<T, NC, kNear, kFull>), grid, th, 0, st, a, s, slices, ws);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

@@ -137,17 +137,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_part_kernel(const LruB
 }
 
 // What enters a sequence's parts: states over H, e from the right over K.  The
-// 16 waves of a work-group each take a run of the parts of 64 channels, join
-// their runs in LDS and walk them again.
-constexpr int kChainWaves = 16;
+// 64 quarters of the 16 waves of a work-group each take a run of the parts of 16
+// channels, join their runs in LDS and walk them again.
+constexpr int kChainWaves = 16, kChainRuns = 4 * kChainWaves, kChainCh = 16;
 __global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const LruBwdArgs b, const SeqTab s, float* seg) {
-  __shared__ float red[3][kChainWaves][64];
-  const int D = b.f.D, blocks = (D + 63) / 64, li = blockIdx.x / blocks, lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), c0 = (blockIdx.x - li * blocks) * 64 + lane;
+  __shared__ float red[3][kChainRuns][kChainCh];
+  const int D = b.f.D, blocks = (D + kChainCh - 1) / kChainCh, li = blockIdx.x / blocks;
+  const int run = threadIdx.x / kChainCh, lane = threadIdx.x % kChainCh, c0 = (blockIdx.x - li * blocks) * kChainCh + lane;
   const bool live = c0 < D;
   const int c = live ? c0 : 0, n = s.n0 + li;
   const int i0 = s.n ? s.cc[li] : li * s.parts, i1 = s.n ? s.cc[li + 1] : i0 + s.parts;
-  const int per = (i1 - i0 + kChainWaves - 1) / kChainWaves, lo = min(i0 + wave * per, i1), hi = min(lo + per, i1);
+  const int per = (i1 - i0 + kChainRuns - 1) / kChainRuns, lo = min(i0 + run * per, i1), hi = min(lo + per, i1);
   float* at = seg + c;
   float P = 1.f, H = 0.f, K = 0.f;
 #pragma unroll 4
@@ -158,13 +158,13 @@ __global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const L
     K = fmaf(P, q[2 * D], K);
     P *= p;
   }
-  red[0][wave][lane] = P;
-  red[1][wave][lane] = H;
-  red[2][wave][lane] = K;
+  red[0][run][lane] = P;
+  red[1][run][lane] = H;
+  red[2][run][lane] = K;
   __syncthreads();
   float h = b.f.h0 ? b.f.h0[(size_t)n * D + c] : 0.f, e = b.dht ? b.dht[(size_t)n * D + c] : 0.f;
-  for (int q = 0; q < wave; ++q) h = fmaf(red[0][q][lane], h, red[1][q][lane]);
-  for (int q = kChainWaves - 1; q > wave; --q) e = fmaf(red[0][q][lane], e, red[2][q][lane]);
+  for (int q = 0; q < run; ++q) h = fmaf(red[0][q][lane], h, red[1][q][lane]);
+  for (int q = kChainRuns - 1; q > run; --q) e = fmaf(red[0][q][lane], e, red[2][q][lane]);
   if (!live) return;
 #pragma unroll 4
   for (int i = lo; i < hi; ++i) {
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const L
     q[2 * D] = e;
     e = fmaf(p, e, v);
   }
-  if (b.dh0 && wave == 0) b.dh0[(size_t)n * D + c] = e;
+  if (b.dh0 && run == 0) b.dh0[(size_t)n * D + c] = e;
 }
 
 // Gradients.  seg null: every sequence is one part.  dcp [items][D]: every
@@ -312,8 +312,8 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
   const int D = b.f.D;
   const unsigned slices = (unsigned)((D + 64 * NC - 1) / (64 * NC));
   if (!seq_tabs_fit(cu, N, B, T_, kPart, max_groups(64 * kWaves) / slices)) return hipErrorInvalidConfiguration;
-  if (!cu && T_ > kPart && (long long)B * ((D + 63) / 64) > max_groups(64 * kChainWaves)) return hipErrorInvalidConfiguration;
-  if (cu && (long long)kMaxVarSeq * ((D + 63) / 64) > max_groups(64 * kChainWaves)) return hipErrorInvalidConfiguration;
+  const long long blocks = (D + kChainCh - 1) / kChainCh, seqs_most = cu ? (N < kMaxVarSeq ? N : kMaxVarSeq) : B;
+  if (T_ > kPart && seqs_most * blocks > max_groups(64 * kChainWaves)) return hipErrorInvalidConfiguration;
   float* dcp = b.dc ? ws : nullptr;
   float* seg = ws + all_items(cu != nullptr, N, B, T_) * D;
   size_t rows = 0;
@@ -326,7 +326,7 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
     const bool one = s.items == seqs;   // no sequence has a second part
     if (!one) {
       hipLaunchKernelGGL((lru_bwd_part_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg);
-      hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)((D + 63) / 64) * (unsigned)seqs), dim3(64 * kChainWaves), 0, st, b, s, seg);
+      hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)(blocks * seqs)), dim3(64 * kChainWaves), 0, st, b, s, seg);
     }
     hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, one ? nullptr : seg, dcp ? dcp + rows * D : nullptr);
     const hipError_t e = hipGetLastError();
