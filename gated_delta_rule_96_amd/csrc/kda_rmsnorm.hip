@@ -10,9 +10,9 @@
 // Backward, u = h r:  dx = r (w dy - u mean(w dy u)) + dh;  dw = sum dy u.
 //
 // Bound by HBM: one pass, every row read and written once.  A row is held in
-// registers by one wave (up to 2048 channels), four or sixteen, eight
-// neighbouring channels a lane, so 16 lanes hold the 128 channels of a scale
-// and its maximum stays inside a DPP row.  All arithmetic is fp32 up to the
+// registers by part of a wave (up to 256 channels), a wave (2048), four or
+// sixteen, eight neighbouring channels a lane, so 16 lanes hold the 128 channels
+// of a scale and its maximum stays inside a DPP row.  All arithmetic is fp32 up to the
 // one rounding of each output.  65536 x 4096 bf16 with the residual to 8 bits 322
 // us (7 bytes a channel, 5.9 TB/s), 8191 x 2056 with an fp32 stream 39 us (5.2),
 // gradients of 32768 x 4096 bf16 with dw 192 us (5.6); 256 rows are bound by the
@@ -44,29 +44,31 @@ template <> struct Raw8<float> {
   __device__ __forceinline__ float at(int i) const { return i < 4 ? a[i] : b[i - 4]; }
 };
 
-// Sum over a wave's 64 lanes, in every lane.
-__device__ __forceinline__ float wave_sum(float x) {
+// L: the lanes that hold a row, 8 to 64 of a wave or those of several waves.
+// Sum over a row's lanes of this wave, in all of them.
+template <int L> __device__ __forceinline__ float lane_sum(float x) {
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) x += __shfl_xor(x, off);
+  for (int off = 1; off < (L < 64 ? L : 64); off <<= 1) x += __shfl_xor(x, off);
   return x;
 }
 
-// Largest x >= 0 of each 16 lanes, in all of them.
-__device__ __forceinline__ float max16(float x) {
+// Largest x >= 0 of each 16 lanes (of 8 with L = 8), in all of them.
+template <int L> __device__ __forceinline__ float max16(float x) {
   x = fmaxf(x, dpp_f<0xB1>(x));    // quad_perm [1,0,3,2]
   x = fmaxf(x, dpp_f<0x4E>(x));    // quad_perm [2,3,0,1]
   x = fmaxf(x, dpp_f<0x141>(x));   // row_half_mirror
-  return fmaxf(x, dpp_f<0x140>(x));   // row_mirror
+  return L == 8 ? x : fmaxf(x, dpp_f<0x140>(x));   // row_mirror
 }
 
 // Sums over the W waves that share a row.  `red` has two sets of slots, used
 // by turns, so one barrier a row is enough: a wave overwrites a set only
 // behind the next row's barrier, which every wave passes after its reads.
-template <int W, int N>
-__device__ __forceinline__ void row_sum(float (&s)[N], float (*red)[N][W], int turn, int wave) {
+constexpr int waves_of(int L) { return L > 64 ? L / 64 : 1; }
+template <int L, int N>
+__device__ __forceinline__ void row_sum(float (&s)[N], float (*red)[N][waves_of(L)], int turn, int wave) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) s[k] = wave_sum(s[k]);
-  if (W == 1) return;
+  for (int k = 0; k < N; ++k) s[k] = lane_sum<L>(s[k]);
+  if (L <= 64) return;
   if ((threadIdx.x & 63) == 0)
 #pragma unroll
     for (int k = 0; k < N; ++k) red[turn][k][wave] = s[k];
@@ -75,39 +77,43 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float (*red)[N][W], int t
   for (int k = 0; k < N; ++k) {
     s[k] = 0.f;
 #pragma unroll
-    for (int q = 0; q < W; ++q) s[k] += red[turn][k][q];
+    for (int q = 0; q < waves_of(L); ++q) s[k] += red[turn][k][q];
   }
 }
 
-// Vector j of a lane: channels 8 (j 64 W + lane) .. + 7 (lane of the W waves).
-template <int W> __device__ __forceinline__ int channel(int j, int lane) { return 8 * (j * (64 * W) + lane); }
+// Vector j of a row's lane: channels 8 (j L + lane) .. + 7.
+template <int L> __device__ __forceinline__ int channel(int j, int lane) { return 8 * (j * L + lane); }
 
-template <int NV, int W> __device__ __forceinline__ void load_weights(const float* w, int D, int lane, float (&wv)[NV][8]) {
+template <int NV, int L> __device__ __forceinline__ void load_weights(const float* w, int D, int lane, float (&wv)[NV][8]) {
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = channel<W>(j, lane);
+    const int c = channel<L>(j, lane);
 #pragma unroll
     for (int i = 0; i < 8; ++i) wv[j][i] = 1.f;
     if (w && c < D) Rows<float, 8>::load(w + c, wv[j]);
   }
 }
 
+// Threads of a work-group, and the rows it holds at once.
+constexpr int group_threads(int L) { return L > kThreads ? L : kThreads; }
+constexpr int group_rows(int L) { return group_threads(L) / L; }
+
 // T: type of x and of y; TH: type of the stream (res and h).
-template <typename T, typename TH, bool kRes, bool kFp8, int NV, int W>
-__global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_fwd_kernel(const NormArgs a, long long groups) {
-  __shared__ float red[2][1][W];
-  constexpr int kPer = W >= 4 ? 1 : kThreads / 64;   // rows a work-group holds at once
-  const int lane = W == 1 ? (threadIdx.x & 63) : threadIdx.x, wave = threadIdx.x >> 6, D = a.D;
+template <typename T, typename TH, bool kRes, bool kFp8, int NV, int L>
+__global__ __launch_bounds__(group_threads(L)) void norm_fwd_kernel(const NormArgs a, long long groups) {
+  __shared__ float red[2][1][waves_of(L)];
+  constexpr int kPer = group_rows(L);
+  const int lane = threadIdx.x % L, wave = threadIdx.x >> 6, D = a.D;
   const float inv = 1.f / (float)D;
   float w[NV][8];
-  load_weights<NV, W>(a.w, D, lane, w);
+  load_weights<NV, L>(a.w, D, lane, w);
   int turn = 0;
-  for (long long m = (long long)blockIdx.x * kPer + (W == 1 ? wave : 0); m < a.rows; m += groups * kPer, turn ^= 1) {
+  for (long long m = (long long)blockIdx.x * kPer + threadIdx.x / L; m < a.rows; m += groups * kPer, turn ^= 1) {
     Raw8<T> x[NV];
     Raw8<TH> r[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = channel<W>(j, lane);
+      const int c = channel<L>(j, lane);
       if (c < D) {
         x[j].load((const T*)a.x + m * a.ldx + c);
         if (kRes) r[j].load((const TH*)a.res + m * a.ldr + c);
@@ -116,7 +122,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_fwd_kernel(con
     float h[NV][8], sq[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = channel<W>(j, lane);
+      const int c = channel<L>(j, lane);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[j][i] = 0.f;
       if (c < D) {
@@ -127,11 +133,11 @@ __global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_fwd_kernel(con
 #pragma unroll
       for (int i = 0; i < 8; ++i) sq[0] = fmaf(h[j][i] * inv, h[j][i], sq[0]);
     }
-    row_sum<W, 1>(sq, red, turn, wave);
+    row_sum<L, 1>(sq, red, turn, wave);
     const float rn = 1.f / sqrtf(sq[0] + a.eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = channel<W>(j, lane);
+      const int c = channel<L>(j, lane);
       float n[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) n[i] = h[j][i] * rn * w[j][i];
@@ -139,7 +145,7 @@ __global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_fwd_kernel(con
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(n[i]));
-        top = max16(top);   // (lanes past D hold zeros)
+        top = max16<L>(top);   // (lanes past D hold zeros)
         const bool live = top >= kBlockMin;
         const float q = live ? kE4m3Max / top : 1.f;
 #pragma unroll
@@ -159,29 +165,28 @@ __global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_fwd_kernel(con
   }
 }
 
-// Gradients.  T: type of h, dh and dx; TG: type of dy.  Each row holder (one
-// wave, or a work-group) walks its rows and keeps the sums of dw of its
-// channels; they are a partial row of the workspace.
-template <typename T, typename TG, int NV, int W>
-__global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_bwd_kernel(const NormArgs a, long long groups) {
-  __shared__ float red[2][2][W];
-  constexpr int kPer = W >= 4 ? 1 : kThreads / 64;
-  const int lane = W == 1 ? (threadIdx.x & 63) : threadIdx.x, wave = threadIdx.x >> 6, D = a.D;
+// Gradients.  T: type of h, dh and dx; TG: type of dy.  The lanes that hold a
+// row walk their rows and keep the sums of dw of their channels; they are
+// partial rows of the workspace.
+template <typename T, typename TG, int NV, int L>
+__global__ __launch_bounds__(group_threads(L)) void norm_bwd_kernel(const NormArgs a, long long groups) {
+  __shared__ float red[2][2][waves_of(L)];
+  constexpr int kPer = group_rows(L);
+  const int lane = threadIdx.x % L, wave = threadIdx.x >> 6, D = a.D;
   const float inv = 1.f / (float)D;
   float w[NV][8], dw[NV][8];
-  load_weights<NV, W>(a.w, D, lane, w);
+  load_weights<NV, L>(a.w, D, lane, w);
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
-  const long long holder = (long long)blockIdx.x * kPer + (W == 1 ? wave : 0);
   int turn = 0;
-  for (long long m = holder; m < a.rows; m += groups * kPer, turn ^= 1) {
+  for (long long m = (long long)blockIdx.x * kPer + threadIdx.x / L; m < a.rows; m += groups * kPer, turn ^= 1) {
     Raw8<T> h[NV], s[NV];
     Raw8<TG> g[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = channel<W>(j, lane);
+      const int c = channel<L>(j, lane);
       if (c < D) {
         h[j].load((const T*)a.x + m * a.ldx + c);
         g[j].load((const TG*)a.dy + m * D + c);
@@ -191,19 +196,19 @@ __global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_bwd_kernel(con
     float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (channel<W>(j, lane) < D)
+      if (channel<L>(j, lane) < D)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = h[j].at(i) * inv;
           sum[0] = fmaf(v, h[j].at(i), sum[0]);
           sum[1] = fmaf(g[j].at(i) * w[j][i], v, sum[1]);
         }
-    row_sum<W, 2>(sum, red, turn, wave);
+    row_sum<L, 2>(sum, red, turn, wave);
     // dx = r (w dy - u mean(w dy h) r): no power of r alone
     const float rn = 1.f / sqrtf(sum[0] + a.eps), k = sum[1] * rn;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = channel<W>(j, lane);
+      const int c = channel<L>(j, lane);
       if (c >= D) continue;
       float o[8];
 #pragma unroll
@@ -217,9 +222,18 @@ __global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_bwd_kernel(con
     }
   }
   if (!a.part) return;
+  // one partial row a wave (a work-group where several waves hold a row)
+  const long long holder = L > 64 ? blockIdx.x : (long long)blockIdx.x * (kThreads / 64) + wave;
+#pragma unroll
+  for (int off = L; off < 64; off <<= 1)
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) dw[j][i] += __shfl_xor(dw[j][i], off);
+  if ((threadIdx.x & 63) >= L) return;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    const int c = channel<W>(j, lane);
+    const int c = channel<L>(j, lane);
     if (c < D) {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -228,37 +242,42 @@ __global__ __launch_bounds__(W == 16 ? 1024 : kThreads) void norm_bwd_kernel(con
   }
 }
 
-// Work-groups at most.  Forward: a row (four, of up to 2048 channels) each, as
-// the next row's loads then come from another work-group while this one sums
-// (64K rows of 4096 to 8 bits: 328 us; 8192 work-groups 356, 2048 386); rows of
+// Work-groups at most.  Forward: a row (of up to 2048 channels four and more)
+// each, as the next row's loads then come from another work-group while this one
+// sums (64K rows of 4096 to 8 bits: 328 us; 8192 work-groups 356, 2048 386); rows of
 // sixteen waves leave no room for another and walk on (8192 rows of 16384: 169;
 // a row each 176).  Backward, where each keeps a partial row of dw (64K rows of
 // 4096: 380 us; 1024 448, 256 460).
 constexpr int kBwdGroups = 512;
 int fwd_groups(int D) { return D <= 8192 ? 1 << 20 : 2048; }
 
-// Waves that hold a row of D channels.
-int row_waves(int D) { return D <= 2048 ? 1 : D <= 8192 ? 4 : 16; }
+// Lanes that hold a row of D channels, and their vectors of eight.  Short rows
+// share a wave (2^20 rows of 64 to 8 bits: 55 us, a wave each 354).
+int row_lanes(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : D <= 2048 ? 64 : D <= 8192 ? 256 : 1024; }
 unsigned norm_groups(long long rows, int D, int most) {
-  const int per = row_waves(D) >= 4 ? 1 : kThreads / 64;
+  const int per = group_rows(row_lanes(D));
   const long long g = (rows + per - 1) / per;
   return (unsigned)(g < most ? g : most);
 }
 long long part_rows(long long rows, int D) {
-  return (long long)norm_groups(rows, D, kBwdGroups) * (row_waves(D) >= 4 ? 1 : kThreads / 64);
+  return (long long)norm_groups(rows, D, kBwdGroups) * (row_lanes(D) > 64 ? 1 : kThreads / 64);
 }
 
 // The instance for rows of D channels.
-#define KDA_NORM_BY_WIDTH(kernel, ...)                                                                           \
-  do {                                                                                                           \
-    const dim3 grid(groups), th(row_waves(a.D) == 16 ? 1024 : kThreads);                                         \
-    if (a.D <= 512) hipLaunchKernelGGL((kernel<__VA_ARGS__, 1, 1>), grid, th, 0, st, a, (long long)groups);      \
-    else if (a.D <= 1024) hipLaunchKernelGGL((kernel<__VA_ARGS__, 2, 1>), grid, th, 0, st, a, (long long)groups); \
-    else if (a.D <= 2048) hipLaunchKernelGGL((kernel<__VA_ARGS__, 4, 1>), grid, th, 0, st, a, (long long)groups); \
-    else if (a.D <= 4096) hipLaunchKernelGGL((kernel<__VA_ARGS__, 2, 4>), grid, th, 0, st, a, (long long)groups); \
-    else if (a.D <= 8192) hipLaunchKernelGGL((kernel<__VA_ARGS__, 4, 4>), grid, th, 0, st, a, (long long)groups); \
-    else hipLaunchKernelGGL((kernel<__VA_ARGS__, 2, 16>), grid, th, 0, st, a, (long long)groups);                 \
-    return hipGetLastError();                                                                                    \
+#define KDA_NORM_LAUNCH(kernel, ...) hipLaunchKernelGGL((kernel<__VA_ARGS__>), grid, th, 0, st, a, (long long)groups)
+#define KDA_NORM_BY_WIDTH(kernel, ...)                                    \
+  do {                                                                    \
+    const dim3 grid(groups), th(group_threads(row_lanes(a.D)));           \
+    if (a.D <= 64) KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 1, 8);            \
+    else if (a.D <= 128) KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 1, 16);     \
+    else if (a.D <= 256) KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 1, 32);     \
+    else if (a.D <= 512) KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 1, 64);     \
+    else if (a.D <= 1024) KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 2, 64);    \
+    else if (a.D <= 2048) KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 4, 64);    \
+    else if (a.D <= 4096) KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 2, 256);   \
+    else if (a.D <= 8192) KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 4, 256);   \
+    else KDA_NORM_LAUNCH(kernel, __VA_ARGS__, 2, 1024);                   \
+    return hipGetLastError();                                             \
   } while (0)
 
 template <typename T, typename TH, bool kRes, bool kFp8>

@@ -181,3 +181,38 @@ def test_refusals():
         kda.add_rms_norm(x, sum_out=x)
     with pytest.raises(TypeError, match="dh"):
         kda.add_rms_norm_bwd(x, None, x.clone(), x.float())
+
+
+@pytest.mark.parametrize("D", [8, 24, 56, 64, 72, 128, 136, 248, 256, 264])
+def test_rows_that_share_a_wave(D):
+    # more and fewer rows than a work-group holds; a row that is not finite leaves
+    # its neighbours alone; the gradients of rows that meet in one partial sum
+    say(f"short rows D={D}")
+    r = np.random.default_rng(D + 2)
+    for rows in (3, 37, 2500):
+        x, s, g = (dev(r.standard_normal((rows, D)), BF) for _ in range(3))
+        w = dev(1 + 0.2 * r.standard_normal(D))
+        (y8, sc), h = kda.add_rms_norm(x, s, w, eps=EPS, fp8=True)
+        y, _ = kda.add_rms_norm(x, s, w, eps=EPS)
+        n = block.rms_norm(f64(h), f64(w), EPS)
+        check("y", y, n, 36 * U * np.abs(n), BF)
+        check8(y8, sc, n)
+        for a in (0, rows - 1):   # a row alone has the same bits
+            (one8, onesc), _ = kda.add_rms_norm(x[a:a + 1], s[a:a + 1], w, eps=EPS, fp8=True)
+            assert torch.equal(one8.view(torch.uint8), y8[a:a + 1].view(torch.uint8)) and torch.equal(onesc, sc[a:a + 1])
+        bad = x.clone()
+        bad[1, D - 1] = float("nan")
+        (b8, bsc), _ = kda.add_rms_norm(bad, s, w, eps=EPS, fp8=True)
+        keep = [m for m in range(rows) if m != 1]
+        assert torch.isnan(b8[1].float()).all()
+        assert torch.equal(b8[keep].view(torch.uint8), y8[keep].view(torch.uint8)) and torch.equal(bsc[keep], sc[keep])
+        got = kda.add_rms_norm_bwd(h, w, g, None, eps=EPS)
+        again = kda.add_rms_norm_bwd(h, w, g, None, eps=EPS)
+        x64, g64 = f64(h), f64(g)
+        dx, dw = block.rms_norm_bwd(x64, f64(w), g64, None, EPS)
+        rr = 1 / np.sqrt((x64 * x64).mean(1, keepdims=True) + EPS)
+        gw = np.abs(g64 * f64(w))
+        m1 = (gw * np.abs(x64)).mean(1, keepdims=True)
+        check("dx", got["dx"], dx, 40 * U * rr * gw + 140 * U * np.abs(x64) * rr ** 3 * m1 + 2 * U * np.abs(dx), BF)
+        check("dw", got["dw"], dw, (40 + rows / HOLDERS + 1) * U * np.abs(g64 * x64 * rr).sum(0), F32)
+        assert torch.equal(got["dx"], again["dx"]) and torch.equal(got["dw"], again["dw"])
