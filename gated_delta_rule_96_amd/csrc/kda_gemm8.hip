@@ -271,15 +271,19 @@ __global__ __launch_bounds__(64 * WM * WN * KG, 2) void gemm8_tile_kernel(const 
   }
 }
 
-// ---------------------------------------------------------------- few rows
-// Up to 16 rows: bound by the weights' bytes.  A work-group takes 16 NT outputs
-// of every row; its WK waves take every WK-th block of K straight from memory
-// and are joined through LDS.
+// ---------------------------------------------------------------- few outputs
+// 16 rows and 16 NT outputs a work-group; its WK waves take every WK-th block of
+// K straight from memory and are joined through LDS.
 template <typename T, int NT, int WK>
-__global__ __launch_bounds__(64 * WK) void gemm8_rows_kernel(const Gemm8Args g) {
+__global__ __launch_bounds__(64 * WK) void gemm8_rows_kernel(const Gemm8Args g, unsigned tn) {
   __shared__ f32x4 part[WK][NT][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, grp = lane >> 4;
-  const int n0 = blockIdx.x * (16 * NT), KB = (g.K + 127) / 128, cols = min(16 * NT, g.N - n0), m = min(r, (int)g.M - 1);
+  const unsigned rb = blockIdx.x / tn;
+  const long long m0 = 16LL * rb;
+  const int n0 = (int)(blockIdx.x - rb * tn) * (16 * NT), KB = (g.K + 127) / 128, cols = min(16 * NT, g.N - n0);
+  const int rows = (int)min(16LL, g.M - m0), m = min(r, rows - 1);
+  const u8* ga = g.a + m0 * g.lda;
+  const float* gsa = g.sa + m0 * g.lsa;
   const u8* gw = g.w + (size_t)n0 * g.K;
   const float* sw = g.sw + (size_t)(n0 / 128) * KB;
   unsigned ow[NT];   // (rows past the last re-read that one)
@@ -297,8 +301,8 @@ __global__ __launch_bounds__(64 * WK) void gemm8_rows_kernel(const Gemm8Args g) 
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       wb[j].set(in0 ? *reinterpret_cast<const i32x4*>(gw + (ow[j] + k)) : z, in1 ? *reinterpret_cast<const i32x4*>(gw + (ow[j] + k + 64)) : z);
-    xa.set(in0 ? *reinterpret_cast<const i32x4*>(g.a + (oa + k)) : z, in1 ? *reinterpret_cast<const i32x4*>(g.a + (oa + k + 64)) : z);
-    const float f = g.sa[os + (unsigned)kb] * sw[kb];
+    xa.set(in0 ? *reinterpret_cast<const i32x4*>(ga + (oa + k)) : z, in1 ? *reinterpret_cast<const i32x4*>(ga + (oa + k + 64)) : z);
+    const float f = gsa[os + (unsigned)kb] * sw[kb];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       const f32x4 p = mma128(wb[j], xa);
@@ -313,7 +317,7 @@ __global__ __launch_bounds__(64 * WK) void gemm8_rows_kernel(const Gemm8Args g) 
     f32x4 v = part[0][j][lane];
 #pragma unroll
     for (int k = 1; k < WK; ++k) v += part[k][j][lane];
-    if (r < g.M) store_out<T>(g, r, n0 + j * 16 + 4 * grp, v);
+    if (r < rows) store_out<T>(g, m0 + r, n0 + j * 16 + 4 * grp, v);
   }
 }
 
@@ -330,9 +334,9 @@ hipError_t tile_go(const Gemm8Args& g, hipStream_t st) {
 
 template <typename T, int NT, int WK>
 hipError_t rows_go(const Gemm8Args& g, hipStream_t st) {
-  const long long n = (g.N + 16 * NT - 1) / (16 * NT);
+  const long long tn = (g.N + 16 * NT - 1) / (16 * NT), n = tn * ((g.M + 15) / 16);
   if (n > max_groups(64 * WK)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((gemm8_rows_kernel<T, NT, WK>), dim3((unsigned)n), dim3(64 * WK), 0, st, g);
+  hipLaunchKernelGGL((gemm8_rows_kernel<T, NT, WK>), dim3((unsigned)n), dim3(64 * WK), 0, st, g, (unsigned)tn);
   return hipGetLastError();
 }
 
@@ -382,11 +386,15 @@ template <typename T> hipError_t tile_by(int i, const Gemm8Args& g, hipStream_t 
 
 template <typename T>
 hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
-  // Few rows: 64 outputs a work-group where those are enough for half the card
-  // (12288 outputs: 12.3 us, 16 outputs 14.5), else 16 (4096 outputs: 9.0 and
-  // 10.5).  32 rows of 12288 outputs: 64 x 64 tiles 14.6, two row sets here 17.6.
-  // (More outputs than a launch has work-groups for: tiles.)
-  if (g.M <= 16 && g.N <= 1 << 27) return g.N >= 8192 ? rows_go<T, 4, 16>(g, st) : rows_go<T, 1, 8>(g, st);
+  // Few outputs: 16 rows and 16 or 32 columns a work-group where those are no
+  // more than the CUs (64 x 1024 x 4096: 8.7 us, 64 x 64 tiles 10.7, in fp32 8.9 and
+  // 15.6; 64 x 2048: 9.0 and 10.8, 9.4 and 15.8; 16 x 8192: 9.6 and 11.6).  Few rows of
+  // more outputs: 64 columns, so that the weights come in longer runs (12288
+  // outputs: 13.6, 32 columns 14.3, 16 columns 14.5).
+  const long long rb = (g.M + 15) / 16;
+  if (rb * ((g.N + 15) / 16) <= 256) return rows_go<T, 1, 8>(g, st);
+  if (rb * ((g.N + 31) / 32) <= 256) return rows_go<T, 2, 8>(g, st);
+  if (g.M <= 16 && g.N <= 1 << 27) return rows_go<T, 4, 16>(g, st);   // (beyond, more work-groups than a launch has)
   float one = 0.f;
   int main_tile = best_tile<T>(g.M, g.N, one), rest_tile = 0;
   // Where a last round would be mostly empty: whole rounds of one tile, and the

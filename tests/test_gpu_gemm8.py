@@ -135,3 +135,29 @@ def test_refusals():
         kda.gemm_fp8(a, sa, w, sw, out_dtype=torch.float16)
     with pytest.raises(kda.KDAError):
         kda.gemm_fp8(a[:, :248], sa, w[:, :248].contiguous(), sw)
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,N,K", [(33, 100, 272), (70, 520, 1296), (250, 250, 400), (4000, 9, 528), (17, 7000, 144), (16, 8200, 256), (300, 900, 1040),
+                                   (90, 8300, 2064), (600, 3900, 1168)])
+def test_few_outputs_and_steps_shared_by_groups(M, N, K, out):
+    say(f"product {M} x {N} x {K} {out}")
+    a, sa, w, sw = make(M, N, K, 17)
+    c = kda.gemm_fp8(a, sa, w, sw, out_dtype=out)
+    again = kda.gemm_fp8(a, sa, w, sw, out_dtype=out)
+    torch.cuda.synchronize()
+    check(a, sa, w, sw, c)
+    assert torch.equal(c, again)
+
+
+@pytest.mark.parametrize("M", [70, 300, 600])
+def test_values_that_are_not_finite_in_tiles(M):
+    a, sa, w, sw = make(M, 5000, 400, 18)
+    clean = kda.gemm_fp8(a, sa, w, sw)
+    a, sa, w = a.clone(), sa.clone(), w.clone()
+    a[M - 1, 399], w[4990, 130] = float("nan"), float("nan")
+    sa[3, 2] = float("inf")
+    c = kda.gemm_fp8(a, sa, w, sw)
+    assert torch.isnan(c[M - 1]).all() and torch.isnan(c[:, 4990]).all() and not torch.isfinite(c[3]).any()
+    rows, cols = [m for m in range(M) if m not in (3, M - 1)], [n for n in range(5000) if n != 4990]
+    assert torch.equal(c[rows][:, cols], clean[rows][:, cols])
