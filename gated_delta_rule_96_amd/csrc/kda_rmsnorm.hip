@@ -97,18 +97,21 @@ template <int NV, int L> __device__ __forceinline__ void load_weights(const floa
 // Threads of a work-group, and the rows it holds at once.
 constexpr int group_threads(int L) { return L > kThreads ? L : kThreads; }
 constexpr int group_rows(int L) { return group_threads(L) / L; }
+// A thread's lane in its row, and its row of the work-group's.
+template <int L> __device__ __forceinline__ int row_lane() { return L > 64 ? threadIdx.x : threadIdx.x % L; }
+template <int L> __device__ __forceinline__ int row_of() { return L > 64 ? 0 : threadIdx.x / L; }
 
 // T: type of x and of y; TH: type of the stream (res and h).
 template <typename T, typename TH, bool kRes, bool kFp8, int NV, int L>
 __global__ __launch_bounds__(group_threads(L)) void norm_fwd_kernel(const NormArgs a, long long groups) {
   __shared__ float red[2][1][waves_of(L)];
   constexpr int kPer = group_rows(L);
-  const int lane = threadIdx.x % L, wave = threadIdx.x >> 6, D = a.D;
+  const int lane = row_lane<L>(), wave = threadIdx.x >> 6, D = a.D;
   const float inv = 1.f / (float)D;
   float w[NV][8];
   load_weights<NV, L>(a.w, D, lane, w);
   int turn = 0;
-  for (long long m = (long long)blockIdx.x * kPer + threadIdx.x / L; m < a.rows; m += groups * kPer, turn ^= 1) {
+  for (long long m = (long long)blockIdx.x * kPer + row_of<L>(); m < a.rows; m += groups * kPer, turn ^= 1) {
     Raw8<T> x[NV];
     Raw8<TH> r[NV];
 #pragma unroll
@@ -172,7 +175,7 @@ template <typename T, typename TG, int NV, int L>
 __global__ __launch_bounds__(group_threads(L)) void norm_bwd_kernel(const NormArgs a, long long groups) {
   __shared__ float red[2][2][waves_of(L)];
   constexpr int kPer = group_rows(L);
-  const int lane = threadIdx.x % L, wave = threadIdx.x >> 6, D = a.D;
+  const int lane = row_lane<L>(), wave = threadIdx.x >> 6, D = a.D;
   const float inv = 1.f / (float)D;
   float w[NV][8], dw[NV][8];
   load_weights<NV, L>(a.w, D, lane, w);
@@ -181,7 +184,7 @@ __global__ __launch_bounds__(group_threads(L)) void norm_bwd_kernel(const NormAr
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.f;
   int turn = 0;
-  for (long long m = (long long)blockIdx.x * kPer + threadIdx.x / L; m < a.rows; m += groups * kPer, turn ^= 1) {
+  for (long long m = (long long)blockIdx.x * kPer + row_of<L>(); m < a.rows; m += groups * kPer, turn ^= 1) {
     Raw8<T> h[NV], s[NV];
     Raw8<TG> g[NV];
 #pragma unroll
