@@ -769,12 +769,12 @@ def _flat_rows(t, name, D):
 
 
 def _rows_beside(t, name, dtype, dev, shape, D):
-    """Pointer and token stride of an input of x's (checked) shape, type and
+    """Pointer and token stride of rows of D of this (checked) shape, type and
     device, or of None."""
     if t is None:
         return None, 0
     if t.dtype is not dtype:
-        raise TypeError(f"{name} dtype {t.dtype} != x dtype {dtype}")
+        raise TypeError(f"{name} dtype {t.dtype} != {dtype}")
     if t.device != dev:
         raise ValueError(f"{name} is on {t.device}, not on {dev}")
     if t.shape == shape and t.is_contiguous():
@@ -836,14 +836,18 @@ def add_rms_norm_bwd(h, w, dy, dh=None, *, eps=1e-6, want_dw=None, workspace=Non
     dev, rows = h.device, math.prod(lead)
     if out is None:
         wanted = w is not None if want_dw is None else want_dw
-        out = {"dx": _given(None, h, "dx"), "dw": torch.empty(D, dtype=torch.float32, device=dev) if wanted else None}
-    ws = None
-    if out.get("dw") is not None:
+        dx, dw = _given(None, h, "dx"), torch.empty(D, dtype=torch.float32, device=dev) if wanted else None
+        out = {"dx": dx, "dw": dw}
+        pdx, pdw = dx.data_ptr(), dw.data_ptr() if wanted else None
+    else:
+        pdx, pdw = _dense(out["dx"], "dx", h.shape, h.dtype, dev), _dense(out.get("dw"), "dw", (D,), torch.float32, dev)
+    pws, nws = None, 0
+    if pdw is not None:
         ws = _scratch(workspace, lib().kda_add_rms_norm_bwd_workspace_bytes(rows, D), dev, "kda_add_rms_norm_bwd_workspace_bytes")
-    _same_device(dev, workspace=ws)
-    _call(dev, "kda_add_rms_norm_bwd", ph, ldh, _dense(w, "w", (D,), torch.float32, dev), float(eps), _dense(dy, "dy", h.shape, dy.dtype, dev),
-          _dtype_code(dy), _dense(dh, "dh", h.shape, h.dtype, dev), _dense(out["dx"], "dx", h.shape, h.dtype, dev),
-          _dense(out.get("dw"), "dw", (D,), torch.float32, dev), _dtype_code(h), rows, D, _ptr(ws), 0 if ws is None else ws.numel())
+        _same_device(dev, workspace=ws)
+        pws, nws = _ptr(ws), ws.numel()
+    _call(dev, "kda_add_rms_norm_bwd", ph, ldh, _dense(w, "w", (D,), torch.float32, dev), eps, _dense(dy, "dy", h.shape, dy.dtype, dev),
+          _dtype_code(dy), _dense(dh, "dh", h.shape, h.dtype, dev), pdx, pdw, _dtype_code(h), rows, D, pws, nws)
     return out
 
 
@@ -852,24 +856,27 @@ def gemm_fp8(a, sa, w, sw, *, out_dtype=torch.bfloat16, out=None):
     weights w [N,K] (torch.float8_e4m3fn; a may be a slice of a wider tensor)
     with fp32 scales sa [..., ceil(K/128)] and sw [ceil(N/128), ceil(K/128)]
     (kda_gemm_fp8): c [..., N] of out_dtype (bf16 or fp32), sums in fp32."""
-    for n, t in (("a", a), ("w", w)):
-        if t.dtype != torch.float8_e4m3fn:
-            raise TypeError(f"{n} must be torch.float8_e4m3fn, got {t.dtype}")
-    if sa.dtype != torch.float32:
+    if a.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"a must be torch.float8_e4m3fn, got {a.dtype}")
+    if w.dtype is not torch.float8_e4m3fn:
+        raise TypeError(f"w must be torch.float8_e4m3fn, got {w.dtype}")
+    if sa.dtype is not torch.float32:
         raise TypeError(f"sa must be torch.float32, got {sa.dtype}")
-    N, K = w.shape
+    wshape = w.shape
+    N, K = wshape
     if N > _INT_MAX or K > _INT_MAX:
-        raise ValueError(f"w: a size is not in 32 bits: {list(w.shape)}")
+        raise ValueError(f"w: a size is not in 32 bits: {list(wshape)}")
     kb = (K + 127) // 128
     pa, lda, lead = _flat_rows(a, "a", K)
-    ps, lsa = _rows(sa, "sa", lead, (kb,))
     dev = a.device
-    _same_device(dev, sa=sa)
+    ps, lsa = _rows_beside(sa, "sa", torch.float32, dev, (*lead, kb), kb)
     if out is None:
         out = torch.empty((*lead, N), dtype=out_dtype, device=dev)
-    _call(dev, "kda_gemm_fp8", pa, lda, ps, lsa, _dense(w, "w", (N, K), torch.float8_e4m3fn, dev),
-          _dense(sw, "sw", ((N + 127) // 128, kb), torch.float32, dev), _dense(out, "out", (*lead, N), out.dtype, dev), _dtype_code(out),
-          math.prod(lead), N, K)
+        pc = out.data_ptr()
+    else:
+        pc = _dense(out, "out", (*lead, N), out.dtype, dev)
+    _call(dev, "kda_gemm_fp8", pa, lda, ps, lsa, _dense(w, "w", wshape, torch.float8_e4m3fn, dev),
+          _dense(sw, "sw", ((N + 127) // 128, kb), torch.float32, dev), pc, _dtype_code(out), math.prod(lead), N, K)
     return out
 
 
@@ -941,13 +948,14 @@ def lru_bwd(x, r, i, c, dy, h0=None, dht=None, *, unit=True, cu_seqlens=None, wo
         out = {n: _given(None, x, n) if t is not None else None for n, t in (("dx", x), ("dr", r), ("di", i))}
         out["dc"] = torch.empty(D, dtype=torch.float32, device=dev) if c is not None else None
         out["dh0"] = torch.empty(st, dtype=torch.float32, device=dev) if h0 is not None else None
+        ps = [t if t is None else t.data_ptr() for t in out.values()]
+    else:
+        ps = [_dense(out.get(n), n, (B, T, D), x.dtype, dev) for n in ("dx", "dr", "di")]
+        ps += [_dense(out.get("dc"), "dc", (D,), torch.float32, dev), _dense(out.get("dh0"), "dh0", st, torch.float32, dev)]
     ws = _scratch(workspace, lib().kda_lru_bwd_workspace_bytes(B, T, D, N if arr is not None else 0), dev, "kda_lru_bwd_workspace_bytes")
     _same_device(dev, workspace=ws)
-    p = {n: _dense(out.get(n), n, (B, T, D), x.dtype, dev) for n in ("dx", "dr", "di")}
     _call(dev, "kda_lru_bwd", *args, _dense(h0, "h0", st, torch.float32, dev), _dense(dy, "dy", (B, T, D), x.dtype, dev),
-          _dense(dht, "dht", st, torch.float32, dev), p["dx"], p["dr"], p["di"], _dense(out.get("dc"), "dc", (D,), torch.float32, dev),
-          _dense(out.get("dh0"), "dh0", st, torch.float32, dev), KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, T, D, arr, N, _ptr(ws),
-          ws.numel())
+          _dense(dht, "dht", st, torch.float32, dev), *ps, KDA_LRU_UNIT if unit else 0, _dtype_code(x), B, T, D, arr, N, _ptr(ws), ws.numel())
     return out
 
 
