@@ -136,18 +136,21 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_part_kernel(const LruB
   }
 }
 
-// What enters a sequence's parts: states over H, e from the right over K.  The
-// 64 quarters of the 16 waves of a work-group each take a run of the parts of 16
-// channels, join their runs in LDS and walk them again.
-constexpr int kChainWaves = 16, kChainRuns = 4 * kChainWaves, kChainCh = 16;
-__global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const LruBwdArgs b, const SeqTab s, float* seg) {
-  __shared__ float red[3][kChainRuns][kChainCh];
-  const int D = b.f.D, blocks = (D + kChainCh - 1) / kChainCh, li = blockIdx.x / blocks;
-  const int run = threadIdx.x / kChainCh, lane = threadIdx.x % kChainCh, c0 = (blockIdx.x - li * blocks) * kChainCh + lane;
+// What enters a sequence's parts: states over H, e from the right over K.  A
+// work-group takes CH channels: CH of its threads at a time take a run of the
+// parts, join their runs in LDS and walk them again.
+constexpr int kChainThreads = 1024;
+template <int CH>
+__global__ __launch_bounds__(kChainThreads) void lru_bwd_chain_kernel(const LruBwdArgs b, const SeqTab s, float* seg) {
+  constexpr int kRuns = kChainThreads / CH;
+  __shared__ float red[3][kRuns][CH];
+  const int D = b.f.D, blocks = (D + CH - 1) / CH, li = blockIdx.x / blocks;
+  const int run = CH == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : threadIdx.x / CH, lane = threadIdx.x % CH;
+  const int c0 = (blockIdx.x - li * blocks) * CH + lane;
   const bool live = c0 < D;
   const int c = live ? c0 : 0, n = s.n0 + li;
   const int i0 = s.n ? s.cc[li] : li * s.parts, i1 = s.n ? s.cc[li + 1] : i0 + s.parts;
-  const int per = (i1 - i0 + kChainRuns - 1) / kChainRuns, lo = min(i0 + run * per, i1), hi = min(lo + per, i1);
+  const int per = (i1 - i0 + kRuns - 1) / kRuns, lo = min(i0 + run * per, i1), hi = min(lo + per, i1);
   float* at = seg + c;
   float P = 1.f, H = 0.f, K = 0.f;
 #pragma unroll 4
@@ -164,7 +167,7 @@ __global__ __launch_bounds__(64 * kChainWaves) void lru_bwd_chain_kernel(const L
   __syncthreads();
   float h = b.f.h0 ? b.f.h0[(size_t)n * D + c] : 0.f, e = b.dht ? b.dht[(size_t)n * D + c] : 0.f;
   for (int q = 0; q < run; ++q) h = fmaf(red[0][q][lane], h, red[1][q][lane]);
-  for (int q = kChainRuns - 1; q > run; --q) e = fmaf(red[0][q][lane], e, red[2][q][lane]);
+  for (int q = kRuns - 1; q > run; --q) e = fmaf(red[0][q][lane], e, red[2][q][lane]);
   if (!live) return;
 #pragma unroll 4
   for (int i = lo; i < hi; ++i) {
@@ -312,8 +315,8 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
   const int D = b.f.D;
   const unsigned slices = (unsigned)((D + 64 * NC - 1) / (64 * NC));
   if (!seq_tabs_fit(cu, N, B, T_, kPart, max_groups(64 * kWaves) / slices)) return hipErrorInvalidConfiguration;
-  const long long blocks = (D + kChainCh - 1) / kChainCh, seqs_most = cu ? (N < kMaxVarSeq ? N : kMaxVarSeq) : B;
-  if (T_ > kPart && seqs_most * blocks > max_groups(64 * kChainWaves)) return hipErrorInvalidConfiguration;
+  const long long wide = (D + 63) / 64, narrow = (D + 15) / 16, most = cu ? (N < kMaxVarSeq ? N : kMaxVarSeq) : B;
+  if (T_ > kPart && most * narrow > max_groups(kChainThreads)) return hipErrorInvalidConfiguration;
   float* dcp = b.dc ? ws : nullptr;
   float* seg = ws + all_items(cu != nullptr, N, B, T_) * D;
   size_t rows = 0;
@@ -326,7 +329,13 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
     const bool one = s.items == seqs;   // no sequence has a second part
     if (!one) {
       hipLaunchKernelGGL((lru_bwd_part_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, seg);
-      hipLaunchKernelGGL(lru_bwd_chain_kernel, dim3((unsigned)(blocks * seqs)), dim3(64 * kChainWaves), 0, st, b, s, seg);
+      // By 64 channels, or by 16 and more runs where a sequence has many parts
+      // (65536 x 64: 61 us in all, by 64 channels 94; 65536 x 512: 184 and 218; 256
+      // parts, 4 sequences of 8192 x 2048: 346 and 342; 8, 64 of 256 x 512: 68 and 49).
+      int longest = s.n ? 0 : s.parts;
+      for (int i = 0; i < s.n; ++i) longest = s.cc[i + 1] - s.cc[i] > longest ? s.cc[i + 1] - s.cc[i] : longest;
+      if (longest <= 256) hipLaunchKernelGGL(lru_bwd_chain_kernel<64>, dim3((unsigned)(wide * seqs)), dim3(kChainThreads), 0, st, b, s, seg);
+      else hipLaunchKernelGGL(lru_bwd_chain_kernel<16>, dim3((unsigned)(narrow * seqs)), dim3(kChainThreads), 0, st, b, s, seg);
     }
     hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, one ? nullptr : seg, dcp ? dcp + rows * D : nullptr);
     const hipError_t e = hipGetLastError();
