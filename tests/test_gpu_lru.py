@@ -316,3 +316,39 @@ def test_refusals():
         kda.lru_fwd(x, x, None, None, torch.zeros(1, 8, device="cuda", dtype=torch.float64))
     with pytest.raises(kda.KDAError):
         kda.lru_bwd(x, x, None, None, x, out=dict(dx=torch.empty_like(x), dr=torch.empty_like(x), di=None, dc=torch.empty(8, device="cuda"), dh0=None))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_sequences_of_many_parts(dtype):
+    # hundreds of parts of few channels: the state comes from far back, and the
+    # gradients' chain takes more runs of them
+    lens = [20000, 9, 300]
+    say(f"recurrence {dtype} {lens} D=48")
+    k = make(lens, 48, dtype, 121, slow=True)
+    kw = dict(cu_seqlens=cuts(lens))
+    y, ht = kda.lru_fwd(k["x"], k["r"], k["i"], k["c"], k["h0"], **kw)
+    g = kda.lru_bwd(k["x"], k["r"], k["i"], k["c"], k["dy"], k["h0"], k["dht"], **kw)
+    torch.cuda.synchronize()
+    want = oracle(k, lens, True, back=True)
+    check("y", y[0], want["y"], want["ty"], dtype)
+    check("ht", ht, want["ht"], want["tht"], F32)
+    compare_grads(k, g, want, dtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_bits_do_not_depend_on_how_the_state_was_found(dtype):
+    # channels are on their own: many of them (each part looks back over a few
+    # parts) and a few of them (over many) give the same bits, every time
+    B, T, D = 2, 12000, 1300
+    say(f"recurrence {dtype} {B} x {T} x {D}")
+    x, r, i = (dev(np.random.default_rng(s).standard_normal((B, T, D)), dtype) for s in (131, 132, 133))
+    c, h0 = dev(-np.log(np.random.default_rng(134).uniform(0.9, 0.999, D))), dev(np.random.default_rng(135).standard_normal((B, D)))
+    y, ht = kda.lru_fwd(x, r, i, c, h0)
+    for n in range(4):
+        lo = 256 * n
+        few = [t[..., lo:lo + 256] for t in (x, r, i)]
+        yf, hf = kda.lru_fwd(*few, c[lo:lo + 256].clone(), h0[:, lo:lo + 256].contiguous())
+        y2, ht2 = kda.lru_fwd(x, r, i, c, h0)
+        torch.cuda.synchronize()
+        assert torch.equal(yf, y[..., lo:lo + 256]) and torch.equal(hf, ht[:, lo:lo + 256])
+        assert torch.equal(y2, y) and torch.equal(ht2, ht)
