@@ -6,11 +6,12 @@
 // joined over the waves in LDS.  Every input is read once: the parts of a
 // sequence hand their states on inside the one launch.
 //
-// Bound by HBM: 65536 x 4096 bf16 419 us (8 bytes an element, 5.1 TB/s), 8191
+// Bound by HBM: 65536 x 4096 bf16 416 us (8 bytes an element, 5.2 TB/s), 8191
 // packed tokens x 4096 fp32 119 us (4.5 TB/s); a token for each of 256 x 4096
-// channels is bound by the launch.  The tile: runs of 8, 24 or 32 tokens, 4 or 16
-// waves, four channels a lane, a look back over 2 or 8 parts were all slower or
-// the same.
+// channels is bound by the launch, few channels by the hops from part to part.
+// The tile: runs of 8, 24 or 32 tokens, 4 or 16 waves, four channels a lane, a look
+// back over 2 or 8 parts were all slower or the same; so were a work-group for all
+// parts of a short sequence (4 parts 27 us, a chain of parts 15).
 #include "kda_lru_dev.h"
 
 namespace kda {

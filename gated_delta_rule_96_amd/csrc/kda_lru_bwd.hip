@@ -20,8 +20,8 @@
 // the formulas need 14.
 //
 // Bound by HBM in both passes, in bf16 nearly as much by the exponentials and
-// roots (4 sequences of 8192 x 2048 with every gradient: sums 120 us, 4.4 TB/s;
-// chain 15; gradients 180, 5.2 TB/s; dc 7; 322 in all.  fp32: 200 and 325 us,
+// roots (4 sequences of 8192 x 2048 with every gradient: sums 121 us, 4.4 TB/s;
+// chain 15; gradients 167, 5.6 TB/s; dc 8; 322 in all.  fp32: 200 and 325 us,
 // 5.3 and 5.8 TB/s).  The tile: runs of 8 in parts of 32 tokens 340 us, runs of 4
 // 358 to 362, parts of 64 375 (timed together).  One sequence behind the other,
 // so that the second pass finds its inputs in the last-level cache, 376 against
