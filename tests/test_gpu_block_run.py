@@ -282,3 +282,26 @@ def test_more_work_than_the_usual_tiles_have_groups_for():
     x = torch.randn((R, 8), dtype=BF, device="cuda")
     y, _ = kda.add_rms_norm(x)
     assert torch.equal(y[-900:], kda.add_rms_norm(x[-900:].contiguous())[0])
+
+
+def test_chains_of_parts_beside_other_work():
+    # two long recurrences (one that looks back near, one far) and products on
+    # streams of their own, all at once: the same bits as one after the other
+    r = np.random.default_rng(81)
+    t = lambda *s: cast(r.standard_normal(s), BF).cuda()
+    a, b = [t(1, 30000, 1400) for _ in range(3)], [t(1, 60000, 64) for _ in range(3)]
+    ca, cb = (cast(-np.log(r.uniform(0.9, 0.999, n)), F32).cuda() for n in (1400, 64))
+    m8, w8 = (torch.randn((n, 2048), device="cuda").to(F8) for n in (3000, 2500))
+    sa, sw = torch.rand((3000, 16), device="cuda"), torch.rand((20, 16), device="cuda")
+    jobs = [lambda: kda.lru_fwd(*a, ca)[0], lambda: kda.lru_fwd(*b, cb)[0], lambda: kda.gemm_fp8(m8, sa, w8, sw), lambda: kda.lru_bwd(*b, cb, b[0])["dr"]]
+    want = [j() for j in jobs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in jobs]
+    got = [[] for _ in jobs]
+    for _ in range(6):
+        for j, s, g in zip(jobs, streams, got):
+            with torch.cuda.stream(s):
+                g.append(j())
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(w, o) for o in g)
