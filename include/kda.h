@@ -600,6 +600,8 @@ int kda_add_rms_norm_bwd(const void* h, long long ldh, const float* w, float eps
  * (off by 1.4e-5 of the sum's rms), blocks in fp32.  KDA_F32: all sums in fp32
  * at half that rate.  One rounding.  What is not finite in a row of a
  * or sa stays in that row of c, in a row of w in that column.
+ * The gradient of a's rows is the same call on 8-bit rows of c's gradient, w
+ * transposed and sw transposed (tiles are square; N a multiple of 16 then).
  * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides), KDA_ERR_DTYPE,
  *         KDA_ERR_ALIGN, KDA_ERR_UNSUPPORTED (K), KDA_ERR_OVERLAP, KDA_ERR_HIP.
  */

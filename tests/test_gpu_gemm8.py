@@ -161,3 +161,17 @@ def test_values_that_are_not_finite_in_tiles(M):
     assert torch.isnan(c[M - 1]).all() and torch.isnan(c[:, 4990]).all() and not torch.isfinite(c[3]).any()
     rows, cols = [m for m in range(M) if m not in (3, M - 1)], [n for n in range(5000) if n != 4990]
     assert torch.equal(c[rows][:, cols], clean[rows][:, cols])
+
+
+def test_gradient_of_the_rows_by_the_transposed_weights():
+    # dx = dc w: rows of dc in 8 bits, w and its scales transposed
+    M, N, K = 300, 400, 272
+    _, _, w, sw = make(M, N, K, 19)
+    d8, sd, _, _ = make(M, 16, N, 20)
+    dx = kda.gemm_fp8(d8, sd, w.t().contiguous(), sw.t().contiguous(), out_dtype=F32)
+    torch.cuda.synchronize()
+    D = f64(d8) * block.spread(f64(sd), N)
+    Wf = f64(w) * block.spread(block.spread(f64(sw), K), N, 0)
+    want, size = D @ Wf, np.abs(D) @ np.abs(Wf)
+    # (the sums' roundings as in check, and those of the scales' products here)
+    assert np.all(np.abs(f64(dx) - want) <= (131 + 4 + 2) * U * size + U * np.abs(want))
