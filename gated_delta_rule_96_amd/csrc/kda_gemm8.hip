@@ -343,15 +343,19 @@ hipError_t rows_go(const Gemm8Args& g, hipStream_t st) {
 // Tiles by the time of a round of 256 work-groups, one a CU, us for K = 4096:
 // what a shape takes is its rounds times that.  Measured, 4096 outputs, bf16:
 // 256 rows 64 x 64 11.2, 64 x 128 14.0; 512 rows 64 x 128 15.0, 64 x 64 20.5; 1024
-// rows 128 x 128 24.5, 64 x 128 28.5; 2048 rows 128 x 256 40, 128 x 128 47; 8192 rows
-// 256 x 256 131, 128 x 256 148.  fp32: 17 and 23, 24 and 30, 41 and 46, 64 and 78; 256
-// x 256 does not fit the registers there.  Two smaller work-groups a CU, each
-// with fewer steps in LDS, took 41 for 2048 rows in 128 x 128.
+// rows 128 x 128 24.5, 64 x 128 28.5; 1536 rows 192 x 128 34.7, 128 x 256 39.2; 2048
+// rows 128 x 256 40, 128 x 128 47; 1536 x 8192 192 x 256 55.8, 256 x 256 61.0; 8192 rows
+// 256 x 256 131, 128 x 256 148.  fp32: 17 and 23, 24 and 30, 41 and 46, 56 and 65, 64
+// and 78; the two largest do not fit the registers there.  Two smaller
+// work-groups a CU, each with fewer steps in LDS, took 41 for 2048 rows in 128 x
+// 128.
 struct TileTime {
   int bm, bn;
   float bf16_us, f32_us;
 };
-constexpr TileTime kTiles[5] = {{64, 64, 11.f, 16.5f}, {64, 128, 15.f, 24.f}, {128, 128, 24.3f, 41.f}, {128, 256, 39.5f, 62.f}, {256, 256, 66.f, 0.f}};
+constexpr TileTime kTiles[7] = {{64, 64, 11.f, 16.5f}, {64, 128, 15.f, 24.f}, {128, 128, 24.3f, 41.f}, {192, 128, 34.5f, 56.f}, {128, 256, 39.5f, 62.f},
+                                {192, 256, 54.f, 0.f}, {256, 256, 66.f, 0.f}};
+template <typename T> constexpr int tile_kinds() { return sizeof(T) == 2 ? 7 : 5; }
 
 template <typename T> float round_us(int i) { return sizeof(T) == 2 ? kTiles[i].bf16_us : kTiles[i].f32_us; }
 long long tiles_of(const TileTime& t, long long M, long long N) { return (M + t.bm - 1) / t.bm * ((N + t.bn - 1) / t.bn); }
@@ -359,9 +363,9 @@ long long tiles_of(const TileTime& t, long long M, long long N) { return (M + t.
 // The tile that takes least for M x N, and its time.  (Of more work-groups than
 // a launch may have: the largest only, which the launch refuses in its turn.)
 template <typename T> int best_tile(long long M, long long N, float& least) {
-  int best = sizeof(T) == 2 ? 4 : 3;
+  int best = tile_kinds<T>() - 1;
   least = (float)((tiles_of(kTiles[best], M, N) + 255) / 256) * round_us<T>(best);
-  for (int i = 0; i < (sizeof(T) == 2 ? 4 : 3); ++i) {
+  for (int i = 0; i < tile_kinds<T>() - 1; ++i) {
     const long long n = tiles_of(kTiles[i], M, N);
     const float us = (float)((n + 255) / 256) * round_us<T>(i);
     if (us < least && n <= max_groups(kTileThreads) - 8) {
@@ -377,10 +381,11 @@ template <typename T> hipError_t tile_by(int i, const Gemm8Args& g, hipStream_t 
     case 0: return tile_go<T, 64, 64, 2, 2, 2, 6, 2>(g, st);
     case 1: return tile_go<T, 64, 128, 2, 2, 2, 6, 2>(g, st);
     case 2: return tile_go<T, 128, 128, 4, 2, 1, 4, 1>(g, st);
-    case 3: return tile_go<T, 128, 256, 2, 4, 1, 3, 1>(g, st);
+    case 3: return tile_go<T, 192, 128, 4, 2, 1, 3, 1>(g, st);
+    case 4: return tile_go<T, 128, 256, 2, 4, 1, 3, 1>(g, st);
     default: break;
   }
-  if constexpr (sizeof(T) == 2) return tile_go<T, 256, 256, 4, 2, 1, 2, 1>(g, st);
+  if constexpr (sizeof(T) == 2) return i == 5 ? tile_go<T, 192, 256, 4, 2, 1, 2, 1>(g, st) : tile_go<T, 256, 256, 4, 2, 1, 2, 1>(g, st);
   return hipErrorInvalidValue;
 }
 
@@ -403,7 +408,7 @@ hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
   constexpr float kGap = 4.f;
   const float k = (float)g.K / 4096.f;
   int cut = 0;
-  for (int i = 0; i < (sizeof(T) == 2 ? 5 : 4); ++i) {
+  for (int i = 0; i < tile_kinds<T>(); ++i) {
     const TileTime& t = kTiles[i];
     const long long rows = (g.M + t.bm - 1) / t.bm, rounds = tiles_of(t, g.M, g.N) / 256, cols = rounds * 256 / rows * t.bn;
     if (rounds == 0 || cols == 0 || cols >= g.N || cols % 128) continue;   // (scales are of 128 columns)

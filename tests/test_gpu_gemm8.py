@@ -175,3 +175,11 @@ def test_gradient_of_the_rows_by_the_transposed_weights():
     want, size = D @ Wf, np.abs(D) @ np.abs(Wf)
     # (the sums' roundings as in check, and those of the scales' products here)
     assert np.all(np.abs(f64(dx) - want) <= (131 + 4 + 2) * U * size + U * np.abs(want))
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("M,N,K", [(760, 8100, 272), (1530, 4090, 144), (1500, 8190, 400), (1537, 8193, 144)])
+def test_tiles_of_192_rows(M, N, K, out):
+    say(f"product {M} x {N} x {K} {out}")
+    a, sa, w, sw = make(M, N, K, 21)
+    check(a, sa, w, sw, kda.gemm_fp8(a, sa, w, sw, out_dtype=out))
