@@ -39,12 +39,12 @@ template <> struct alignas(4) LruPack<bf16, 2, true> {
   }
 };
 
-// a = e^g, g <= 0, by way of d = 1 - a from the series of 1 - e^g where g is
-// small: a is then within half a unit of its last place to either side (the
+// a = e^g by way of d = 1 - a from the series of 1 - e^g where g is near 0, on
+// either side: a is then within half a unit of its last place to either side (the
 // exponential instruction's error has a bias, which a state that remembers
 // thousands of tokens adds up), and 1 - a^2 = d (1 + a) loses nothing near
-// a = 1.  Four terms below 2^-4 (bf16 inputs: what is left out is 2^-23 of d),
-// eight below 2^-1 (2^-26).
+// a = 1.  Four terms for |g| below 2^-4 (bf16 inputs: what is left out is 2^-23
+// of d), eight below 2^-1 (2^-26).
 template <typename T> constexpr float lru_near() { return sizeof(T) == 2 ? 0.0625f : 0.5f; }
 template <typename T> __device__ __forceinline__ float one_minus_decay_near(float g) {
   constexpr bool kShort = sizeof(T) == 2;
@@ -63,7 +63,7 @@ template <typename T> __device__ __forceinline__ float one_minus_decay_near(floa
 template <typename T> __device__ __forceinline__ float one_minus_decay(float g, float& a) {
   float d = one_minus_decay_near<T>(g);
   a = 1.f - d;
-  const bool far = !(g > -lru_near<T>());
+  const bool far = !(__builtin_fabsf(g) < lru_near<T>());   // (NaN too)
   if (__any(far)) {
     const float e = exp2_fast(g * kLog2e);
     a = far ? e : a;

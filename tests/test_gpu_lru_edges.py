@@ -1,0 +1,40 @@
+"""Places of the gated linear recurrence that its own tests do not reach.
+
+Tolerances are those of test_gpu_lru.py where nothing else is said.
+"""
+import numpy as np
+import pytest
+import torch
+
+import test_gpu_lru as tl
+from gated_delta_rule_96_amd import kda
+from kda_testutil import say
+
+pytestmark = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+DTYPES = [F32, BF]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("lens,top", [([12, 5], 3.0), ([300], 0.15)], ids=str)
+def test_log_decays_above_zero_are_computed_as_they_are(dtype, lens, top):
+    say(f"recurrence {dtype} {lens} log-decays to {top}")
+    for D in (130, 7):
+        k = tl.make(lens, D, dtype, 201 + D, gate=False)
+        r = np.random.default_rng(202)
+        g = r.uniform(-top, top, (1, sum(lens), D))
+        g[0, 0], g[0, 3], g[0, 4] = top / 3, top, 0.0
+        k["r"] = tl.dev(g, dtype)
+        kw = dict(unit=False, cu_seqlens=tl.cuts(lens))
+        y, ht = kda.lru_fwd(k["x"], k["r"], k["i"], None, k["h0"], **kw)
+        gr = kda.lru_bwd(k["x"], k["r"], k["i"], None, k["dy"], k["h0"], k["dht"], **kw)
+        state = k["h0"][:1].clone()
+        steps = [kda.lru_step(k["x"][:, t], k["r"][:, t], k["i"][:, t], None, state, unit=False) for t in range(5)]
+        m, _ = kda.lru_fwd(k["x"], k["r"], k["i"], None, k["h0"], cu_seqlens=tl.cuts(lens))
+        torch.cuda.synchronize()
+        want = tl.oracle(k, lens, False, back=True)
+        tl.check("y", y[0], want["y"], want["ty"], dtype)
+        tl.check("ht", ht, want["ht"], want["tht"], F32)
+        tl.check("steps", torch.cat(steps), want["y"][:5], want["ty"][:5], dtype)
+        tl.compare_grads(k, gr, want, dtype)
+        assert torch.isnan(m[0, 0]).all()   # (its root of 1 - a^2)
