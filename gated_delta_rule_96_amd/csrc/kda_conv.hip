@@ -416,12 +416,13 @@ bool seq_tabs_fit(const int* cu, int N, int B, int T, int part, long long most) 
 constexpr int kSumThreads = 1024;
 // out[c]: sum of column c of part [nrows][n0 + n1 + n2] over its rows, the
 // columns in three outputs.  A work-group takes 64 columns; its 16 waves take
-// every 16th row and are joined through LDS, always in the same order.
+// every 16th row and are joined through LDS, always in the same order.  `first`:
+// columns of the launches before.
 __global__ __launch_bounds__(kSumThreads) void sum_rows_kernel(const float* __restrict__ part, size_t nrows, unsigned n0, unsigned n1,
-                                                        unsigned n2, float* __restrict__ out0, float* __restrict__ out1,
+                                                        unsigned n2, unsigned first, float* __restrict__ out0, float* __restrict__ out1,
                                                         float* __restrict__ out2) {
   __shared__ double red[16][64];
-  const unsigned l = threadIdx.x & 63, q = threadIdx.x >> 6, col = blockIdx.x * 64 + l, cols = n0 + n1 + n2;
+  const unsigned l = threadIdx.x & 63, q = threadIdx.x >> 6, col = first + blockIdx.x * 64 + l, cols = n0 + n1 + n2;
   double v = 0.0;
   if (col < cols)
 #pragma unroll 8
@@ -438,8 +439,15 @@ __global__ __launch_bounds__(kSumThreads) void sum_rows_kernel(const float* __re
 
 hipError_t launch_sum_rows(const float* part, size_t nrows, unsigned n0, unsigned n1, unsigned n2, float* out0, float* out1,
                            float* out2, hipStream_t st) {
-  hipLaunchKernelGGL(sum_rows_kernel, dim3((n0 + n1 + n2 + 63) / 64), dim3(kSumThreads), 0, st, part, nrows, n0, n1, n2, out0, out1, out2);
-  return hipGetLastError();
+  const long long cols = (long long)n0 + n1 + n2, most = max_groups(kSumThreads) * 64;
+  for (long long first = 0; first < cols; first += most) {
+    const long long n = cols - first < most ? cols - first : most;
+    hipLaunchKernelGGL(sum_rows_kernel, dim3((unsigned)((n + 63) / 64)), dim3(kSumThreads), 0, st, part, nrows, n0, n1, n2, (unsigned)first, out0,
+                       out1, out2);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_conv_fwd(int is_bf16, const ConvArgs& a, const int* cu, int N, int B, int T, hipStream_t st) {

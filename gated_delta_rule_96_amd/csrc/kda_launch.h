@@ -132,7 +132,8 @@ bool seq_tabs_fit(const int* cu, int N, int B, int T, int part, long long most);
 constexpr long long max_groups(int threads) { return 0xffffffffLL / threads; }
 
 // out[0][c], then out[1], out[2]: column sums of part [nrows][n0 + n1 + n2], in
-// a fixed order (any output may be null).
+// a fixed order (any output may be null).  Up to 2^31 columns, in several launches
+// where one has not the work-groups.
 hipError_t launch_sum_rows(const float* part, size_t nrows, unsigned n0, unsigned n1, unsigned n2, float* out0, float* out1,
                            float* out2, hipStream_t stream);
 

@@ -38,3 +38,25 @@ def test_log_decays_above_zero_are_computed_as_they_are(dtype, lens, top):
         tl.check("steps", torch.cat(steps), want["y"][:5], want["ty"][:5], dtype)
         tl.compare_grads(k, gr, want, dtype)
         assert torch.isnan(m[0, 0]).all()   # (its root of 1 - a^2)
+
+
+def test_dc_of_more_channels_than_one_launch_sums():
+    # a column sum of 64 channels a work-group of 1024: one launch has them for
+    # 64 (2^22 - 1) channels.  Channels are on their own, so halves have the same bits.
+    B, D = 2, (1 << 28) + 128
+    say(f"recurrence gradients {B} x 1 x {D}")
+    gen = torch.Generator(device="cuda").manual_seed(271)
+    x = torch.randn((B, 1, D), dtype=BF, device="cuda", generator=gen)
+    c = torch.rand(D, device="cuda", generator=gen)
+    h0 = torch.full((B, D), 0.5, device="cuda")
+    dc = torch.full((D,), float("nan"), device="cuda")
+    got = kda.lru_bwd(x, x, None, c, x, h0, out=dict(dx=torch.empty_like(x), dr=torch.empty_like(x), di=None, dc=dc, dh0=None))
+    for lo in (0, D // 2):
+        part, at = x[..., lo:lo + D // 2].contiguous(), slice(lo, lo + D // 2)
+        half = kda.lru_bwd(part, part, None, c[at].clone(), part, h0[:, at].contiguous())
+        torch.cuda.synchronize()
+        assert torch.equal(dc[at], half["dc"]) and torch.equal(got["dr"][..., at], half["dr"])
+        del half, part
+    assert float(dc.abs().min()) >= 0 and int((dc != 0).sum()) > 0.9 * D
+    del got, x, c, h0, dc
+    torch.cuda.empty_cache()
