@@ -138,15 +138,17 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_bwd_part_kernel(const LruB
 
 // What enters a sequence's parts: states over H, e from the right over K.  A
 // work-group takes CH channels: CH of its threads at a time take a run of the
-// parts, join their runs in LDS and walk them again.
+// parts, join their runs in LDS and walk them again.  `first`: work-groups of the
+// launches before.
 constexpr int kChainThreads = 1024;
 template <int CH>
-__global__ __launch_bounds__(kChainThreads) void lru_bwd_chain_kernel(const LruBwdArgs b, const SeqTab s, float* seg) {
+__global__ __launch_bounds__(kChainThreads) void lru_bwd_chain_kernel(const LruBwdArgs b, const SeqTab s, float* seg, unsigned first) {
   constexpr int kRuns = kChainThreads / CH;
   __shared__ float red[3][kRuns][CH];
-  const int D = b.f.D, blocks = (D + CH - 1) / CH, li = blockIdx.x / blocks;
+  const unsigned id = first + blockIdx.x;
+  const int D = b.f.D, blocks = (D + CH - 1) / CH, li = id / blocks;
   const int run = CH == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) : threadIdx.x / CH, lane = threadIdx.x % CH;
-  const int c0 = (blockIdx.x - li * blocks) * CH + lane;
+  const int c0 = (id - li * blocks) * CH + lane;
   const bool live = c0 < D;
   const int c = live ? c0 : 0, n = s.n0 + li;
   const int i0 = s.n ? s.cc[li] : li * s.parts, i1 = s.n ? s.cc[li + 1] : i0 + s.parts;
@@ -298,6 +300,21 @@ __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBw
   for (int j = 0; j < NC; ++j) dcp[(size_t)item * D + l.c + j] = -sum[j];
 }
 
+// The chain's work-groups, in several launches where one cannot have them (the
+// parts' launch has fewer than 2^24 of 64 or 128 channels of a part, so there are
+// fewer than 2^27 here).
+template <int CH>
+hipError_t chain_go(const LruBwdArgs& b, const SeqTab& s, int seqs, float* seg, hipStream_t st) {
+  const long long all = (long long)((b.f.D + CH - 1) / CH) * seqs;
+  for (long long first = 0; first < all; first += max_groups(kChainThreads)) {
+    const long long n = all - first < max_groups(kChainThreads) ? all - first : max_groups(kChainThreads);
+    hipLaunchKernelGGL(lru_bwd_chain_kernel<CH>, dim3((unsigned)n), dim3(kChainThreads), 0, st, b, s, seg, (unsigned)first);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 bool pairs(const LruBwdArgs& b, size_t esz) {
   const LruArgs& a = b.f;
   if (a.D % 2 || a.ldx % 2 || a.ldr % 2 || (a.i && a.ldi % 2)) return false;
@@ -315,8 +332,6 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
   const int D = b.f.D;
   const unsigned slices = (unsigned)((D + 64 * NC - 1) / (64 * NC));
   if (!seq_tabs_fit(cu, N, B, T_, kPart, max_groups(64 * kWaves) / slices)) return hipErrorInvalidConfiguration;
-  const long long wide = (D + 63) / 64, narrow = (D + 15) / 16, most = cu ? (N < kMaxVarSeq ? N : kMaxVarSeq) : B;
-  if (T_ > kPart && most * narrow > max_groups(kChainThreads)) return hipErrorInvalidConfiguration;
   float* dcp = b.dc ? ws : nullptr;
   float* seg = ws + all_items(cu != nullptr, N, B, T_) * D;
   size_t rows = 0;
@@ -334,8 +349,8 @@ hipError_t bwd_go(const LruBwdArgs& b, const int* cu, int N, int B, int T_, floa
       // parts, 4 sequences of 8192 x 2048: 346 and 342; 8, 64 of 256 x 512: 68 and 49).
       int longest = s.n ? 0 : s.parts;
       for (int i = 0; i < s.n; ++i) longest = s.cc[i + 1] - s.cc[i] > longest ? s.cc[i + 1] - s.cc[i] : longest;
-      if (longest <= 256) hipLaunchKernelGGL(lru_bwd_chain_kernel<64>, dim3((unsigned)(wide * seqs)), dim3(kChainThreads), 0, st, b, s, seg);
-      else hipLaunchKernelGGL(lru_bwd_chain_kernel<16>, dim3((unsigned)(narrow * seqs)), dim3(kChainThreads), 0, st, b, s, seg);
+      const hipError_t e = longest <= 256 ? chain_go<64>(b, s, seqs, seg, st) : chain_go<16>(b, s, seqs, seg, st);
+      if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((lru_bwd_out_kernel<T, NC, kFull>), grid, th, 0, st, b, s, slices, one ? nullptr : seg, dcp ? dcp + rows * D : nullptr);
     const hipError_t e = hipGetLastError();

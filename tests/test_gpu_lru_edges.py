@@ -60,3 +60,26 @@ def test_dc_of_more_channels_than_one_launch_sums():
     assert float(dc.abs().min()) >= 0 and int((dc != 0).sum()) > 0.9 * D
     del got, x, c, h0, dc
     torch.cuda.empty_cache()
+
+
+def test_gradients_of_more_chains_than_one_launch_carries():
+    # 131072 sequences of two parts: 33 work-groups of 64 channels each, over 2^22
+    # together.  256 sequences over and over, so every repetition has their bits.
+    B, T, D, few = 1 << 17, 33, 2056, 256
+    say(f"recurrence gradients {B} x {T} x {D}")
+    torch.cuda.empty_cache()
+    gen = torch.Generator(device="cuda").manual_seed(281)
+    part = torch.randn((few, T, D), dtype=BF, device="cuda", generator=gen)
+    c = torch.rand(D, device="cuda", generator=gen)
+    want = kda.lru_bwd(part, part, None, c, part)
+    x = torch.empty((B, T, D), dtype=BF, device="cuda")
+    x.view(B // few, few, T, D).copy_(part)
+    got = kda.lru_bwd(x, x, None, c, x)
+    torch.cuda.synchronize()
+    for n in ("dx", "dr"):
+        all_of = got[n].view(B // few, few, T, D)
+        assert all(torch.equal(all_of[k], want[n]) for k in range(B // few)), n
+    # (dc: the same terms B / few times, joined in 64 bits and rounded once on each side)
+    torch.testing.assert_close(got["dc"].double(), want["dc"].double() * (B // few), rtol=2.0 ** -22, atol=0)
+    del x, got, all_of
+    torch.cuda.empty_cache()
