@@ -11,6 +11,7 @@ from gated_delta_rule_96_amd import kda
 from kda_testutil import say
 
 pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
 BF, F32 = torch.bfloat16, torch.float32
 DTYPES = [F32, BF]
 
@@ -83,3 +84,36 @@ def test_gradients_of_more_chains_than_one_launch_carries():
     torch.testing.assert_close(got["dc"].double(), want["dc"].double() * (B // few), rtol=2.0 ** -22, atol=0)
     del x, got, all_of
     torch.cuda.empty_cache()
+
+
+def test_gradients_of_the_recurrence_along_themselves():
+    # Every leaf along its own gradient G, d = G / max |G|: the slope is sum G^2 /
+    # max |G|, which no wrong sign, place or factor gives.  The forward's central
+    # difference on the GPU has the error of its two values (the forward's
+    # tolerance, and half a unit of y, weighted by |dy|, over 2 e), and that of the step itself,
+    # which the oracle's difference of the same inputs has too.
+    lens = [40]
+    k = tl.make(lens, 16, F32, 211)
+    want = tl.oracle(k, lens, True, back=True)
+    g = kda.lru_bwd(k["x"], k["r"], k["i"], k["c"], k["dy"], k["h0"], k["dht"])
+    e = 2.0 ** -6
+    for n in ("x", "r", "i", "c", "h0"):
+        G, tol = want["d" + n], want["td" + n]
+        d = tl.dev((G / np.abs(G).max()).reshape(k[n].shape))
+
+        def sides(s):
+            v = dict(k, **{n: k[n] + s * d})
+            y, ht = kda.lru_fwd(v["x"], v["r"], v["i"], v["c"], v["h0"])
+            o = tl.oracle(v, lens, True)
+            f = lambda y, ht: float((y * tl.f64(k["dy"])[0]).sum() + (ht * tl.f64(k["dht"])).sum())
+            err = float(((o["ty"] + U * np.abs(o["y"])) * np.abs(tl.f64(k["dy"])[0])).sum() + (o["tht"] * np.abs(tl.f64(k["dht"]))).sum())
+            return f(tl.f64(y[0]), tl.f64(ht)), f(o["y"], o["ht"]), err
+        (a, a64, ea), (b, b64, eb) = sides(e), sides(-e)
+        d64 = tl.f64(d).reshape(G.shape)
+        slope, slope64, exact = (a - b) / (2 * e), (a64 - b64) / (2 * e), float((G * d64).sum())
+        lim = (ea + eb) / (2 * e)
+        step = abs(slope64 - exact)
+        grad = float(((tol + U * np.abs(G)) * np.abs(d64)).sum())
+        got = float((tl.f64(g["d" + n]).reshape(G.shape) * d64).sum())
+        assert lim + step + grad <= 0.1 * exact, (n, lim, step, grad, exact)
+        assert abs(slope - slope64) <= lim and abs(got - exact) <= grad and abs(got - slope) <= lim + step + grad, n
