@@ -117,3 +117,29 @@ def test_gradients_of_the_recurrence_along_themselves():
         got = float((tl.f64(g["d" + n]).reshape(G.shape) * d64).sum())
         assert lim + step + grad <= 0.1 * exact, (n, lim, step, grad, exact)
         assert abs(slope - slope64) <= lim and abs(got - exact) <= grad and abs(got - slope) <= lim + step + grad, n
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_states_that_start_on_four_bytes(dtype):
+    # pairs of channels fit the rows but not the states
+    D, T, B = 34, 300, 3
+    k = tl.make([T] * B, D, dtype, 261)
+    rows = [k[n].reshape(B, T, D) for n in ("x", "r", "i")]
+    odd = lambda: torch.full((B * D + 8,), 5.0, device="cuda")
+    want, wht = kda.lru_fwd(*rows, k["c"], k["h0"])
+    gw = kda.lru_bwd(*rows, k["c"], k["dy"].reshape(B, T, D), k["h0"], k["dht"])
+    for src, dst in ((1, 0), (0, 1), (1, 1)):
+        a, b = odd(), odd()
+        h0, ht = a[src:src + B * D].view(B, D), b[dst:dst + B * D].view(B, D)
+        h0.copy_(k["h0"])
+        y, _ = kda.lru_fwd(*rows, k["c"], h0, ht=ht)
+        assert torch.equal(y, want) and torch.equal(ht, wht) and bool((b[:dst] == 5).all()) and bool((b[dst + B * D:] == 5).all())
+        ht.copy_(h0)
+        y = kda.lru_step(*(t[:, 0] for t in rows), k["c"], ht)
+        so = torch.empty((B, D), device="cuda")
+        y2 = kda.lru_step(*(t[:, 0].contiguous() for t in rows), k["c"], k["h0"], state_out=so)
+        assert torch.equal(y, y2) and torch.equal(ht, so) and torch.equal(y2, want[:, 0]) and bool((b[dst + B * D:] == 5).all())
+        dht, dh0 = odd()[src:src + B * D].view(B, D), b[dst:dst + B * D].view(B, D)
+        dht.copy_(k["dht"])
+        g = kda.lru_bwd(*rows, k["c"], k["dy"].reshape(B, T, D), h0, dht, out=dict(gw, dh0=dh0, dx=torch.empty_like(gw["dx"])))
+        assert torch.equal(g["dx"], gw["dx"]) and torch.equal(dh0, kda.lru_bwd(*rows, k["c"], k["dy"].reshape(B, T, D), k["h0"], k["dht"])["dh0"])
