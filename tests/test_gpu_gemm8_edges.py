@@ -60,3 +60,34 @@ def test_large_products_among_small_ones(M, N, K):
         tol = (131 + kb) * U * size + (7 * 2.0 ** -13 * eights if out == BF else 0.0)
         bad = ~(np.abs(got - want) <= tol * (1 + h) + h * np.abs(want))
         assert not bad.any(), (out, int(bad.sum()), np.argwhere(bad)[:4].tolist())
+
+# (in order of the variants: two of few outputs, 64 columns, tiles from 64 x 64 to 256 x 256)
+@pytest.mark.parametrize("M,N,K", [(9, 300, 8336), (40, 2100, 8336), (16, 9000, 8336), (300, 900, 8336), (500, 4000, 8464), (600, 3900, 16400), (760, 8100, 8336),
+                                   (1000, 8190, 8336), (1500, 8190, 8336), (2040, 8190, 8464)])
+def test_products_of_more_than_64_blocks(M, N, K):
+    # a tile takes its weights' scales 64 steps at a time
+    a, sa, w, sw = tg.make(M, N, K, 241, pad=16 if M == 300 else 0)
+    bytes_of = lambda t, n: t.view(torch.uint8)[n].view(F8)
+    rows = sorted(set(range(0, M, max(1, M // 24))) | {M - 1})
+    for out in (BF, F32):
+        say(f"product {M} x {N} x {K} {out}")
+        c = kda.gemm_fp8(a, sa, w, sw, out_dtype=out)
+        again = kda.gemm_fp8(a, sa, w, sw, out_dtype=out)
+        torch.cuda.synchronize()
+        assert torch.equal(c, again)
+        for n0 in range(0, N, 128):   # some columns of every tile of the weights
+            n = list(range(n0, min(n0 + 128, N), 37)) + [min(n0 + 127, N - 1)]
+            tg.check(bytes_of(a, rows), sa[rows], bytes_of(w, n), sw[n0 // 128:n0 // 128 + 1], c[rows][:, n])
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+def test_whole_numbers_are_summed_exactly(out):
+    # small whole numbers and scales of one: a block's sum is below 2^11 and a
+    # result below 2^14, so only the output's type rounds
+    r = np.random.default_rng(251)
+    for M, N, K in ((5, 70, 272), (20, 5000, 1024), (150, 200, 1024), (1100, 1000, 528), (2300, 2100, 256)):
+        a, w = (cast(r.integers(-3, 4, s).astype(np.float64), F32) for s in ((M, K), (N, K)))
+        one = lambda *s: torch.ones(s, device="cuda")
+        kb = (K + 127) // 128
+        c = kda.gemm_fp8(a.to(F8).cuda(), one(M, kb), w.to(F8).cuda(), one((N + 127) // 128, kb), out_dtype=out)
+        assert torch.equal(c.cpu(), (a.double() @ w.double().T).to(out))
