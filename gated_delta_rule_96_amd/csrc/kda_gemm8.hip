@@ -36,9 +36,10 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 // are not summed in 32 bits: of every 8 neighbouring k each is cut towards zero at
 // 2^-13 of their largest power of two (measured for every place in a block; factors
 // below 2^-6 count as 2^-6), so a block is off by at most 7 x 2^-13 of the sum of
-// those, 2^-10 of sum |a w|; the output rounds by 2^-9 to 2^-8.  Only where large products cancel does it show.
-// Random rows: 1.4e-5 of the sum's rms.  fp32 outputs take fp16 operands, which hold
-// e4m3 and its products exactly: 5e-8 to 8e-8 over 4096 indices.
+// those, 2^-10 of sum |a w|; the output rounds by 2^-9 to 2^-8.  Only where large
+// products cancel does it show.  Random rows: 1.4e-5 of the sum's rms.  fp32 outputs
+// take fp16 operands, which hold e4m3 and its products exactly: 5e-8 to 8e-8 over 4096
+// indices.
 template <typename T> struct Frag;
 template <> struct Frag<bf16> {
   i32x8 v;

@@ -93,6 +93,7 @@ __device__ __forceinline__ void run_sum(const float (&a)[R][NC], const float (&u
 // ordered by fences, which would write back the caches.
 struct Words {
   unsigned* ticket;             // parts and slices given out so far
+  unsigned* status;             // not 0: a wait of this call has expired (kda_fwd_status)
   unsigned long long* own;      // [items][D]
   unsigned* into;               // [items][D]
 };
@@ -105,14 +106,19 @@ __device__ __forceinline__ unsigned word_of(float x) {
 __device__ __forceinline__ Words words_at(void* ws, size_t n) {
   Words w;
   w.ticket = static_cast<unsigned*>(ws);
+  w.status = w.ticket + 8;
   w.own = reinterpret_cast<unsigned long long*>(w.ticket + 64);
   w.into = reinterpret_cast<unsigned*>(w.own + n);
   return w;
 }
-__global__ __launch_bounds__(256) void lru_fill_kernel(unsigned* ws, size_t n) {   // n words of ones behind the ticket
+// `begin`: a call's first launch, which clears the status.
+__global__ __launch_bounds__(256) void lru_fill_kernel(unsigned* ws, size_t n, int begin) {   // n words of ones behind the ticket
   typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
   const size_t id = (size_t)blockIdx.x * 256 + threadIdx.x, step = (size_t)gridDim.x * 256;
-  if (id == 0) ws[0] = 0;
+  if (id == 0) {
+    ws[0] = 0;
+    if (begin) ws[8] = 0;
+  }
   for (size_t q = id; q < n / 4; q += step) reinterpret_cast<u32x4*>(ws + 64)[q] = u32x4{kNone, kNone, kNone, kNone};
   if (id < n % 4) ws[64 + n / 4 * 4 + id] = kNone;
 }
@@ -164,15 +170,20 @@ __device__ __forceinline__ float carry_over(unsigned long long own, float h) {
   return fmaf(__uint_as_float((unsigned)own), h, __uint_as_float((unsigned)(own >> 32)));
 }
 
+__device__ __forceinline__ void expired(const Words& w, int lane) {
+  if (lane == 0) __hip_atomic_store(w.status, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // Outputs.  kNear and kFar: each work-group takes the next (part, slice) by a
 // ticket and waits for parts before its own only, all of which have lower
 // tickets: the lowest ticket that is not done waits for nothing, so every wait
 // ends, however many work-groups run at once.  A part publishes its own (P, H),
 // goes back to the nearest part that has its state published, if the (P, H) of
 // those in between are, and carries the state over them one by one, as each of
-// them does, so that the bits do not depend on which was found.
+// them does, so that the bits do not depend on which was found.  A wait is bounded
+// all the same: the states behind one that expires are NaN, and the status says so.
 template <typename T, int NC, LruWay kWay, bool kFull>
-__global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g, const SeqTab s, unsigned slices, void* ws) {
+__global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g, const SeqTab s, unsigned slices, void* ws, int begin) {
   constexpr bool kChain = kWay == kNear || kWay == kFar;
   __shared__ float red[2][kWaves][64 * NC];
   __shared__ float carry[64 * NC];
@@ -185,6 +196,8 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
     __syncthreads();
     id = __builtin_amdgcn_readfirstlane(given);
     if (id >= gridDim.x) return;
+  } else if (begin && blockIdx.x == 0 && threadIdx.x == 0) {
+    *w.status = 0;
   }
   unsigned item = id / slices;
   const LruLane l = lru_lane<NC>((int)(id - item * slices), g.D);
@@ -228,9 +241,11 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
         if (found || poll == kPolls) break;
         __builtin_amdgcn_s_sleep(1);
       }
-      if (!found)
+      if (!found) {
+        expired(w, lane);
 #pragma unroll
         for (int j = 0; j < NC; ++j) h[j] = __builtin_nanf("");
+      }
 #pragma unroll
       for (int d = kBack - 1; d >= 0; --d)
 #pragma unroll
@@ -266,6 +281,7 @@ __global__ __launch_bounds__(64 * kWaves, 4) void lru_out_kernel(const LruArgs g
         for (int j = 0; j < NC; ++j) far[wave * kBack + d][lane * NC + j] = wave * kBack + d + 1 == found ? b.in[d][j] : b.own[d][j];
     __syncthreads();
     if (wave == 0) {
+      if (!found) expired(w, lane);
 #pragma unroll
       for (int j = 0; j < NC; ++j) h[j] = found ? __uint_as_float((unsigned)far[max(found, 1) - 1][lane * NC + j]) : __builtin_nanf("");
 #pragma unroll 4
@@ -349,19 +365,20 @@ hipError_t fwd_go(const LruArgs& a, const int* cu, int N, int B, int T_, void* w
   const int end = cu ? N : B;
   for (int n = 0; n < end;) {
     SeqTab s;
+    const int begin = n == 0;
     n = make_seq_tab(s, cu, N, n, B, T_, kPart);
     const unsigned seqs = (unsigned)(s.n ? s.n : B);
     const dim3 grid((unsigned)s.items * slices), th(64 * kWaves);
     if ((unsigned)s.items == seqs) {   // no sequence has a second part
-      hipLaunchKernelGGL((lru_out_kernel<T, NC, kOne, kFull>), grid, th, 0, st, a, s, slices, ws);
+      hipLaunchKernelGGL((lru_out_kernel<T, NC, kOne, kFull>), grid, th, 0, st, a, s, slices, ws, begin);
     } else {
       const size_t words = (size_t)s.items * a.D * 3, groups = (words + 1023) / 1024;
-      hipLaunchKernelGGL(lru_fill_kernel, dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, st, static_cast<unsigned*>(ws), words);
+      hipLaunchKernelGGL(lru_fill_kernel, dim3((unsigned)(groups < 2048 ? groups : 2048)), dim3(256), 0, st, static_cast<unsigned*>(ws), words, begin);
       // Few chains at once wait for their states, hop by hop (65536 tokens of 512
       // channels: 87 us by kFar, 167 by kNear; 1024: 157 and 180); with many the
       // words read count (2048: 269 and 244; 4096: 492 and 425).
-      if (seqs * slices <= 8) hipLaunchKernelGGL((lru_out_kernel<T, NC, kFar, kFull>), grid, th, 0, st, a, s, slices, ws);
-      else hipLaunchKernelGGL((lru_out_kernel<T, NC, kNear, kFull>), grid, th, 0, st, a, s, slices, ws);
+      if (seqs * slices <= 8) hipLaunchKernelGGL((lru_out_kernel<T, NC, kFar, kFull>), grid, th, 0, st, a, s, slices, ws, begin);
+      else hipLaunchKernelGGL((lru_out_kernel<T, NC, kNear, kFull>), grid, th, 0, st, a, s, slices, ws, begin);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;

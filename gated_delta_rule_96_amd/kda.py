@@ -202,9 +202,9 @@ def alloc_workspace(B, T, H, dk, dv, dtype=torch.bfloat16, device="cuda", chunk=
 
 
 def workspace_error(workspace: torch.Tensor) -> int:
-    """Status of the last call on a prefill (or backward) workspace through
-    kda_fwd_status: 0, or KDA_ERR_INCOMPLETE (9) when a hand-off wait of the
-    fused kernel expired and the outputs are incomplete.  Synchronises the
+    """Status of the last call on a workspace of a prefill, of its backward or
+    of lru_fwd through kda_fwd_status: 0, or KDA_ERR_INCOMPLETE (9) when a
+    hand-off wait expired and the outputs are incomplete.  Synchronises the
     current stream."""
     s = int(lib().kda_fwd_status(_ptr(workspace), _stream(workspace.device)))
     if s not in (0, KDA_ERR_INCOMPLETE):

@@ -287,8 +287,8 @@ int kda_fwd_chunked_varlen(const void* q, const void* k, const void* v, const vo
 
 /*
  * Status of the last call that used `workspace` (a workspace of the fused
- * prefill calls: kda_fwd_chunked, _unbounded, _layer, _varlen, or of
- * kda_bwd_chunked, whose forward recompute it covers): synchronises
+ * prefill calls: kda_fwd_chunked, _unbounded, _layer, _varlen, of
+ * kda_bwd_chunked, whose forward recompute it covers, or of kda_lru_fwd): synchronises
  * `stream`, then returns KDA_OK, or KDA_ERR_INCOMPLETE if a hand-off wait
  * of that call expired (its outputs are incomplete).  workspace NULL: the
  * scratch of kda_fwd_chunked_noalloc on the current device.  Errors:
@@ -601,9 +601,10 @@ int kda_add_rms_norm_bwd(const void* h, long long ldh, const float* w, float eps
  * among its 8 neighbours in k: off by at most 2^-10 of the sum of the largest |a w|
  * of every 8, factors below 2^-6 taken as 2^-6 (1.4e-5 of its rms for normally
  * distributed rows).  That is below the output's rounding except where large
- * products cancel: small ones beside them are then lost.  Blocks are joined in fp32.  KDA_F32: all sums in fp32, at half
- * that rate.  One rounding.  sa sw is formed first, in fp32.  What is not finite
- * in a row of a or sa stays in that row of c, in a row of w in that column.
+ * products cancel: small ones beside them are then lost.  Blocks are joined in
+ * fp32.  KDA_F32: all sums in fp32, at half that rate.  One rounding.  sa sw is
+ * formed first, in fp32.  What is not finite in a row of a or sa stays in that row
+ * of c, in a row of w in that column.
  * The gradient of a's rows is the same call on 8-bit rows of c's gradient, w
  * transposed and sw transposed (tiles are square; N a multiple of 16 then).
  * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides), KDA_ERR_DTYPE,
@@ -630,7 +631,11 @@ int kda_gemm_fp8(const void* a, long long lda, const float* sa, long long lsa, c
  * its own and later tokens of its sequence only.
  * workspace: kda_lru_workspace_bytes (0 for invalid sizes; N = 0 for a
  * batch), 256-byte aligned, contents ignored on entry; calls that share one
- * must not overlap on the device.
+ * must not overlap on the device.  The parts of a sequence wait for each other,
+ * never for what other calls do; the waits are bounded (seconds) all the same.
+ * If one expires (calls that do overlap on a workspace), the rest of that sequence
+ * is NaN and the workspace's status word is set (kda_fwd_status,
+ * kda_fwd_status_word; cleared by every call).
  * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides, cu_seqlens, flags),
  *         KDA_ERR_DTYPE, KDA_ERR_ALIGN, KDA_ERR_WORKSPACE, KDA_ERR_OVERLAP,
  *         KDA_ERR_HIP.

@@ -143,3 +143,15 @@ def test_states_that_start_on_four_bytes(dtype):
         dht.copy_(k["dht"])
         g = kda.lru_bwd(*rows, k["c"], k["dy"].reshape(B, T, D), h0, dht, out=dict(gw, dh0=dh0, dx=torch.empty_like(gw["dx"])))
         assert torch.equal(g["dx"], gw["dx"]) and torch.equal(dh0, kda.lru_bwd(*rows, k["c"], k["dy"].reshape(B, T, D), k["h0"], k["dht"])["dh0"])
+
+
+@pytest.mark.parametrize("lens,D", [([100], 64), ([700], 64), ([700], 2048), ([128] * 200, 40), ([5] * 130 + [900], 40), ([900] + [5] * 200, 2048)], ids=lambda v: str(v)[:24])
+def test_status_word_of_the_workspace(lens, D):
+    # every schedule (sequences of one part; parts that look back far and near;
+    # several launches) clears what was there, and a sound call leaves it clear
+    k = tl.make(lens, D, BF, 301)
+    ws = torch.full((kda.lib().kda_lru_workspace_bytes(1, sum(lens), D, len(lens)),), 255, dtype=torch.uint8, device="cuda")
+    assert kda.workspace_error(ws) == kda.KDA_ERR_INCOMPLETE
+    kda.lru_fwd(k["x"], k["r"], k["i"], k["c"], k["h0"], cu_seqlens=tl.cuts(lens), workspace=ws)
+    kda.check_workspace(ws)
+    assert kda.workspace_error(ws) == 0
