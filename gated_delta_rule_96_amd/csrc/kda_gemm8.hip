@@ -8,7 +8,7 @@
 // The weights are the MFMA's left operand, so that a lane holds four
 // neighbouring outputs of one row (an 8- or 16-byte store) and needs one scale
 // per 16 rows instead of four.
-// Measured: 8192 x 12288 x 4096 391 us (2.11 PFLOP/s; a library's product of
+// Measured: 8192 x 12288 x 4096 389 to 400 us (2.1 PFLOP/s; a library's product of
 // such operands with one scale each 338), 8191 x 8480 x 4096 281, 256 rows of the
 // first 22.5, one row 11.  Of the large tile's time the matrix instructions take
 // 49%, and no single part binds it: without the loads to LDS it ran at 2.31
@@ -396,10 +396,13 @@ template <typename T> hipError_t tile_by(int i, const Gemm8Args& g, hipStream_t 
 template <typename T>
 hipError_t gemm8_go(const Gemm8Args& g, hipStream_t st) {
   // Few outputs: 16 rows and 16 or 32 columns a work-group where those are no
-  // more than the CUs (64 x 1024 x 4096: 8.7 us, 64 x 64 tiles 10.7, in fp32 8.9 and
-  // 15.6; 64 x 2048: 9.0 and 10.8, 9.4 and 15.8; 16 x 8192: 9.6 and 11.6).  Few rows of
-  // more outputs: 64 columns, so that the weights come in longer runs (12288
-  // outputs: 13.6, 32 columns 14.3, 16 columns 14.5).
+  // more than the CUs (us, beside 64 x 64 tiles: 64 x 1024 x 4096 7.7 and 13.4, in fp32
+  // 7.7 and 16.2; 64 x 2048: 8.8 and 13.6, 9.0 and 16.2; 16 x 8192: 9.9 and 12.4, 10.0
+  // and 16.1).  Few rows of more outputs: 64 columns, so that the weights come in
+  // longer runs (8 x 12288 x 4096: 13.1; 32 columns 15.5, 16 columns 15.2, tiles 13.4; in
+  // fp32 13.5; 15.6, 15.6, 16.6).  The rule goes by the work-groups alone and is not
+  // the best everywhere: 16 x 12288 in bf16 14.1, tiles 13.6; 1 x 8192 x 8192 by 32
+  // columns 19.5, by 16 15.0.
   const long long rb = (g.M + 15) / 16;
   if (rb * ((g.N + 15) / 16) <= 256) return rows_go<T, 1, 8>(g, st);
   if (rb * ((g.N + 31) / 32) <= 256) return rows_go<T, 2, 8>(g, st);

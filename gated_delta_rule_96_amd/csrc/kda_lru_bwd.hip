@@ -13,11 +13,12 @@
 // Three launches where a sequence has several parts (one otherwise): every
 // part's P, H, K; the states and the e that enter the parts; the gradients.  The
 // last walks the parts from the end, so that what the first read last is still
-// in the cache.  A single launch, as the forward's, would have to hold every
-// input between the state that comes from the left and the e from the right,
-// which the registers of the whole card cannot for more than a few thousand
-// tokens; so the inputs are read twice, and 22 bytes an element pass (bf16) where
-// the formulas need 14.
+// in the cache.  The inputs are read twice: 22 bytes an element pass (bf16) where
+// the formulas need 14.  (One launch that carries both ways would have to hold
+// every input between the state that comes from the left and the e from the right.
+// With the states known, from a walk over x, r and i alone or from the forward,
+// one launch could take the e from part to part as the forward takes the state, in
+// 20 bytes or 14; that has not been built.)
 //
 // Bound by HBM in both passes, in bf16 nearly as much by the exponentials and
 // roots (4 sequences of 8192 x 2048 with every gradient: sums 121 us, 4.4 TB/s;
@@ -189,7 +190,8 @@ __global__ __launch_bounds__(kChainThreads) void lru_bwd_chain_kernel(const LruB
 }
 
 // Gradients.  seg null: every sequence is one part.  dcp [items][D]: every
-// part's -sum of dg Sigmoid(r), or null.
+// part's -sum of dg Sigmoid(r), or null (32 tokens in fp32; the parts are summed in
+// 64 bits).
 template <typename T, int NC, bool kFull>
 __global__ __launch_bounds__(64 * kWaves, 3) void lru_bwd_out_kernel(const LruBwdArgs b, const SeqTab s, unsigned slices, const float* seg, float* dcp) {
   constexpr int R = kR;

@@ -170,7 +170,10 @@ __global__ __launch_bounds__(group_threads(L)) void norm_fwd_kernel(const NormAr
 
 // Gradients.  T: type of h, dh and dx; TG: type of dy.  The lanes that hold a
 // row walk their rows and keep the sums of dw of their channels; they are
-// partial rows of the workspace.
+// partial rows of the workspace.  (fp32, as the eight to 32 sums of a lane would
+// take twice the registers in 64 bits: up to rows / 512 terms one after the other,
+// off by that many units of the terms' absolute sum at worst; the partial rows are
+// summed in 64 bits.)
 template <typename T, typename TG, int NV, int L>
 __global__ __launch_bounds__(group_threads(L)) void norm_bwd_kernel(const NormArgs a, long long groups) {
   __shared__ float red[2][2][waves_of(L)];

@@ -565,7 +565,9 @@ int kda_ssm_bwd_chunked(const void* x, long long ldx, const void* dt, long long 
  * every 128 channels: s = max |n| / 448, y = e4m3(n / s), nearest with ties to
  * even.  A block whose largest |n| is below 2^-100 has s = 1 and zeros.  NaN
  * stays NaN; the largest value is taken over the others.
- * eps may be 0: a row of zeros is then NaN.
+ * eps may be 0: a row of zeros is then NaN.  The mean of squares is fp32: a row
+ * whose rms is beyond 1.8e19 gives n = 0, and with eps = 0 one whose rms is below
+ * 1e-18 loses accuracy and is not finite where its squares vanish.
  * D a multiple of 8, at most 16384; row strides in multiples of 16 bytes.
  * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides, eps), KDA_ERR_DTYPE,
  *         KDA_ERR_ALIGN, KDA_ERR_UNSUPPORTED (D), KDA_ERR_OVERLAP, KDA_ERR_HIP.
@@ -605,8 +607,10 @@ int kda_add_rms_norm_bwd(const void* h, long long ldh, const float* w, float eps
  * fp32.  KDA_F32: all sums in fp32, at half that rate.  One rounding.  sa sw is
  * formed first, in fp32.  What is not finite in a row of a or sa stays in that row
  * of c, in a row of w in that column.
- * The gradient of a's rows is the same call on 8-bit rows of c's gradient, w
+ * The gradient of a's rows is the same call on 8-bit rows of c's gradient (which
+ * the caller makes: kda_add_rms_norm makes 8-bit rows of a norm only), w
  * transposed and sw transposed (tiles are square; N a multiple of 16 then).
+ * The gradient of the weights is not offered.
  * Errors: KDA_ERR_NULL, KDA_ERR_SHAPE (sizes, strides), KDA_ERR_DTYPE,
  *         KDA_ERR_ALIGN, KDA_ERR_UNSUPPORTED (K), KDA_ERR_OVERLAP, KDA_ERR_HIP.
  */
