@@ -33,7 +33,7 @@ const char* kda_status_str(int s) {
     case KDA_ERR_RANGE: return "input value out of range (log-decay outside [gmin, 0], or gmin outside [-5, 0))";
     case KDA_ERR_HIP: return "HIP launch failed";
     case KDA_ERR_INCOMPLETE:
-      return "the fused prefill gave up on a hand-off wait (GPU shared with other work?): outputs incomplete";
+      return "a hand-off wait was given up (GPU shared with other work, or calls that overlap on a workspace?): outputs incomplete";
     case KDA_ERR_OVERLAP: return "an output overlaps a tensor it must be apart from";
     default: return "unknown status";
   }

@@ -86,8 +86,8 @@ typedef enum kda_status {
   KDA_ERR_RANGE = 7,       /* a value outside its documented range (KDA_VALIDATE=1 */
                            /* checks, and gmin of kda_prepare_decay)              */
   KDA_ERR_HIP = 8,         /* a HIP launch failed (hipGetLastError)               */
-  KDA_ERR_INCOMPLETE = 9,  /* kda_fwd_status: a hand-off wait of the fused        */
-                           /* prefill expired; the call's outputs are incomplete  */
+  KDA_ERR_INCOMPLETE = 9,  /* kda_fwd_status: a hand-off wait of the fused prefill */
+                           /* or of kda_lru_fwd expired; outputs are incomplete   */
   KDA_ERR_OVERLAP = 10     /* an output overlaps a tensor it must be apart from   */
                            /* (the token-mixing and scan calls below)             */
 } kda_status;
@@ -549,7 +549,8 @@ int kda_ssm_bwd_chunked(const void* x, long long ldx, const void* dt, long long 
  * the norm of the residual stream, the projection of its rows in 8 bits, and
  * the gated linear recurrence with one state a channel.  Conventions as for
  * the operators around the recurrence (rows with a stride, fp32 parameters,
- * outputs apart from inputs, no atomics: the same call gives the same bits).
+ * outputs apart from inputs; nothing is summed by atomics: the same call gives the
+ * same bits).  The opt-in range check is not made here.
  */
 
 /*
